@@ -69,7 +69,9 @@ typedef enum {
   NYS_ERR_UNSUPPORTED = -4, /* no GPU of compute capability 10.3 current   */
   NYS_ERR_NOMEM = -5,       /* workspace allocation failed / too small     */
   NYS_ERR_CUDA = -6,        /* a CUDA runtime call or launch failed        */
-  NYS_ERR_TIMEOUT = -7      /* a device-side bounded wait ran out          */
+  NYS_ERR_TIMEOUT = -7,     /* a device-side bounded wait ran out          */
+  NYS_ERR_INDEX = -8        /* a device-side index (page, position, length)
+                               lay outside its range and was skipped       */
 } nys_status_t;
 
 /*
@@ -311,10 +313,183 @@ int nystrom_plan_describe(int B, int H, int n, int d, int m, int iters,
                           int conv_ks, int dtype, char* buf, int len);
 
 /*
+ * Queries and keys on their way into attention, and the cache that keeps keys
+ * and values for later queries. These operators take heads of any stride:
+ * a row is the d contiguous channels of one (batch entry, head, token), and
+ * nys_strides_t gives the distance between rows in ELEMENTS along each of the
+ * three, so [B][H][n][d] (the layout of the forward pass) and [B][n][H][d]
+ * (a projection's output, or a slice of a packed one) are both read and
+ * written in place. Row addresses are 16-byte aligned (else NYS_ERR_ALIGN),
+ * strides are not negative, and rows of an output do not overlap.
+ */
+typedef struct { long long batch, head, token; } nys_strides_t;
+
+/*
+ * nystrom_qk_norm_rope_fwd - per-head RMS norm of queries and keys and the
+ * rotation of their positions, in one pass. For each row x of q (k alike):
+ *   z = w * x / sqrt(mean(x^2) + eps)      (norm = 0: z = x)
+ *   (y_a, y_b) = (z_a cos t - z_b sin t, z_b cos t + z_a sin t)
+ * for the rot/2 pairs (a, b) of channels among the first `rot`, with the angle
+ *   t = position on pair i's axis * inv_freq[i];
+ * channels from rot on pass through. Pair i is channels (i, i + rot/2) for
+ * NYS_ROPE_HALVES and (2i, 2i + 1) for NYS_ROPE_PAIRS. The first section[0]
+ * pairs turn with axis 0, the next section[1] with axis 1, and so on (text:
+ * one axis; images and video: time, height, width).
+ * positions: device int32 [axes][B][n], any value; or NULL for positions
+ *   0 .. n-1 on every axis. inv_freq_host: HOST double [rot/2], radians per
+ *   position (read during the call). Angles are reduced exactly, as 64-bit
+ *   fractions of a turn, so far positions lose nothing.
+ * q_weight, k_weight: device float [d], or NULL for all ones.
+ * q, k in `dtype` with strides p->q, p->k; q_out, k_out likewise with
+ *   p->q_out, p->k_out. An output may be its own input (same pointer, same
+ *   strides), else they do not overlap. k (and k_out) may be NULL with Hk = 0.
+ * Arithmetic in fp32, one rounding to dtype at the end.
+ * Shape rules (else NYS_ERR_SHAPE): B, n, Hq >= 1, Hk >= 0, d % 8 == 0,
+ *   8 <= d <= 128, rot even, 0 <= rot <= d, 1 <= axes <= 4, sections >= 0 that
+ *   sum to rot/2, B*n < 2^31, (Hq + Hk) <= 65535. NYS_ERR_ARG for NULL
+ *   pointers, an unknown pairing or dtype, a negative or non-finite eps, a
+ *   non-finite frequency.
+ *
+ * nystrom_qk_norm_rope_bwd - its gradients: from the inputs q, k (strides
+ * p->q, p->k) and the gradients gq, gk of the outputs (strides p->q_out,
+ * p->k_out), with g the rotation undone on a row of gq, h = x / sqrt(mean(x^2)
+ * + eps):
+ *   dx = (w g - h mean(w g h)) / sqrt(mean(x^2) + eps),  dw = sum of g h
+ * over all rows (norm = 0: dx = g). dq, dk in `dtype`, strides p->dq, p->dk;
+ * dq may be gq and dk may be gk (same strides). dq_weight, dk_weight: device
+ * float [d], overwritten; NULL if not wanted. The sums are fp32 in a fixed
+ * order: the same call gives the same bits.
+ * workspace: device, 256-byte aligned, ws_bytes >=
+ * nystrom_qk_norm_rope_workspace_bytes(p); needed only when a weight gradient
+ * is asked for. NULL uses the library's cached workspace, which a stream
+ * under capture may not do (NYS_ERR_ARG): a captured call brings its own.
+ */
+typedef enum { NYS_ROPE_HALVES = 0, NYS_ROPE_PAIRS = 1 } nys_rope_pairing_t;
+typedef struct {
+  int B, n, Hq, Hk, d;
+  int rot;        /* rotated channels, from channel 0 on */
+  int axes;       /* 1 .. 4 */
+  int section[4]; /* pairs per axis */
+  int pairing;    /* nys_rope_pairing_t */
+  int norm;       /* 1: RMS norm first; 0: rotation alone */
+  int dtype;
+  float eps;
+  nys_strides_t q, k, q_out, k_out;
+  nys_strides_t dq, dk; /* backward only */
+} nys_qk_rope_t;
+int nystrom_qk_norm_rope_fwd(const nys_qk_rope_t* p, const void* q, const void* k,
+                             const float* q_weight, const float* k_weight, const int* positions,
+                             const double* inv_freq_host, void* q_out, void* k_out,
+                             nys_stream_t stream);
+size_t nystrom_qk_norm_rope_workspace_bytes(const nys_qk_rope_t* p);
+int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* p, const void* q, const void* k,
+                             const void* gq, const void* gk, const float* q_weight,
+                             const float* k_weight, const int* positions,
+                             const double* inv_freq_host, void* dq, void* dk, float* dq_weight,
+                             float* dk_weight, void* workspace, size_t ws_bytes,
+                             nys_stream_t stream);
+
+/*
+ * A key/value cache held in 4 bits. Each 32 consecutive channels of a token's
+ * key (or value) share one scale: with a the largest magnitude among them,
+ *   scale = a / 7 rounded towards zero to bfloat16,
+ *   code  = x / scale rounded to the nearest integer (ties to even), in -7..7,
+ * and the cache stands for code * scale, so nothing grows in magnitude and no
+ * value is off by more than half a scale. A block that holds an infinity or a
+ * NaN gets a NaN scale and reads back as NaN.
+ * The cache is a pool of pages; page p of sequence b is block_table[b][p], an
+ * index into the pool, and holds tokens [p page_size, (p+1) page_size). In
+ * memory the pool is [num_pages][Hk][page_size/16] blocks of 16 tokens, 18*d
+ * bytes each (4.5 bits per value):
+ *   key codes 8d bytes | key scales d | value codes 8d | value scales d.
+ * Scales are bfloat16 [d/32][16 tokens]. A code + 8 is a 4-bit field; even
+ * channels sit in the low half of a byte. With token r of the block, channel
+ * c, group y = c/32, w = c%32: the key field is in byte
+ *   r (d/2) + (w/8)(d/8) + 4y + (w%8)/2
+ * of the key codes, the value field in byte
+ *   (r/8) 4d + ((w/4) 4 + (r%8)/2)(d/8) + (r%2)(d/16) + 2y + (w%4)/2
+ * of the value codes (the order in which the attention's matrix instructions
+ * take them).
+ * data: device, 16-byte aligned, nystrom_kv4_cache_bytes(...) bytes, never
+ * initialised by the library: tokens that were not written hold whatever the
+ * memory held, and no operator lets them into a result.
+ * block_table: device int32 [B][max_pages]. Sequences may share pages that
+ * are only read. Shape rules: num_pages, max_pages, Hk >= 1; page_size a
+ * multiple of 16 in 16 .. 4096; d in {32, 64, 128}; max_pages * page_size <
+ * 2^31.
+ */
+typedef struct {
+  void* data;
+  const int* block_table;
+  int num_pages, max_pages, page_size, Hk, d;
+} nys_kv4_cache_t;
+size_t nystrom_kv4_cache_bytes(int num_pages, int page_size, int Hk, int d);
+
+/*
+ * nystrom_kv4_write - quantises rows i < counts[b] of k, v [B, Hk, n, d] (any
+ * strides, NYS_FP32 or NYS_BF16) into the cache at positions starts[b] + i.
+ * nystrom_kv4_read - the reverse: what the cache holds at positions starts[b]
+ * + i, in `dtype`, to rows i < counts[b] of k, v; rows behind are left as they
+ * were. (Read into [B][H][n][d], a cached context is the k and v of
+ * nystrom_attn_fwd.)
+ * starts: device int32 [B], or NULL for 0. counts: device int32 [B], or NULL
+ * for n; a count above n is taken as n, one below 0 as 0.
+ * A page outside the pool or a position outside the block table is skipped
+ * (its rows of a read come back as zeros) and makes nystrom_get_status report
+ * NYS_ERR_INDEX. Two sequences of one write must not name the same
+ * page for positions they write.
+ * B, n >= 1, B <= 65535 (else NYS_ERR_SHAPE).
+ */
+int nystrom_kv4_write(const nys_kv4_cache_t* cache, const void* k, const void* v,
+                      const nys_strides_t* k_strides, const nys_strides_t* v_strides,
+                      const int* starts, const int* counts, int B, int n, int dtype,
+                      nys_stream_t stream);
+int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
+                     const nys_strides_t* k_strides, const nys_strides_t* v_strides,
+                     const int* starts, const int* counts, int B, int n, int dtype,
+                     nys_stream_t stream);
+
+/*
+ * nystrom_kv4_attn_fwd - attention of nq new queries of each sequence over its
+ * cached keys and values:
+ *   out = softmax(q K^T * scale) V
+ * q, out [B, Hq, nq, d] in `dtype`, any strides; query head h reads cache head
+ * h / (Hq/Hk). lengths: device int32 [B], the tokens of each sequence in the
+ * cache (the new ones included). q_counts: device int32 [B], the real queries
+ * of each sequence (NULL: nq); rows of out behind them are left as they were.
+ * causal = 1: query i of c sees keys 0 .. length - c + i; causal = 0: all
+ * `length` keys. A query that sees no key gives zeros. max_length: an upper
+ * bound of the lengths that the host knows; the launch is planned by it.
+ * A length outside 0 .. min(max_length, max_pages * page_size) is brought to
+ * the nearer end, a page outside the pool counts as keys that are not seen;
+ * both make nystrom_get_status report NYS_ERR_INDEX. scale: 0 means 1/sqrt(d).
+ * Scores, the softmax and all sums are fp32. For NYS_BF16 the probabilities
+ * enter the product with V as bf16; for NYS_FP32 queries and probabilities
+ * enter as sums of 16-bit terms that keep at least 22 and 24 bits.
+ * Shape rules: B, nq, Hk >= 1, Hq a multiple of Hk, Hq <= 65535, B <= 65535,
+ * max_length >= 0, nq * (Hq/Hk) < 2^30 (else NYS_ERR_SHAPE); scale finite
+ * (else NYS_ERR_ARG).
+ * workspace: device, 256-byte aligned, ws_bytes >=
+ * nystrom_kv4_attn_workspace_bytes(...) (which may be 0), not shared with a
+ * call that may run at the same time. NULL uses the library's cached
+ * workspace, which a stream under capture may not do (NYS_ERR_ARG).
+ * nystrom_get_status reports NYS_ERR_INDEX and NYS_ERR_TIMEOUT of these cache
+ * operators until they are read: they are not cleared by a later call.
+ */
+size_t nystrom_kv4_attn_workspace_bytes(const nys_kv4_cache_t* cache, int B, int nq, int Hq,
+                                        int max_length, int dtype);
+int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
+                         const nys_strides_t* q_strides, const nys_strides_t* out_strides,
+                         const int* lengths, const int* q_counts, int B, int nq, int Hq,
+                         int max_length, int causal, float scale, int dtype, void* workspace,
+                         size_t ws_bytes, nys_stream_t stream);
+
+/*
  * nystrom_get_status - waits for `stream`, then returns and clears the
  * device-side status word of the most recent call on the current device
- * (NYS_OK, or NYS_ERR_TIMEOUT if a bounded wait inside a kernel ran out).
- * Returns NYS_ERR_CUDA if the stream reports an error.
+ * (NYS_OK, or NYS_ERR_TIMEOUT if a bounded wait inside a kernel ran out),
+ * then that of the cache operators (nystrom_kv4_*: NYS_ERR_INDEX or
+ * NYS_ERR_TIMEOUT since it was last read). Returns NYS_ERR_CUDA if the stream reports an error.
  */
 int nystrom_get_status(nys_stream_t stream);
 

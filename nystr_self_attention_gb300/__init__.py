@@ -13,4 +13,8 @@ from ._binding import (  # noqa: F401
     nystrom_attn_stage_offset, nystrom_attn_workspace_bytes, nystrom_get_status,
     nystrom_last_error_string, nystrom_launch_count, nystrom_mha_fwd, nystrom_mha_workspace_bytes, nystrom_plan_describe, nystrom_profile_enable,
     nystrom_profile_read, nystrom_strerror,
+    NYS_ERR_INDEX, NYS_ROPE_HALVES, NYS_ROPE_PAIRS, NysKv4Cache, NysQkRope, NysStrides,
+    NystromKv4Cache, nystrom_kv4_attn_fwd, nystrom_kv4_attn_workspace_bytes, nystrom_kv4_cache_bytes,
+    nystrom_kv4_read, nystrom_kv4_write, nystrom_qk_norm_rope_bwd, nystrom_qk_norm_rope_fwd,
+    nystrom_qk_norm_rope_workspace_bytes,
 )

@@ -10,6 +10,8 @@ import os
 NYS_FP32, NYS_BF16 = 0, 1
 NYS_OK, NYS_ERR_ARG, NYS_ERR_SHAPE, NYS_ERR_ALIGN = 0, -1, -2, -3
 NYS_ERR_UNSUPPORTED, NYS_ERR_NOMEM, NYS_ERR_CUDA, NYS_ERR_TIMEOUT = -4, -5, -6, -7
+NYS_ERR_INDEX = -8
+NYS_ROPE_HALVES, NYS_ROPE_PAIRS = 0, 1
 NYS_STAGE_Q_TILDE, NYS_STAGE_K_TILDE, NYS_STAGE_G, NYS_STAGE_A_S, NYS_STAGE_W, NYS_STAGE_Z = range(6)
 NYS_CONV_PER_HEAD, NYS_CONV_PER_CHANNEL = 0, 1
 NYS_CSTAGE_ASSIGN, NYS_CSTAGE_CENTROIDS_PREV, NYS_CSTAGE_CENTROIDS, NYS_CSTAGE_G = range(4)
@@ -19,6 +21,27 @@ _lib = None
 
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+
+
+class NysStrides(ctypes.Structure):
+    """nys_strides_t: distances between rows, in elements."""
+    _fields_ = [("batch", ctypes.c_longlong), ("head", ctypes.c_longlong), ("token", ctypes.c_longlong)]
+
+
+class NysQkRope(ctypes.Structure):
+    """nys_qk_rope_t."""
+    _fields_ = [("B", _I), ("n", _I), ("Hq", _I), ("Hk", _I), ("d", _I), ("rot", _I), ("axes", _I),
+                ("section", _I * 4), ("pairing", _I), ("norm", _I), ("dtype", _I),
+                ("eps", ctypes.c_float), ("q", NysStrides), ("k", NysStrides),
+                ("q_out", NysStrides), ("k_out", NysStrides), ("dq", NysStrides), ("dk", NysStrides)]
+
+
+class NysKv4Cache(ctypes.Structure):
+    """nys_kv4_cache_t."""
+    _fields_ = [("data", _P), ("block_table", _P), ("num_pages", _I), ("max_pages", _I),
+                ("page_size", _I), ("Hk", _I), ("d", _I)]
+
+
 _SIG = {
     "nystrom_attn_fwd": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P]),
     "nystrom_attn_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I]),
@@ -43,6 +66,16 @@ _SIG = {
                                         ctypes.c_size_t, _P]),
     "nystrom_mha_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _P,
                              ctypes.c_size_t, _P]),
+    "nystrom_qk_norm_rope_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P]),
+    "nystrom_qk_norm_rope_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "nystrom_qk_norm_rope_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P,
+                                      ctypes.c_size_t, _P]),
+    "nystrom_kv4_cache_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "nystrom_kv4_write": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "nystrom_kv4_read": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _P]),
+    "nystrom_kv4_attn_workspace_bytes": (ctypes.c_size_t, [_P, _I, _I, _I, _I, _I]),
+    "nystrom_kv4_attn_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, ctypes.c_float, _I,
+                                  _P, ctypes.c_size_t, _P]),
     "nystrom_profile_read": (_I, [_I, ctypes.c_char_p, _I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_longlong)]),
 }
@@ -270,3 +303,231 @@ def nystrom_profile_read(max_kernels: int = 16) -> dict:
         nm = names.raw[i * name_len:(i + 1) * name_len].split(b"\0", 1)[0].decode()
         out[nm] = (ms[i], cnt[i])
     return out
+
+
+# ------------------------------------------- around a cached attention layer
+#
+# These take torch tensors whose strides they pass on: heads are [B, H, n, d]
+# views with contiguous channels (a token-major [B, n, H, d] tensor or a slice
+# of a packed projection: its transpose).
+
+def _code(t) -> int:
+    import torch
+    if t.dtype == torch.bfloat16:
+        return NYS_BF16
+    if t.dtype == torch.float32:
+        return NYS_FP32
+    raise ValueError("dtype must be float32 or bfloat16")
+
+
+def _heads(name, t, like=None, shape=None):
+    """Strides of a [B, H, n, d] view. An axis with one entry has no stride."""
+    if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
+        raise ValueError(f"{name} must be a CUDA tensor [B, H, n, d] with contiguous channels")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if like is not None and (t.dtype != like.dtype or t.device != like.device):
+        raise ValueError(f"{name} must have the dtype and device of the other heads")
+    n = t.shape
+    s = t.stride()
+    return NysStrides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+
+
+def _flat(name, t, dtype, shape, device):
+    """A contiguous device array of the given type and shape, or None."""
+    if t is None:
+        return None
+    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    return t.data_ptr()
+
+
+def _on_current_device(t):
+    import torch
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+
+
+def _scratch(nbytes, workspace, device, stream):
+    """(pointer, bytes, tensor to keep until the launch) of a call's workspace:
+    the caller's, or memory of torch's allocator that belongs to the call's
+    stream, so that it is reused only behind the call."""
+    import torch
+    if workspace is not None:
+        if workspace.device != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
+    if nbytes == 0:
+        return None, 0, None
+    if stream is None:
+        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    else:
+        handle = stream if isinstance(stream, int) else stream.cuda_stream
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
+            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return t.data_ptr(), nbytes, t
+
+
+def _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing):
+    import numpy as np
+    import torch
+    strides = _heads("q", q)
+    _on_current_device(q)
+    B, Hq, n, d = q.shape
+    Hk = 0 if k is None else k.shape[1]
+    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
+    if freq.ndim != 1:
+        raise ValueError("inv_freq must be one-dimensional")
+    sections = [len(freq)] if sections is None else list(sections)
+    if len(sections) > 4:
+        raise ValueError("at most four axes")
+    a = NysQkRope(B, n, Hq, Hk, d, 2 * len(freq), len(sections), (_I * 4)(*sections), pairing,
+                  1 if norm else 0, _code(q), eps, strides)
+    pos = _flat("positions", positions, torch.int32, (len(sections), B, n), q.device)
+    return a, freq, pos
+
+
+def nystrom_qk_norm_rope_fwd(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, *,
+                             sections=None, pairing=NYS_ROPE_HALVES, norm=True, eps=1e-6, stream=None):
+    """Per-head RMS norm and position rotation of queries q [B, Hq, n, d] and
+    keys k [B, Hk, n, d] (or None) into q_out, k_out (see include/nystrom.h).
+    positions: int32 [axes, B, n] on the device, or None for 0 .. n-1.
+    inv_freq: host sequence of rot/2 radians per position. sections: pairs per
+    axis (None: one axis). q_weight, k_weight: float32 [d], or None."""
+    import torch
+    lib = load_library()
+    a, freq, pos = _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing)
+    a.q_out = _heads("q_out", q_out, q, q.shape)
+    if k is not None:
+        a.k = _heads("k", k, q, (q.shape[0], k.shape[1], q.shape[2], q.shape[3]))
+        a.k_out = _heads("k_out", k_out, q, k.shape)
+    d = (q.shape[3],)
+    return _check(lib.nystrom_qk_norm_rope_fwd(
+        ctypes.byref(a), q.data_ptr(), None if k is None else k.data_ptr(),
+        _flat("q_weight", q_weight, torch.float32, d, q.device),
+        _flat("k_weight", k_weight, torch.float32, d, q.device), pos, freq.ctypes.data,
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(), _stream(stream)),
+        "nystrom_qk_norm_rope_fwd")
+
+
+def nystrom_qk_norm_rope_workspace_bytes(desc: NysQkRope) -> int:
+    return load_library().nystrom_qk_norm_rope_workspace_bytes(ctypes.byref(desc))
+
+
+def nystrom_qk_norm_rope_bwd(q, k, gq, gk, dq, dk, positions, inv_freq, q_weight=None, k_weight=None,
+                             dq_weight=None, dk_weight=None, *, sections=None, pairing=NYS_ROPE_HALVES,
+                             norm=True, eps=1e-6, workspace=None, stream=None):
+    """Gradients of nystrom_qk_norm_rope_fwd: from its inputs q, k and the
+    outputs' gradients gq, gk into dq, dk (which may be gq, gk) and, where
+    given, dq_weight, dk_weight (float32 [d])."""
+    import torch
+    lib = load_library()
+    a, freq, pos = _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing)
+    a.q_out = _heads("gq", gq, q, q.shape)
+    a.dq = _heads("dq", dq, q, q.shape)
+    if k is not None:
+        a.k = _heads("k", k, q, (q.shape[0], k.shape[1], q.shape[2], q.shape[3]))
+        a.k_out = _heads("gk", gk, q, k.shape)
+        a.dk = _heads("dk", dk, q, k.shape)
+    d, f32, dev = (q.shape[3],), torch.float32, q.device
+    need = 0
+    if dq_weight is not None or dk_weight is not None:
+        need = lib.nystrom_qk_norm_rope_workspace_bytes(ctypes.byref(a))
+    ws, nbytes, keep = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_qk_norm_rope_bwd(
+        ctypes.byref(a), q.data_ptr(), None if k is None else k.data_ptr(), gq.data_ptr(),
+        None if k is None else gk.data_ptr(), _flat("q_weight", q_weight, f32, d, dev),
+        _flat("k_weight", k_weight, f32, d, dev), pos, freq.ctypes.data, dq.data_ptr(),
+        None if k is None else dk.data_ptr(), _flat("dq_weight", dq_weight, f32, d, dev),
+        _flat("dk_weight", dk_weight, f32, d, dev), ws, nbytes, _stream(stream))
+    del keep
+    return _check(rc, "nystrom_qk_norm_rope_bwd")
+
+
+def nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d) -> int:
+    return load_library().nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d)
+
+
+class NystromKv4Cache:
+    """A 4-bit key/value cache over the caller's memory (format: see
+    include/nystrom.h). data: uint8 CUDA tensor, a whole number of pages;
+    block_table: int32 [B, max_pages], sequence b's pages in order."""
+
+    def __init__(self, data, block_table, page_size, Hk, d):
+        import torch
+        page = nystrom_kv4_cache_bytes(1, page_size, Hk, d)
+        if page == 0:
+            raise NystromError(NYS_ERR_SHAPE, "NystromKv4Cache")
+        if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous():
+            raise ValueError("data must be a contiguous uint8 CUDA tensor")
+        pages = data.numel() // page
+        if pages < 1 or pages * page != data.numel():
+            raise ValueError(f"data must be a whole number of {page}-byte pages")
+        if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != data.device
+                or not block_table.is_contiguous()):
+            raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages] beside the data")
+        self.data, self.block_table = data, block_table
+        self.B = block_table.shape[0]
+        self.struct = NysKv4Cache(data.data_ptr(), block_table.data_ptr(), pages, block_table.shape[1],
+                                  page_size, Hk, d)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _kv4_io(cache, k, v, starts, counts):
+    import torch
+    _on_current_device(cache.data)
+    B, n, dev = cache.B, k.shape[2], cache.data.device
+    shape = (B, cache.struct.Hk, n, cache.struct.d)
+    ks, vs = _heads("k", k, None, shape), _heads("v", v, k, shape)
+    if k.device != dev:
+        raise ValueError("k and v must be on the cache's device")
+    return (k.data_ptr(), v.data_ptr(), ctypes.byref(ks), ctypes.byref(vs),
+            _flat("starts", starts, torch.int32, (B,), dev), _flat("counts", counts, torch.int32, (B,), dev),
+            B, n, _code(k))
+
+
+def nystrom_kv4_write(cache, k, v, starts=None, counts=None, stream=None):
+    """Quantises rows i < counts[b] of k, v [B, Hk, n, d] into the cache at
+    positions starts[b] + i (int32 device tensors; None: n rows, from 0)."""
+    return _check(load_library().nystrom_kv4_write(cache.ref, *_kv4_io(cache, k, v, starts, counts),
+                                                   _stream(stream)), "nystrom_kv4_write")
+
+
+def nystrom_kv4_read(cache, k, v, starts=None, counts=None, stream=None):
+    """What the cache holds at positions starts[b] + i to rows i < counts[b]
+    of k, v [B, Hk, n, d]; rows behind are left as they were."""
+    return _check(load_library().nystrom_kv4_read(cache.ref, *_kv4_io(cache, k, v, starts, counts),
+                                                  _stream(stream)), "nystrom_kv4_read")
+
+
+def nystrom_kv4_attn_workspace_bytes(cache, B, nq, Hq, max_length, dtype) -> int:
+    return load_library().nystrom_kv4_attn_workspace_bytes(cache.ref, B, nq, Hq, max_length, dtype)
+
+
+def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, causal=True, scale=None,
+                         workspace=None, stream=None):
+    """Attention of queries q [B, Hq, nq, d] over the cached tokens of each
+    sequence into out (same shape). lengths: int32 [B], tokens in the cache;
+    max_length: an upper bound of them; q_counts: int32 [B], real queries
+    (None: nq); scale: None for 1/sqrt(d)."""
+    import torch
+    lib = load_library()
+    if scale == 0:
+        raise ValueError("scale must not be zero (None: 1/sqrt(d))")
+    _on_current_device(cache.data)
+    dev = cache.data.device
+    qs = _heads("q", q)
+    B, Hq, nq, d = q.shape
+    if B != cache.B or d != cache.struct.d or q.device != dev:
+        raise ValueError("q must be [B, Hq, nq, d] with the cache's B and d, on its device")
+    os_ = _heads("out", out, q, q.shape)
+    dt = _code(q)
+    need = lib.nystrom_kv4_attn_workspace_bytes(cache.ref, B, nq, Hq, max_length, dt)
+    ws, nbytes, keep = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_kv4_attn_fwd(
+        cache.ref, q.data_ptr(), out.data_ptr(), ctypes.byref(qs), ctypes.byref(os_),
+        _flat("lengths", lengths, torch.int32, (B,), dev),
+        _flat("q_counts", q_counts, torch.int32, (B,), dev), B, nq, Hq, max_length,
+        1 if causal else 0, 0.0 if scale is None else scale, dt, ws, nbytes, _stream(stream))
+    del keep
+    return _check(rc, "nystrom_kv4_attn_fwd")

@@ -117,6 +117,11 @@ struct DeviceCache {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* last_ws = nullptr;  // status word of the most recent call
+  // the operators around a cached attention layer: their cached workspace
+  // and their status word (operator_workspace, operator_status)
+  void* op_ws = nullptr;
+  size_t op_ws_bytes = 0;
+  int* op_status = nullptr;
   void* stage = nullptr;    // host-entry staging buffers
   size_t stage_bytes = 0;
   // host entry: one call at a time per device (it owns the staging buffers);
@@ -172,6 +177,38 @@ void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc) {
   std::lock_guard<std::mutex> lk(g_dev[dev].mu);
   *rc = ensure_buffer(&g_dev[dev].ws, &g_dev[dev].ws_bytes, bytes, stream);
   return *rc == NYS_OK ? g_dev[dev].ws : nullptr;
+}
+
+namespace {
+// Set by the cache operators' kernels, read and cleared by
+// nystrom_get_status. A device variable: no call has to allocate or clear it.
+__device__ int g_op_status;
+}  // namespace
+
+int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out) {
+  // a graph would keep the buffer's address past the next growth
+  cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
+    cudaGetLastError();
+    return NYS_ERR_ARG;
+  }
+  if (capturing != cudaStreamCaptureStatusNone) return NYS_ERR_ARG;
+  std::lock_guard<std::mutex> lk(g_dev[dev].mu);
+  const int rc = ensure_buffer(&g_dev[dev].op_ws, &g_dev[dev].op_ws_bytes, bytes, stream);
+  if (rc == NYS_OK) *out = g_dev[dev].op_ws;
+  return rc;
+}
+
+int operator_status(int dev, int** out) {
+  std::lock_guard<std::mutex> lk(g_dev[dev].mu);
+  if (!g_dev[dev].op_status) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, g_op_status);
+    if (e != cudaSuccess) return set_cuda_error(e);
+    g_dev[dev].op_status = static_cast<int*>(p);
+  }
+  *out = g_dev[dev].op_status;
+  return NYS_OK;
 }
 
 int run(const Shape& s, const void* q, const void* k, const void* v, const float* conv_w,
@@ -451,17 +488,22 @@ int nystrom_get_status(nys_stream_t stream) {
   if (rc != NYS_OK) return rc;
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return set_cuda_error(e);
-  void* ws = nullptr;
+  void* words[2];  // the most recent forward call's, the cache operators'
   {
     std::lock_guard<std::mutex> lk(g_dev[dev].mu);
-    ws = g_dev[dev].last_ws;
+    words[0] = g_dev[dev].last_ws;
+    words[1] = g_dev[dev].op_status;
   }
-  if (!ws) return NYS_OK;
-  int status = 0;
-  if ((e = cudaMemcpy(&status, ws, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess)
-    return set_cuda_error(e);
-  if (status != 0 && (e = cudaMemset(ws, 0, sizeof(int))) != cudaSuccess) return set_cuda_error(e);
-  return status;
+  for (void* word : words) {
+    if (!word) continue;
+    int status = 0;
+    if ((e = cudaMemcpy(&status, word, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess)
+      return set_cuda_error(e);
+    if (status == 0) continue;
+    if ((e = cudaMemset(word, 0, sizeof(int))) != cudaSuccess) return set_cuda_error(e);
+    return status;
+  }
+  return NYS_OK;
 }
 
 const char* nystrom_strerror(int code) {
@@ -474,6 +516,7 @@ const char* nystrom_strerror(int code) {
     case NYS_ERR_NOMEM: return "workspace allocation failed or too small";
     case NYS_ERR_CUDA: return "CUDA runtime error";
     case NYS_ERR_TIMEOUT: return "a device-side bounded wait ran out";
+    case NYS_ERR_INDEX: return "a device-side page, position or length was out of range";
     default: return "unknown status code";
   }
 }

@@ -97,6 +97,13 @@ int begin_call(char* ws, const Layout& L, cudaStream_t stream, int dev, bool cle
 // The library's cached workspace of this device, grown to `bytes` (NULL and
 // *rc < 0 on failure).
 void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc);
+// The cached workspace of the operators around a cached attention layer, in a
+// buffer of its own (nystrom_get_status reads the other one's first word).
+// NYS_ERR_ARG while `stream` is being captured.
+int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out);
+// Device address of those operators' status word on device `dev` (current):
+// zero until a kernel sets it, cleared when nystrom_get_status reports it.
+int operator_status(int dev, int** out);
 // Clears the status word (unless told not to) and enqueues the forward
 // pass with workspace `ws`.
 int run(const Shape& s, const void* q, const void* k, const void* v, const float* conv_w,

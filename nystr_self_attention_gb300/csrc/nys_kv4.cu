@@ -1,0 +1,373 @@
+// The 4-bit key/value cache: tokens quantised as they are written, and read
+// back (declared, with the format, in include/nystrom.h). Both directions are
+// bound by HBM: 2 d elements on one side, 9 d / 8 bytes on the other, per token
+// and head.
+//
+// A warp handles one block of 16 tokens of one head: d/8 lanes per row, each
+// eight channels (16 bytes of bf16), so four lanes share a scale and agree on
+// it by two shuffles. The block's 18 d bytes are put together (or taken
+// apart) in shared memory and cross to or from HBM as whole 16-byte vectors;
+// a block that gets only some of its tokens is written piece by piece, never
+// read and rewritten, so its other tokens are not touched.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include "nys_kv4.h"
+
+namespace nys {
+namespace kv4 {
+
+int check_cache(const nys_kv4_cache_t* c) {
+  if (!c || !c->data || !c->block_table) return NYS_ERR_ARG;
+  if (c->num_pages < 1 || c->max_pages < 1 || c->Hk < 1 || c->Hk > 65535) return NYS_ERR_SHAPE;
+  if (c->page_size < 16 || c->page_size > 4096 || c->page_size % 16) return NYS_ERR_SHAPE;
+  if (c->d != 32 && c->d != 64 && c->d != 128) return NYS_ERR_SHAPE;
+  if ((long long)c->max_pages * c->page_size >= (1ll << 31)) return NYS_ERR_SHAPE;
+  if (reinterpret_cast<uintptr_t>(c->data) & 15u) return NYS_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(c->block_table) & 3u) return NYS_ERR_ALIGN;
+  return NYS_OK;
+}
+
+namespace {
+
+constexpr int kWarps = 4;
+
+struct IoParams {
+  View cache;
+  nys_strides_t ks, vs;
+  const int *starts, *counts;
+  int* status;
+  int n, blocks_per_seq;
+  long long items;  // sequences x blocks x heads
+};
+
+// Eight channels of a row as fp32.
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Eight 4-bit fields (code + 8) of x / s rounded to the nearest integer, ties
+// to even; channel i in bits 4i. The integers come out of the mantissa of
+// 1.5 * 2^23 + 8 + code, whose low four bits they are.
+//
+// bf16 values over a bf16 scale: x / s is a tie (k + 1/2) or at least
+// (k + 1/2) * 2^-12 away from one, since both have 8 significant bits. x *
+// (1/s) is off by less than 2^-20 here; rounding it to multiples of 2^-16
+// first (C = 192: 1.5 * 2^7) puts ties exactly on k + 1/2 and keeps the others
+// on their side, so the product decides as the exact quotient would.
+__device__ __forceinline__ uint32_t fields_bf16(const float (&x)[8], float inv) {
+  constexpr float C = 192.f, M = 12582920.f;
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i)
+    w = w * 16u + __float_as_uint(__fadd_rn(__fsub_rn(fmaf(x[i], inv, C), C), M));
+  // each term brought 0x4B400000 along: its sum over 16^i, modulo 2^32
+  return w - 0x4B400000u * 0x11111111u;
+}
+
+// Any fp32 value: a first guess, then the exact remainder x - q s (one fused
+// multiply-add; no rounding, as q s has at most 12 bits) decides.
+__device__ __forceinline__ uint32_t fields_exact(const float (&x)[8], float s, float inv) {
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) {
+    float q = fminf(fmaxf(rintf(x[i] * inv), -8.f), 8.f);
+    const float e = 2.f * fmaf(-q, s, x[i]);
+    const bool odd = ((int)q & 1) != 0;
+    if (e > s || (e == s && odd)) q += 1.f;
+    else if (e < -s || (e == -s && odd)) q -= 1.f;
+    q = fminf(fmaxf(q, -7.f), 7.f);
+    w = w * 16u + (uint32_t)((int)q + 8);
+  }
+  return w;
+}
+
+// Scale of the 32 channels that this lane shares with three others, and its
+// eight fields.
+template <typename T>
+__device__ __forceinline__ uint32_t quantise(float (&x)[8], uint16_t& scale_bits) {
+  uint32_t top = 0;  // magnitudes compare as integers, NaN above infinity
+#pragma unroll
+  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  if (top >= 0x7f800000u) {
+    scale_bits = 0x7fc0;
+    return 0x88888888u;
+  }
+  const uint32_t sb = __float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) & 0xffff0000u;
+  scale_bits = (uint16_t)(sb >> 16);
+  if (sb == 0u) return 0x88888888u;
+  float s = __uint_as_float(sb);
+  if (s >= 0x1p-100f) {
+    const float inv = __fdiv_rn(1.f, s);
+    return sizeof(T) == 2 ? fields_bf16(x, inv) : fields_exact(x, s, inv);
+  }
+  // tiny scales: 1/s may be out of range, a subnormal s may be short of bits
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
+  s *= 0x1p64f;
+  return fields_exact(x, s, __fdiv_rn(1.f, s));
+}
+
+// The rows of a sequence that fall into one of its blocks.
+struct Rows {
+  int b, h, lo, hi;    // rows [lo, hi) of the block
+  long long pos, row;  // position of the block's row 0; i of row 0 (may be < 0)
+};
+
+__device__ __forceinline__ bool rows_of(const IoParams& p, long long item, Rows& r) {
+  r.h = (int)(item % p.cache.Hk);
+  const long long rest = item / p.cache.Hk;
+  r.b = (int)(rest / p.blocks_per_seq);
+  const long long start = p.starts ? p.starts[r.b] : 0;
+  const long long count = p.counts ? min(max(p.counts[r.b], 0), p.n) : p.n;
+  // arithmetic shift: rounds down for negative starts too
+  r.pos = ((start >> 4) + rest % p.blocks_per_seq) * kBlock;
+  r.row = r.pos - start;
+  r.lo = (int)max(0ll, -r.row);
+  r.hi = (int)max(min((long long)kBlock, count - r.row), 0ll);
+  return r.lo < r.hi;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+kv4_write(const __grid_constant__ IoParams p, const T* __restrict__ k, const T* __restrict__ v) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR, ITER = kBlock / RPI;
+  __shared__ __align__(16) uint8_t image[kWarps][block_bytes(D)];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kWarps + warp;
+  Rows r;
+  if (item >= p.items || !rows_of(p, item, r)) return;  // warp-uniform
+  uint8_t* dst = block_at(p.cache, r.b, r.h, r.pos, D);
+  if (!dst) {
+    if (lane == 0) report_index(p.status);
+    return;
+  }
+  uint8_t* im = image[warp];
+  const int unit = lane % LPR, t = unit & 3, y = unit >> 2;
+#pragma unroll
+  for (int kind = 0; kind < 2; ++kind) {
+    const nys_strides_t& st = kind ? p.vs : p.ks;
+    const T* src = (kind ? v : k) + r.b * st.batch + r.h * st.head + r.row * st.token + unit * 8;
+    float x[ITER][8];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int row = i * RPI + lane / LPR;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
+      if (row >= r.lo && row < r.hi) load8(src + row * st.token, x[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+      const int row = i * RPI + lane / LPR;
+      uint16_t scale;
+      const uint32_t w = quantise<T>(x[i], scale);
+      if (kind == 0) {
+        *reinterpret_cast<uint32_t*>(im + row * (D / 2) + t * (D / 8) + y * 4) = w;
+        if (t == 0) *reinterpret_cast<uint16_t*>(im + k_scales(D) + (y * kBlock + row) * 2) = scale;
+      } else {
+        uint8_t* at = im + v_codes(D) + (row >> 3) * 4 * D + (8 * t + ((row & 7) >> 1)) * (D / 8) +
+                      (row & 1) * (D / 16) + 2 * y;
+        *reinterpret_cast<uint16_t*>(at) = (uint16_t)w;
+        *reinterpret_cast<uint16_t*>(at + D / 2) = (uint16_t)(w >> 16);
+        if (t == 0) *reinterpret_cast<uint16_t*>(im + v_scales(D) + (y * kBlock + row) * 2) = scale;
+      }
+    }
+  }
+  __syncwarp();
+  if (r.hi - r.lo == kBlock) {
+    for (int e = lane; e < block_bytes(D) / 16; e += 32)
+      reinterpret_cast<uint4*>(dst)[e] = reinterpret_cast<const uint4*>(im)[e];
+    return;
+  }
+  // some rows only: key codes are d/2 bytes in a row, value codes 2-byte
+  // pieces, scales 2 bytes each
+  const int rows = r.hi - r.lo;
+  for (int e = lane; e < rows * (D / 8); e += 32) {
+    const int at = (r.lo + e / (D / 8)) * (D / 2) + (e % (D / 8)) * 4;
+    *reinterpret_cast<uint32_t*>(dst + at) = *reinterpret_cast<const uint32_t*>(im + at);
+  }
+  for (int e = lane; e < rows * (D / 4); e += 32) {
+    const int row = r.lo + e / (D / 4), piece = e % (D / 4);  // piece: (g, y)
+    const int at = v_codes(D) + (row >> 3) * 4 * D + ((piece & 7) * 4 + ((row & 7) >> 1)) * (D / 8) +
+                   (row & 1) * (D / 16) + 2 * (piece >> 3);
+    *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(im + at);
+  }
+  for (int e = lane; e < rows * (D / 16); e += 32) {
+    const int row = r.lo + e / (D / 16), s = e % (D / 16);  // s: K's groups, then V's
+    const int at = (s < D / 32 ? k_scales(D) : v_scales(D)) + ((s % (D / 32)) * kBlock + row) * 2;
+    *reinterpret_cast<uint16_t*>(dst + at) = *reinterpret_cast<const uint16_t*>(im + at);
+  }
+}
+
+__device__ __forceinline__ void decode8(uint32_t w, uint16_t scale_bits, float (&x)[8]) {
+  const float s = __uint_as_float((uint32_t)scale_bits << 16);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = ((float)((w >> (4 * i)) & 15u) - 8.f) * s;
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kWarps * 32)
+kv4_read(const __grid_constant__ IoParams p, T* __restrict__ k, T* __restrict__ v) {
+  constexpr int LPR = D / 8, RPI = 32 / LPR, ITER = kBlock / RPI;
+  __shared__ __align__(16) uint8_t image[kWarps][block_bytes(D)];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const long long item = (long long)blockIdx.x * kWarps + warp;
+  Rows r;
+  if (item >= p.items || !rows_of(p, item, r)) return;  // warp-uniform
+  const uint8_t* src = block_at(p.cache, r.b, r.h, r.pos, D);
+  if (!src && lane == 0) report_index(p.status);
+  uint8_t* im = image[warp];
+  for (int e = lane; e < block_bytes(D) / 16; e += 32)  // no block: scales of zero
+    reinterpret_cast<uint4*>(im)[e] =
+        src ? reinterpret_cast<const uint4*>(src)[e] : make_uint4(0u, 0u, 0u, 0u);
+  __syncwarp();
+  const int unit = lane % LPR, t = unit & 3, y = unit >> 2;
+  T* kd = k + r.b * p.ks.batch + r.h * p.ks.head + r.row * p.ks.token + unit * 8;
+  T* vd = v + r.b * p.vs.batch + r.h * p.vs.head + r.row * p.vs.token + unit * 8;
+#pragma unroll
+  for (int i = 0; i < ITER; ++i) {
+    const int row = i * RPI + lane / LPR;
+    if (row < r.lo || row >= r.hi) continue;
+    float x[8];
+    decode8(*reinterpret_cast<const uint32_t*>(im + row * (D / 2) + t * (D / 8) + y * 4),
+            *reinterpret_cast<const uint16_t*>(im + k_scales(D) + (y * kBlock + row) * 2), x);
+    store8(kd + row * p.ks.token, x);
+    const uint8_t* at = im + v_codes(D) + (row >> 3) * 4 * D + (8 * t + ((row & 7) >> 1)) * (D / 8) +
+                        (row & 1) * (D / 16) + 2 * y;
+    decode8(*reinterpret_cast<const uint16_t*>(at) |
+                (uint32_t)*reinterpret_cast<const uint16_t*>(at + D / 2) << 16,
+            *reinterpret_cast<const uint16_t*>(im + v_scales(D) + (y * kBlock + row) * 2), x);
+    store8(vd + row * p.vs.token, x);
+  }
+}
+
+int check_io(const nys_kv4_cache_t* c, const void* k, const void* v, const nys_strides_t* ks,
+             const nys_strides_t* vs, const int* starts, const int* counts, int B, int n, int dtype,
+             bool out) {
+  if (!k || !v || !ks || !vs) return NYS_ERR_ARG;
+  if (dtype != NYS_FP32 && dtype != NYS_BF16) return NYS_ERR_ARG;
+  const int rc = check_cache(c);
+  if (rc != NYS_OK) return rc;
+  if (B < 1 || B > 65535 || n < 1) return NYS_ERR_SHAPE;
+  if (!strides_ok(*ks) || !strides_ok(*vs)) return NYS_ERR_ARG;
+  if (out && (!rows_apart(*ks, B, c->Hk, n, c->d) || !rows_apart(*vs, B, c->Hk, n, c->d)))
+    return NYS_ERR_ARG;
+  if (!rows_aligned(k, *ks, dtype) || !rows_aligned(v, *vs, dtype)) return NYS_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(counts)) & 3u)
+    return NYS_ERR_ALIGN;
+  return NYS_OK;
+}
+
+int io_params(const nys_kv4_cache_t& c, const nys_strides_t& ks, const nys_strides_t& vs,
+              const int* starts, const int* counts, int B, int n, int dev, IoParams* p) {
+  p->cache = view_of(c);
+  p->ks = ks;
+  p->vs = vs;
+  p->starts = starts;
+  p->counts = counts;
+  p->n = n;
+  // n tokens from any start touch at most this many blocks
+  p->blocks_per_seq = (int)(((long long)n + 14) / 16 + 1);
+  p->items = (long long)B * p->blocks_per_seq * c.Hk;
+  if ((p->items + kWarps - 1) / kWarps >= (1ll << 31)) return NYS_ERR_SHAPE;
+  return operator_status(dev, &p->status);
+}
+
+template <typename F>
+int by_type(int dtype, int d, F&& f) {
+  auto by_d = [&](auto type) -> int {
+    switch (d) {
+      case 32: return f(type, std::integral_constant<int, 32>{});
+      case 64: return f(type, std::integral_constant<int, 64>{});
+      default: return f(type, std::integral_constant<int, 128>{});
+    }
+  };
+  return dtype == NYS_BF16 ? by_d(__nv_bfloat16{}) : by_d(float{});
+}
+
+}  // namespace
+}  // namespace kv4
+}  // namespace nys
+
+using namespace nys;
+using namespace nys::kv4;
+
+extern "C" {
+
+size_t nystrom_kv4_cache_bytes(int num_pages, int page_size, int Hk, int d) {
+  alignas(16) static const int some[4] = {};
+  const nys_kv4_cache_t c{const_cast<int*>(some), some, num_pages, 1, page_size, Hk, d};
+  if (check_cache(&c) != NYS_OK) return 0;
+  return (size_t)num_pages * Hk * (page_size / kBlock) * block_bytes(d);
+}
+
+int nystrom_kv4_write(const nys_kv4_cache_t* cache, const void* k, const void* v,
+                      const nys_strides_t* k_strides, const nys_strides_t* v_strides,
+                      const int* starts, const int* counts, int B, int n, int dtype,
+                      nys_stream_t stream) {
+  int rc = check_io(cache, k, v, k_strides, v_strides, starts, counts, B, n, dtype, false);
+  if (rc != NYS_OK) return rc;
+  int dev = 0;
+  rc = check_device(&dev);
+  if (rc != NYS_OK) return rc;
+  IoParams p{};
+  rc = io_params(*cache, *k_strides, *v_strides, starts, counts, B, n, dev, &p);
+  if (rc != NYS_OK) return rc;
+  return by_type(dtype, cache->d, [&](auto type, auto d) {
+    using T = decltype(type);
+    KernelScope scope("kv4_write", stream);
+    nys::kv4::kv4_write<T, decltype(d)::value>
+        <<<(unsigned)((p.items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
+            p, static_cast<const T*>(k), static_cast<const T*>(v));
+    return launch_status();
+  });
+}
+
+int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v, const nys_strides_t* k_strides,
+                     const nys_strides_t* v_strides, const int* starts, const int* counts, int B,
+                     int n, int dtype, nys_stream_t stream) {
+  int rc = check_io(cache, k, v, k_strides, v_strides, starts, counts, B, n, dtype, true);
+  if (rc != NYS_OK) return rc;
+  int dev = 0;
+  rc = check_device(&dev);
+  if (rc != NYS_OK) return rc;
+  IoParams p{};
+  rc = io_params(*cache, *k_strides, *v_strides, starts, counts, B, n, dev, &p);
+  if (rc != NYS_OK) return rc;
+  return by_type(dtype, cache->d, [&](auto type, auto d) {
+    using T = decltype(type);
+    KernelScope scope("kv4_read", stream);
+    nys::kv4::kv4_read<T, decltype(d)::value>
+        <<<(unsigned)((p.items + kWarps - 1) / kWarps), kWarps * 32, 0, stream>>>(
+            p, static_cast<T*>(k), static_cast<T*>(v));
+    return launch_status();
+  });
+}
+
+}  // extern "C"
