@@ -392,7 +392,8 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* p, const void* q, const void* 
 /*
  * A key/value cache held in 4 bits. Each 32 consecutive channels of a token's
  * key (or value) share one scale: with a the largest magnitude among them,
- *   scale = a / 7 rounded towards zero to bfloat16,
+ *   scale = a * (1/7), both and the product rounded to fp32, then rounded
+ *           towards zero to bfloat16,
  *   code  = x / scale rounded to the nearest integer (ties to even), in -7..7,
  * and the cache stands for code * scale, so nothing grows in magnitude and no
  * value is off by more than half a scale. A block that holds an infinity or a

@@ -6,6 +6,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 NYS_FP32, NYS_BF16 = 0, 1
 NYS_OK, NYS_ERR_ARG, NYS_ERR_SHAPE, NYS_ERR_ALIGN = 0, -1, -2, -3
@@ -309,82 +310,116 @@ def nystrom_profile_read(max_kernels: int = 16) -> dict:
 #
 # These take torch tensors whose strides they pass on: heads are [B, H, n, d]
 # views with contiguous channels (a token-major [B, n, H, d] tensor or a slice
-# of a packed projection: its transpose).
+# of a packed projection: its transpose). The descriptors go over as packed
+# bytes (a fraction of the time that filling ctypes structures takes).
 
-def _code(t) -> int:
-    import torch
-    if t.dtype == torch.bfloat16:
-        return NYS_BF16
-    if t.dtype == torch.float32:
-        return NYS_FP32
-    raise ValueError("dtype must be float32 or bfloat16")
+_ROPE_DESC = struct.Struct("=14if4x18q")  # nys_qk_rope_t
+_KV4_DESC = struct.Struct("=QQ5i4x")      # nys_kv4_cache_t
+_STRIDES = struct.Struct("=3q")           # nys_strides_t
+_NO_STRIDES = (0, 0, 0)
+_torch = None
 
 
-def _heads(name, t, like=None, shape=None):
-    """Strides of a [B, H, n, d] view. An axis with one entry has no stride."""
-    if not t.is_cuda or t.dim() != 4 or t.stride(3) != 1:
-        raise ValueError(f"{name} must be a CUDA tensor [B, H, n, d] with contiguous channels")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if like is not None and (t.dtype != like.dtype or t.device != like.device):
-        raise ValueError(f"{name} must have the dtype and device of the other heads")
-    n = t.shape
-    s = t.stride()
-    return NysStrides(s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+def _lazy_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch
+
+
+def _heads(name, t, dtype=None, shape=None):
+    """(batch, head, token) strides of a [B, H, n, d] view on the current
+    device. An axis with one entry has no stride."""
+    torch = _torch or _lazy_torch()
+    if not t.is_cuda or t.dim() != 4:
+        raise ValueError(f"{name} must be a CUDA tensor [B, H, n, d]")
+    s, n = t.stride(), t.shape
+    if s[3] != 1:
+        raise ValueError(f"{name}'s channels must be contiguous")
+    if shape is not None and n != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(n)}")
+    if dtype is None:
+        dtype = t.dtype
+        if dtype != torch.bfloat16 and dtype != torch.float32:
+            raise ValueError(f"{name} must be float32 or bfloat16")
+    elif t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} like the other heads")
+    if t.get_device() != torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on {t.device}, which is not the current device")
+    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
 
 
 def _flat(name, t, dtype, shape, device):
-    """A contiguous device array of the given type and shape, or None."""
+    """Address of a contiguous array of the given type, shape and device
+    index, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on {device}")
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}")
     return t.data_ptr()
 
 
-def _on_current_device(t):
-    import torch
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {t.device}, which is not the current device")
+def _raw_stream(stream, device):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(device)
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _scratch(nbytes, workspace, device, stream):
-    """(pointer, bytes, tensor to keep until the launch) of a call's workspace:
+    """(address, bytes, tensor to keep until the launch) of a call's workspace:
     the caller's, or memory of torch's allocator that belongs to the call's
     stream, so that it is reused only behind the call."""
-    import torch
+    torch = _torch
     if workspace is not None:
-        if workspace.device != device or not workspace.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {device}")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous tensor on device {device}")
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
     if stream is None:
-        t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     else:
-        handle = stream if isinstance(stream, int) else stream.cuda_stream
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle, device=device)):
-            t = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(_raw_stream(stream, device))):
+            t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     return t.data_ptr(), nbytes, t
 
 
-def _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing):
+def _rope_args(names, tensors, inv_freq, positions, sections, norm, eps, pairing):
+    """Packed descriptor, frequencies as bytes, address of the positions and
+    device of a call on (q, k, q_out or gq, k_out or gk[, dq, dk])."""
+    q, k = tensors[0], tensors[1]
+    qs = _heads(names[0], q)
+    torch, dtype, shape = _torch, q.dtype, q.shape
+    B, Hq, n, d = shape
+    if k is None:
+        strides = [x for i in range(0, len(tensors), 2)
+                   for x in (qs if i == 0 else _heads(names[i], tensors[i], dtype, shape)) + _NO_STRIDES]
+        Hk = 0
+    else:
+        ks = _heads(names[1], k, dtype)
+        kshape = k.shape
+        Hk = kshape[1]
+        if kshape[0] != B or kshape[2] != n or kshape[3] != d:
+            raise ValueError(f"k must have shape {(B, Hk, n, d)}, not {tuple(kshape)}")
+        strides = [*qs, *ks]
+        for i in range(2, len(tensors)):
+            strides += _heads(names[i], tensors[i], dtype, kshape if i % 2 else shape)
+    if len(tensors) == 4:
+        strides += _NO_STRIDES * 2
     import numpy as np
-    import torch
-    strides = _heads("q", q)
-    _on_current_device(q)
-    B, Hq, n, d = q.shape
-    Hk = 0 if k is None else k.shape[1]
-    freq = np.ascontiguousarray(inv_freq, dtype=np.float64)
-    if freq.ndim != 1:
-        raise ValueError("inv_freq must be one-dimensional")
-    sections = [len(freq)] if sections is None else list(sections)
-    if len(sections) > 4:
-        raise ValueError("at most four axes")
-    a = NysQkRope(B, n, Hq, Hk, d, 2 * len(freq), len(sections), (_I * 4)(*sections), pairing,
-                  1 if norm else 0, _code(q), eps, strides)
-    pos = _flat("positions", positions, torch.int32, (len(sections), B, n), q.device)
-    return a, freq, pos
+    freq = np.asarray(inv_freq, dtype=np.float64)
+    if freq.ndim != 1 or len(freq) > 64:
+        raise ValueError("inv_freq must be one-dimensional, at most 64 long")
+    half = len(freq)
+    axes = 1 if sections is None else len(sections)
+    if not 1 <= axes <= 4:
+        raise ValueError("one to four axes")
+    sec = (half, 0, 0, 0) if sections is None else (*sections, *(0,) * (4 - axes))
+    desc = _ROPE_DESC.pack(B, n, Hq, Hk, d, 2 * half, axes, *sec, pairing, 1 if norm else 0,
+                           NYS_BF16 if dtype == torch.bfloat16 else NYS_FP32, eps, *strides)
+    device = q.get_device()
+    return desc, freq.tobytes(), _flat("positions", positions, torch.int32, (axes, B, n), device), device
 
 
 def nystrom_qk_norm_rope_fwd(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, *,
@@ -394,24 +429,21 @@ def nystrom_qk_norm_rope_fwd(q, k, q_out, k_out, positions, inv_freq, q_weight=N
     positions: int32 [axes, B, n] on the device, or None for 0 .. n-1.
     inv_freq: host sequence of rot/2 radians per position. sections: pairs per
     axis (None: one axis). q_weight, k_weight: float32 [d], or None."""
-    import torch
-    lib = load_library()
-    a, freq, pos = _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing)
-    a.q_out = _heads("q_out", q_out, q, q.shape)
-    if k is not None:
-        a.k = _heads("k", k, q, (q.shape[0], k.shape[1], q.shape[2], q.shape[3]))
-        a.k_out = _heads("k_out", k_out, q, k.shape)
-    d = (q.shape[3],)
-    return _check(lib.nystrom_qk_norm_rope_fwd(
-        ctypes.byref(a), q.data_ptr(), None if k is None else k.data_ptr(),
-        _flat("q_weight", q_weight, torch.float32, d, q.device),
-        _flat("k_weight", k_weight, torch.float32, d, q.device), pos, freq.ctypes.data,
-        q_out.data_ptr(), None if k is None else k_out.data_ptr(), _stream(stream)),
-        "nystrom_qk_norm_rope_fwd")
+    lib = _lib or load_library()
+    desc, freq, pos, dev = _rope_args(("q", "k", "q_out", "k_out"), (q, k, q_out, k_out), inv_freq,
+                                      positions, sections, norm, eps, pairing)
+    d, f32 = (q.shape[3],), _torch.float32
+    rc = lib.nystrom_qk_norm_rope_fwd(
+        desc, q.data_ptr(), None if k is None else k.data_ptr(),
+        _flat("q_weight", q_weight, f32, d, dev), _flat("k_weight", k_weight, f32, d, dev), pos, freq,
+        q_out.data_ptr(), None if k is None else k_out.data_ptr(), _raw_stream(stream, dev))
+    return rc if rc >= 0 else _check(rc, "nystrom_qk_norm_rope_fwd")
 
 
-def nystrom_qk_norm_rope_workspace_bytes(desc: NysQkRope) -> int:
-    return load_library().nystrom_qk_norm_rope_workspace_bytes(ctypes.byref(desc))
+def nystrom_qk_norm_rope_workspace_bytes(desc) -> int:
+    """desc: NysQkRope."""
+    return load_library().nystrom_qk_norm_rope_workspace_bytes(
+        ctypes.byref(desc) if isinstance(desc, NysQkRope) else desc)
 
 
 def nystrom_qk_norm_rope_bwd(q, k, gq, gk, dq, dk, positions, inv_freq, q_weight=None, k_weight=None,
@@ -420,28 +452,22 @@ def nystrom_qk_norm_rope_bwd(q, k, gq, gk, dq, dk, positions, inv_freq, q_weight
     """Gradients of nystrom_qk_norm_rope_fwd: from its inputs q, k and the
     outputs' gradients gq, gk into dq, dk (which may be gq, gk) and, where
     given, dq_weight, dk_weight (float32 [d])."""
-    import torch
-    lib = load_library()
-    a, freq, pos = _rope_args(q, k, inv_freq, positions, sections, norm, eps, pairing)
-    a.q_out = _heads("gq", gq, q, q.shape)
-    a.dq = _heads("dq", dq, q, q.shape)
-    if k is not None:
-        a.k = _heads("k", k, q, (q.shape[0], k.shape[1], q.shape[2], q.shape[3]))
-        a.k_out = _heads("gk", gk, q, k.shape)
-        a.dk = _heads("dk", dk, q, k.shape)
-    d, f32, dev = (q.shape[3],), torch.float32, q.device
+    lib = _lib or load_library()
+    desc, freq, pos, dev = _rope_args(("q", "k", "gq", "gk", "dq", "dk"), (q, k, gq, gk, dq, dk), inv_freq,
+                                      positions, sections, norm, eps, pairing)
+    d, f32 = (q.shape[3],), _torch.float32
     need = 0
     if dq_weight is not None or dk_weight is not None:
-        need = lib.nystrom_qk_norm_rope_workspace_bytes(ctypes.byref(a))
+        need = lib.nystrom_qk_norm_rope_workspace_bytes(desc)
     ws, nbytes, keep = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_qk_norm_rope_bwd(
-        ctypes.byref(a), q.data_ptr(), None if k is None else k.data_ptr(), gq.data_ptr(),
+        desc, q.data_ptr(), None if k is None else k.data_ptr(), gq.data_ptr(),
         None if k is None else gk.data_ptr(), _flat("q_weight", q_weight, f32, d, dev),
-        _flat("k_weight", k_weight, f32, d, dev), pos, freq.ctypes.data, dq.data_ptr(),
+        _flat("k_weight", k_weight, f32, d, dev), pos, freq, dq.data_ptr(),
         None if k is None else dk.data_ptr(), _flat("dq_weight", dq_weight, f32, d, dev),
-        _flat("dk_weight", dk_weight, f32, d, dev), ws, nbytes, _stream(stream))
+        _flat("dk_weight", dk_weight, f32, d, dev), ws, nbytes, _raw_stream(stream, dev))
     del keep
-    return _check(rc, "nystrom_qk_norm_rope_bwd")
+    return rc if rc >= 0 else _check(rc, "nystrom_qk_norm_rope_bwd")
 
 
 def nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d) -> int:
@@ -453,55 +479,58 @@ class NystromKv4Cache:
     include/nystrom.h). data: uint8 CUDA tensor, a whole number of pages;
     block_table: int32 [B, max_pages], sequence b's pages in order."""
 
+    __slots__ = ("data", "block_table", "B", "Hk", "d", "device", "desc")
+
     def __init__(self, data, block_table, page_size, Hk, d):
-        import torch
-        page = nystrom_kv4_cache_bytes(1, page_size, Hk, d)
-        if page == 0:
+        torch = _torch or _lazy_torch()
+        if page_size % 16 or not 16 <= page_size <= 4096 or Hk < 1 or d not in (32, 64, 128):
             raise NystromError(NYS_ERR_SHAPE, "NystromKv4Cache")
         if not data.is_cuda or data.dtype != torch.uint8 or not data.is_contiguous():
             raise ValueError("data must be a contiguous uint8 CUDA tensor")
-        pages = data.numel() // page
-        if pages < 1 or pages * page != data.numel():
+        page = Hk * (page_size // 16) * 18 * d
+        pages, rest = divmod(data.numel(), page)
+        if pages < 1 or rest:
             raise ValueError(f"data must be a whole number of {page}-byte pages")
-        if (block_table.dtype != torch.int32 or block_table.dim() != 2 or block_table.device != data.device
-                or not block_table.is_contiguous()):
+        if (block_table.dtype != torch.int32 or block_table.dim() != 2
+                or block_table.get_device() != data.get_device() or not block_table.is_contiguous()):
             raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages] beside the data")
         self.data, self.block_table = data, block_table
-        self.B = block_table.shape[0]
-        self.struct = NysKv4Cache(data.data_ptr(), block_table.data_ptr(), pages, block_table.shape[1],
-                                  page_size, Hk, d)
-        self.ref = ctypes.byref(self.struct)
+        self.B, max_pages = block_table.shape
+        self.Hk, self.d, self.device = Hk, d, data.get_device()
+        self.desc = _KV4_DESC.pack(data.data_ptr(), block_table.data_ptr(), pages, max_pages, page_size, Hk, d)
 
 
 def _kv4_io(cache, k, v, starts, counts):
-    import torch
-    _on_current_device(cache.data)
-    B, n, dev = cache.B, k.shape[2], cache.data.device
-    shape = (B, cache.struct.Hk, n, cache.struct.d)
-    ks, vs = _heads("k", k, None, shape), _heads("v", v, k, shape)
-    if k.device != dev:
+    n, dev, B = k.shape[2], cache.device, cache.B
+    shape = (B, cache.Hk, n, cache.d)
+    ks = _heads("k", k, None, shape)
+    vs = _heads("v", v, k.dtype, shape)
+    if k.get_device() != dev:
         raise ValueError("k and v must be on the cache's device")
-    return (k.data_ptr(), v.data_ptr(), ctypes.byref(ks), ctypes.byref(vs),
-            _flat("starts", starts, torch.int32, (B,), dev), _flat("counts", counts, torch.int32, (B,), dev),
-            B, n, _code(k))
+    i32 = _torch.int32
+    return (k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks), _STRIDES.pack(*vs),
+            _flat("starts", starts, i32, (B,), dev), _flat("counts", counts, i32, (B,), dev),
+            B, n, NYS_BF16 if k.dtype == _torch.bfloat16 else NYS_FP32)
 
 
 def nystrom_kv4_write(cache, k, v, starts=None, counts=None, stream=None):
     """Quantises rows i < counts[b] of k, v [B, Hk, n, d] into the cache at
     positions starts[b] + i (int32 device tensors; None: n rows, from 0)."""
-    return _check(load_library().nystrom_kv4_write(cache.ref, *_kv4_io(cache, k, v, starts, counts),
-                                                   _stream(stream)), "nystrom_kv4_write")
+    rc = (_lib or load_library()).nystrom_kv4_write(cache.desc, *_kv4_io(cache, k, v, starts, counts),
+                                                    _raw_stream(stream, cache.device))
+    return rc if rc >= 0 else _check(rc, "nystrom_kv4_write")
 
 
 def nystrom_kv4_read(cache, k, v, starts=None, counts=None, stream=None):
     """What the cache holds at positions starts[b] + i to rows i < counts[b]
     of k, v [B, Hk, n, d]; rows behind are left as they were."""
-    return _check(load_library().nystrom_kv4_read(cache.ref, *_kv4_io(cache, k, v, starts, counts),
-                                                  _stream(stream)), "nystrom_kv4_read")
+    rc = (_lib or load_library()).nystrom_kv4_read(cache.desc, *_kv4_io(cache, k, v, starts, counts),
+                                                   _raw_stream(stream, cache.device))
+    return rc if rc >= 0 else _check(rc, "nystrom_kv4_read")
 
 
 def nystrom_kv4_attn_workspace_bytes(cache, B, nq, Hq, max_length, dtype) -> int:
-    return load_library().nystrom_kv4_attn_workspace_bytes(cache.ref, B, nq, Hq, max_length, dtype)
+    return load_library().nystrom_kv4_attn_workspace_bytes(cache.desc, B, nq, Hq, max_length, dtype)
 
 
 def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, causal=True, scale=None,
@@ -510,24 +539,23 @@ def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, caus
     sequence into out (same shape). lengths: int32 [B], tokens in the cache;
     max_length: an upper bound of them; q_counts: int32 [B], real queries
     (None: nq); scale: None for 1/sqrt(d)."""
-    import torch
-    lib = load_library()
+    lib = _lib or load_library()
     if scale == 0:
         raise ValueError("scale must not be zero (None: 1/sqrt(d))")
-    _on_current_device(cache.data)
-    dev = cache.data.device
+    dev = cache.device
     qs = _heads("q", q)
-    B, Hq, nq, d = q.shape
-    if B != cache.B or d != cache.struct.d or q.device != dev:
+    shape, dtype = q.shape, q.dtype
+    B, Hq, nq, d = shape
+    if B != cache.B or d != cache.d or q.get_device() != dev:
         raise ValueError("q must be [B, Hq, nq, d] with the cache's B and d, on its device")
-    os_ = _heads("out", out, q, q.shape)
-    dt = _code(q)
-    need = lib.nystrom_kv4_attn_workspace_bytes(cache.ref, B, nq, Hq, max_length, dt)
+    os_ = _heads("out", out, dtype, shape)
+    dt, i32 = (NYS_BF16 if dtype == _torch.bfloat16 else NYS_FP32), _torch.int32
+    need = lib.nystrom_kv4_attn_workspace_bytes(cache.desc, B, nq, Hq, max_length, dt)
     ws, nbytes, keep = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_kv4_attn_fwd(
-        cache.ref, q.data_ptr(), out.data_ptr(), ctypes.byref(qs), ctypes.byref(os_),
-        _flat("lengths", lengths, torch.int32, (B,), dev),
-        _flat("q_counts", q_counts, torch.int32, (B,), dev), B, nq, Hq, max_length,
-        1 if causal else 0, 0.0 if scale is None else scale, dt, ws, nbytes, _stream(stream))
+        cache.desc, q.data_ptr(), out.data_ptr(), _STRIDES.pack(*qs), _STRIDES.pack(*os_),
+        _flat("lengths", lengths, i32, (B,), dev), _flat("q_counts", q_counts, i32, (B,), dev), B, nq, Hq,
+        max_length, 1 if causal else 0, 0.0 if scale is None else scale, dt, ws, nbytes,
+        _raw_stream(stream, dev))
     del keep
-    return _check(rc, "nystrom_kv4_attn_fwd")
+    return rc if rc >= 0 else _check(rc, "nystrom_kv4_attn_fwd")

@@ -41,34 +41,48 @@ struct IoParams {
   long long items;  // sequences x blocks x heads
 };
 
-// Eight channels of a row as fp32.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight channels of a row as they lie in memory, as fp32, and their largest
+// magnitude's bits (magnitudes compare as integers, NaN above infinity).
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void clear() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const uint4*>(p)[0];
+    b = reinterpret_cast<const uint4*>(p)[1];
   }
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
-  *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
-}
-__device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
-  uint32_t w[4];
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fffffffu;
+    return max(max(max(a.x & m, a.y & m), max(a.z & m, a.w & m)),
+               max(max(b.x & m, b.y & m), max(b.z & m, b.w & m)));
+  }
+};
+template <>
+struct Raw8<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ uint32_t top() const {
+    const uint32_t m = 0x7fff7fffu;  // two magnitudes per word
+    const uint32_t t = __vmaxu2(__vmaxu2(a.x & m, a.y & m), __vmaxu2(a.z & m, a.w & m));
+    return max(t & 0xffff0000u, t << 16);
+  }
+};
 
 // Eight 4-bit fields (code + 8) of x / s rounded to the nearest integer, ties
 // to even; channel i in bits 4i. The integers come out of the mantissa of
@@ -76,7 +90,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 //
 // bf16 values over a bf16 scale: x / s is a tie (k + 1/2) or at least
 // (k + 1/2) * 2^-12 away from one, since both have 8 significant bits. x *
-// (1/s) is off by less than 2^-20 here; rounding it to multiples of 2^-16
+// (1/s) is off by less than 2^-19 here (the reciprocal by two steps); rounding it to multiples of 2^-16
 // first (C = 192: 1.5 * 2^7) puts ties exactly on k + 1/2 and keeps the others
 // on their side, so the product decides as the exact quotient would.
 __device__ __forceinline__ uint32_t fields_bf16(const float (&x)[8], float inv) {
@@ -106,32 +120,39 @@ __device__ __forceinline__ uint32_t fields_exact(const float (&x)[8], float s, f
   return w;
 }
 
+// 1/x to within a step or two of fp32, for normal x and 1/x.
+__device__ __forceinline__ float reciprocal(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Scale of the 32 channels that this lane shares with three others, and its
 // eight fields.
 template <typename T>
-__device__ __forceinline__ uint32_t quantise(float (&x)[8], uint16_t& scale_bits) {
-  uint32_t top = 0;  // magnitudes compare as integers, NaN above infinity
-#pragma unroll
-  for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(x[i]) & 0x7fffffffu);
+__device__ __forceinline__ uint32_t quantise(const Raw8<T>& raw, uint16_t& scale_bits) {
+  uint32_t top = raw.top();
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
   top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
   if (top >= 0x7f800000u) {
     scale_bits = 0x7fc0;
     return 0x88888888u;
   }
-  const uint32_t sb = __float_as_uint(__fdiv_rn(__uint_as_float(top), 7.f)) & 0xffff0000u;
+  const uint32_t sb = __float_as_uint(__fmul_rn(__uint_as_float(top), 1.f / 7.f)) & 0xffff0000u;
   scale_bits = (uint16_t)(sb >> 16);
   if (sb == 0u) return 0x88888888u;
   float s = __uint_as_float(sb);
+  float x[8];
+  raw.widen(x);
   if (s >= 0x1p-100f) {
-    const float inv = __fdiv_rn(1.f, s);
+    const float inv = reciprocal(s);
     return sizeof(T) == 2 ? fields_bf16(x, inv) : fields_exact(x, s, inv);
   }
   // tiny scales: 1/s may be out of range, a subnormal s may be short of bits
 #pragma unroll
   for (int i = 0; i < 8; ++i) x[i] *= 0x1p64f;
   s *= 0x1p64f;
-  return fields_exact(x, s, __fdiv_rn(1.f, s));
+  return fields_exact(x, s, reciprocal(s));
 }
 
 // The rows of a sequence that fall into one of its blocks.
@@ -174,13 +195,12 @@ kv4_write(const __grid_constant__ IoParams p, const T* __restrict__ k, const T* 
   for (int kind = 0; kind < 2; ++kind) {
     const nys_strides_t& st = kind ? p.vs : p.ks;
     const T* src = (kind ? v : k) + r.b * st.batch + r.h * st.head + r.row * st.token + unit * 8;
-    float x[ITER][8];
+    Raw8<T> x[ITER];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
       const int row = i * RPI + lane / LPR;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[i][j] = 0.f;
-      if (row >= r.lo && row < r.hi) load8(src + row * st.token, x[i]);
+      x[i].clear();
+      if (row >= r.lo && row < r.hi) x[i].load(src + row * st.token);
     }
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
@@ -225,10 +245,31 @@ kv4_write(const __grid_constant__ IoParams p, const T* __restrict__ k, const T* 
   }
 }
 
-__device__ __forceinline__ void decode8(uint32_t w, uint16_t scale_bits, float (&x)[8]) {
+// code * scale of the eight fields of w to eight channels in memory.
+__device__ __forceinline__ void decode8(uint32_t w, uint16_t scale_bits, float* p) {
   const float s = __uint_as_float((uint32_t)scale_bits << 16);
+  float x[8];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = ((float)((w >> (4 * i)) & 15u) - 8.f) * s;
+  for (int i = 0; i < 8; ++i)  // 2^23 + field, less 2^23 + 8
+    x[i] = (__uint_as_float(((w >> (4 * i)) & 15u) | 0x4B000000u) - 8388616.f) * s;
+  reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+  reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+}
+// Two fields at a time: 128 + field as bf16 by putting the field into the
+// mantissa of 128, less 136 (exact), times the scale (one rounding).
+__device__ __forceinline__ void decode8(uint32_t w, uint16_t scale_bits, __nv_bfloat16* p) {
+  const uint32_t ss = scale_bits * 0x10001u, off = 0x43084308u;  // 136
+  uint32_t x[4];  // fields (i, i + 4)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t f = ((w >> (4 * i)) & 0x000f000fu) | 0x43004300u;
+    const __nv_bfloat162 v = __hmul2(__hsub2(reinterpret_cast<const __nv_bfloat162&>(f),
+                                             reinterpret_cast<const __nv_bfloat162&>(off)),
+                                     reinterpret_cast<const __nv_bfloat162&>(ss));
+    x[i] = reinterpret_cast<const uint32_t&>(v);
+  }
+  *reinterpret_cast<uint4*>(p) = make_uint4(__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[2], x[3], 0x5410),
+                                            __byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
 }
 
 template <typename T, int D>
@@ -254,16 +295,15 @@ kv4_read(const __grid_constant__ IoParams p, T* __restrict__ k, T* __restrict__ 
   for (int i = 0; i < ITER; ++i) {
     const int row = i * RPI + lane / LPR;
     if (row < r.lo || row >= r.hi) continue;
-    float x[8];
     decode8(*reinterpret_cast<const uint32_t*>(im + row * (D / 2) + t * (D / 8) + y * 4),
-            *reinterpret_cast<const uint16_t*>(im + k_scales(D) + (y * kBlock + row) * 2), x);
-    store8(kd + row * p.ks.token, x);
+            *reinterpret_cast<const uint16_t*>(im + k_scales(D) + (y * kBlock + row) * 2),
+            kd + row * p.ks.token);
     const uint8_t* at = im + v_codes(D) + (row >> 3) * 4 * D + (8 * t + ((row & 7) >> 1)) * (D / 8) +
                         (row & 1) * (D / 16) + 2 * y;
     decode8(*reinterpret_cast<const uint16_t*>(at) |
                 (uint32_t)*reinterpret_cast<const uint16_t*>(at + D / 2) << 16,
-            *reinterpret_cast<const uint16_t*>(im + v_scales(D) + (y * kBlock + row) * 2), x);
-    store8(vd + row * p.vs.token, x);
+            *reinterpret_cast<const uint16_t*>(im + v_scales(D) + (y * kBlock + row) * 2),
+            vd + row * p.vs.token);
   }
 }
 

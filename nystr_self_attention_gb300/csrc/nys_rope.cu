@@ -49,16 +49,6 @@ struct RopeParams {
   nys_strides_t dq, dk;
 };
 
-// Four channels as fp32.
-__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
-  const float4 x = *reinterpret_cast<const float4*>(p);
-  v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&v)[4]) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
-}
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -69,8 +59,6 @@ __device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
 __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
@@ -106,24 +94,76 @@ __device__ __forceinline__ int channel_of(const Place& pl, int j, bool second) {
   return i + (second ? pl.half : 0);
 }
 
+// A lane's channels of one row as they lie in memory: held while earlier rows
+// are worked on, in half the registers (bf16) that their values take.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<float> {
+  uint4 lo, hi;
+};
+template <>
+struct Raw<__nv_bfloat16> {
+  uint2 lo, hi;
+};
+
+template <int MODE>
+__device__ __forceinline__ void load_raw(const float* row, const Place& pl, Raw<float>& r) {
+  if (MODE != kHalvesScalar) {
+    r.lo = *reinterpret_cast<const uint4*>(row + pl.lo);
+    r.hi = *reinterpret_cast<const uint4*>(row + pl.hi);
+  } else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row);
+    r.lo = make_uint4(w[channel_of<MODE>(pl, 0, false)], w[channel_of<MODE>(pl, 1, false)],
+                      w[channel_of<MODE>(pl, 2, false)], w[channel_of<MODE>(pl, 3, false)]);
+    r.hi = make_uint4(w[channel_of<MODE>(pl, 0, true)], w[channel_of<MODE>(pl, 1, true)],
+                      w[channel_of<MODE>(pl, 2, true)], w[channel_of<MODE>(pl, 3, true)]);
+  }
+}
+template <int MODE>
+__device__ __forceinline__ void load_raw(const __nv_bfloat16* row, const Place& pl,
+                                         Raw<__nv_bfloat16>& r) {
+  if (MODE == kPairs) {
+    const uint4 u = *reinterpret_cast<const uint4*>(row + pl.lo);
+    r.lo = make_uint2(u.x, u.y);
+    r.hi = make_uint2(u.z, u.w);
+  } else if (MODE == kHalves) {
+    r.lo = *reinterpret_cast<const uint2*>(row + pl.lo);
+    r.hi = *reinterpret_cast<const uint2*>(row + pl.hi);
+  } else {
+    const uint16_t* w = reinterpret_cast<const uint16_t*>(row);
+    auto two = [&](int j, bool second) {
+      return (uint32_t)w[channel_of<MODE>(pl, j, second)] |
+             (uint32_t)w[channel_of<MODE>(pl, j + 1, second)] << 16;
+    };
+    r.lo = make_uint2(two(0, false), two(2, false));
+    r.hi = make_uint2(two(0, true), two(2, true));
+  }
+}
+
+__device__ __forceinline__ void widen(const uint4& u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
+  v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+}
+__device__ __forceinline__ void widen(const uint2& u, float (&v)[4]) {
+  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
+  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+}
+
 template <int MODE, typename T>
-__device__ __forceinline__ void load_pairs(const T* row, const Place& pl, Pairs& x) {
-  if (MODE == kHalves) {
-    load4(row + pl.lo, x.a);
-    load4(row + pl.hi, x.b);
-  } else if (MODE == kPairs) {
+__device__ __forceinline__ Pairs pairs_of(const Raw<T>& r) {
+  Pairs x;
+  if (MODE == kPairs) {
     float u[4], v[4];
-    load4(row + pl.lo, u);
-    load4(row + pl.hi, v);
+    widen(r.lo, u);
+    widen(r.hi, v);
     x.a[0] = u[0]; x.b[0] = u[1]; x.a[1] = u[2]; x.b[1] = u[3];
     x.a[2] = v[0]; x.b[2] = v[1]; x.a[3] = v[2]; x.b[3] = v[3];
   } else {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      x.a[j] = load1(row + channel_of<MODE>(pl, j, false));
-      x.b[j] = load1(row + channel_of<MODE>(pl, j, true));
-    }
+    widen(r.lo, x.a);
+    widen(r.hi, x.b);
   }
+  return x;
 }
 
 template <int MODE, typename T>
@@ -217,39 +257,53 @@ __device__ __forceinline__ void load_weights(const float* w, const Place& pl, bo
   }
 }
 
-// Heads [h0, h1) of one tensor for one token.
+// Heads [h0, h1) of one tensor for one token: UNROLL rows at a time, the next
+// ones' loads in flight while these are worked on.
 template <typename T, int LP, int MODE, int UNROLL>
 __device__ __forceinline__ void walk_forward(const T* x, T* y, long long xs, long long ys, int h0,
                                              int h1, const float* w, const Turn& turn,
                                              const Place& pl, bool live, const RopeParams& p) {
+  Raw<T> next[UNROLL];
+  auto fetch = [&](int h) {
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k)
+      if (live && h + k < h1) load_raw<MODE>(x + (h + k) * xs, pl, next[k]);
+  };
+  fetch(h0);
   Pairs wt;
   if (p.norm) load_weights<MODE>(w, pl, live, wt);
   for (int h = h0; h < h1; h += UNROLL) {
-    Pairs v[UNROLL];
+    Raw<T> now[UNROLL];
 #pragma unroll
-    for (int k = 0; k < UNROLL; ++k)
-      if (live && h + k < h1) load_pairs<MODE>(x + (h + k) * xs, pl, v[k]);
+    for (int k = 0; k < UNROLL; ++k) now[k] = next[k];
+    fetch(h + UNROLL);
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) {
+      const bool on = live && h + k < h1;
+      Pairs v = pairs_of<MODE, T>(now[k]);
       if (p.norm) {
-        const float ss = row_sum<LP>(live && h + k < h1 ? square_sum(v[k]) : 0.f);
+        const float ss = row_sum<LP>(on ? square_sum(v) : 0.f);
         const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          v[k].a[j] *= r * wt.a[j];
-          v[k].b[j] *= r * wt.b[j];
+          v.a[j] *= r * wt.a[j];
+          v.b[j] *= r * wt.b[j];
         }
       }
       Pairs o;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        o.a[j] = fmaf(v[k].a[j], turn.c[j], -v[k].b[j] * turn.s[j]);
-        o.b[j] = fmaf(v[k].b[j], turn.c[j], v[k].a[j] * turn.s[j]);
+        o.a[j] = fmaf(v.a[j], turn.c[j], -v.b[j] * turn.s[j]);
+        o.b[j] = fmaf(v.b[j], turn.c[j], v.a[j] * turn.s[j]);
       }
-      if (live && h + k < h1) store_pairs<MODE>(y + (h + k) * ys, pl, o);
+      if (on) store_pairs<MODE>(y + (h + k) * ys, pl, o);
     }
   }
 }
+
+// Rows in flight per lane: 64 bytes' worth.
+template <typename T>
+constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 
 template <typename T, int LP, int MODE>
 __global__ void __launch_bounds__(kThreads)
@@ -267,149 +321,143 @@ qk_norm_rope(const __grid_constant__ RopeParams p, const T* q, const T* k, T* qo
   const int h0 = blockIdx.y * p.heads_per_chunk;
   const int h1 = min(p.Hq + p.Hk, h0 + p.heads_per_chunk);
   if (h0 < p.Hq)
-    walk_forward<T, LP, MODE, 4>(q + b * p.qi.batch + t * p.qi.token, qo + b * p.qo.batch + t * p.qo.token,
+    walk_forward<T, LP, MODE, kAhead<T>>(q + b * p.qi.batch + t * p.qi.token, qo + b * p.qo.batch + t * p.qo.token,
                                  p.qi.head, p.qo.head, h0, min(h1, p.Hq), p.qw, turn, pl, live, p);
   if (h1 > p.Hq)
-    walk_forward<T, LP, MODE, 4>(k + b * p.ki.batch + t * p.ki.token, ko + b * p.ko.batch + t * p.ko.token,
+    walk_forward<T, LP, MODE, kAhead<T>>(k + b * p.ki.batch + t * p.ki.token, ko + b * p.ko.batch + t * p.ko.token,
                                  p.ki.head, p.ko.head, max(h0 - p.Hq, 0), h1 - p.Hq, p.kw, turn, pl,
                                  live, p);
 }
 
-// Backward over heads [h0, h1) of one tensor; acc += g h of this lane's
-// channels.
-template <typename T, int LP, int MODE, int UNROLL>
-__device__ __forceinline__ void walk_backward(const T* x, const T* gy, T* dx, long long xs,
-                                              long long gs, long long ds, int h0, int h1,
-                                              const float* w, const Turn& turn, const Place& pl,
-                                              bool live, const RopeParams& p, Pairs& acc) {
-  Pairs wt;
-  if (p.norm) load_weights<MODE>(w, pl, live, wt);
-  for (int h = h0; h < h1; h += UNROLL) {
-    Pairs v[UNROLL], g[UNROLL];
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k)
-      if (live && h + k < h1) {
-        load_pairs<MODE>(gy + (h + k) * gs, pl, g[k]);
-        if (p.norm) load_pairs<MODE>(x + (h + k) * xs, pl, v[k]);
-      }
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k) {
-      const bool on = live && h + k < h1;
-      Pairs o;  // the rotation undone
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o.a[j] = fmaf(g[k].a[j], turn.c[j], g[k].b[j] * turn.s[j]);
-        o.b[j] = fmaf(g[k].b[j], turn.c[j], -g[k].a[j] * turn.s[j]);
-      }
-      if (p.norm) {
-        float dot = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          dot = fmaf(wt.a[j] * o.a[j], v[k].a[j], fmaf(wt.b[j] * o.b[j], v[k].b[j], dot));
-        const float ss = row_sum<LP>(on ? square_sum(v[k]) : 0.f);
-        dot = row_sum<LP>(on ? dot : 0.f);
-        const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-        const float m = r * dot * p.inv_d;  // mean(w g h)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float ha = v[k].a[j] * r, hb = v[k].b[j] * r;
-          if (on) {
-            acc.a[j] = fmaf(o.a[j], ha, acc.a[j]);
-            acc.b[j] = fmaf(o.b[j], hb, acc.b[j]);
-          }
-          o.a[j] = r * fmaf(wt.a[j], o.a[j], -ha * m);
-          o.b[j] = r * fmaf(wt.b[j], o.b[j], -hb * m);
-        }
-      }
-      if (on) store_pairs<MODE>(dx + (h + k) * ds, pl, o);
-    }
-  }
-}
-
-// part: [CTAs][2][d] sums of g h over the CTA's rows (q's, then k's), or null.
+// Gradients of one tensor's heads in chunks: CTAs y < q_chunks take q's, the
+// others k's, so that a thread keeps one set of weight sums. part: [CTAs][d]
+// sums of g h over a CTA's rows (q's CTAs first), or null.
 template <typename T, int LP, int MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 2)
 qk_norm_rope_back(const __grid_constant__ RopeParams p, const T* q, const T* k, const T* gq,
-                  const T* gk, T* dq, T* dk, float* part) {
+                  const T* gk, T* dq, T* dk, float* part, int q_chunks) {
   __shared__ unsigned long long freq[kMaxPairs];
-  __shared__ float sums[kThreads / 32][LP][17];
+  __shared__ float sums[kThreads / 32][LP][9];
   if (threadIdx.x < p.half) freq[threadIdx.x] = p.freq[threadIdx.x];
   __syncthreads();
+  constexpr int UNROLL = kAhead<T>;
+  const bool keys = (int)blockIdx.y >= q_chunks;  // CTA-uniform
+  const nys_strides_t &xs = keys ? p.ki : p.qi, &gs = keys ? p.ko : p.qo, &ds = keys ? p.dk : p.dq;
   const int unit = threadIdx.x % LP;
   const Place pl = place_of<MODE>(unit, p.half);
-  const int h0 = blockIdx.y * p.heads_per_chunk;
-  const int h1 = min(p.Hq + p.Hk, h0 + p.heads_per_chunk);
+  const int h0 = ((int)blockIdx.y - (keys ? q_chunks : 0)) * p.heads_per_chunk;
+  const int h1 = min(keys ? p.Hk : p.Hq, h0 + p.heads_per_chunk);
   constexpr int kRows = kThreads / LP;
   const long long tiles = (p.tokens + kRows - 1) / kRows;
-  Pairs aq{}, ak{};
+  Pairs acc{}, wt;
+  if (p.norm) load_weights<MODE>(keys ? p.kw : p.qw, pl, 8 * unit < p.d, wt);
   for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
     const long long token = tile * kRows + threadIdx.x / LP;
     const bool live = token < p.tokens && 8 * unit < p.d;
     const long long b = live ? token / p.n : 0, t = live ? token - b * p.n : 0;
+    const T* x = (keys ? k : q) + b * xs.batch + t * xs.token;
+    const T* gy = (keys ? gk : gq) + b * gs.batch + t * gs.token;
+    T* dx = (keys ? dk : dq) + b * ds.batch + t * ds.token;
+    Raw<T> next_x[UNROLL], next_g[UNROLL];
+    auto fetch = [&](int h) {
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i)
+        if (live && h + i < h1) {
+          load_raw<MODE>(gy + (h + i) * gs.head, pl, next_g[i]);
+          if (p.norm) load_raw<MODE>(x + (h + i) * xs.head, pl, next_x[i]);
+        }
+    };
+    fetch(h0);
     Turn turn{};
     if (live) turn = turn_of<sizeof(T) == 4>(p, freq, unit, token, (int)t);
-    if (h0 < p.Hq)
-      walk_backward<T, LP, MODE, 2>(q + b * p.qi.batch + t * p.qi.token,
-                                    gq + b * p.qo.batch + t * p.qo.token,
-                                    dq + b * p.dq.batch + t * p.dq.token, p.qi.head, p.qo.head,
-                                    p.dq.head, h0, min(h1, p.Hq), p.qw, turn, pl, live, p, aq);
-    if (h1 > p.Hq)
-      walk_backward<T, LP, MODE, 2>(k + b * p.ki.batch + t * p.ki.token,
-                                    gk + b * p.ko.batch + t * p.ko.token,
-                                    dk + b * p.dk.batch + t * p.dk.token, p.ki.head, p.ko.head,
-                                    p.dk.head, max(h0 - p.Hq, 0), h1 - p.Hq, p.kw, turn, pl, live,
-                                    p, ak);
+    for (int h = h0; h < h1; h += UNROLL) {
+      Raw<T> now_x[UNROLL], now_g[UNROLL];
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        now_x[i] = next_x[i];
+        now_g[i] = next_g[i];
+      }
+      fetch(h + UNROLL);
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        const bool on = live && h + i < h1;
+        const Pairs g = pairs_of<MODE, T>(now_g[i]);
+        Pairs o;  // the rotation undone
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          o.a[j] = fmaf(g.a[j], turn.c[j], g.b[j] * turn.s[j]);
+          o.b[j] = fmaf(g.b[j], turn.c[j], -g.a[j] * turn.s[j]);
+        }
+        if (p.norm) {
+          const Pairs v = pairs_of<MODE, T>(now_x[i]);
+          float dot = 0.f;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            dot = fmaf(wt.a[j] * o.a[j], v.a[j], fmaf(wt.b[j] * o.b[j], v.b[j], dot));
+          const float ss = row_sum<LP>(on ? square_sum(v) : 0.f);
+          dot = row_sum<LP>(on ? dot : 0.f);
+          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+          const float m = r * dot * p.inv_d;  // mean(w g h)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float ha = v.a[j] * r, hb = v.b[j] * r;
+            if (on) {
+              acc.a[j] = fmaf(o.a[j], ha, acc.a[j]);
+              acc.b[j] = fmaf(o.b[j], hb, acc.b[j]);
+            }
+            o.a[j] = r * fmaf(wt.a[j], o.a[j], -ha * m);
+            o.b[j] = r * fmaf(wt.b[j], o.b[j], -hb * m);
+          }
+        }
+        if (on) store_pairs<MODE>(dx + (h + i) * ds.head, pl, o);
+      }
+    }
   }
   if (!part) return;
   // lanes of one unit: over the warp by shuffles, over the warps in order
-  float v[16];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    v[j] = aq.a[j];
-    v[4 + j] = aq.b[j];
-    v[8 + j] = ak.a[j];
-    v[12 + j] = ak.b[j];
-  }
+  const float v[8] = {acc.a[0], acc.a[1], acc.a[2], acc.a[3], acc.b[0], acc.b[1], acc.b[2], acc.b[3]};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
+  for (int j = 0; j < 8; ++j) {
+    float s = v[j];
 #pragma unroll
-    for (int o = 16; o >= LP; o >>= 1) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
-    if (lane < LP) sums[warp][lane][j] = v[j];
+    for (int o = 16; o >= LP; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (lane < LP) sums[warp][lane][j] = s;
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < LP * 16; e += kThreads) {
-    const int u = e / 16, j = e % 16;
+  for (int e = threadIdx.x; e < LP * 8; e += kThreads) {
+    const int u = e / 8, j = e % 8;
     if (8 * u >= p.d) continue;
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) s += sums[w][u][j];
     const int c = channel_of<MODE>(place_of<MODE>(u, p.half), j & 3, (j & 4) != 0);
-    const size_t cta = (size_t)blockIdx.y * gridDim.x + blockIdx.x;
-    part[(cta * 2 + (j >> 3)) * p.d + c] = s;
+    part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d + c] = s;
   }
 }
 
-// dw[c] = sum over CTAs of part, columns 0 .. 2d-1 (q's, then k's). 32 columns
-// and 32 row slices per CTA; fixed order.
+// dw[c] = sum over CTAs of part, 32 channels per CTA in 32 row slices: fixed
+// order. CTAs y = 0: q's rows [0, q_ctas) of part, y = 1: k's behind them.
 __global__ void __launch_bounds__(1024)
-qk_weight_grad(const float* __restrict__ part, float* dqw, float* dkw, int d, int ctas) {
+qk_weight_grad(const float* __restrict__ part, float* dqw, float* dkw, int d, int q_ctas, int k_ctas) {
   __shared__ float s[32][33];
-  const int col = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
+  float* dst = blockIdx.y ? dkw : dqw;
+  if (!dst) return;
+  const float* rows = part + (blockIdx.y ? (size_t)q_ctas * d : 0);
+  const int ctas = blockIdx.y ? k_ctas : q_ctas;
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), slice = threadIdx.x >> 5;
   float v = 0.f;
-  if (col < 2 * d)
-    for (int r = slice; r < ctas; r += 32) v += part[(size_t)r * 2 * d + col];
+  if (c < d) {
+#pragma unroll 8
+    for (int r = slice; r < ctas; r += 32) v += rows[(size_t)r * d + c];
+  }
   s[slice][threadIdx.x & 31] = v;
   __syncthreads();
-  // warp `slice` sums column `slice` of this CTA's 32
+  // warp `slice` sums channel `slice` of this CTA's 32
   float x = s[threadIdx.x & 31][slice];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  const int c = blockIdx.x * 32 + slice;
-  if ((threadIdx.x & 31) == 0 && c < 2 * d) {
-    float* dst = c < d ? dqw : dkw;
-    if (dst) dst[c < d ? c : c - d] = x;
-  }
+  if ((threadIdx.x & 31) == 0 && blockIdx.x * 32 + slice < d) dst[blockIdx.x * 32 + slice] = x;
 }
 
 int lanes_per_row(int d) { return d <= 32 ? 4 : (d <= 64 ? 8 : 16); }
@@ -421,11 +469,14 @@ Mode mode_of(const nys_qk_rope_t& a) {
 
 struct Grid {
   int x, y, heads_per_chunk;
+  int q_chunks;  // backward: of y
 };
 
 // One CTA per (tile of 256 / LP tokens, chunk of heads). All heads in one
 // chunk when the tiles alone give four CTAs per SM; else as many chunks as
-// that takes, so that a single token's heads run side by side.
+// that takes, so that a single token's heads run side by side. Backward CTAs
+// walk several tiles (one partial of the weight sums each) and take heads of
+// q or of k.
 Grid grid_of(const nys_qk_rope_t& a, bool back) {
   const int rows = kThreads / lanes_per_row(a.d);
   const long long tiles = ((long long)a.B * a.n + rows - 1) / rows;
@@ -436,11 +487,15 @@ Grid grid_of(const nys_qk_rope_t& a, bool back) {
   if (chunks > heads) chunks = heads;
   Grid g;
   g.heads_per_chunk = (int)((heads + chunks - 1) / chunks);
+  g.x = (int)tiles;
   g.y = (heads + g.heads_per_chunk - 1) / g.heads_per_chunk;
-  // backward CTAs walk several tiles: one partial of the weight sums per CTA
-  long long x = tiles;
-  if (back && x > want) x = want;
-  g.x = (int)x;
+  g.q_chunks = 0;
+  if (back) {
+    g.q_chunks = (a.Hq + g.heads_per_chunk - 1) / g.heads_per_chunk;
+    g.y = g.q_chunks + (a.Hk + g.heads_per_chunk - 1) / g.heads_per_chunk;
+    const long long most = want / g.y > 0 ? want / g.y : 1;
+    if (g.x > most) g.x = (int)most;
+  }
   return g;
 }
 
@@ -535,7 +590,7 @@ int launch_bwd(const RopeParams& p, const Grid& g, const void* q, const void* k,
   KernelScope scope("qk_norm_rope_back", st);
   qk_norm_rope_back<T, LP, MODE><<<dim3(g.x, g.y), kThreads, 0, st>>>(
       p, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(gq),
-      static_cast<const T*>(gk), static_cast<T*>(dq), static_cast<T*>(dk), part);
+      static_cast<const T*>(gk), static_cast<T*>(dq), static_cast<T*>(dk), part, g.q_chunks);
   return launch_status();
 }
 
@@ -563,7 +618,7 @@ int dispatch(const nys_qk_rope_t& a, F&& f) {
 
 size_t weight_part_bytes(const nys_qk_rope_t& a) {
   const Grid g = grid_of(a, true);
-  return ((size_t)g.x * g.y * 2 * a.d * sizeof(float) + 255) & ~size_t(255);
+  return ((size_t)g.x * g.y * a.d * sizeof(float) + 255) & ~size_t(255);
 }
 
 }  // namespace
@@ -659,7 +714,8 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* a, const void* q, const void* 
   });
   if (rc != NYS_OK || !sums) return rc;
   KernelScope scope("qk_weight_grad", stream);
-  qk_weight_grad<<<(2 * a->d + 31) / 32, 1024, 0, stream>>>(part, dq_weight, dk_weight, a->d, g.x * g.y);
+  qk_weight_grad<<<dim3((a->d + 31) / 32, a->Hk > 0 ? 2 : 1), 1024, 0, stream>>>(
+      part, dq_weight, dk_weight, a->d, g.x * g.q_chunks, g.x * (g.y - g.q_chunks));
   return launch_status();
 }
 

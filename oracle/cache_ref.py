@@ -75,7 +75,7 @@ def quantise(x):
     top = np.abs(g).max(-1)
     bad = ~np.isfinite(g).all(-1)
     with np.errstate(invalid="ignore", over="ignore"):
-        bits = bf16_bits_toward_zero((top / np.float32(7)).astype(np.float32))
+        bits = bf16_bits_toward_zero((top * np.float32(1 / 7)).astype(np.float32))
     bits = np.where(bad, np.uint16(0x7FC0), bits)
     s = bf16_value(bits)
     zero = bad | (bits == 0)

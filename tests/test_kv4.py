@@ -410,7 +410,7 @@ def test_caller_and_cached_workspaces_agree():
 
     def raw(stream):
         return N.load_library().nystrom_kv4_attn_fwd(
-            c.dev.ref, q.data_ptr(), b.data_ptr(), ctypes.byref(s), ctypes.byref(s), lens.data_ptr(), None,
+            c.dev.desc, q.data_ptr(), b.data_ptr(), ctypes.byref(s), ctypes.byref(s), lens.data_ptr(), None,
             1, 1, 8, 4096, 1, 0.0, N.NYS_BF16, None, 0, stream)
 
     assert raw(torch.cuda.current_stream().cuda_stream) == N.NYS_OK

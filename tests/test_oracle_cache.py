@@ -87,7 +87,7 @@ def test_quantise_against_rational_arithmetic():
     for row, cs, sb in zip(x, codes, bits):
         top = max(abs(Fraction(float(v))) for v in row)
         s = Fraction(float(C.bf16_value(sb[0])))
-        # fp32 division, then truncated: within an fp32 step below top/7
+        # 1/7 and the product in fp32, then truncated: an fp32 step above top/7 at most
         assert s <= top / 7 * (1 + Fraction(1, 2 ** 23))
         assert s >= top / 7 * (1 - Fraction(1, 2 ** 7)) - Fraction(1, 2 ** 133)
         for v, c in zip(row, cs):
