@@ -3,7 +3,7 @@
 //
 // kv4_attn_split: up to 16 query rows (queries x heads of one cache head) per
 // item. The keys of all items, in tiles of 32, form one line that is cut into
-// equal ranges, one per CTA (three CTAs per SM): a long sequence is shared by
+// equal ranges, one per CTA (four CTAs per SM): a long sequence is shared by
 // many CTAs, a ragged batch loads them evenly. Inside a CTA four warps take
 // tiles in turn, each with its own running maximum, sum and output, and join
 // at the item's end; where ranges cut an item, kv4_attn_join adds up the parts.
@@ -18,13 +18,18 @@
 // takes p from. A 4-bit field u = code + 8 becomes fp16 by masking alone (as a
 // subnormal it is u 2^-24, in the upper half of a byte u 2^-20; the queries
 // carry the factors and are scaled to the top of fp16's range), its offset 8
-// goes into the product's starting value. For V it becomes bf16 128 + u by one
-// more shift, less 136. The bound is HBM; what comes next is unpacking, about
-// 0.7 integer instructions per code of K and one per code of V.
+// is the product's starting value. V's fields are masked out as bf16 subnormals
+// and brought to (u - 8) 2^-6 by one fused multiply-add per pair.
+//
+// One token over 8 ragged sequences of up to 32768, 32 + 8 heads, d = 128 (203
+// MB): 50 us, the join included 58; four times as long 172 us (5.0 TB/s). What
+// bounds it is the unpacking: per 16 keys and head about 310 instructions of a
+// warp, 120 of them on the integer pipe.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "nys_kv4.h"
@@ -38,9 +43,14 @@ using namespace sm100;
 
 constexpr int kTile = 32;    // keys per tile: two blocks
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 3;
+constexpr int kCtasPerSm = 4;
 constexpr int kStages = 2;   // tiles per warp in flight or in use
 constexpr int kMinTiles = 4; // a CTA's range: at least one tile per warp
+// What starting on an item and joining its warps costs a CTA, in tiles: each
+// item is that much longer on the line, so that a CTA whose range crosses into
+// one gets fewer tiles (8 ragged sequences of up to 32768 tokens, 8 heads:
+// the last CTA ended 7.6 us behind the median one without it).
+constexpr int kItemCost = 6;
 constexpr float kRebase = 8.0f;  // move the running maximum when it grows by 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -51,7 +61,6 @@ struct AttnParams {
   int* status;
   float* part;      // [CTAs][2][rows][D]: unnormalised outputs of cut items
   float2* part_ml;  // [CTAs][2][16]: their (maximum in log2 units, sum)
-  int2* item_ctas;  // [items]: first CTA (-1 - CTA: its part is in slot 1), last
   int B, nq, rep, row_tiles, max_length, causal;
   int ctas;
   float scale_log2;  // scale * log2(e)
@@ -126,48 +135,57 @@ __device__ __forceinline__ int tiles_of(const AttnParams& p, int b) {
   return (length_of(p, b, &bad) + kTile - 1) / kTile;
 }
 
+// Places that an item of `tiles` takes on the line.
+__device__ __forceinline__ int line_of(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
+
+// Tiles per CTA of a line of `total` (the host keeps lines below 2^31).
+__device__ __forceinline__ int range_of(const AttnParams& p, int total) {
+  return max((total + p.ctas - 1) / p.ctas, kMinTiles);
+}
+
 // Where the CTA's range of the line of tiles starts.
 struct Start {
-  long long total, per;
-  long long base;  // first tile of sequence b
+  int total, per;
+  int base;  // first tile of sequence b
   int b;
 };
 
 // Block-wide: sums the sequences' tiles in thread chunks, and finds the
 // sequence that tile blockIdx.x * per falls into.
-__device__ __forceinline__ void find_start(const AttnParams& p, Start* s, long long* warp_sums) {
+__device__ __forceinline__ void find_start(const AttnParams& p, Start* s, int* warp_sums) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int chunk = (p.B + kWarps * 32 - 1) / (kWarps * 32);
   const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
-  const long long per_item = (long long)p.cache.Hk * p.row_tiles;
-  long long sum = 0;
+  const int per_item = p.cache.Hk * p.row_tiles;
+  int sum = 0;
+#pragma unroll 1
   for (int b = b0; b < b1; ++b) {
     bool bad;
-    sum += (length_of(p, b, &bad) + kTile - 1) / kTile * per_item;
+    sum += line_of((length_of(p, b, &bad) + kTile - 1) / kTile) * per_item;
     if (bad && blockIdx.x == 0) report_index(p.status);
   }
-  long long incl = sum;
+  int incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
   if (lane == 31) warp_sums[warp] = incl;
   __syncthreads();
-  long long before = 0, total = 0;
+  int before = 0, total = 0;
 #pragma unroll
   for (int w = 0; w < kWarps; ++w) {
     if (w < warp) before += warp_sums[w];
     total += warp_sums[w];
   }
-  long long per = (total + p.ctas - 1) / p.ctas;
-  if (per < kMinTiles) per = kMinTiles;
-  const long long r0 = blockIdx.x * per;
-  long long at = before + incl - sum;
+  const int per = range_of(p, total);
+  const int r0 = min((long long)blockIdx.x * per, (long long)total);
+  int at = before + incl - sum;
   if (r0 >= at && r0 < at + sum) {  // one thread, if any
     int b = b0;
+#pragma unroll 1
     for (; b < b1; ++b) {
-      const long long n = tiles_of(p, b) * per_item;
+      const int n = line_of(tiles_of(p, b)) * per_item;
       if (r0 < at + n) break;
       at += n;
     }
@@ -184,10 +202,28 @@ __device__ __forceinline__ void find_start(const AttnParams& p, Start* s, long l
 template <int D>
 constexpr int ring_bytes() { return kWarps * kStages * 2 * block_bytes(D); }
 template <int D, int NT>
-constexpr int split_smem() { return ring_bytes<D>() + 2 * NT * 8 * D * 4; }
+constexpr int merge_bytes() { return 2 * NT * 8 * D * 4; }
+// per group: the queries' operands (two steps, each fp16 term), starting values
+template <typename T>
+constexpr int kTable = sizeof(T) == 4 ? 4 : 3;
+// fp32 scales of a warp's tile: [K, V][group][32 tokens]
+template <int D>
+constexpr int scales_bytes() { return 2 * D / 32 * kTile * 4; }
+template <typename T, int D, int NT>
+constexpr int split_smem() {
+  return ring_bytes<D>() + merge_bytes<D, NT>() + D / 32 * kTable<T> * 512 + kWarps * scales_bytes<D>();
+}
 
-// NT: 8-row groups of query rows (1 or 2). TERMS: fp16 terms of a query, and
-// EXACT codes with three bf16 terms of a probability, for fp32.
+// The part of a CTA's range that lies in one item, and what its rows see.
+struct Segment {
+  int b, h, rt, tile0, ntile, len, count, rows, seen_min, seen_max;
+};
+
+// NT: 8-row groups of query rows (1 or 2). fp32: a query is the sum of two
+// fp16 terms, the codes lose their offset before the product, a probability
+// times its scale is the sum of three bf16 terms.
+// The code is kept short (one copy of each step, masks as uniform branches):
+// a decoding step finds none of it in the instruction caches.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && NT == 1 ? kCtasPerSm : 2)
 kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T* __restrict__ out) {
@@ -197,123 +233,275 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ Start start;
-  __shared__ long long warp_sums[kWarps];
+  __shared__ int warp_sums[kWarps];
   __shared__ float2 ml_s[kWarps][16];
   __shared__ int abort_s;
   volatile int* abort_flag = &abort_s;
   float* merge = reinterpret_cast<float*>(smem + ring_bytes<D>());  // [2][NT * 8][D]
+  // [G][kTable][lane]: operands of the segment's queries, shared by the warps
+  uint4* table = reinterpret_cast<uint4*>(smem + ring_bytes<D>() + merge_bytes<D, NT>());
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  float* scales = reinterpret_cast<float*>(table + G * kTable<T> * 32) + warp * (scales_bytes<D>() / 4);
   uint8_t* ring = smem + warp * kStages * 2 * BB;
-  if (tid == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(&bars[w][s], 2);
-    abort_s = 0;
-    fence_barrier_init();
-  }
+  if (tid < kWarps * kStages) mbar_init(&bars[0][0] + tid, 2);
+  if (tid == 0) abort_s = 0;
+  fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up meanwhile
   find_start(p, &start, warp_sums);  // two block syncs
-  const long long r0 = blockIdx.x * start.per, r1 = min(start.total, r0 + start.per);
-  long long pos = r0, base = start.base;
-  int b = start.b;
+  const int r0 = (int)min((long long)blockIdx.x * start.per, (long long)start.total);
+  const int r1 = min(start.total, r0 + start.per);
+  int pos = r0, base = start.base, b = start.b;
   uint32_t used = 0;  // tiles this warp has put through its ring
 
-  while (pos < r1) {
-    // ------------------------------------------------- the next segment
-    bool bad;
-    const int len = length_of(p, b, &bad);
-    const int T_b = (len + kTile - 1) / kTile;
-    const int items = p.cache.Hk * p.row_tiles;
-    if (pos >= base + (long long)T_b * items) {
-      base += (long long)T_b * items;
-      ++b;
-      continue;
-    }
-    const long long off = pos - base;
-    const int item = (int)(off / T_b), tile0 = (int)(off - (long long)item * T_b);
-    const int ntile = (int)min((long long)(T_b - tile0), r1 - pos);
-    const bool whole = ntile == T_b;
-    const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
-    const long long gitem = (long long)b * items + item;
-    // only a range's first and last segment can be cut: two slots per CTA
-    const int slot = pos == r0 ? 0 : 1;
-    if (tile0 == 0 && tid == 0)
-      p.item_ctas[gitem] = make_int2(slot ? -1 - (int)blockIdx.x : (int)blockIdx.x,
-                                     (int)((pos + T_b - 1) / start.per));
-    pos += ntile;
+  Segment seg;
+  int mine = 0;                  // this warp's tiles of seg: tile0 + warp + 4 i
+  const uint8_t* src = nullptr;  // this lane's block of the window of 16 tiles
+  uint32_t there = 0, there_before = 0;  // blocks that exist in this window, the last
+  float O[2 * G][NT][4];
+  float m[NT], l[NT], rf[NT];  // rf: score units -> log2 units
 
-    // ------------------------------------- this lane's rows g and g + 8
-    const int count = count_of(p, b);
-    const int rows = min(16, count * p.rep - rt * 16);  // may be <= 0
-    uint32_t qa[QT][G][2][2 * NT];  // [step][row half + NT * channel half]
-    float first[G][4];              // starting value of a group's product
-    float rf[NT];                   // score units -> log2 units
+  auto issue = [&](const Segment& sg, int i) {
+    if ((i & 15) == 0) {
+      const int wi = i + (lane >> 1);
+      const int key = (sg.tile0 + warp + kWarps * wi) * kTile + (lane & 1) * kBlock;
+      src = nullptr;
+      if (wi < mine && key < sg.seen_max) {
+        src = block_at(p.cache, sg.b, sg.h, key, D);
+        if (!src) report_index(p.status);
+      }
+      there_before = there;
+      there = __ballot_sync(0xffffffffu, src != nullptr);
+    }
+    const uint32_t st = (used + i) % kStages;
+    if ((lane >> 1) == (i & 15)) {
+      if (src) {
+        mbar_arrive_expect_tx(&bars[warp][st], BB);
+        bulk_load(ring + (st * 2 + (lane & 1)) * BB, src, BB, &bars[warp][st]);
+      } else {
+        mbar_arrive(&bars[warp][st]);
+      }
+    }
+  };
+
+  for (bool any = false;; any = true) {
+    // ------------------- the next segment, its first tiles on their way ...
+    Segment next;
+    bool more = false;
+    const int items = p.cache.Hk * p.row_tiles;
+#pragma unroll 1
+    while (pos < r1) {
+      bool bad;
+      next.len = length_of(p, b, &bad);
+      const int T_b = (next.len + kTile - 1) / kTile, line = line_of(T_b);
+      if (pos >= base + line * items) {
+        base += line * items;
+        ++b;
+        continue;
+      }
+      const int item = (pos - base) / line;
+      next.b = b;
+      next.tile0 = pos - base - item * line - kItemCost;
+      if (next.tile0 < 0) {  // to the item's first tile
+        pos -= next.tile0;
+        next.tile0 = 0;
+        if (pos >= r1) break;
+      }
+      next.ntile = min(T_b - next.tile0, r1 - pos);
+      next.h = item / p.row_tiles;
+      next.rt = item - next.h * p.row_tiles;
+      next.count = count_of(p, b);
+      next.rows = min(16, next.count * p.rep - next.rt * 16);  // may be <= 0
+      next.seen_min = next.seen_max = next.len;
+      if (p.causal) {
+        const int last = next.len - next.count + 1;  // keys the first query sees
+        next.seen_min = max(0, last + next.rt * 16 / p.rep);
+        next.seen_max = max(0, last + (next.rt * 16 + next.rows - 1) / p.rep);
+      }
+      if (next.rows <= 0) next.seen_max = 0;
+      pos += next.ntile;
+      more = true;
+      break;
+    }
+    if (more) {
+      // tiles with a key that some row sees
+      const int live = min(next.tile0 + next.ntile, (next.seen_max + kTile - 1) / kTile) - next.tile0;
+      mine = live > warp ? (live - warp + kWarps - 1) / kWarps : 0;
+      if (__any_sync(0xffffffffu, *abort_flag)) mine = 0;
+      {  // the queries towards L2 while the page table is read
+        const int row = next.rt * 16 + (lane & 15), qi = row / p.rep;
+        if ((lane & 15) < next.rows)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(q + next.b * p.qs.batch +
+                                                       (next.h * p.rep + row - qi * p.rep) * p.qs.head +
+                                                       qi * p.qs.token + (lane >> 4) * (D / 2)));
+      }
+#pragma unroll 1
+      for (int i = 0; i < min(kStages, mine); ++i) issue(next, i);
+    }
+
+    // -------------------------- ... while the warps join the one just done
+    if (any) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
+        l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
+        if (t == 0) ml_s[warp][nt * 8 + g] = make_float2(m[nt] == -INFINITY ? -INFINITY : m[nt] * rf[nt], l[nt]);
+      }
+      __syncthreads();
+      float top[NT][2], sum[NT][2];  // of rows 2t, 2t + 1
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * t + e;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml_s[w][r].x);
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          float s = 0.f;
+#pragma unroll
+          for (int w = 0; w < kWarps; ++w) s = fmaf(ml_s[w][r].y, fast_exp2(ml_s[w][r].x - ref), s);
+          const float own = fast_exp2(ml_s[warp][r].x - ref) * 64.f;  // codes carry 2^-6
+#pragma unroll
+          for (int j = 0; j < 2 * G; ++j) {
+            O[j][nt][e] *= own;
+            O[j][nt][2 + e] *= own;
+          }
+          top[nt][e] = mx;
+          sum[nt][e] = s;
+        }
+      // warps 2, 3 into 0, 1, then 1 into 0
+#pragma unroll 1
+      for (int half = 2; half > 0; half >>= 1) {
+        float4* at = reinterpret_cast<float4*>(merge + ((warp & (half - 1)) * NT * 8 + 2 * t) * D + 4 * g);
+        if (warp >= half && warp < 2 * half) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int y = 0; y < G; ++y)
+                at[((nt * 8 + e) * D + 32 * y) / 4] = make_float4(O[2 * y][nt][e], O[2 * y][nt][2 + e],
+                                                                  O[2 * y + 1][nt][e], O[2 * y + 1][nt][2 + e]);
+        }
+        __syncthreads();
+        if (warp < half) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
+#pragma unroll
+              for (int y = 0; y < G; ++y) {
+                const float4 o = at[((nt * 8 + e) * D + 32 * y) / 4];
+                O[2 * y][nt][e] += o.x;
+                O[2 * y][nt][2 + e] += o.y;
+                O[2 * y + 1][nt][e] += o.z;
+                O[2 * y + 1][nt][2 + e] += o.w;
+              }
+        }
+        __syncthreads();
+      }
+      if (warp == 0) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + 2 * t + e, row = seg.rt * 16 + r;
+            if (r >= seg.rows) continue;
+            // a range holds at most one item cut in front (slot 0) and one
+            // that starts in it and is cut behind (slot 1)
+            const bool whole = seg.ntile == (seg.len + kTile - 1) / kTile;
+            const float norm = !whole ? 1.f : sum[nt][e] == 0.f ? 0.f : 1.f / sum[nt][e];
+            const int qi = row / p.rep, hq = seg.h * p.rep + row - qi * p.rep;
+            T* dst = out + seg.b * p.os.batch + hq * p.os.head + qi * p.os.token + 4 * g;
+            const size_t part = (size_t)blockIdx.x * 2 + (seg.tile0 > 0 ? 0 : 1);
+            float* prt = p.part + (part * (NT * 8) + r) * D + 4 * g;
+#pragma unroll
+            for (int y = 0; y < G; ++y) {
+              const float v[4] = {O[2 * y][nt][e] * norm, O[2 * y][nt][2 + e] * norm,
+                                  O[2 * y + 1][nt][e] * norm, O[2 * y + 1][nt][2 + e] * norm};
+              if (whole) store4(dst + 32 * y, v);
+              else store4(prt + 32 * y, v);
+            }
+            if (!whole && g == 0) p.part_ml[part * 16 + r] = make_float2(top[nt][e], sum[nt][e]);
+          }
+      }
+    }
+    if (!more) break;
+    seg = next;
+
+    // -------------------------------- the queries: this lane's rows g, g + 8
+    uint32_t qa[QT][2][4];  // of group `warp`: [step][row half + 2 channel half]
+    float first[4] = {0.f, 0.f, 0.f, 0.f};  // -8 x the group's sum of the row
+#pragma unroll
+    for (int i = 0; i < QT * 8; ++i) qa[i / 8][i / 4 % 2][i % 4] = 0u;
     int seen[NT];
-    int seen_min = 0x7fffffff, seen_max = 0;
 #pragma unroll
     for (int hr = 0; hr < NT; ++hr) {
-      const int r = hr * 8 + g, row = rt * 16 + r;
-      const bool live = r < rows;
-      const int qi = live ? row / p.rep : 0, hq = h * p.rep + (live ? row - qi * p.rep : 0);
-      seen[hr] = !live ? 0 : (p.causal ? max(0, len - count + 1 + qi) : len);
-      if (live) seen_min = min(seen_min, seen[hr]);
-      seen_max = max(seen_max, seen[hr]);
-      const T* src = q + b * p.qs.batch + hq * p.qs.head + qi * p.qs.token + 8 * t;
-      float x[G][8], top = 0.f;
+      const int r = hr * 8 + g, row = seg.rt * 16 + r;
+      const bool live = r < seg.rows;
+      const int qi = live ? row / p.rep : 0, hq = seg.h * p.rep + (live ? row - qi * p.rep : 0);
+      seen[hr] = !live ? 0 : (p.causal ? max(0, seg.len - seg.count + 1 + qi) : seg.len);
+      const T* at = q + seg.b * p.qs.batch + hq * p.qs.head + qi * p.qs.token + 8 * t;
+      float x[8], top = 0.f;  // x: of the group this warp prepares
       bool finite = true;
 #pragma unroll
       for (int y = 0; y < G; ++y) {
+        float v[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[y][j] = 0.f;
-        if (live) load8(src + 32 * y, x[y]);
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+        if (live) load8(at + 32 * y, v);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          top = fmaxf(top, fabsf(x[y][j]));
-          finite = finite && fabsf(x[y][j]) < INFINITY;
+          top = fmaxf(top, fabsf(v[j]));
+          finite = finite && fabsf(v[j]) < INFINITY;
+          x[j] = y == 0 || y == warp ? v[j] : x[j];
         }
       }
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       finite = (__ballot_sync(0xffffffffu, finite) >> (lane & 28) & 15u) == 15u;
-      // scale the row so that its largest magnitude lies in [2^13, 2^14)
+      // scale the row so that its largest magnitude lies in [2^13, 2^14); its
+      // scores come out in units of that and of the fields' 2^-24
       const bool tiny = top < 0x1p-60f;
       if (tiny) top *= 0x1p80f;
       const int e = top > 0.f ? (int)(__float_as_uint(top) >> 23) - 127 : 13;
       const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
-      rf[hr] = !finite ? NAN : scalbnf(fabsf(p.scale_log2), e - 13 + 24 - (tiny ? 80 : 0));
+      const float down = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
+      rf[hr] = !finite ? NAN : down * 0x1p24f * (tiny ? 0x1p-80f : 1.f);
+      float sum = 0.f;
 #pragma unroll
-      for (int y = 0; y < G; ++y) {
-        float sum = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          // odd fields sit four bits higher
-          float v = finite ? (tiny ? x[y][j] * 0x1p80f : x[y][j]) * up : 0.f;
-          x[y][j] = (j & 1) ? v * 0.0625f : v;
-          sum += round_half(x[y][j]) * ((j & 1) ? 16.f : 1.f);
-        }
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        first[y][2 * hr] = first[y][2 * hr + 1] = EXACT ? 0.f : sum * (-8.f * 0x1p-24f);
-        if (NT == 1) first[y][2] = first[y][3] = 0.f;
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int ch = 0; ch < 2; ++ch) {
-            const float lo = x[y][2 * st + ch], hi = x[y][2 * st + ch + 4];
-            qa[0][y][st][hr + NT * ch] = half2_bits(lo, hi);
-            if (EXACT) qa[QT - 1][y][st][hr + NT * ch] = half2_bits(lo - round_half(lo), hi - round_half(hi));
-          }
+      for (int j = 0; j < 8; ++j) {
+        // odd fields sit four bits higher
+        const float v = finite ? (tiny ? x[j] * 0x1p80f : x[j]) * up : 0.f;
+        x[j] = (j & 1) ? v * 0.0625f : v;
+        sum += round_half(x[j]) * ((j & 1) ? 16.f : 1.f);
       }
-    }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      first[2 * hr] = first[2 * hr + 1] = sum * (-8.f * 0x1p-24f);
 #pragma unroll
-    for (int o = 4; o < 32; o <<= 1) {
-      seen_min = min(seen_min, __shfl_xor_sync(0xffffffffu, seen_min, o));
-      seen_max = max(seen_max, __shfl_xor_sync(0xffffffffu, seen_max, o));
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          const float lo = x[2 * st + ch], hi = x[2 * st + ch + 4];
+          qa[0][st][hr + 2 * ch] = half2_bits(lo, hi);
+          if (EXACT) qa[QT - 1][st][hr + 2 * ch] = half2_bits(lo - round_half(lo), hi - round_half(hi));
+        }
     }
-    if (rows <= 0) seen_max = 0;
+    if (warp < G) {
+      uint4* to = table + warp * kTable<T> * 32 + lane;
+#pragma unroll
+      for (int k = 0; k < 2 * QT; ++k) {
+        const uint32_t(&a)[4] = qa[k / 2][k % 2];
+        to[k * 32] = make_uint4(a[0], a[1], a[2], a[3]);
+      }
+      if (!EXACT)
+        to[64] = make_uint4(__float_as_uint(first[0]), __float_as_uint(first[1]),
+                            __float_as_uint(first[2]), __float_as_uint(first[3]));
+    }
+    __syncthreads();
 
-    float O[2 * G][NT][4];
-    float m[NT], l[NT];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       m[nt] = -INFINITY;
@@ -324,62 +512,81 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
         for (int e = 0; e < 4; ++e) O[i][nt][e] = 0.f;
     }
 
-    // -------------------------------------------------- stream the tiles
-    // tiles with a key that some row sees; this warp's are tile0 + warp + 4 i
-    const int live_tiles = min(tile0 + ntile, (seen_max + kTile - 1) / kTile) - tile0;
-    int mine = live_tiles > warp ? (live_tiles - warp + kWarps - 1) / kWarps : 0;
-    if (__any_sync(0xffffffffu, *abort_flag)) mine = 0;
-    const uint8_t* src = nullptr;  // this lane's block of the window
-    uint32_t there[2] = {0u, 0u};  // blocks that exist, of even and odd windows
-    auto issue = [&](int i) {
-      if ((i & 15) == 0) {  // window of 16 tiles: a block per lane
-        const int wi = i + (lane >> 1);
-        const int key = (tile0 + warp + kWarps * wi) * kTile + (lane & 1) * kBlock;
-        src = nullptr;
-        if (wi < mine && key < seen_max) {
-          src = block_at(p.cache, b, h, key, D);
-          if (!src) report_index(p.status);
+    // ---------------------------------------------------- stream the tiles
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      const uint32_t at_tile = used + i, st = at_tile % kStages;
+      if (!__all_sync(0xffffffffu, mbar_wait(&bars[warp][st], (at_tile / kStages) & 1u, abort_flag, kWaitNs))) {
+        if (lane == 0) {
+          abort_s = 1;
+          atomicExch(p.status, (int)NYS_ERR_TIMEOUT);
+#pragma unroll 1
+          for (int j = i; j < min(mine, i + kStages); ++j)  // copies still in flight
+            mbar_wait(&bars[warp][(used + j) % kStages], ((used + j) / kStages) & 1u, nullptr, kWaitNs);
         }
-        there[(i >> 4) & 1] = __ballot_sync(0xffffffffu, src != nullptr);
+        __syncwarp();
+        break;
       }
-      const uint32_t st = (used + i) % kStages;
-      if ((lane >> 1) == (i & 15)) {
-        if (src) {
-          mbar_arrive_expect_tx(&bars[warp][st], BB);
-          bulk_load(ring + (st * 2 + (lane & 1)) * BB, src, BB, &bars[warp][st]);
-        } else {
-          mbar_arrive(&bars[warp][st]);
-        }
-      }
-    };
-
-    auto tile_step = [&](int i, auto masked) {
-      constexpr bool MASK = decltype(masked)::value;
-      const uint32_t st = (used + i) % kStages;
       const uint8_t* blk = ring + st * 2 * BB;
-      const int key0 = (tile0 + warp + kWarps * i) * kTile;
+      const int key0 = (seg.tile0 + warp + kWarps * i) * kTile;
+      // the window ahead of this tile's may have been opened already
+      const uint32_t window = (min(i + kStages - 1, mine - 1) ^ i) & 16 ? there_before : there;
+      const uint32_t have = window >> (2 * (i & 15)) & 3u;
+      const bool masked = key0 + kTile > seg.seen_min || have != 3u;  // warp-uniform
+
+      // The tile's scales to fp32, once for all lanes: a lane takes 8 tokens of
+      // one group (a quarter-warp per kind and block for d = 128). Tokens that
+      // no row sees get zeros, whatever their memory holds.
+      bool odd = false;  // an infinity or a NaN among those that are seen
+      __syncwarp();
+      if (lane < 8 * G) {
+        const int kind = lane / (4 * G), y = lane / 4 % G, part = lane & 3;  // part: 8 of 32 tokens
+        const uint4 u = *reinterpret_cast<const uint4*>(blk + (part >> 1) * BB + (kind ? v_scales(D) : k_scales(D)) +
+                                                        y * 32 + (part & 1) * 16);
+        uint32_t x[8] = {u.x << 16, u.x & 0xffff0000u, u.y << 16, u.y & 0xffff0000u,
+                         u.z << 16, u.z & 0xffff0000u, u.w << 16, u.w & 0xffff0000u};
+        if (masked) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (key0 + part * 8 + j >= seg.seen_max || !(have >> (part >> 1) & 1u)) x[j] = 0u;
+            odd = odd || (x[j] & 0x7f800000u) == 0x7f800000u;
+          }
+        }
+        uint4* to = reinterpret_cast<uint4*>(scales + (kind * G + y) * kTile + part * 8);
+        to[0] = make_uint4(x[0], x[1], x[2], x[3]);
+        to[1] = make_uint4(x[4], x[5], x[6], x[7]);
+      }
+      odd = __any_sync(0xffffffffu, odd);
+      __syncwarp();
+
       // scores: n-tile 2 blk + half holds keys 16 blk + 8 half + (2t, 2t + 1)
       float S[4][2 * NT];
+      uint32_t w[4][G];
 #pragma unroll
       for (int n8 = 0; n8 < 4; ++n8) {
-        const uint8_t* kb = blk + (n8 >> 1) * BB;
-        const uint8_t* row = kb + ((n8 & 1) * 8 + g) * (D / 2) + t * (D / 8);
-        uint32_t w[G];
+        const uint8_t* row = blk + (n8 >> 1) * BB + ((n8 & 1) * 8 + g) * (D / 2) + t * (D / 8);
         if (G == 4) {
           const uint4 u = *reinterpret_cast<const uint4*>(row);
-          w[0] = u.x; w[1 % G] = u.y; w[2 % G] = u.z; w[3 % G] = u.w;
+          w[n8][0] = u.x; w[n8][1 % G] = u.y; w[n8][2 % G] = u.z; w[n8][3 % G] = u.w;
         } else if (G == 2) {
           const uint2 u = *reinterpret_cast<const uint2*>(row);
-          w[0] = u.x; w[1 % G] = u.y;
+          w[n8][0] = u.x; w[n8][1 % G] = u.y;
         } else {
-          w[0] = *reinterpret_cast<const uint32_t*>(row);
+          w[n8][0] = *reinterpret_cast<const uint32_t*>(row);
         }
 #pragma unroll
         for (int e = 0; e < 2 * NT; ++e) S[n8][e] = 0.f;
+      }
 #pragma unroll
-        for (int y = 0; y < G; ++y) {
-          uint32_t f[4] = {w[y] & 0x000f000fu, w[y] & 0x00f000f0u, (w[y] >> 8) & 0x000f000fu,
-                           (w[y] >> 8) & 0x00f000f0u};
+      for (int y = 0; y < G; ++y) {
+        uint4 a[2 * QT], c = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int k = 0; k < 2 * QT; ++k) a[k] = table[(y * kTable<T> + k) * 32 + lane];
+        if (!EXACT) c = table[(y * kTable<T> + 2) * 32 + lane];
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) {
+          uint32_t f[4] = {w[n8][y] & 0x000f000fu, w[n8][y] & 0x00f000f0u, (w[n8][y] >> 8) & 0x000f000fu,
+                           (w[n8][y] >> 8) & 0x00f000f0u};
           if (EXACT) {  // fields less 8, exact in subnormals too
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
@@ -389,36 +596,29 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
               f[j] = reinterpret_cast<const uint32_t&>(v);
             }
           }
-          float acc[4];
+          float acc[4] = {__uint_as_float(c.x), __uint_as_float(c.y), __uint_as_float(c.z), __uint_as_float(c.w)};
 #pragma unroll
-          for (int qt = QT - 1; qt >= 0; --qt)
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-              const uint32_t(&a)[2 * NT] = qa[qt][y][s];
-              if (qt == QT - 1 && s == 0)
-                mma_f16(acc, a[0], NT == 2 ? a[NT - 1] : 0u, a[NT], NT == 2 ? a[2 * NT - 1] : 0u, f[0], f[1],
-                        first[y]);
-              else
-                mma_f16(acc, a[0], NT == 2 ? a[NT - 1] : 0u, a[NT], NT == 2 ? a[2 * NT - 1] : 0u, f[2 * s],
-                        f[2 * s + 1], acc);
-            }
-          const uint32_t sc = *reinterpret_cast<const uint32_t*>(kb + k_scales(D) + y * 32 + (n8 & 1) * 16 + t * 4);
-          const float s0 = low_bf16(sc), s1 = high_bf16(sc);
+          for (int k = 2 * QT - 1; k >= 0; --k)  // the smaller terms first
+            mma_f16(acc, a[k].x, a[k].y, a[k].z, a[k].w, f[2 * (k & 1)], f[2 * (k & 1) + 1], acc);
+          const float2 sc = *reinterpret_cast<const float2*>(scales + y * kTile + n8 * 8 + 2 * t);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            S[n8][2 * nt] = fmaf(s0, acc[2 * nt], S[n8][2 * nt]);
-            S[n8][2 * nt + 1] = fmaf(s1, acc[2 * nt + 1], S[n8][2 * nt + 1]);
+            S[n8][2 * nt] = fmaf(sc.x, acc[2 * nt], S[n8][2 * nt]);
+            S[n8][2 * nt + 1] = fmaf(sc.y, acc[2 * nt + 1], S[n8][2 * nt + 1]);
           }
         }
       }
-      if (MASK) {
-        const uint32_t have = there[(i >> 4) & 1] >> (2 * (i & 15));
+      uint32_t hidden = 0;  // of this lane's scores
+      if (masked) {
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8)
 #pragma unroll
           for (int e = 0; e < 2 * NT; ++e) {
             const int key = key0 + 8 * n8 + 2 * t + (e & 1);
-            if (key >= seen[e >> 1] || !(have >> (n8 >> 1) & 1u)) S[n8][e] = -INFINITY;
+            if (key >= seen[e >> 1] || !(have >> (n8 >> 1) & 1u)) {
+              S[n8][e] = -INFINITY;
+              hidden |= 1u << (n8 * 2 * NT + e);
+            }
           }
       }
       // running maximum and sum per row; the sum stays split over the lanes
@@ -442,11 +642,19 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8)
 #pragma unroll
-          for (int e = 2 * nt; e < 2 * nt + 2; ++e) {
-            S[n8][e] = MASK && S[n8][e] == -INFINITY ? 0.f : fast_exp2(fmaf(S[n8][e], rf[nt], -off));
-            l[nt] += S[n8][e];
-          }
+          for (int e = 2 * nt; e < 2 * nt + 2; ++e) S[n8][e] = fast_exp2(fmaf(S[n8][e], rf[nt], -off));
       }
+      if (masked) {
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8)
+#pragma unroll
+          for (int e = 0; e < 2 * NT; ++e)
+            if (hidden >> (n8 * 2 * NT + e) & 1u) S[n8][e] = 0.f;
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int n8 = 0; n8 < 4; ++n8) l[nt] += S[n8][2 * nt] + S[n8][2 * nt + 1];
       if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -459,229 +667,188 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
           }
         }
       }
-      // out^T += V^T (p s): channel rows, query columns
+      // out^T += V^T (p s): channel rows, query columns. `careful`: rows that
+      // do not see a token must not meet its infinite or NaN scale.
+      auto add_values = [&](auto careful) {
 #pragma unroll
-      for (int bk = 0; bk < 2; ++bk) {
-        const uint8_t* vb = blk + bk * BB;
-        uint32_t wa[2][(G + 1) / 2], wb[2][(G + 1) / 2];  // [token half]: tokens 2t, 2t + 1
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const uint8_t* at = vb + v_codes(D) + hf * 4 * D + lane * (D / 8);
-          if (G == 4) {
-            const uint4 u = *reinterpret_cast<const uint4*>(at);
-            wa[hf][0] = u.x; wa[hf][1 % ((G + 1) / 2)] = u.y; wb[hf][0] = u.z; wb[hf][1 % ((G + 1) / 2)] = u.w;
-          } else if (G == 2) {
-            const uint2 u = *reinterpret_cast<const uint2*>(at);
-            wa[hf][0] = u.x; wb[hf][0] = u.y;
-          } else {
-            wa[hf][0] = *reinterpret_cast<const uint32_t*>(at);  // both tokens' halves
-            wb[hf][0] = 0u;
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < G; ++y) {
-          uint32_t v[2][4];  // [token half][field]: bf16 codes of tokens (2t, 2t + 1)
+        for (int bk = 0; bk < 2; ++bk) {
+          const uint8_t* vb = blk + bk * BB;
+          uint32_t wa[2][(G + 1) / 2], wb[2][(G + 1) / 2];  // [token half]: tokens 2t, 2t + 1
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
-            const uint32_t x = G == 1 ? wa[hf][0]
-                                      : __byte_perm(wa[hf][y >> 1], wb[hf][y >> 1], (y & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t f = ((x >> (4 * j)) & 0x000f000fu) | 0x43004300u, o = 0x43084308u;
-              const __nv_bfloat162 c = __hsub2(reinterpret_cast<const __nv_bfloat162&>(f),
-                                               reinterpret_cast<const __nv_bfloat162&>(o));
-              v[hf][j] = reinterpret_cast<const uint32_t&>(c);
+            const uint8_t* at = vb + v_codes(D) + hf * 4 * D + lane * (D / 8);
+            if (G == 4) {
+              const uint4 u = *reinterpret_cast<const uint4*>(at);
+              wa[hf][0] = u.x; wa[hf][1 % ((G + 1) / 2)] = u.y; wb[hf][0] = u.z; wb[hf][1 % ((G + 1) / 2)] = u.w;
+            } else if (G == 2) {
+              const uint2 u = *reinterpret_cast<const uint2*>(at);
+              wa[hf][0] = u.x; wb[hf][0] = u.y;
+            } else {
+              wa[hf][0] = *reinterpret_cast<const uint32_t*>(at);  // both tokens' halves
+              wb[hf][0] = 0u;
             }
           }
-          const uint32_t sc0 = *reinterpret_cast<const uint32_t*>(vb + v_scales(D) + y * 32 + t * 4);
-          const uint32_t sc1 = *reinterpret_cast<const uint32_t*>(vb + v_scales(D) + y * 32 + 16 + t * 4);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            float w[4];
+          for (int y = 0; y < G; ++y) {
+            uint32_t v[2][4];  // [token half][field]: bf16 codes of tokens (2t, 2t + 1)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float pr = S[2 * bk + (e >> 1)][2 * nt + (e & 1)];
-              const float s = (e & 1) ? high_bf16(e < 2 ? sc0 : sc1) : low_bf16(e < 2 ? sc0 : sc1);
-              w[e] = MASK && pr == 0.f ? 0.f : pr * s;  // what is not seen may be NaN
+            for (int hf = 0; hf < 2; ++hf) {
+              const uint32_t x = G == 1 ? wa[hf][0]
+                                        : __byte_perm(wa[hf][y >> 1], wb[hf][y >> 1], (y & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                // u 2^-133 or, four bits up, u 2^-129; to (u - 8) 2^-6
+                const uint32_t f = (j < 2 ? x : x >> 8) & ((j & 1) ? 0x00f000f0u : 0x000f000fu);
+                const uint32_t up = (j & 1) ? 0x7d007d00u : 0x7f007f00u, o = 0xbe00be00u;  // 2^123, 2^127; -1/8
+                const __nv_bfloat162 c = __hfma2(reinterpret_cast<const __nv_bfloat162&>(f),
+                                                 reinterpret_cast<const __nv_bfloat162&>(up),
+                                                 reinterpret_cast<const __nv_bfloat162&>(o));
+                v[hf][j] = reinterpret_cast<const uint32_t&>(c);
+              }
             }
+            const float2 sc0 = *reinterpret_cast<const float2*>(scales + (G + y) * kTile + bk * 16 + 2 * t);
+            const float2 sc1 = *reinterpret_cast<const float2*>(scales + (G + y) * kTile + bk * 16 + 8 + 2 * t);
 #pragma unroll
-            for (int pt = 0; pt < PT; ++pt) {
-              const uint32_t b0 = pack_bf16x2(w[0], w[1]), b1 = pack_bf16x2(w[2], w[3]);
-              mma_bf16_acc(O[2 * y][nt], v[0][0], v[0][1], v[1][0], v[1][1], b0, b1);
-              mma_bf16_acc(O[2 * y + 1][nt], v[0][2], v[0][3], v[1][2], v[1][3], b0, b1);
-              if (PT > 1) {
-                w[0] -= low_bf16(b0); w[1] -= high_bf16(b0);
-                w[2] -= low_bf16(b1); w[3] -= high_bf16(b1);
+            for (int nt = 0; nt < NT; ++nt) {
+              float z[4] = {S[2 * bk][2 * nt] * sc0.x, S[2 * bk][2 * nt + 1] * sc0.y,
+                            S[2 * bk + 1][2 * nt] * sc1.x, S[2 * bk + 1][2 * nt + 1] * sc1.y};
+              if (decltype(careful)::value) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (hidden >> ((2 * bk + (e >> 1)) * 2 * NT + 2 * nt + (e & 1)) & 1u) z[e] = 0.f;
+              }
+#pragma unroll
+              for (int pt = 0; pt < PT; ++pt) {
+                const uint32_t b0 = pack_bf16x2(z[0], z[1]), b1 = pack_bf16x2(z[2], z[3]);
+                mma_bf16_acc(O[2 * y][nt], v[0][0], v[0][1], v[1][0], v[1][1], b0, b1);
+                mma_bf16_acc(O[2 * y + 1][nt], v[0][2], v[0][3], v[1][2], v[1][3], b0, b1);
+                if (PT > 1) {
+                  z[0] -= low_bf16(b0); z[1] -= high_bf16(b0);
+                  z[2] -= low_bf16(b1); z[3] -= high_bf16(b1);
+                }
               }
             }
           }
         }
-      }
-    };
-
-    for (int i = 0; i < min(kStages, mine); ++i) issue(i);
-    for (int i = 0; i < mine; ++i) {
-      const uint32_t at = used + i;
-      bool ok = mbar_wait(&bars[warp][at % kStages], (at / kStages) & 1u, abort_flag, kWaitNs);
-      if (!__all_sync(0xffffffffu, ok)) {
-        if (lane == 0) {
-          abort_s = 1;
-          atomicExch(p.status, (int)NYS_ERR_TIMEOUT);
-          for (int j = i; j < min(mine, i + kStages); ++j)  // copies still in flight
-            mbar_wait(&bars[warp][(used + j) % kStages], ((used + j) / kStages) & 1u, nullptr, kWaitNs);
-        }
-        __syncwarp();
-        break;
-      }
-      const int end = (tile0 + warp + kWarps * i + 1) * kTile;
-      const bool all = end <= seen_min && (there[(i >> 4) & 1] >> (2 * (i & 15)) & 3u) == 3u;
-      if (all)
-        tile_step(i, std::integral_constant<bool, false>{});
-      else
-        tile_step(i, std::integral_constant<bool, true>{});
+      };
+      if (odd) add_values(std::integral_constant<bool, true>{});
+      else add_values(std::integral_constant<bool, false>{});
       __syncwarp();  // the stage has been read
-      if (i + kStages < mine) issue(i + kStages);
+      if (i + kStages < mine) issue(seg, i + kStages);
     }
     used += mine;
-
-    // --------------------------------------------------- join the warps
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 1);
-      l[nt] += __shfl_xor_sync(0xffffffffu, l[nt], 2);
-      if (t == 0) ml_s[warp][nt * 8 + g] = make_float2(m[nt] == -INFINITY ? -INFINITY : m[nt] * rf[nt], l[nt]);
-    }
-    __syncthreads();
-    float top[NT][2], sum[NT][2];  // of rows 2t, 2t + 1
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * t + e;
-        float mx = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml_s[w][r].x);
-        const float ref = mx == -INFINITY ? 0.f : mx;
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) s = fmaf(ml_s[w][r].y, fast_exp2(ml_s[w][r].x - ref), s);
-        const float own = fast_exp2(ml_s[warp][r].x - ref);
-#pragma unroll
-        for (int j = 0; j < 2 * G; ++j) {
-          O[j][nt][e] *= own;
-          O[j][nt][2 + e] *= own;
-        }
-        top[nt][e] = mx;
-        sum[nt][e] = s;
-      }
-    auto exchange = [&](int buf, bool put) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e)
-#pragma unroll
-          for (int y = 0; y < G; ++y) {
-            float4* at = reinterpret_cast<float4*>(merge + ((buf * NT * 8) + nt * 8 + 2 * t + e) * D + 32 * y + 4 * g);
-            if (put) {
-              *at = make_float4(O[2 * y][nt][e], O[2 * y][nt][2 + e], O[2 * y + 1][nt][e], O[2 * y + 1][nt][2 + e]);
-            } else {
-              const float4 o = *at;
-              O[2 * y][nt][e] += o.x;
-              O[2 * y][nt][2 + e] += o.y;
-              O[2 * y + 1][nt][e] += o.z;
-              O[2 * y + 1][nt][2 + e] += o.w;
-            }
-          }
-    };
-    if (warp >= 2) exchange(warp - 2, true);
-    __syncthreads();
-    if (warp < 2) exchange(warp, false);
-    __syncthreads();
-    if (warp == 1) exchange(0, true);
-    __syncthreads();
-    if (warp == 0) {
-      exchange(0, false);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = nt * 8 + 2 * t + e, row = rt * 16 + r;
-          if (r >= rows) continue;
-          const float norm = sum[nt][e] == 0.f ? 0.f : 1.f / sum[nt][e];
-          const int qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
-          T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token;
-          float* prt = p.part + (((size_t)blockIdx.x * 2 + slot) * (NT * 8) + r) * D;
-#pragma unroll
-          for (int y = 0; y < G; ++y) {
-            float v[4] = {O[2 * y][nt][e], O[2 * y][nt][2 + e], O[2 * y + 1][nt][e], O[2 * y + 1][nt][2 + e]};
-            if (whole) {
-#pragma unroll
-              for (int j = 0; j < 4; ++j) v[j] *= norm;
-              store4(dst + 32 * y + 4 * g, v);
-            } else {
-              store4(prt + 32 * y + 4 * g, v);
-            }
-          }
-          if (!whole && g == 0)
-            p.part_ml[((size_t)blockIdx.x * 2 + slot) * 16 + r] = make_float2(top[nt][e], sum[nt][e]);
-        }
-    }
-    __syncthreads();  // ml_s and the exchange buffer are free again
   }
 }
 
 // Adds up the parts of items that several CTAs shared, and writes the zeros
-// of sequences without keys. A CTA per item, a warp per row.
+// of sequences without keys. A CTA takes consecutive items, a warp a row. It
+// is launched while the split kernel runs (which items were cut follows from
+// the lengths alone) and waits for it before it reads a part.
 template <typename T, int D>
 __global__ void __launch_bounds__(kWarps * 32)
-kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows) {
-  constexpr int V = D / 32;  // channels per lane
-  const int items = p.cache.Hk * p.row_tiles, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int b = blockIdx.x / items, item = blockIdx.x - b * items;
-  const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
-  const int rows = min(16, count_of(p, b) * p.rep - rt * 16);
-  const int tiles = tiles_of(p, b);
-  cudaGridDependencySynchronize();  // launched while the split kernel ran
-  int c0 = 0, c1 = -1, slot0 = 0;
-  if (tiles > 0) {
-    const int2 ctas = p.item_ctas[blockIdx.x];
-    slot0 = ctas.x < 0 ? 1 : 0;
-    c0 = slot0 ? -1 - ctas.x : ctas.x;
-    c1 = ctas.y;
-    if (c0 == c1) return;  // written whole
+kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows,
+              int items_per_cta, int n_items) {
+  constexpr int V = D / 32, AHEAD = 8;  // channels per lane; parts in flight
+  __shared__ int warp_sums[2][kWarps];
+  const int per_b = p.cache.Hk * p.row_tiles, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int i0 = blockIdx.x * items_per_cta, i1 = min(n_items, i0 + items_per_cta);
+  int b = i0 / per_b;
+  int before = 0, all = 0;
+#pragma unroll 1
+  for (int j = tid; j < p.B; j += kWarps * 32) {
+    const int n = line_of(tiles_of(p, j));
+    all += n;
+    if (j < b) before += n;
   }
-  for (int r = warp; r < rows; r += kWarps) {
-    const int row = rt * 16 + r, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
-    float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
-    for (int j = 0; j < V; ++j) acc[j] = 0.f;
-    for (int c = c0 + lane; c <= c1; c += 32)
-      top = fmaxf(top, p.part_ml[((size_t)c * 2 + (c == c0 ? slot0 : 0)) * 16 + r].x);
+  for (int o = 16; o > 0; o >>= 1) {
+    before += __shfl_xor_sync(0xffffffffu, before, o);
+    all += __shfl_xor_sync(0xffffffffu, all, o);
+  }
+  if (lane == 0) {
+    warp_sums[0][warp] = before;
+    warp_sums[1][warp] = all;
+  }
+  __syncthreads();
+  before = all = 0;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const float ref = top == -INFINITY ? 0.f : top;
-#pragma unroll 4
-    for (int c = c0; c <= c1; ++c) {
-      const size_t at = (size_t)c * 2 + (c == c0 ? slot0 : 0);
-      const float2 ml = p.part_ml[at * 16 + r];
-      const float w = fast_exp2(ml.x - ref);
-      sum = fmaf(w, ml.y, sum);
-      const float* src = p.part + (at * part_rows + r) * D + lane * V;
-      if (V == 4) {
-        const float4 x = *reinterpret_cast<const float4*>(src);
-        acc[0] = fmaf(w, x.x, acc[0]); acc[1 % V] = fmaf(w, x.y, acc[1 % V]);
-        acc[2 % V] = fmaf(w, x.z, acc[2 % V]); acc[3 % V] = fmaf(w, x.w, acc[3 % V]);
+  for (int w = 0; w < kWarps; ++w) {
+    before += warp_sums[0][w];
+    all += warp_sums[1][w];
+  }
+  const int per = range_of(p, all * per_b);
+  int base = before * per_b;  // first tile of sequence b
+  cudaGridDependencySynchronize();
+  for (int i = i0; i < i1; ++i) {
+    if (i >= (b + 1) * per_b) {
+      base += line_of(tiles_of(p, b)) * per_b;
+      ++b;
+    }
+    const int tiles = tiles_of(p, b), item = i - b * per_b;
+    const int t0 = base + item * line_of(tiles) + kItemCost;
+    int c0 = 0, c1 = -1;
+    if (tiles > 0) {
+      c0 = t0 / per;
+      c1 = (t0 + tiles - 1) / per;
+      if (c0 == c1) continue;  // written whole
+    }
+    const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
+    const int rows = min(16, count_of(p, b) * p.rep - rt * 16);
+    for (int r = warp; r < rows; r += kWarps) {
+      float top = -INFINITY, sum = 0.f, acc[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] = 0.f;
+      for (int c = c0; c <= c1; c += AHEAD) {
+        float2 ml[AHEAD];
+        float x[AHEAD][V];
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+#pragma unroll
+          for (int j = 0; j < V; ++j) x[k][j] = 0.f;
+          if (c + k <= c1) {
+            const size_t at = (size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0);
+            ml[k] = p.part_ml[at * 16 + r];
+            const float* src = p.part + (at * part_rows + r) * D + lane * V;
+            if (V == 4) {
+              const float4 f = *reinterpret_cast<const float4*>(src);
+              x[k][0] = f.x; x[k][1 % V] = f.y; x[k][2 % V] = f.z; x[k][3 % V] = f.w;
+            } else {
+#pragma unroll
+              for (int j = 0; j < V; ++j) x[k][j] = src[j];
+            }
+          }
+        }
+        float now = top;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) now = fmaxf(now, ml[k].x);
+        const float ref = now == -INFINITY ? 0.f : now, keep = fast_exp2(top - ref);
+        sum *= keep;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[j] *= keep;
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+          const float w = fast_exp2(ml[k].x - ref);
+          sum = fmaf(w, ml[k].y, sum);
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[j] = fmaf(w, x[k][j], acc[j]);
+        }
+        top = now;
+      }
+      const int row = rt * 16 + r, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
+      const float norm = sum == 0.f ? 0.f : 1.f / sum;
+      T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token + lane * V;
+#pragma unroll
+      for (int j = 0; j < V; ++j) acc[j] *= norm;
+      if constexpr (V == 4) {
+        store4(dst, acc);
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] = fmaf(w, src[j], acc[j]);
+        for (int j = 0; j < V; ++j) {
+          if (sizeof(T) == 4) reinterpret_cast<float*>(dst)[j] = acc[j];
+          else reinterpret_cast<__nv_bfloat16*>(dst)[j] = __float2bfloat16_rn(acc[j]);
+        }
       }
-    }
-    const float norm = sum == 0.f ? 0.f : 1.f / sum;
-    T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token + lane * V;
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-      if (sizeof(T) == 4) reinterpret_cast<float*>(dst)[j] = acc[j] * norm;
-      else reinterpret_cast<__nv_bfloat16*>(dst)[j] = __float2bfloat16_rn(acc[j] * norm);
     }
   }
 }
@@ -691,7 +858,7 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
 struct Plan {
   int nt, row_tiles, ctas;
   long long items;
-  size_t ml, item_ctas, total;  // workspace offsets after the parts, bytes
+  size_t ml, total;  // workspace: offset behind the parts, bytes
 };
 
 Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int dtype) {
@@ -703,8 +870,7 @@ Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int dtype) {
   pl.ctas = plan_sms() * (dtype == NYS_BF16 && pl.nt == 1 ? kCtasPerSm : 2);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   pl.ml = up((size_t)pl.ctas * 2 * pl.nt * 8 * c.d * sizeof(float));
-  pl.item_ctas = up(pl.ml + (size_t)pl.ctas * 2 * 16 * sizeof(float2));
-  pl.total = up(pl.item_ctas + (size_t)pl.items * sizeof(int2));
+  pl.total = up(pl.ml + (size_t)pl.ctas * 2 * 16 * sizeof(float2));
   return pl;
 }
 
@@ -715,14 +881,17 @@ int check_attn(const nys_kv4_cache_t* c, int B, int nq, int Hq, int max_length, 
   if (B < 1 || B > 65535 || nq < 1 || Hq < 1 || Hq > 65535 || Hq % c->Hk || max_length < 0)
     return NYS_ERR_SHAPE;
   if ((long long)nq * (Hq / c->Hk) >= (1ll << 30)) return NYS_ERR_SHAPE;
-  if (plan_of(*c, B, nq, Hq, dtype).items >= (1ll << 31)) return NYS_ERR_SHAPE;
+  // the line of tiles (and the items) of the longest sequences allowed
+  const long long length = std::min((long long)max_length, (long long)c->max_pages * c->page_size);
+  const long long items = plan_of(*c, B, nq, Hq, dtype).items;
+  if (items >= (1ll << 31) || items * ((length + kTile - 1) / kTile + kItemCost) >= (1ll << 31) - 65536) return NYS_ERR_SHAPE;
   return NYS_OK;
 }
 
 template <typename T, int D, int NT>
 int launch_split(const AttnParams& p, const Plan& pl, const void* q, void* out, int dev,
                  cudaStream_t st) {
-  constexpr int smem = split_smem<D, NT>();
+  constexpr int smem = split_smem<T, D, NT>();
   static bool ready[64] = {};  // per device; setting it twice does no harm
   if (!ready[dev]) {
     if (cudaFuncSetAttribute(kv4_attn_split<T, D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
@@ -742,12 +911,14 @@ int launch_split(const AttnParams& p, const Plan& pl, const void* q, void* out, 
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)pl.items);
+  const long long most = 8ll * plan_sms();
+  const int per = (int)((pl.items + most - 1) / most);
+  cfg.gridDim = dim3((unsigned)((pl.items + per - 1) / per));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kv4_attn_join<T, D>, p, static_cast<T*>(out), NT * 8);
+  cudaLaunchKernelEx(&cfg, kv4_attn_join<T, D>, p, static_cast<T*>(out), NT * 8, per, (int)pl.items);
   return launch_status();
 }
 
@@ -802,7 +973,6 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   char* ws = static_cast<char*>(workspace);
   p.part = reinterpret_cast<float*>(ws);
   p.part_ml = reinterpret_cast<float2*>(ws + pl.ml);
-  p.item_ctas = reinterpret_cast<int2*>(ws + pl.item_ctas);
   p.B = B;
   p.nq = nq;
   p.rep = Hq / cache->Hk;
