@@ -465,8 +465,11 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * the nearer end, a page outside the pool counts as keys that are not seen;
  * both make nystrom_get_status report NYS_ERR_INDEX. scale: 0 means 1/sqrt(d).
  * Scores, the softmax and all sums are fp32. For NYS_BF16 the probabilities
- * enter the product with V as bf16; for NYS_FP32 queries and probabilities
- * enter as sums of 16-bit terms that keep at least 22 and 24 bits.
+ * enter the product with V as bf16; with more than 48 query rows per cache
+ * head (nq * Hq/Hk, d in {64, 128}) they, and codes times scales, enter as
+ * fp16 scaled by powers of two, or as bf16 where the value scales of 32 tokens
+ * span more than 2^8. For NYS_FP32 queries and probabilities enter as sums of
+ * 16-bit terms that keep at least 22 and 24 bits.
  * Shape rules: B, nq, Hk >= 1, Hq a multiple of Hk, Hq <= 65535, B <= 65535,
  * max_length >= 0, nq * (Hq/Hk) < 2^30 (else NYS_ERR_SHAPE); scale finite
  * (else NYS_ERR_ARG).

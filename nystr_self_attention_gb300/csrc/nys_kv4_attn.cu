@@ -32,8 +32,7 @@
 #include <algorithm>
 #include <cmath>
 
-#include "nys_kv4.h"
-#include "nys_sm100.h"
+#include "nys_kv4_attn.h"
 
 namespace nys {
 namespace kv4 {
@@ -41,30 +40,16 @@ namespace {
 
 using namespace sm100;
 
-constexpr int kTile = 32;    // keys per tile: two blocks
 constexpr int kWarps = 4;
 constexpr int kCtasPerSm = 4;
 constexpr int kStages = 2;   // tiles per warp in flight or in use
-constexpr int kMinTiles = 4; // a CTA's range: at least one tile per warp
-// What starting on an item and joining its warps costs a CTA, in tiles: each
-// item is that much longer on the line, so that a CTA whose range crosses into
-// one gets fewer tiles (8 ragged sequences of up to 32768 tokens, 8 heads:
-// the last CTA ended 7.6 us behind the median one without it).
-constexpr int kItemCost = 6;
+// Tiles of two blocks, 16 query rows, at least a tile per warp. With the item's
+// start and join counted as 6 tiles the last CTA's end came 3 us nearer to the
+// median one (8 ragged sequences of up to 32768 tokens, 8 heads).
+using SplitLine = Line<32, 16, 6, 4>;
+constexpr int kTile = SplitLine::TILE;
 constexpr float kRebase = 8.0f;  // move the running maximum when it grows by 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
-
-struct AttnParams {
-  View cache;
-  nys_strides_t qs, os;
-  const int *lengths, *q_counts;
-  int* status;
-  float* part;      // [CTAs][2][rows][D]: unnormalised outputs of cut items
-  float2* part_ml;  // [CTAs][2][16]: their (maximum in log2 units, sum)
-  int B, nq, rep, row_tiles, max_length, causal;
-  int ctas;
-  float scale_log2;  // scale * log2(e)
-};
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
@@ -119,86 +104,6 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// Tokens of sequence b that its queries may see, and its real queries.
-__device__ __forceinline__ int length_of(const AttnParams& p, int b, bool* bad) {
-  const int given = p.lengths[b];
-  const int limit = (int)min((long long)p.max_length, (long long)p.cache.max_pages * p.cache.page);
-  const int len = min(max(given, 0), limit);
-  *bad = len != given;
-  return len;
-}
-__device__ __forceinline__ int count_of(const AttnParams& p, int b) {
-  return p.q_counts ? min(max(p.q_counts[b], 0), p.nq) : p.nq;
-}
-__device__ __forceinline__ int tiles_of(const AttnParams& p, int b) {
-  bool bad;
-  return (length_of(p, b, &bad) + kTile - 1) / kTile;
-}
-
-// Places that an item of `tiles` takes on the line.
-__device__ __forceinline__ int line_of(int tiles) { return tiles > 0 ? tiles + kItemCost : 0; }
-
-// Tiles per CTA of a line of `total` (the host keeps lines below 2^31).
-__device__ __forceinline__ int range_of(const AttnParams& p, int total) {
-  return max((total + p.ctas - 1) / p.ctas, kMinTiles);
-}
-
-// Where the CTA's range of the line of tiles starts.
-struct Start {
-  int total, per;
-  int base;  // first tile of sequence b
-  int b;
-};
-
-// Block-wide: sums the sequences' tiles in thread chunks, and finds the
-// sequence that tile blockIdx.x * per falls into.
-__device__ __forceinline__ void find_start(const AttnParams& p, Start* s, int* warp_sums) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int chunk = (p.B + kWarps * 32 - 1) / (kWarps * 32);
-  const int b0 = min(p.B, tid * chunk), b1 = min(p.B, b0 + chunk);
-  const int per_item = p.cache.Hk * p.row_tiles;
-  int sum = 0;
-#pragma unroll 1
-  for (int b = b0; b < b1; ++b) {
-    bool bad;
-    sum += line_of((length_of(p, b, &bad) + kTile - 1) / kTile) * per_item;
-    if (bad && blockIdx.x == 0) report_index(p.status);
-  }
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) warp_sums[warp] = incl;
-  __syncthreads();
-  int before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += warp_sums[w];
-    total += warp_sums[w];
-  }
-  const int per = range_of(p, total);
-  const int r0 = min((long long)blockIdx.x * per, (long long)total);
-  int at = before + incl - sum;
-  if (r0 >= at && r0 < at + sum) {  // one thread, if any
-    int b = b0;
-#pragma unroll 1
-    for (; b < b1; ++b) {
-      const int n = line_of(tiles_of(p, b)) * per_item;
-      if (r0 < at + n) break;
-      at += n;
-    }
-    s->base = at;
-    s->b = b;
-  }
-  if (tid == 0) {
-    s->total = total;
-    s->per = per;
-  }
-  __syncthreads();
-}
-
 template <int D>
 constexpr int ring_bytes() { return kWarps * kStages * 2 * block_bytes(D); }
 template <int D, int NT>
@@ -213,11 +118,6 @@ template <typename T, int D, int NT>
 constexpr int split_smem() {
   return ring_bytes<D>() + merge_bytes<D, NT>() + D / 32 * kTable<T> * 512 + kWarps * scales_bytes<D>();
 }
-
-// The part of a CTA's range that lies in one item, and what its rows see.
-struct Segment {
-  int b, h, rt, tile0, ntile, len, count, rows, seen_min, seen_max;
-};
 
 // NT: 8-row groups of query rows (1 or 2). fp32: a query is the sum of two
 // fp16 terms, the codes lose their offset before the product, a probability
@@ -248,7 +148,7 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   if (tid == 0) abort_s = 0;
   fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up meanwhile
-  find_start(p, &start, warp_sums);  // two block syncs
+  find_start<SplitLine, kWarps * 32>(p, &start, warp_sums);  // two block syncs
   const int r0 = (int)min((long long)blockIdx.x * start.per, (long long)start.total);
   const int r1 = min(start.total, r0 + start.per);
   int pos = r0, base = start.base, b = start.b;
@@ -287,42 +187,7 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   for (bool any = false;; any = true) {
     // ------------------- the next segment, its first tiles on their way ...
     Segment next;
-    bool more = false;
-    const int items = p.cache.Hk * p.row_tiles;
-#pragma unroll 1
-    while (pos < r1) {
-      bool bad;
-      next.len = length_of(p, b, &bad);
-      const int T_b = (next.len + kTile - 1) / kTile, line = line_of(T_b);
-      if (pos >= base + line * items) {
-        base += line * items;
-        ++b;
-        continue;
-      }
-      const int item = (pos - base) / line;
-      next.b = b;
-      next.tile0 = pos - base - item * line - kItemCost;
-      if (next.tile0 < 0) {  // to the item's first tile
-        pos -= next.tile0;
-        next.tile0 = 0;
-        if (pos >= r1) break;
-      }
-      next.ntile = min(T_b - next.tile0, r1 - pos);
-      next.h = item / p.row_tiles;
-      next.rt = item - next.h * p.row_tiles;
-      next.count = count_of(p, b);
-      next.rows = min(16, next.count * p.rep - next.rt * 16);  // may be <= 0
-      next.seen_min = next.seen_max = next.len;
-      if (p.causal) {
-        const int last = next.len - next.count + 1;  // keys the first query sees
-        next.seen_min = max(0, last + next.rt * 16 / p.rep);
-        next.seen_max = max(0, last + (next.rt * 16 + next.rows - 1) / p.rep);
-      }
-      if (next.rows <= 0) next.seen_max = 0;
-      pos += next.ntile;
-      more = true;
-      break;
-    }
+    const bool more = next_segment<SplitLine>(p, pos, r1, base, b, next);
     if (more) {
       // tiles with a key that some row sees
       const int live = min(next.tile0 + next.ntile, (next.seen_max + kTile - 1) / kTile) - next.tile0;
@@ -408,13 +273,11 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
           for (int e = 0; e < 2; ++e) {
             const int r = nt * 8 + 2 * t + e, row = seg.rt * 16 + r;
             if (r >= seg.rows) continue;
-            // a range holds at most one item cut in front (slot 0) and one
-            // that starts in it and is cut behind (slot 1)
-            const bool whole = seg.ntile == (seg.len + kTile - 1) / kTile;
+            const bool whole = seg.whole(kTile);
             const float norm = !whole ? 1.f : sum[nt][e] == 0.f ? 0.f : 1.f / sum[nt][e];
             const int qi = row / p.rep, hq = seg.h * p.rep + row - qi * p.rep;
             T* dst = out + seg.b * p.os.batch + hq * p.os.head + qi * p.os.token + 4 * g;
-            const size_t part = (size_t)blockIdx.x * 2 + (seg.tile0 > 0 ? 0 : 1);
+            const size_t part = part_slot(seg);
             float* prt = p.part + (part * (NT * 8) + r) * D + 4 * g;
 #pragma unroll
             for (int y = 0; y < G; ++y) {
@@ -423,7 +286,7 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
               if (whole) store4(dst + 32 * y, v);
               else store4(prt + 32 * y, v);
             }
-            if (!whole && g == 0) p.part_ml[part * 16 + r] = make_float2(top[nt][e], sum[nt][e]);
+            if (!whole && g == 0) p.part_ml[part * (NT * 8) + r] = make_float2(top[nt][e], sum[nt][e]);
           }
       }
     }
@@ -744,19 +607,20 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
 // of sequences without keys. A CTA takes consecutive items, a warp a row. It
 // is launched while the split kernel runs (which items were cut follows from
 // the lengths alone) and waits for it before it reads a part.
-template <typename T, int D>
+template <typename T, int D, typename L>
 __global__ void __launch_bounds__(kWarps * 32)
 kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows,
               int items_per_cta, int n_items) {
+  constexpr int SUB = L::ROWS / 16;  // a unit of work: 16 rows of an item
   constexpr int V = D / 32, AHEAD = 8;  // channels per lane; parts in flight
   __shared__ int warp_sums[2][kWarps];
-  const int per_b = p.cache.Hk * p.row_tiles, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int per_b = p.cache.Hk * p.row_tiles * SUB, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i0 = blockIdx.x * items_per_cta, i1 = min(n_items, i0 + items_per_cta);
   int b = i0 / per_b;
   int before = 0, all = 0;
 #pragma unroll 1
   for (int j = tid; j < p.B; j += kWarps * 32) {
-    const int n = line_of(tiles_of(p, j));
+    const int n = L::places(L::tiles(p, j));
     all += n;
     if (j < b) before += n;
   }
@@ -776,16 +640,16 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
     before += warp_sums[0][w];
     all += warp_sums[1][w];
   }
-  const int per = range_of(p, all * per_b);
-  int base = before * per_b;  // first tile of sequence b
+  const int per = L::range(p, all * (per_b / SUB));
+  int base = before * (per_b / SUB);  // first place of sequence b
   cudaGridDependencySynchronize();
   for (int i = i0; i < i1; ++i) {
     if (i >= (b + 1) * per_b) {
-      base += line_of(tiles_of(p, b)) * per_b;
+      base += L::places(L::tiles(p, b)) * (per_b / SUB);
       ++b;
     }
-    const int tiles = tiles_of(p, b), item = i - b * per_b;
-    const int t0 = base + item * line_of(tiles) + kItemCost;
+    const int tiles = L::tiles(p, b), item = (i - b * per_b) / SUB, sub = (i - b * per_b) % SUB;
+    const int t0 = base + item * L::places(tiles) + L::COST;
     int c0 = 0, c1 = -1;
     if (tiles > 0) {
       c0 = t0 / per;
@@ -793,8 +657,8 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
       if (c0 == c1) continue;  // written whole
     }
     const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
-    const int rows = min(16, count_of(p, b) * p.rep - rt * 16);
-    for (int r = warp; r < rows; r += kWarps) {
+    const int rows = min(L::ROWS, count_of(p, b) * p.rep - rt * L::ROWS);
+    for (int r = sub * 16 + warp; r < min(rows, sub * 16 + 16); r += kWarps) {
       float top = -INFINITY, sum = 0.f, acc[V];
 #pragma unroll
       for (int j = 0; j < V; ++j) acc[j] = 0.f;
@@ -808,7 +672,7 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
           for (int j = 0; j < V; ++j) x[k][j] = 0.f;
           if (c + k <= c1) {
             const size_t at = (size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0);
-            ml[k] = p.part_ml[at * 16 + r];
+            ml[k] = p.part_ml[at * part_rows + r];
             const float* src = p.part + (at * part_rows + r) * D + lane * V;
             if (V == 4) {
               const float4 f = *reinterpret_cast<const float4*>(src);
@@ -835,7 +699,7 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
         }
         top = now;
       }
-      const int row = rt * 16 + r, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
+      const int row = rt * L::ROWS + r, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
       const float norm = sum == 0.f ? 0.f : 1.f / sum;
       T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token + lane * V;
 #pragma unroll
@@ -855,7 +719,12 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
 
 // --------------------------------------------------------------------- host
 
+// bf16 calls with more query rows per cache head than this go to the tensor
+// core kernel (d = 32 stays: its rows are half a swizzled operand row).
+constexpr int kChunkRows = 48;
+
 struct Plan {
+  bool chunk;
   int nt, row_tiles, ctas;
   long long items;
   size_t ml, total;  // workspace: offset behind the parts, bytes
@@ -864,13 +733,22 @@ struct Plan {
 Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int dtype) {
   Plan pl{};
   const long long rows = (long long)nq * (Hq / c.Hk);
+  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
+  pl.chunk = dtype == NYS_BF16 && c.d >= 64 && rows > kChunkRows;
+  if (pl.chunk) {
+    pl.row_tiles = (int)((rows + ChunkLine::ROWS - 1) / ChunkLine::ROWS);
+    pl.items = (long long)B * c.Hk * pl.row_tiles;
+    pl.ctas = plan_sms();
+    pl.ml = up((size_t)pl.ctas * 2 * ChunkLine::ROWS * c.d * sizeof(float));
+    pl.total = up(pl.ml + (size_t)pl.ctas * 2 * ChunkLine::ROWS * sizeof(float2));
+    return pl;
+  }
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (int)((rows + 15) / 16);
   pl.items = (long long)B * c.Hk * pl.row_tiles;
   pl.ctas = plan_sms() * (dtype == NYS_BF16 && pl.nt == 1 ? kCtasPerSm : 2);
-  auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   pl.ml = up((size_t)pl.ctas * 2 * pl.nt * 8 * c.d * sizeof(float));
-  pl.total = up(pl.ml + (size_t)pl.ctas * 2 * 16 * sizeof(float2));
+  pl.total = up(pl.ml + (size_t)pl.ctas * 2 * pl.nt * 8 * sizeof(float2));
   return pl;
 }
 
@@ -883,9 +761,32 @@ int check_attn(const nys_kv4_cache_t* c, int B, int nq, int Hq, int max_length, 
   if ((long long)nq * (Hq / c->Hk) >= (1ll << 30)) return NYS_ERR_SHAPE;
   // the line of tiles (and the items) of the longest sequences allowed
   const long long length = std::min((long long)max_length, (long long)c->max_pages * c->page_size);
-  const long long items = plan_of(*c, B, nq, Hq, dtype).items;
-  if (items >= (1ll << 31) || items * ((length + kTile - 1) / kTile + kItemCost) >= (1ll << 31) - 65536) return NYS_ERR_SHAPE;
+  const Plan pl = plan_of(*c, B, nq, Hq, dtype);
+  const long long places = pl.chunk ? ChunkLine::places((int)((length + ChunkLine::TILE - 1) / ChunkLine::TILE))
+                                    : SplitLine::places((int)((length + kTile - 1) / kTile));
+  const long long units = pl.chunk ? pl.items * (ChunkLine::ROWS / 16) : pl.items;
+  if (units >= (1ll << 31) || pl.items * places >= (1ll << 31) - 65536) return NYS_ERR_SHAPE;
   return NYS_OK;
+}
+
+// units: items, or for items of more than 16 rows their 16-row pieces
+template <typename T, int D, typename L>
+int launch_join(const AttnParams& p, void* out, int part_rows, cudaStream_t st) {
+  const long long units = (long long)p.B * p.cache.Hk * p.row_tiles * (L::ROWS / 16);
+  KernelScope scope("kv4_attn_join", st);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  const long long most = 8ll * plan_sms();
+  const int per = (int)((units + most - 1) / most);
+  cfg.gridDim = dim3((unsigned)((units + per - 1) / per));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.stream = st;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kv4_attn_join<T, D, L>, p, static_cast<T*>(out), part_rows, per, (int)units);
+  return launch_status();
 }
 
 template <typename T, int D, int NT>
@@ -906,20 +807,7 @@ int launch_split(const AttnParams& p, const Plan& pl, const void* q, void* out, 
     const int rc = launch_status();
     if (rc != NYS_OK) return rc;
   }
-  KernelScope scope("kv4_attn_join", st);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  const long long most = 8ll * plan_sms();
-  const int per = (int)((pl.items + most - 1) / most);
-  cfg.gridDim = dim3((unsigned)((pl.items + per - 1) / per));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kv4_attn_join<T, D>, p, static_cast<T*>(out), NT * 8, per, (int)pl.items);
-  return launch_status();
+  return launch_join<T, D, SplitLine>(p, out, NT * 8, st);
 }
 
 }  // namespace
@@ -981,6 +869,12 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   p.causal = causal;
   p.ctas = pl.ctas;
   p.scale_log2 = (scale == 0.f ? 1.f / std::sqrt((float)cache->d) : scale) * 1.4426950408889634f;
+  if (pl.chunk) {
+    rc = launch_kv4_chunk(p, cache->d, q, out, stream);
+    if (rc != NYS_OK) return rc;
+    return cache->d == 64 ? launch_join<__nv_bfloat16, 64, ChunkLine>(p, out, ChunkLine::ROWS, stream)
+                          : launch_join<__nv_bfloat16, 128, ChunkLine>(p, out, ChunkLine::ROWS, stream);
+  }
   auto go = [&](auto type, auto d) {
     using T = decltype(type);
     constexpr int D = decltype(d)::value;
