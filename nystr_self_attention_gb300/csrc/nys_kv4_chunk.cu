@@ -13,7 +13,7 @@
 //   O_g += P V              tcgen05, P from tensor memory, V channels innermost
 // Warps 0-3, 4-7: the groups' softmax. Warps 8-11 (K) and 12-15 (V): unpack 32
 // keys each of every tile into swizzled fp16 operands. Warps 16, 17: issue the
-// two products.
+// two products (18 and 19 make up a warpgroup).
 //
 // fp16 operands: code * scale has 12 bits and is rounded to 11 (bf16 would keep
 // 8, which alone would cost as much as rounding the result does). fp16's range
@@ -43,12 +43,17 @@ namespace {
 using namespace sm100;
 using L = ChunkLine;
 
-constexpr int kThreads = 18 * 32;
+// Registers: launched with 96 a thread (640 threads), of which the softmax
+// groups take 128, the unpackers 80 and the issuers' warpgroup 64.
+constexpr int kThreads = 20 * 32;
+constexpr int kSoftmaxRegs = 128, kUnpackRegs = 80, kIssueRegs = 64;
+static_assert(128 * (2 * kSoftmaxRegs + 2 * kUnpackRegs + kIssueRegs) <= kThreads * 96, "register split");
 constexpr int kSlots = 2;  // K tiles and V tiles in shared memory
 constexpr int kInfo = 4;   // tiles whose facts are kept
 constexpr float kRebase = 8.0f;
 constexpr int kNarrow = 8;  // value scales of 32 tokens within 2^8: fp16
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kSpins = 1 << 20;  // waits of up to 20 us each: a bound, never met
 
 // What a tile's softmax has to know, per 32 tokens: the powers of two of keys
 // and values, and the tokens that must not enter a sum as they are.
@@ -73,13 +78,18 @@ struct Shared {
   int abort;
 };
 
+// The code is kept short where it can be (plain bounded spins, loops over
+// pairs of 32 keys): the roles' loops share the SM's instruction caches.
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int* status,
                                              volatile int* abort_flag) {
-  if (mbar_wait(bar, parity, abort_flag, kWaitNs)) return true;
-  if (!*abort_flag) {
-    *abort_flag = 1;
-    atomicExch(status, (int)NYS_ERR_TIMEOUT);
+  if (mbar_test(bar, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < kSpins; ++i) {
+    if (mbar_try_wait_sleep(bar, parity, 20000u)) return true;
+    if (*abort_flag) return false;
   }
+  *abort_flag = 1;
+  atomicExch(status, (int)NYS_ERR_TIMEOUT);
   return false;
 }
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status,
@@ -125,6 +135,25 @@ __device__ __forceinline__ uint4 unpack8_wide(uint32_t w, uint32_t a) {
   };
   return make_uint4(one(w & 0x000f000fu, 0x7f007f00u), one(w & 0x00f000f0u, 0x7d007d00u),
                     one((w >> 8) & 0x000f000fu, 0x7f007f00u), one((w >> 8) & 0x00f000f0u, 0x7d007d00u));
+}
+
+template <int N>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// a * b + c on two values at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(reinterpret_cast<unsigned long long&>(a)), "l"(reinterpret_cast<unsigned long long&>(b)),
+        "l"(reinterpret_cast<unsigned long long&>(c)));
+  return reinterpret_cast<float2&>(d);
 }
 
 // Tiles of a segment that some row sees, and the groups of rows it has.
@@ -202,14 +231,15 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
         else raw_s.x = *reinterpret_cast<const uint32_t*>(at);
       }
     };
-    if (tiles > 0) fetch(0);
-    for (int i = 0; i < tiles; ++i, ++n) {
+#pragma unroll 1
+    for (int i = -1; i < tiles; ++i) {
       uint4 now[4];
 #pragma unroll
       for (int k = 0; k < 4; ++k) now[k] = raw[k];
       const uint2 now_s = raw_s;
       const uint32_t now_have = have;
       if (i + 1 < tiles) fetch(i + 1);
+      if (i < 0) continue;
       const int slot = n % kSlots;
       TileInfo& info = sh.info[n % kInfo];
       // ---- scales: the largest one's exponent, then fp16 in [token][group]
@@ -264,11 +294,14 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
           if ((bits[j] >> 23 & 255u) == 255u) atomicOr(&info.odd_of[part][y], 1u << (tok + j));
       }
       __syncwarp();
-      // ---- codes
+      // ---- codes, a vector at a time (rolled: the registers move up)
       uint8_t* dst = slots + slot * tile_bytes<D>();
-#pragma unroll
+#pragma unroll 1
       for (int k = 0; k < 4; ++k) {
-        const uint32_t w[4] = {now[k].x, now[k].y, now[k].z, now[k].w};
+        const uint32_t w[4] = {now[0].x, now[0].y, now[0].z, now[0].w};
+        now[0] = now[1];
+        now[1] = now[2];
+        now[2] = now[3];
         if (KEYS) {
           const int token = k * 8 + (lane & 7), row = part * 32 + token;
           const uint16_t* a = reinterpret_cast<const uint16_t*>(stage) + token * G;
@@ -279,23 +312,27 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
                 unpack8(w[g], a[g] * 0x10001u);
           }
         } else {
+          // tokens 2t, 2t + 1 of the half block, pairs of groups
+          auto values = [&](auto&& unpack) {
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {  // tokens 2t, 2t + 1 of the half block
-            const int token = k * 8 + 2 * (lane & 3) + e, row = part * 32 + token;
-            const uint32_t* a = reinterpret_cast<const uint32_t*>(stage) + token * (G / 2);
-#pragma unroll
-            for (int pr = 0; pr < G / 2; ++pr) {  // pairs of groups
+            for (int e = 0; e < 2; ++e) {
+              const int token = k * 8 + 2 * (lane & 3) + e, row = part * 32 + token;
+              const uint32_t* a = reinterpret_cast<const uint32_t*>(stage) + token * (G / 2);
               const uint32_t chunk = (uint32_t)(lane >> 2) ^ (row & 7u);
-              const uint32_t f = w[e * (G / 2) + pr];
-              *reinterpret_cast<uint4*>(dst + pr * 16384 + row * 128 + (chunk << 4)) =
-                  wide ? unpack8_wide(f, a[pr]) : unpack8(f, a[pr]);
+#pragma unroll
+              for (int pr = 0; pr < G / 2; ++pr)
+                *reinterpret_cast<uint4*>(dst + pr * 16384 + row * 128 + (chunk << 4)) =
+                    unpack(w[e * (G / 2) + pr], a[pr]);
             }
-          }
+          };
+          if (wide) values([](uint32_t f, uint32_t a) { return unpack8_wide(f, a); });
+          else values([](uint32_t f, uint32_t a) { return unpack8(f, a); });
         }
       }
       fence_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[slot]);
+      ++n;
     }
   }
 }
@@ -333,7 +370,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       float top = 0.f;
       bool finite = true;
       const uint4* src = reinterpret_cast<const uint4*>(q + sg.b * p.qs.batch + hq * p.qs.head + qi * p.qs.token);
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -353,7 +390,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       // units of a score, less the keys' power of two
       float rf = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
       rf = !finite ? NAN : rf * 0x1p10f * (tiny ? 0x1p-80f : 1.f);
-#pragma unroll 4
+#pragma unroll 2
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -385,22 +422,29 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
         const bool all = key0 + L::TILE <= warp_seen &&
                          (info.have[0] & info.have[1] & info.have[2] & info.have[3]) == 0xffffffffu;
         float cand = -INFINITY;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32];
-          tmem_ld32(scol + 32 * c, s);
+        uint32_t x[2][32];
+        // two passes over pairs of 32 keys; the second starts on the pair that
+        // the first left in registers
+#pragma unroll 1
+        for (int pr = 1; pr >= 0; --pr) {
+          tmem_ld32(scol + 64 * pr, x[0]);
+          tmem_ld32(scol + 64 * pr + 32, x[1]);
           tmem_ld_wait();
-          float mx = -INFINITY;
-          if (all) {
 #pragma unroll
-            for (int e2 = 0; e2 < 32; ++e2) mx = fmaxf(mx, __uint_as_float(s[e2]));
-          } else {
-            const uint32_t vis = visible(c);
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * pr + h;
+            if (!all) {
+              const uint32_t vis = visible(c);
 #pragma unroll
-            for (int e2 = 0; e2 < 32; ++e2)
-              if (vis >> e2 & 1u) mx = fmaxf(mx, __uint_as_float(s[e2]));
+              for (int k = 0; k < 32; ++k)
+                if (!(vis >> k & 1u)) x[h][k] = 0xff800000u;
+            }
+            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[h][k]));
+            const float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+            if (mx > -INFINITY) cand = fmaxf(cand, fmaf(mx, rf * info.k2e[c], info.ev[c]));
           }
-          if (mx > -INFINITY) cand = fmaxf(cand, fmaf(mx, rf * info.k2e[c], info.ev[c]));
         }
         float alpha = 1.f;
         if (cand > m && (m == -INFINITY || cand - m > kRebase)) {
@@ -409,40 +453,47 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
           m = cand;
         }
         const float ref = m == -INFINITY ? 0.f : m;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t s[32], pk[16];
-          tmem_ld32(scol + 32 * c, s);
-          tmem_ld_wait();
-          const float f = rf * info.k2e[c], off = info.ev[c] - ref;
-          float sum = 0.f;
-          if (all) {
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float e2 = fast_exp2(fmaf(__uint_as_float(s[k]), f, off));
-              sum += e2;
-              s[k] = __float_as_uint(e2);
-            }
-          } else {
-            const uint32_t vis = visible(c);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) {
-              const float e2 = (vis >> k & 1u) ? fast_exp2(fmaf(__uint_as_float(s[k]), f, off)) : 0.f;
-              sum += e2;
-              s[k] = __float_as_uint(e2);
-            }
+#pragma unroll 1
+        for (int pr = 0; pr < 2; ++pr) {
+          if (pr) {
+            tmem_ld32(scol + 64, x[0]);
+            tmem_ld32(scol + 96, x[1]);
+            tmem_ld_wait();
           }
-          if (info.wide[c]) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int c = 2 * pr + h;
+            const float f = rf * info.k2e[c], off = info.ev[c] - ref;
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              float2 e2 = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
+                               make_float2(f, f), make_float2(off, off));
+              x[h][2 * k] = __float_as_uint(fast_exp2(e2.x));
+              x[h][2 * k + 1] = __float_as_uint(fast_exp2(e2.y));
+            }
+            if (!all) {
+              const uint32_t vis = visible(c);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(vis >> k & 1u)) x[h][k] = 0u;
+            }
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-              pk[k] = pack_bf16x2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
-          } else {
+              sum[k & 1] = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
+                                make_float2(1.f, 1.f), sum[k & 1]);
+            if (info.wide[c]) {  // packed in place
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              pk[k] = pack_half2(__uint_as_float(s[2 * k]), __uint_as_float(s[2 * k + 1]));
+              for (int k = 0; k < 16; ++k)
+                x[h][k] = pack_bf16x2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
+            } else {
+#pragma unroll
+              for (int k = 0; k < 16; ++k)
+                x[h][k] = pack_half2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
+            }
+            tmem_st16(scol + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(x[h]));
+            l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), info.vinv[c], l);
           }
-          l = fmaf(sum, info.vinv[c], l);
-          tmem_st16(scol + 16 * c, pk);
         }
         if (info.odd[0] | info.odd[1] | info.odd[2] | info.odd[3]) {
 #pragma unroll 1
@@ -562,12 +613,17 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
   int base = sh.start.base, b = sh.start.b;
 
   if (warp < 8) {
+    take_registers<kSoftmaxRegs>();
     softmax_rows<D>(p, sh, q_s, tmem, warp >> 2, q, out, pos, r1, base, b);
   } else if (warp < 12) {
+    give_registers<kUnpackRegs>();
     unpack_tiles<D, true>(p, sh, k_s, stage + (warp - 8) * 32 * (D / 32), warp - 8, pos, r1, base, b);
   } else if (warp < 16) {
+    give_registers<kUnpackRegs>();
     unpack_tiles<D, false>(p, sh, v_s, stage + (warp - 8) * 32 * (D / 32), warp - 12, pos, r1, base, b);
-  } else if (lane == 0) {
+  } else {
+    give_registers<kIssueRegs>();
+    if (warp < 18 && lane == 0) {
     const bool scores = warp == 16;
     const uint32_t id_s = idesc_f16(128, 128), id_v = idesc_f16(128, D, true);
     const uint32_t id_w = idesc_bf16(128, D, false, true);
@@ -578,9 +634,11 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
     while (ok && next_segment<L>(p, pos, r1, base, b, sg)) {
       const int tiles = tiles_seen(sg), groups = groups_of(sg);
       if (tiles <= 0) continue;
+#pragma unroll 1
       for (int i = 0; i < tiles && ok; ++i, ++n) {
         const int slot = n % kSlots;
         const uint32_t ph = (n / kSlots) & 1u;
+#pragma unroll 1
         for (int g = 0; g < groups && ok; ++g) {
           if (scores) {
             if (i == 0) ok = wait_or_fail(&sh.q_full[g], segs[g] & 1u, p.status, abort_flag);
@@ -621,6 +679,8 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
       for (int g = 0; g < groups; ++g) ++segs[g];
     }
     mma_commit(&sh.fin);
+    }
+    __syncwarp();
   }
   // both issuers have committed to fin: no product is in flight after it
   if (warp == 16) {
