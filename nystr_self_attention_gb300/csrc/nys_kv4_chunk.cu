@@ -11,9 +11,10 @@
 //                           overwrites S; the running maximum moves when it
 //                           grows by more than 2^8 (O_g is rescaled then)
 //   O_g += P V              tcgen05, P from tensor memory, V channels innermost
-// Warps 0-3, 4-7: the groups' softmax. Warps 8-11 (K) and 12-15 (V): unpack 32
-// keys each of every tile into swizzled fp16 operands. Warps 16, 17: issue the
-// two products (18 and 19 make up a warpgroup).
+// Warps 0-3, 4-7: the groups' softmax; one thread of a group issues its products
+// (P V of a tile, then S of the next), so that nobody else has to be woken.
+// Warps 8-11 (K) and 12-15 (V): unpack 32 keys each of every tile into swizzled
+// fp16 operands.
 //
 // fp16 operands: code * scale has 12 bits and is rounded to 11 (bf16 would keep
 // 8, which alone would cost as much as rounding the result does). fp16's range
@@ -43,11 +44,7 @@ namespace {
 using namespace sm100;
 using L = ChunkLine;
 
-// Registers: launched with 96 a thread (640 threads), of which the softmax
-// groups take 128, the unpackers 80 and the issuers' warpgroup 64.
-constexpr int kThreads = 20 * 32;
-constexpr int kSoftmaxRegs = 128, kUnpackRegs = 80, kIssueRegs = 64;
-static_assert(128 * (2 * kSoftmaxRegs + 2 * kUnpackRegs + kIssueRegs) <= kThreads * 96, "register split");
+constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 2;  // K tiles and V tiles in shared memory
 constexpr int kInfo = 4;   // tiles whose facts are kept
 constexpr float kRebase = 8.0f;
@@ -69,8 +66,7 @@ struct TileInfo {
 
 struct Shared {
   uint64_t k_full[kSlots], k_empty[kSlots], v_full[kSlots], v_empty[kSlots];
-  uint64_t q_full[2], s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2];
-  uint64_t fin;
+  uint64_t s_full[2], pv_done[2], fin;
   TileInfo info[kInfo];
   Start start;
   int warp_sums[kThreads / 32];
@@ -135,15 +131,6 @@ __device__ __forceinline__ uint4 unpack8_wide(uint32_t w, uint32_t a) {
   };
   return make_uint4(one(w & 0x000f000fu, 0x7f007f00u), one(w & 0x00f000f0u, 0x7d007d00u),
                     one((w >> 8) & 0x000f000fu, 0x7f007f00u), one((w >> 8) & 0x00f000f0u, 0x7d007d00u));
-}
-
-template <int N>
-__device__ __forceinline__ void take_registers() {
-  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void give_registers() {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // a * b + c on two values at once.
@@ -337,9 +324,23 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
   }
 }
 
+// The 128 threads of a group meet (named barriers 1 and 2); true for all of
+// them if any gave up at a wait, so that they leave together.
+__device__ __forceinline__ bool group_failed(int g, bool failed) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, %2, 128, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"(failed ? 1u : 0u), "r"(g + 1)
+      : "memory");
+  return any != 0;
+}
+
 // A softmax group: 128 query rows, one per thread.
 template <int D>
-__device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, uint8_t* q_s, uint32_t tmem, int g,
+__device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, uint8_t* q_s, const uint8_t* k_s,
+                                             const uint8_t* v_s, uint32_t tmem, int g,
                                              const __nv_bfloat16* q, __nv_bfloat16* out, int pos, int r1,
                                              int base, int b) {
   constexpr int G = D / 32;
@@ -349,7 +350,39 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   const uint32_t lo = (uint32_t)((warp & 3) * 32) << 16;
   const uint32_t scol = tmem + lo + 128 * g, ocol = tmem + lo + 256 + g * D;
   uint8_t* qs = q_s + g * tile_bytes<D>();
-  uint32_t n = 0, n_s = 0, n_o = 0;  // tiles of the CTA; of this group; its outputs
+  const uint32_t id_s = idesc_f16(128, 128), id_v = idesc_f16(128, D, true);
+  const uint32_t id_w = idesc_bf16(128, D, false, true);
+  uint32_t n = 0, n_s = 0;  // tiles of the CTA; of this group
+  // One thread of the group: S of tile t (slot k), once its keys are there; and
+  // P V of tile t. A segment without a second group frees the slots for both.
+  auto issue_scores = [&](uint32_t t, int groups) {
+    const int slot = t % kSlots;
+    if (!wait_or_fail(&sh.k_full[slot], (t / kSlots) & 1u, p.status, abort_flag)) return;
+    tc_fence_after_sync();
+    const uint64_t a0 = smem_desc(smem_u32(qs), 16, 1024, SW_128B);
+    const uint64_t b0 = smem_desc(smem_u32(k_s + slot * tile_bytes<D>()), 16, 1024, SW_128B);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);  // 16 KB chunk, 32 B step
+      mma_bf16(tmem + 128 * g, a0 + off, b0 + off, id_s, kk > 0);
+    }
+    mma_commit(&sh.s_full[g]);
+    for (int k = groups; k < 3; ++k) mma_commit(&sh.k_empty[slot]);
+  };
+  auto issue_values = [&](uint32_t t, bool first, int groups) {
+    const int slot = t % kSlots;
+    tc_fence_after_sync();
+    const uint64_t v0 = smem_desc(smem_u32(v_s + slot * tile_bytes<D>()), 16384, 1024, SW_128B);
+    const TileInfo& info = sh.info[t % kInfo];
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)  // 16 keys: 2 KB of V, 8 columns of P
+      mma_bf16_tA(tmem + 256 + g * D, tmem + 128 * g + kk * 8, v0 + (uint64_t)(kk * 128),
+                  info.wide[kk >> 1] ? id_w : id_v, (!first || kk > 0) ? 1u : 0u);
+    mma_commit(&sh.pv_done[g]);
+    for (int k = groups; k < 3; ++k) mma_commit(&sh.v_empty[slot]);
+  };
+  const bool leader = lr == 0;
+  bool ok = true;
   Segment sg;
   while (next_segment<L>(p, pos, r1, base, b, sg)) {
     const int tiles = max(0, tiles_seen(sg));
@@ -405,13 +438,22 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
             make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]),
                        pack_half2(v[3], v[7]));
       }
+      const int groups = groups_of(sg);
       fence_async_smem();
-      mbar_arrive(&sh.q_full[g]);
+      tc_fence_before_sync();  // the previous segment's output has been read
+      if (group_failed(g, !ok)) return;
+      if (leader) issue_scores(n, groups);
+      __syncwarp();
 
+#pragma unroll 1
       for (int i = 0; i < tiles; ++i, ++n, ++n_s) {
         const int key0 = (sg.tile0 + i) * L::TILE;
-        if (!warp_wait(&sh.v_full[n % kSlots], (n / kSlots) & 1u, p.status, abort_flag)) return;
-        if (!warp_wait(&sh.s_full[g], n_s & 1u, p.status, abort_flag)) return;
+        ok = warp_wait(&sh.v_full[n % kSlots], (n / kSlots) & 1u, p.status, abort_flag) &&
+             warp_wait(&sh.s_full[g], n_s & 1u, p.status, abort_flag);
+        if (!ok) {
+          group_failed(g, true);
+          return;
+        }
         tc_fence_after_sync();
         const TileInfo& info = sh.info[n % kInfo];
         // tokens of 32-key chunk c that this row sees
@@ -517,10 +559,17 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&sh.p_full[g]);
+        if (group_failed(g, false)) return;
+        if (leader) {
+          issue_values(n, i == 0, groups);
+          // S is this tile's P until its product is done
+          if (i + 1 < tiles && wait_or_fail(&sh.pv_done[g], n_s & 1u, p.status, abort_flag))
+            issue_scores(n + 1, groups);
+        }
+        __syncwarp();
       }
-      if (!warp_wait(&sh.o_full[g], n_o & 1u, p.status, abort_flag)) return;
-      ++n_o;
+      ok = warp_wait(&sh.pv_done[g], (n_s - 1) & 1u, p.status, abort_flag);
+      if (!ok) continue;  // to where the group meets next
       tc_fence_after_sync();
     }
     // ---- the row's output: columns back in channels' order
@@ -564,10 +613,6 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       }
     }
     if (live && !whole) p.part_ml[part] = make_float2(m, l);
-    if (tiles > 0) {
-      tc_fence_before_sync();
-      mbar_arrive(&sh.o_empty[g]);
-    }
   }
 }
 
@@ -581,29 +626,24 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
   uint8_t* sm = align1024(smem_raw);
   uint8_t *q_s = sm, *k_s = sm + 2 * TILE, *v_s = k_s + kSlots * TILE;
   __half* stage = reinterpret_cast<__half*>(v_s + kSlots * TILE);
-  volatile int* abort_flag = &sh.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   if (tid == 0) {
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh.k_full[i], 4);
       mbar_init(&sh.v_full[i], 4);
-      mbar_init(&sh.k_empty[i], 1);
-      mbar_init(&sh.v_empty[i], 1);
+      mbar_init(&sh.k_empty[i], 2);
+      mbar_init(&sh.v_empty[i], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh.q_full[i], 128);
       mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.p_full[i], 128);
       mbar_init(&sh.pv_done[i], 1);
-      mbar_init(&sh.o_full[i], 1);
-      mbar_init(&sh.o_empty[i], 128);
     }
     mbar_init(&sh.fin, 2);
     sh.abort = 0;
     fence_barrier_init();
   }
   cudaTriggerProgrammaticLaunchCompletion();
-  if (warp == 16) tmem_alloc(&sh.tmem, 512);
+  if (warp == 8) tmem_alloc(&sh.tmem, 512);
   tc_fence_before_sync();
   find_start<L, kThreads>(p, &sh.start, sh.warp_sums);  // two block syncs
   tc_fence_after_sync();
@@ -613,83 +653,20 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
   int base = sh.start.base, b = sh.start.b;
 
   if (warp < 8) {
-    take_registers<kSoftmaxRegs>();
-    softmax_rows<D>(p, sh, q_s, tmem, warp >> 2, q, out, pos, r1, base, b);
+    softmax_rows<D>(p, sh, q_s, k_s, v_s, tmem, warp >> 2, q, out, pos, r1, base, b);
+    if ((warp & 3) == 0 && lane == 0) mma_commit(&sh.fin);  // behind all this thread issued
   } else if (warp < 12) {
-    give_registers<kUnpackRegs>();
     unpack_tiles<D, true>(p, sh, k_s, stage + (warp - 8) * 32 * (D / 32), warp - 8, pos, r1, base, b);
-  } else if (warp < 16) {
-    give_registers<kUnpackRegs>();
-    unpack_tiles<D, false>(p, sh, v_s, stage + (warp - 8) * 32 * (D / 32), warp - 12, pos, r1, base, b);
   } else {
-    give_registers<kIssueRegs>();
-    if (warp < 18 && lane == 0) {
-    const bool scores = warp == 16;
-    const uint32_t id_s = idesc_f16(128, 128), id_v = idesc_f16(128, D, true);
-    const uint32_t id_w = idesc_bf16(128, D, false, true);
-    uint32_t n = 0;           // tiles of the CTA
-    uint32_t segs[2] = {0, 0}, done[2] = {0, 0};  // per group: segments, tiles
-    Segment sg;
-    bool ok = true;
-    while (ok && next_segment<L>(p, pos, r1, base, b, sg)) {
-      const int tiles = tiles_seen(sg), groups = groups_of(sg);
-      if (tiles <= 0) continue;
-#pragma unroll 1
-      for (int i = 0; i < tiles && ok; ++i, ++n) {
-        const int slot = n % kSlots;
-        const uint32_t ph = (n / kSlots) & 1u;
-#pragma unroll 1
-        for (int g = 0; g < groups && ok; ++g) {
-          if (scores) {
-            if (i == 0) ok = wait_or_fail(&sh.q_full[g], segs[g] & 1u, p.status, abort_flag);
-            if (ok && g == 0) ok = wait_or_fail(&sh.k_full[slot], ph, p.status, abort_flag);
-            // S is the group's last P until its product is done
-            if (ok && done[g] > 0) ok = wait_or_fail(&sh.pv_done[g], (done[g] - 1) & 1u, p.status, abort_flag);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t a0 = smem_desc(smem_u32(q_s + g * TILE), 16, 1024, SW_128B);
-            const uint64_t b0 = smem_desc(smem_u32(k_s + slot * TILE), 16, 1024, SW_128B);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint64_t off = (uint64_t)((kk >> 2) * 1024 + (kk & 3) * 2);  // 16 KB chunk, 32 B step
-              mma_bf16(tmem + 128 * g, a0 + off, b0 + off, id_s, kk > 0);
-            }
-            mma_commit(&sh.s_full[g]);
-            if (g == groups - 1) mma_commit(&sh.k_empty[slot]);
-          } else {
-            ok = wait_or_fail(&sh.p_full[g], done[g] & 1u, p.status, abort_flag);
-            if (ok && i == 0 && segs[g] > 0)
-              ok = wait_or_fail(&sh.o_empty[g], (segs[g] - 1) & 1u, p.status, abort_flag);
-            if (ok && g == 0) ok = wait_or_fail(&sh.v_full[slot], ph, p.status, abort_flag);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint64_t v0 = smem_desc(smem_u32(v_s + slot * TILE), 16384, 1024, SW_128B);
-            const uint32_t o = tmem + 256 + g * D, a = tmem + 128 * g;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)  // 16 keys: 2 KB of V, 8 columns of P
-              mma_bf16_tA(o, a + kk * 8, v0 + (uint64_t)(kk * 128), sh.info[n % kInfo].wide[kk >> 1] ? id_w : id_v,
-                          (i > 0 || kk > 0) ? 1u : 0u);
-            mma_commit(&sh.pv_done[g]);
-            if (g == groups - 1) mma_commit(&sh.v_empty[slot]);
-            if (i == tiles - 1) mma_commit(&sh.o_full[g]);
-          }
-          ++done[g];
-        }
-      }
-      for (int g = 0; g < groups; ++g) ++segs[g];
-    }
-    mma_commit(&sh.fin);
-    }
-    __syncwarp();
+    unpack_tiles<D, false>(p, sh, v_s, stage + (warp - 8) * 32 * (D / 32), warp - 12, pos, r1, base, b);
   }
-  // both issuers have committed to fin: no product is in flight after it
-  if (warp == 16) {
+  if (warp == 8) {  // no product is in flight when tensor memory is freed
     if (lane == 0) mbar_wait(&sh.fin, 0, nullptr, kWaitNs);
     __syncwarp();
   }
   tc_fence_before_sync();
   __syncthreads();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 template <int D>
