@@ -612,7 +612,9 @@ __global__ void __launch_bounds__(kWarps * 32)
 kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows,
               int items_per_cta, int n_items) {
   constexpr int SUB = L::ROWS / 16;  // a unit of work: 16 rows of an item
-  constexpr int V = D / 32, AHEAD = 8;  // channels per lane; parts in flight
+  // channels per lane; rows of a warp and their parts in flight: an item of few
+  // rows has many parts, one of many rows a few
+  constexpr int V = D / 32, AT_ONCE = SUB > 1 ? 4 : 1, AHEAD = SUB > 1 ? 2 : 8;
   __shared__ int warp_sums[2][kWarps];
   const int per_b = p.cache.Hk * p.row_tiles * SUB, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i0 = blockIdx.x * items_per_cta, i1 = min(n_items, i0 + items_per_cta);
@@ -658,59 +660,76 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
     }
     const int h = item / p.row_tiles, rt = item - h * p.row_tiles;
     const int rows = min(L::ROWS, count_of(p, b) * p.rep - rt * L::ROWS);
-    for (int r = sub * 16 + warp; r < min(rows, sub * 16 + 16); r += kWarps) {
-      float top = -INFINITY, sum = 0.f, acc[V];
+    const int end = min(rows, sub * 16 + 16);
+#pragma unroll 1
+    for (int r0 = sub * 16 + warp * AT_ONCE; r0 < end; r0 += kWarps * AT_ONCE) {
+      float top[AT_ONCE], sum[AT_ONCE], acc[AT_ONCE][V];
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] = 0.f;
+      for (int u = 0; u < AT_ONCE; ++u) {
+        top[u] = -INFINITY;
+        sum[u] = 0.f;
+#pragma unroll
+        for (int j = 0; j < V; ++j) acc[u][j] = 0.f;
+      }
+#pragma unroll 1
       for (int c = c0; c <= c1; c += AHEAD) {
-        float2 ml[AHEAD];
-        float x[AHEAD][V];
+        float2 ml[AT_ONCE][AHEAD];
+        float x[AT_ONCE][AHEAD][V];
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-          ml[k] = make_float2(-INFINITY, 0.f);
+        for (int u = 0; u < AT_ONCE; ++u)
 #pragma unroll
-          for (int j = 0; j < V; ++j) x[k][j] = 0.f;
-          if (c + k <= c1) {
-            const size_t at = (size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0);
-            ml[k] = p.part_ml[at * part_rows + r];
-            const float* src = p.part + (at * part_rows + r) * D + lane * V;
-            if (V == 4) {
-              const float4 f = *reinterpret_cast<const float4*>(src);
-              x[k][0] = f.x; x[k][1 % V] = f.y; x[k][2 % V] = f.z; x[k][3 % V] = f.w;
-            } else {
+          for (int k = 0; k < AHEAD; ++k) {
+            ml[u][k] = make_float2(-INFINITY, 0.f);
 #pragma unroll
-              for (int j = 0; j < V; ++j) x[k][j] = src[j];
+            for (int j = 0; j < V; ++j) x[u][k][j] = 0.f;
+            if (c + k <= c1 && r0 + u < end) {
+              const size_t at = ((size_t)(c + k) * 2 + (c + k == c0 ? 1 : 0)) * part_rows + r0 + u;
+              ml[u][k] = p.part_ml[at];
+              const float* src = p.part + at * D + lane * V;
+              if (V == 4) {
+                const float4 f = *reinterpret_cast<const float4*>(src);
+                x[u][k][0] = f.x; x[u][k][1 % V] = f.y; x[u][k][2 % V] = f.z; x[u][k][3 % V] = f.w;
+              } else {
+#pragma unroll
+                for (int j = 0; j < V; ++j) x[u][k][j] = src[j];
+              }
             }
           }
+#pragma unroll
+        for (int u = 0; u < AT_ONCE; ++u) {
+          float now = top[u];
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) now = fmaxf(now, ml[u][k].x);
+          const float ref = now == -INFINITY ? 0.f : now, keep = fast_exp2(top[u] - ref);
+          sum[u] *= keep;
+#pragma unroll
+          for (int j = 0; j < V; ++j) acc[u][j] *= keep;
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const float w = fast_exp2(ml[u][k].x - ref);
+            sum[u] = fmaf(w, ml[u][k].y, sum[u]);
+#pragma unroll
+            for (int j = 0; j < V; ++j) acc[u][j] = fmaf(w, x[u][k][j], acc[u][j]);
+          }
+          top[u] = now;
         }
-        float now = top;
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) now = fmaxf(now, ml[k].x);
-        const float ref = now == -INFINITY ? 0.f : now, keep = fast_exp2(top - ref);
-        sum *= keep;
-#pragma unroll
-        for (int j = 0; j < V; ++j) acc[j] *= keep;
-#pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-          const float w = fast_exp2(ml[k].x - ref);
-          sum = fmaf(w, ml[k].y, sum);
-#pragma unroll
-          for (int j = 0; j < V; ++j) acc[j] = fmaf(w, x[k][j], acc[j]);
-        }
-        top = now;
       }
-      const int row = rt * L::ROWS + r, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
-      const float norm = sum == 0.f ? 0.f : 1.f / sum;
-      T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token + lane * V;
 #pragma unroll
-      for (int j = 0; j < V; ++j) acc[j] *= norm;
-      if constexpr (V == 4) {
-        store4(dst, acc);
-      } else {
+      for (int u = 0; u < AT_ONCE; ++u) {
+        if (r0 + u >= end) continue;
+        const int row = rt * L::ROWS + r0 + u, qi = row / p.rep, hq = h * p.rep + row - qi * p.rep;
+        const float norm = sum[u] == 0.f ? 0.f : 1.f / sum[u];
+        T* dst = out + b * p.os.batch + hq * p.os.head + qi * p.os.token + lane * V;
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-          if (sizeof(T) == 4) reinterpret_cast<float*>(dst)[j] = acc[j];
-          else reinterpret_cast<__nv_bfloat16*>(dst)[j] = __float2bfloat16_rn(acc[j]);
+        for (int j = 0; j < V; ++j) acc[u][j] *= norm;
+        if constexpr (V == 4) {
+          store4(dst, acc[u]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j) {
+            if (sizeof(T) == 4) reinterpret_cast<float*>(dst)[j] = acc[u][j];
+            else reinterpret_cast<__nv_bfloat16*>(dst)[j] = __float2bfloat16_rn(acc[u][j]);
+          }
         }
       }
     }

@@ -403,7 +403,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       float top = 0.f;
       bool finite = true;
       const uint4* src = reinterpret_cast<const uint4*>(q + sg.b * p.qs.batch + hq * p.qs.head + qi * p.qs.token);
-#pragma unroll 2
+#pragma unroll 8
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -423,7 +423,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       // units of a score, less the keys' power of two
       float rf = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
       rf = !finite ? NAN : rf * 0x1p10f * (tiny ? 0x1p-80f : 1.f);
-#pragma unroll 2
+#pragma unroll 8
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
         const uint32_t w[4] = {x.x, x.y, x.z, x.w};
@@ -463,80 +463,85 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
         };
         const bool all = key0 + L::TILE <= warp_seen &&
                          (info.have[0] & info.have[1] & info.have[2] & info.have[3]) == 0xffffffffu;
-        float cand = -INFINITY;
-        uint32_t x[2][32];
-        // two passes over pairs of 32 keys; the second starts on the pair that
-        // the first left in registers
-#pragma unroll 1
-        for (int pr = 1; pr >= 0; --pr) {
-          tmem_ld32(scol + 64 * pr, x[0]);
-          tmem_ld32(scol + 64 * pr + 32, x[1]);
-          tmem_ld_wait();
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * pr + h;
-            if (!all) {
-              const uint32_t vis = visible(c);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(vis >> k & 1u)) x[h][k] = 0xff800000u;
-            }
-            float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[h][k]));
-            const float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
-            if (mx > -INFINITY) cand = fmaxf(cand, fmaf(mx, rf * info.k2e[c], info.ev[c]));
-          }
-        }
         float alpha = 1.f;
-        if (cand > m && (m == -INFINITY || cand - m > kRebase)) {
-          alpha = m == -INFINITY ? 0.f : fast_exp2(m - cand);
-          l *= alpha;
-          m = cand;
-        }
-        const float ref = m == -INFINITY ? 0.f : m;
+        // `masked` in a copy of its own: the common tiles run without its code
+        auto weigh = [&](auto masked) {
+          float cand = -INFINITY;
+          uint32_t x[2][32];
+          // two passes over pairs of 32 keys; the second starts on the pair that
+          // the first left in registers
 #pragma unroll 1
-        for (int pr = 0; pr < 2; ++pr) {
-          if (pr) {
-            tmem_ld32(scol + 64, x[0]);
-            tmem_ld32(scol + 96, x[1]);
+          for (int pr = 1; pr >= 0; --pr) {
+            tmem_ld32(scol + 64 * pr, x[0]);
+            tmem_ld32(scol + 64 * pr + 32, x[1]);
             tmem_ld_wait();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int c = 2 * pr + h;
+              if (decltype(masked)::value) {
+                const uint32_t vis = visible(c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(vis >> k & 1u)) x[h][k] = 0xff800000u;
+              }
+              float t[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+              for (int k = 0; k < 32; ++k) t[k & 3] = fmaxf(t[k & 3], __uint_as_float(x[h][k]));
+              const float mx = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+              if (mx > -INFINITY) cand = fmaxf(cand, fmaf(mx, rf * info.k2e[c], info.ev[c]));
+            }
           }
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int c = 2 * pr + h;
-            const float f = rf * info.k2e[c], off = info.ev[c] - ref;
-            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              float2 e2 = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
-                               make_float2(f, f), make_float2(off, off));
-              x[h][2 * k] = __float_as_uint(fast_exp2(e2.x));
-              x[h][2 * k + 1] = __float_as_uint(fast_exp2(e2.y));
-            }
-            if (!all) {
-              const uint32_t vis = visible(c);
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!(vis >> k & 1u)) x[h][k] = 0u;
+          if (cand > m && (m == -INFINITY || cand - m > kRebase)) {
+            alpha = m == -INFINITY ? 0.f : fast_exp2(m - cand);
+            l *= alpha;
+            m = cand;
+          }
+          const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll 1
+          for (int pr = 0; pr < 2; ++pr) {
+            if (pr) {
+              tmem_ld32(scol + 64, x[0]);
+              tmem_ld32(scol + 96, x[1]);
+              tmem_ld_wait();
             }
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-              sum[k & 1] = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
-                                make_float2(1.f, 1.f), sum[k & 1]);
-            if (info.wide[c]) {  // packed in place
+            for (int h = 0; h < 2; ++h) {
+              const int c = 2 * pr + h;
+              const float f = rf * info.k2e[c], off = info.ev[c] - ref;
+              float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                float2 e2 = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
+                                 make_float2(f, f), make_float2(off, off));
+                x[h][2 * k] = __float_as_uint(fast_exp2(e2.x));
+                x[h][2 * k + 1] = __float_as_uint(fast_exp2(e2.y));
+              }
+              if (decltype(masked)::value) {
+                const uint32_t vis = visible(c);
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (!(vis >> k & 1u)) x[h][k] = 0u;
+              }
 #pragma unroll
               for (int k = 0; k < 16; ++k)
-                x[h][k] = pack_bf16x2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
-            } else {
+                sum[k & 1] = fma2(make_float2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1])),
+                                  make_float2(1.f, 1.f), sum[k & 1]);
+              if (info.wide[c]) {  // packed in place
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                x[h][k] = pack_half2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
+                for (int k = 0; k < 16; ++k)
+                  x[h][k] = pack_bf16x2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
+              } else {
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  x[h][k] = pack_half2(__uint_as_float(x[h][2 * k]), __uint_as_float(x[h][2 * k + 1]));
+              }
+              tmem_st16(scol + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(x[h]));
+              l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), info.vinv[c], l);
             }
-            tmem_st16(scol + 16 * c, reinterpret_cast<const uint32_t(&)[16]>(x[h]));
-            l = fmaf((sum[0].x + sum[0].y) + (sum[1].x + sum[1].y), info.vinv[c], l);
           }
-        }
+        };
+        if (all) weigh(std::integral_constant<bool, false>{});
+        else weigh(std::integral_constant<bool, true>{});
         if (info.odd[0] | info.odd[1] | info.odd[2] | info.odd[3]) {
 #pragma unroll 1
           for (int c = 0; c < 4; ++c)
@@ -606,9 +611,13 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
           to[1] = make_uint4(pack_bf16x2(v[8], v[9]), pack_bf16x2(v[10], v[11]), pack_bf16x2(v[12], v[13]),
                              pack_bf16x2(v[14], v[15]));
         } else {
-          float4* to = reinterpret_cast<float4*>(p.part + part * D + ch);
+          // whole sectors: 32 bytes a lane
 #pragma unroll
-          for (int k = 0; k < 4; ++k) to[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+          for (int k = 0; k < 16; k += 8)
+            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p.part + part * D + ch + k),
+                         "f"(v[k]), "f"(v[k + 1]), "f"(v[k + 2]), "f"(v[k + 3]), "f"(v[k + 4]), "f"(v[k + 5]),
+                         "f"(v[k + 6]), "f"(v[k + 7])
+                         : "memory");
         }
       }
     }
