@@ -95,10 +95,22 @@ struct Raw8<__nv_bfloat16> {
 // on their side, so the product decides as the exact quotient would.
 __device__ __forceinline__ uint32_t fields_bf16(const float (&x)[8], float inv) {
   constexpr float C = 192.f, M = 12582920.f;
+  float t[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {  // two at a time
+    unsigned long long v;
+    asm("{\n\t.reg .b64 x, i, c, n, m;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 i, {%3, %3};\n\t"
+        "mov.b64 c, {%4, %4};\n\tmov.b64 n, {%5, %5};\n\tmov.b64 m, {%6, %6};\n\t"
+        "fma.rn.f32x2 x, x, i, c;\n\tadd.rn.f32x2 x, x, n;\n\tadd.rn.f32x2 %0, x, m;\n\t}"
+        : "=l"(v)
+        : "f"(x[i]), "f"(x[i + 1]), "f"(inv), "f"(C), "f"(-C), "f"(M));
+    const float2 two = reinterpret_cast<const float2&>(v);
+    t[i] = two.x;
+    t[i + 1] = two.y;
+  }
   uint32_t w = 0;
 #pragma unroll
-  for (int i = 7; i >= 0; --i)
-    w = w * 16u + __float_as_uint(__fadd_rn(__fsub_rn(fmaf(x[i], inv, C), C), M));
+  for (int i = 7; i >= 0; --i) w = w * 16u + __float_as_uint(t[i]);
   // each term brought 0x4B400000 along: its sum over 16^i, modulo 2^32
   return w - 0x4B400000u * 0x11111111u;
 }

@@ -39,7 +39,7 @@ struct RopeParams {
   unsigned long long freq[kMaxPairs];  // turns per position, units of 2^-64
   const int* positions;                // [axes][B][n], or null: 0 .. n-1
   const float *qw, *kw;                // [d] or null
-  long long tokens;                    // B * n
+  int tokens;                          // B * n
   int n, Hq, Hk, d, half;              // half: rotated pairs
   int end[kMaxAxes];                   // first pair past each axis
   int heads_per_chunk;                 // heads of q and k a CTA walks
@@ -53,18 +53,35 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
 }
-__device__ __forceinline__ void store4(float* p, const float (&v)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+__device__ __forceinline__ void store4(float* p, float2 u, float2 v) {
+  *reinterpret_cast<float4*>(p) = make_float4(u.x, u.y, v.x, v.y);
 }
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+__device__ __forceinline__ void store4(__nv_bfloat16* p, float2 u, float2 v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(u.x, u.y), pack2(v.x, v.y));
 }
 __device__ __forceinline__ void store1(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 
-// The eight channels of one lane: a[j], b[j] are the members of its pair j.
+// Two fp32 values in one instruction.
+__device__ __forceinline__ unsigned long long bits(const float2& v) {
+  return reinterpret_cast<const unsigned long long&>(v);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+
+// The eight channels of one lane: a, b hold the members of its pairs 0, 1 and
+// 2, 3.
 struct Pairs {
-  float a[4], b[4];
+  float2 a[2], b[2];
 };
 
 // Where a lane's channels sit in a row. Past the rotated channels a "pair" is
@@ -75,7 +92,8 @@ struct Place {
 };
 
 template <int MODE>
-__device__ __forceinline__ Place place_of(int unit, int half) {
+__device__ __forceinline__ Place place_of(int unit, int half, int d) {
+  if (8 * unit >= d) unit = 0;  // a lane without channels reads the first ones
   Place pl;
   pl.unit = unit;
   pl.half = half;
@@ -141,27 +159,30 @@ __device__ __forceinline__ void load_raw(const __nv_bfloat16* row, const Place& 
   }
 }
 
-__device__ __forceinline__ void widen(const uint4& u, float (&v)[4]) {
-  v[0] = __uint_as_float(u.x); v[1] = __uint_as_float(u.y);
-  v[2] = __uint_as_float(u.z); v[3] = __uint_as_float(u.w);
+__device__ __forceinline__ void widen(const uint4& u, float2& v, float2& w) {
+  v = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  w = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
 }
-__device__ __forceinline__ void widen(const uint2& u, float (&v)[4]) {
-  v[0] = __uint_as_float(u.x << 16); v[1] = __uint_as_float(u.x & 0xffff0000u);
-  v[2] = __uint_as_float(u.y << 16); v[3] = __uint_as_float(u.y & 0xffff0000u);
+__device__ __forceinline__ void widen(const uint2& u, float2& v, float2& w) {
+  v = make_float2(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u));
+  w = make_float2(__uint_as_float(u.y << 16), __uint_as_float(u.y & 0xffff0000u));
 }
 
 template <int MODE, typename T>
 __device__ __forceinline__ Pairs pairs_of(const Raw<T>& r) {
   Pairs x;
   if (MODE == kPairs) {
-    float u[4], v[4];
-    widen(r.lo, u);
-    widen(r.hi, v);
-    x.a[0] = u[0]; x.b[0] = u[1]; x.a[1] = u[2]; x.b[1] = u[3];
-    x.a[2] = v[0]; x.b[2] = v[1]; x.a[3] = v[2]; x.b[3] = v[3];
+    float2 u[4];
+    widen(r.lo, u[0], u[1]);
+    widen(r.hi, u[2], u[3]);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      x.a[j] = make_float2(u[2 * j].x, u[2 * j + 1].x);
+      x.b[j] = make_float2(u[2 * j].y, u[2 * j + 1].y);
+    }
   } else {
-    widen(r.lo, x.a);
-    widen(r.hi, x.b);
+    widen(r.lo, x.a[0], x.a[1]);
+    widen(r.hi, x.b[0], x.b[1]);
   }
   return x;
 }
@@ -169,17 +190,16 @@ __device__ __forceinline__ Pairs pairs_of(const Raw<T>& r) {
 template <int MODE, typename T>
 __device__ __forceinline__ void store_pairs(T* row, const Place& pl, const Pairs& x) {
   if (MODE == kHalves) {
-    store4(row + pl.lo, x.a);
-    store4(row + pl.hi, x.b);
+    store4(row + pl.lo, x.a[0], x.a[1]);
+    store4(row + pl.hi, x.b[0], x.b[1]);
   } else if (MODE == kPairs) {
-    const float u[4] = {x.a[0], x.b[0], x.a[1], x.b[1]}, v[4] = {x.a[2], x.b[2], x.a[3], x.b[3]};
-    store4(row + pl.lo, u);
-    store4(row + pl.hi, v);
+    store4(row + pl.lo, make_float2(x.a[0].x, x.b[0].x), make_float2(x.a[0].y, x.b[0].y));
+    store4(row + pl.hi, make_float2(x.a[1].x, x.b[1].x), make_float2(x.a[1].y, x.b[1].y));
   } else {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      store1(row + channel_of<MODE>(pl, j, false), x.a[j]);
-      store1(row + channel_of<MODE>(pl, j, true), x.b[j]);
+      store1(row + channel_of<MODE>(pl, j, false), (j & 1) ? x.a[j / 2].y : x.a[j / 2].x);
+      store1(row + channel_of<MODE>(pl, j, true), (j & 1) ? x.b[j / 2].y : x.b[j / 2].x);
     }
   }
 }
@@ -205,31 +225,33 @@ __device__ __forceinline__ void turn_cos_sin(unsigned long long phase, float& c,
 }
 
 struct Turn {
-  float c[4], s[4];
+  float2 c[2], s[2], ns[2];  // cos, sin, -sin
 };
 
 template <bool EXACT>
 __device__ __forceinline__ Turn turn_of(const RopeParams& p, const unsigned long long* freq,
-                                        int unit, long long token, int t) {
-  Turn r;
+                                        int unit, int token, int t) {
+  float c[4], s[4];
   int axis = -1;
   unsigned long long pos = 0;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int i = 4 * unit + j;
-    r.c[j] = 1.f;
-    r.s[j] = 0.f;
+    c[j] = 1.f;
+    s[j] = 0.f;
     if (i < p.half) {
       int ax = 0;
       while (i >= p.end[ax]) ++ax;  // sections sum to half, so ax stays below axes
       if (ax != axis) {
         axis = ax;
-        pos = (unsigned long long)(long long)(p.positions ? p.positions[ax * p.tokens + token] : t);
+        pos = (unsigned long long)(long long)(p.positions ? p.positions[(size_t)ax * p.tokens + token] : t);
       }
-      turn_cos_sin<EXACT>(freq[i] * pos, r.c[j], r.s[j]);
+      turn_cos_sin<EXACT>(freq[i] * pos, c[j], s[j]);
     }
   }
-  return r;
+  return Turn{{make_float2(c[0], c[1]), make_float2(c[2], c[3])},
+              {make_float2(s[0], s[1]), make_float2(s[2], s[3])},
+              {make_float2(-s[0], -s[1]), make_float2(-s[2], -s[3])}};
 }
 
 // Sum over the LP lanes of a row, in every one of them.
@@ -240,64 +262,81 @@ __device__ __forceinline__ float row_sum(float v) {
   return v;
 }
 
-__device__ __forceinline__ float square_sum(const Pairs& x) {
-  float s = 0.f;
-#pragma unroll
-  for (int j = 0; j < 4; ++j) s = fmaf(x.a[j], x.a[j], fmaf(x.b[j], x.b[j], s));
-  return s;
+// Sum of x y over the lane's channels.
+__device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) {
+  const float2 s = fma2(x.a[0], y.a[0], mul2(x.a[1], y.a[1])), t = fma2(x.b[0], y.b[0], mul2(x.b[1], y.b[1]));
+  return (s.x + s.y) + (t.x + t.y);
 }
 
 template <int MODE>
-__device__ __forceinline__ void load_weights(const float* w, const Place& pl, bool live, Pairs& x) {
-  const bool given = w && live;  // 4-byte aligned: scalar loads, once per walk
+__device__ __forceinline__ void load_weights(const float* w, const Place& pl, Pairs& x) {
+  // 4-byte aligned: scalar loads, once per walk
+  auto at = [&](int j, bool second) { return w ? w[channel_of<MODE>(pl, j, second)] : 1.f; };
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x.a[j] = given ? w[channel_of<MODE>(pl, j, false)] : 1.f;
-    x.b[j] = given ? w[channel_of<MODE>(pl, j, true)] : 1.f;
+  for (int j = 0; j < 2; ++j) {
+    x.a[j] = make_float2(at(2 * j, false), at(2 * j + 1, false));
+    x.b[j] = make_float2(at(2 * j, true), at(2 * j + 1, true));
   }
 }
 
 // Heads [h0, h1) of one tensor for one token: UNROLL rows at a time, the next
-// ones' loads in flight while these are worked on.
+// ones' loads in flight while these are worked on. Lanes without channels and
+// groups without a token (`live` false) read some row's first channels and
+// write none.
 template <typename T, int LP, int MODE, int UNROLL>
 __device__ __forceinline__ void walk_forward(const T* x, T* y, long long xs, long long ys, int h0,
                                              int h1, const float* w, const Turn& turn,
                                              const Place& pl, bool live, const RopeParams& p) {
   Raw<T> next[UNROLL];
-  auto fetch = [&](int h) {
+  Pairs wt;
+  if (p.norm) load_weights<MODE>(w, pl, wt);
+  x += h0 * xs;
+  y += h0 * ys;
+  int left = h1 - h0;
+  auto fetch = [&](int count) {
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k)
-      if (live && h + k < h1) load_raw<MODE>(x + (h + k) * xs, pl, next[k]);
+      if (k < count) load_raw<MODE>(x + k * xs, pl, next[k]);
+    x += count * xs;
   };
-  fetch(h0);
-  Pairs wt;
-  if (p.norm) load_weights<MODE>(w, pl, live, wt);
-  for (int h = h0; h < h1; h += UNROLL) {
-    Raw<T> now[UNROLL];
-#pragma unroll
-    for (int k = 0; k < UNROLL; ++k) now[k] = next[k];
-    fetch(h + UNROLL);
+  auto turn_rows = [&](const Raw<T>(&now)[UNROLL], int count) {
 #pragma unroll
     for (int k = 0; k < UNROLL; ++k) {
-      const bool on = live && h + k < h1;
+      if (k >= count) break;
       Pairs v = pairs_of<MODE, T>(now[k]);
       if (p.norm) {
-        const float ss = row_sum<LP>(on ? square_sum(v) : 0.f);
+        const float ss = row_sum<LP>(live ? dot(v, v) : 0.f);
         const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v.a[j] *= r * wt.a[j];
-          v.b[j] *= r * wt.b[j];
+        for (int j = 0; j < 2; ++j) {
+          v.a[j] = mul2(v.a[j], mul2(both(r), wt.a[j]));
+          v.b[j] = mul2(v.b[j], mul2(both(r), wt.b[j]));
         }
       }
       Pairs o;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        o.a[j] = fmaf(v.a[j], turn.c[j], -v.b[j] * turn.s[j]);
-        o.b[j] = fmaf(v.b[j], turn.c[j], v.a[j] * turn.s[j]);
+      for (int j = 0; j < 2; ++j) {
+        o.a[j] = fma2(v.a[j], turn.c[j], mul2(v.b[j], turn.ns[j]));
+        o.b[j] = fma2(v.b[j], turn.c[j], mul2(v.a[j], turn.s[j]));
       }
-      if (on) store_pairs<MODE>(y + (h + k) * ys, pl, o);
+      if (live) store_pairs<MODE>(y + k * ys, pl, o);
     }
+    y += count * ys;
+  };
+  if (left >= UNROLL) fetch(UNROLL);
+#pragma unroll 1
+  while (left >= UNROLL) {
+    Raw<T> now[UNROLL];
+#pragma unroll
+    for (int k = 0; k < UNROLL; ++k) now[k] = next[k];
+    left -= UNROLL;
+    if (left >= UNROLL) fetch(UNROLL);
+    turn_rows(now, UNROLL);
+  }
+#pragma unroll 1
+  for (; left > 0; --left) {
+    fetch(1);
+    turn_rows(next, 1);
   }
 }
 
@@ -312,12 +351,13 @@ qk_norm_rope(const __grid_constant__ RopeParams p, const T* q, const T* k, T* qo
   if (threadIdx.x < p.half) freq[threadIdx.x] = p.freq[threadIdx.x];
   __syncthreads();
   const int unit = threadIdx.x % LP;
-  const long long token = (long long)blockIdx.x * (kThreads / LP) + threadIdx.x / LP;
-  const bool live = token < p.tokens && 8 * unit < p.d;
-  const long long b = live ? token / p.n : 0, t = live ? token - b * p.n : 0;
-  const Place pl = place_of<MODE>(unit, p.half);
+  const unsigned token = blockIdx.x * (unsigned)(kThreads / LP) + threadIdx.x / LP;  // below 2^31 + 64
+  const bool live = token < (unsigned)p.tokens && 8 * unit < p.d;
+  const int bi = live ? (int)(token / (unsigned)p.n) : 0;
+  const long long b = bi, t = live ? (int)token - bi * p.n : 0;
+  const Place pl = place_of<MODE>(unit, p.half, p.d);
   Turn turn{};
-  if (live) turn = turn_of<sizeof(T) == 4>(p, freq, unit, token, (int)t);
+  if (live) turn = turn_of<sizeof(T) == 4>(p, freq, unit, (int)token, (int)t);
   const int h0 = blockIdx.y * p.heads_per_chunk;
   const int h1 = min(p.Hq + p.Hk, h0 + p.heads_per_chunk);
   if (h0 < p.Hq)
@@ -344,78 +384,98 @@ qk_norm_rope_back(const __grid_constant__ RopeParams p, const T* q, const T* k, 
   const bool keys = (int)blockIdx.y >= q_chunks;  // CTA-uniform
   const nys_strides_t &xs = keys ? p.ki : p.qi, &gs = keys ? p.ko : p.qo, &ds = keys ? p.dk : p.dq;
   const int unit = threadIdx.x % LP;
-  const Place pl = place_of<MODE>(unit, p.half);
+  const Place pl = place_of<MODE>(unit, p.half, p.d);
   const int h0 = ((int)blockIdx.y - (keys ? q_chunks : 0)) * p.heads_per_chunk;
   const int h1 = min(keys ? p.Hk : p.Hq, h0 + p.heads_per_chunk);
   constexpr int kRows = kThreads / LP;
-  const long long tiles = (p.tokens + kRows - 1) / kRows;
+  const int tiles = (int)(((long long)p.tokens + kRows - 1) / kRows);
   Pairs acc{}, wt;
-  if (p.norm) load_weights<MODE>(keys ? p.kw : p.qw, pl, 8 * unit < p.d, wt);
-  for (long long tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const long long token = tile * kRows + threadIdx.x / LP;
-    const bool live = token < p.tokens && 8 * unit < p.d;
-    const long long b = live ? token / p.n : 0, t = live ? token - b * p.n : 0;
-    const T* x = (keys ? k : q) + b * xs.batch + t * xs.token;
-    const T* gy = (keys ? gk : gq) + b * gs.batch + t * gs.token;
-    T* dx = (keys ? dk : dq) + b * ds.batch + t * ds.token;
+  if (p.norm) load_weights<MODE>(keys ? p.kw : p.qw, pl, wt);
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const unsigned token = tile * (unsigned)kRows + threadIdx.x / LP;
+    const bool live = token < (unsigned)p.tokens && 8 * unit < p.d;
+    const int bi = live ? (int)(token / (unsigned)p.n) : 0;
+    const long long b = bi, t = live ? (int)token - bi * p.n : 0;
+    const T* x = (keys ? k : q) + b * xs.batch + t * xs.token + h0 * xs.head;
+    const T* gy = (keys ? gk : gq) + b * gs.batch + t * gs.token + h0 * gs.head;
+    T* dx = (keys ? dk : dq) + b * ds.batch + t * ds.token + h0 * ds.head;
     Raw<T> next_x[UNROLL], next_g[UNROLL];
-    auto fetch = [&](int h) {
+    int left = h1 - h0;
+    auto fetch = [&](int count) {
 #pragma unroll
-      for (int i = 0; i < UNROLL; ++i)
-        if (live && h + i < h1) {
-          load_raw<MODE>(gy + (h + i) * gs.head, pl, next_g[i]);
-          if (p.norm) load_raw<MODE>(x + (h + i) * xs.head, pl, next_x[i]);
-        }
+      for (int i = 0; i < UNROLL; ++i) {
+        if (i >= count) break;
+        load_raw<MODE>(gy, pl, next_g[i]);
+        if (p.norm) load_raw<MODE>(x, pl, next_x[i]);
+        gy += gs.head;
+        x += xs.head;
+      }
     };
-    fetch(h0);
+    auto turn_back = [&](const Raw<T>(&now_x)[UNROLL], const Raw<T>(&now_g)[UNROLL], const Turn& turn, int count) {
+#pragma unroll
+      for (int i = 0; i < UNROLL; ++i) {
+        if (i >= count) break;
+        const Pairs g = pairs_of<MODE, T>(now_g[i]);
+        Pairs o;  // the rotation undone
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          o.a[j] = fma2(g.a[j], turn.c[j], mul2(g.b[j], turn.s[j]));
+          o.b[j] = fma2(g.b[j], turn.c[j], mul2(g.a[j], turn.ns[j]));
+        }
+        if (p.norm) {
+          const Pairs v = pairs_of<MODE, T>(now_x[i]);
+          Pairs wo, ov;  // w g, g x
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            wo.a[j] = mul2(wt.a[j], o.a[j]);
+            wo.b[j] = mul2(wt.b[j], o.b[j]);
+            ov.a[j] = mul2(v.a[j], o.a[j]);
+            ov.b[j] = mul2(v.b[j], o.b[j]);
+          }
+          const float ss = row_sum<LP>(live ? dot(v, v) : 0.f);
+          const float gh = row_sum<LP>(live ? dot(wt, ov) : 0.f);
+          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
+          // dx = r (w g - h mean(w g h)) with h = r x, mean = r gh / d
+          const float2 m = both(-r * gh * p.inv_d), rr = both(r);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (live) {
+              acc.a[j] = fma2(ov.a[j], rr, acc.a[j]);
+              acc.b[j] = fma2(ov.b[j], rr, acc.b[j]);
+            }
+            o.a[j] = mul2(rr, fma2(mul2(v.a[j], rr), m, wo.a[j]));
+            o.b[j] = mul2(rr, fma2(mul2(v.b[j], rr), m, wo.b[j]));
+          }
+        }
+        if (live) store_pairs<MODE>(dx, pl, o);
+        dx += ds.head;
+      }
+    };
+    if (left >= UNROLL) fetch(UNROLL);
     Turn turn{};
-    if (live) turn = turn_of<sizeof(T) == 4>(p, freq, unit, token, (int)t);
-    for (int h = h0; h < h1; h += UNROLL) {
+    if (live) turn = turn_of<sizeof(T) == 4>(p, freq, unit, (int)token, (int)t);
+#pragma unroll 1
+    while (left >= UNROLL) {
       Raw<T> now_x[UNROLL], now_g[UNROLL];
 #pragma unroll
       for (int i = 0; i < UNROLL; ++i) {
         now_x[i] = next_x[i];
         now_g[i] = next_g[i];
       }
-      fetch(h + UNROLL);
-#pragma unroll
-      for (int i = 0; i < UNROLL; ++i) {
-        const bool on = live && h + i < h1;
-        const Pairs g = pairs_of<MODE, T>(now_g[i]);
-        Pairs o;  // the rotation undone
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          o.a[j] = fmaf(g.a[j], turn.c[j], g.b[j] * turn.s[j]);
-          o.b[j] = fmaf(g.b[j], turn.c[j], -g.a[j] * turn.s[j]);
-        }
-        if (p.norm) {
-          const Pairs v = pairs_of<MODE, T>(now_x[i]);
-          float dot = 0.f;
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            dot = fmaf(wt.a[j] * o.a[j], v.a[j], fmaf(wt.b[j] * o.b[j], v.b[j], dot));
-          const float ss = row_sum<LP>(on ? square_sum(v) : 0.f);
-          dot = row_sum<LP>(on ? dot : 0.f);
-          const float r = rsqrtf(fmaf(ss, p.inv_d, p.eps));
-          const float m = r * dot * p.inv_d;  // mean(w g h)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float ha = v.a[j] * r, hb = v.b[j] * r;
-            if (on) {
-              acc.a[j] = fmaf(o.a[j], ha, acc.a[j]);
-              acc.b[j] = fmaf(o.b[j], hb, acc.b[j]);
-            }
-            o.a[j] = r * fmaf(wt.a[j], o.a[j], -ha * m);
-            o.b[j] = r * fmaf(wt.b[j], o.b[j], -hb * m);
-          }
-        }
-        if (on) store_pairs<MODE>(dx + (h + i) * ds.head, pl, o);
-      }
+      left -= UNROLL;
+      if (left >= UNROLL) fetch(UNROLL);
+      turn_back(now_x, now_g, turn, UNROLL);
+    }
+#pragma unroll 1
+    for (; left > 0; --left) {
+      fetch(1);
+      turn_back(next_x, next_g, turn, 1);
     }
   }
   if (!part) return;
   // lanes of one unit: over the warp by shuffles, over the warps in order
-  const float v[8] = {acc.a[0], acc.a[1], acc.a[2], acc.a[3], acc.b[0], acc.b[1], acc.b[2], acc.b[3]};
+  const float v[8] = {acc.a[0].x, acc.a[0].y, acc.a[1].x, acc.a[1].y,
+                      acc.b[0].x, acc.b[0].y, acc.b[1].x, acc.b[1].y};
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
@@ -431,7 +491,7 @@ qk_norm_rope_back(const __grid_constant__ RopeParams p, const T* q, const T* k, 
     float s = 0.f;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) s += sums[w][u][j];
-    const int c = channel_of<MODE>(place_of<MODE>(u, p.half), j & 3, (j & 4) != 0);
+    const int c = channel_of<MODE>(place_of<MODE>(u, p.half, p.d), j & 3, (j & 4) != 0);
     part[((size_t)blockIdx.y * gridDim.x + blockIdx.x) * p.d + c] = s;
   }
 }
@@ -552,7 +612,7 @@ RopeParams params_of(const nys_qk_rope_t& a, const float* qw, const float* kw, c
   p.positions = positions;
   p.qw = qw;
   p.kw = kw;
-  p.tokens = (long long)a.B * a.n;
+  p.tokens = a.B * a.n;
   p.n = a.n;
   p.Hq = a.Hq;
   p.Hk = a.Hk;
