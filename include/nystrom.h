@@ -439,7 +439,7 @@ size_t nystrom_kv4_cache_bytes(int num_pages, int page_size, int Hk, int d);
  * (its rows of a read come back as zeros) and makes nystrom_get_status report
  * NYS_ERR_INDEX. Two sequences of one write must not name the same
  * page for positions they write.
- * B, n >= 1, B <= 65535 (else NYS_ERR_SHAPE).
+ * B, n >= 1, B <= 65535, n * Hk < 2^33 (else NYS_ERR_SHAPE).
  */
 int nystrom_kv4_write(const nys_kv4_cache_t* cache, const void* k, const void* v,
                       const nys_strides_t* k_strides, const nys_strides_t* v_strides,

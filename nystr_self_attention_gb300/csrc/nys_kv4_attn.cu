@@ -17,8 +17,11 @@
 // so that the scores come out in the very registers that the second product
 // takes p from. A 4-bit field u = code + 8 becomes fp16 by masking alone (as a
 // subnormal it is u 2^-24, in the upper half of a byte u 2^-20; the queries
-// carry the factors and are scaled to the top of fp16's range), its offset 8
-// is the product's starting value. V's fields are masked out as bf16 subnormals
+// carry the factors and are scaled to the top of fp16's range), its offset 8 is
+// the product's starting value. (fp32: fields less 8, times two fp16 terms of
+// the query. The fields are e4m3 numbers as they lie, too, but the e4m3 form of
+// the instruction took 11 instructions more a product: 62 us against 57 on the
+// case below.) V's fields are masked out as bf16 subnormals
 // and brought to (u - 8) 2^-6 by one fused multiply-add per pair.
 //
 // One token over 8 ragged sequences of up to 32768, 32 + 8 heads, d = 128 (203
@@ -41,7 +44,6 @@ namespace {
 using namespace sm100;
 
 constexpr int kWarps = 4;
-constexpr int kCtasPerSm = 4;
 constexpr int kStages = 2;   // tiles per warp in flight or in use
 // Tiles of two blocks, 16 query rows, at least a tile per warp. With the item's
 // start and join counted as 6 tiles the last CTA's end came 3 us nearer to the
@@ -104,19 +106,23 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
+// CTAs per SM, by the registers a variant needs.
+template <typename T, int D, int NT>
+constexpr int kCtas = sizeof(T) == 2 ? (NT == 1 ? 4 : D == 128 ? 2 : 3) : (D == 128 ? 2 : 3);
+
 template <int D>
 constexpr int ring_bytes() { return kWarps * kStages * 2 * block_bytes(D); }
 template <int D, int NT>
 constexpr int merge_bytes() { return 2 * NT * 8 * D * 4; }
-// per group: the queries' operands (two steps, each fp16 term), starting values
-template <typename T>
-constexpr int kTable = sizeof(T) == 4 ? 4 : 3;
+// per group: the queries' operands, and for bf16 the product's starting values
+template <typename T, int NT>
+constexpr int kTable = sizeof(T) == 4 ? 2 * NT : 3;
 // fp32 scales of a warp's tile: [K, V][group][32 tokens]
 template <int D>
 constexpr int scales_bytes() { return 2 * D / 32 * kTile * 4; }
 template <typename T, int D, int NT>
 constexpr int split_smem() {
-  return ring_bytes<D>() + merge_bytes<D, NT>() + D / 32 * kTable<T> * 512 + kWarps * scales_bytes<D>();
+  return ring_bytes<D>() + merge_bytes<D, NT>() + D / 32 * kTable<T, NT> * 512 + kWarps * scales_bytes<D>();
 }
 
 // NT: 8-row groups of query rows (1 or 2). fp32: a query is the sum of two
@@ -125,11 +131,11 @@ constexpr int split_smem() {
 // The code is kept short (one copy of each step, masks as uniform branches):
 // a decoding step finds none of it in the instruction caches.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kWarps * 32, sizeof(T) == 2 && NT == 1 ? kCtasPerSm : 2)
+__global__ void __launch_bounds__(kWarps * 32, kCtas<T, D, NT>)
 kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T* __restrict__ out) {
   constexpr int G = D / 32, BB = block_bytes(D);
   constexpr bool EXACT = sizeof(T) == 4;
-  constexpr int QT = EXACT ? 2 : 1, PT = EXACT ? 3 : 1;
+  constexpr int PT = EXACT ? 3 : 1, ENTRIES = kTable<T, NT>;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t bars[kWarps][kStages];
   __shared__ Start start;
@@ -142,16 +148,22 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   uint4* table = reinterpret_cast<uint4*>(smem + ring_bytes<D>() + merge_bytes<D, NT>());
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  float* scales = reinterpret_cast<float*>(table + G * kTable<T> * 32) + warp * (scales_bytes<D>() / 4);
+  float* scales = reinterpret_cast<float*>(table + G * kTable<T, NT> * 32) + warp * (scales_bytes<D>() / 4);
   uint8_t* ring = smem + warp * kStages * 2 * BB;
   if (tid < kWarps * kStages) mbar_init(&bars[0][0] + tid, 2);
   if (tid == 0) abort_s = 0;
   fence_barrier_init();
   cudaTriggerProgrammaticLaunchCompletion();  // the join may be set up meanwhile
-  find_start<SplitLine, kWarps * 32>(p, &start, warp_sums);  // two block syncs
-  const int r0 = (int)min((long long)blockIdx.x * start.per, (long long)start.total);
-  const int r1 = min(start.total, r0 + start.per);
-  int pos = r0, base = start.base, b = start.b;
+  int pos = 0, r1 = 0, base = 0, b = 0;
+  if (p.whole) {
+    __syncthreads();
+  } else {
+    find_start<SplitLine, kWarps * 32>(p, &start, warp_sums);  // two block syncs
+    pos = (int)min((long long)blockIdx.x * start.per, (long long)start.total);
+    r1 = min(start.total, pos + start.per);
+    base = start.base;
+    b = start.b;
+  }
   uint32_t used = 0;  // tiles this warp has put through its ring
 
   Segment seg;
@@ -187,7 +199,9 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   for (bool any = false;; any = true) {
     // ------------------- the next segment, its first tiles on their way ...
     Segment next;
-    const bool more = next_segment<SplitLine>(p, pos, r1, base, b, next);
+    bool more = !any;
+    if (!p.whole) more = next_segment<SplitLine>(p, pos, r1, base, b, next);
+    else if (more) whole_segment<SplitLine>(p, blockIdx.x, next);
     if (more) {
       // tiles with a key that some row sees
       const int live = min(next.tile0 + next.ntile, (next.seen_max + kTile - 1) / kTile) - next.tile0;
@@ -294,10 +308,10 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
     seg = next;
 
     // -------------------------------- the queries: this lane's rows g, g + 8
-    uint32_t qa[QT][2][4];  // of group `warp`: [step][row half + 2 channel half]
+    uint32_t qa[4][4];  // of group `warp`: the table's operands
     float first[4] = {0.f, 0.f, 0.f, 0.f};  // -8 x the group's sum of the row
 #pragma unroll
-    for (int i = 0; i < QT * 8; ++i) qa[i / 8][i / 4 % 2][i % 4] = 0u;
+    for (int i = 0; i < 16; ++i) qa[i / 4][i % 4] = 0u;
     int seen[NT];
 #pragma unroll
     for (int hr = 0; hr < NT; ++hr) {
@@ -340,28 +354,31 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
         x[j] = (j & 1) ? v * 0.0625f : v;
         sum += round_half(x[j]) * ((j & 1) ? 16.f : 1.f);
       }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      first[2 * hr] = first[2 * hr + 1] = sum * (-8.f * 0x1p-24f);
+      if (!EXACT) {
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        first[2 * hr] = first[2 * hr + 1] = sum * (-8.f * 0x1p-24f);
+      }
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int ch = 0; ch < 2; ++ch) {
           const float lo = x[2 * st + ch], hi = x[2 * st + ch + 4];
-          qa[0][st][hr + 2 * ch] = half2_bits(lo, hi);
-          if (EXACT) qa[QT - 1][st][hr + 2 * ch] = half2_bits(lo - round_half(lo), hi - round_half(hi));
+          qa[st][hr + 2 * ch] = half2_bits(lo, hi);
+          if (EXACT) {  // the second term: up to 8 rows leave the others free for it
+            const uint32_t two = half2_bits(lo - round_half(lo), hi - round_half(hi));
+            if (NT == 1) qa[st][1 + 2 * ch] = two;
+            else qa[2 + st][hr + 2 * ch] = two;
+          }
         }
     }
     if (warp < G) {
-      uint4* to = table + warp * kTable<T> * 32 + lane;
+      uint4* to = table + warp * ENTRIES * 32 + lane;
 #pragma unroll
-      for (int k = 0; k < 2 * QT; ++k) {
-        const uint32_t(&a)[4] = qa[k / 2][k % 2];
-        to[k * 32] = make_uint4(a[0], a[1], a[2], a[3]);
-      }
+      for (int k = 0; k < (EXACT ? 2 * NT : 2); ++k) to[k * 32] = make_uint4(qa[k][0], qa[k][1], qa[k][2], qa[k][3]);
       if (!EXACT)
         to[64] = make_uint4(__float_as_uint(first[0]), __float_as_uint(first[1]),
-                            __float_as_uint(first[2]), __float_as_uint(first[3]));
+                                 __float_as_uint(first[2]), __float_as_uint(first[3]));
     }
     __syncthreads();
 
@@ -442,10 +459,9 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
       }
 #pragma unroll
       for (int y = 0; y < G; ++y) {
-        uint4 a[2 * QT], c = make_uint4(0u, 0u, 0u, 0u);
+        uint4 a[ENTRIES];
 #pragma unroll
-        for (int k = 0; k < 2 * QT; ++k) a[k] = table[(y * kTable<T> + k) * 32 + lane];
-        if (!EXACT) c = table[(y * kTable<T> + 2) * 32 + lane];
+        for (int k = 0; k < ENTRIES; ++k) a[k] = table[(y * ENTRIES + k) * 32 + lane];
 #pragma unroll
         for (int n8 = 0; n8 < 4; ++n8) {
           uint32_t f[4] = {w[n8][y] & 0x000f000fu, w[n8][y] & 0x00f000f0u, (w[n8][y] >> 8) & 0x000f000fu,
@@ -459,10 +475,19 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
               f[j] = reinterpret_cast<const uint32_t&>(v);
             }
           }
-          float acc[4] = {__uint_as_float(c.x), __uint_as_float(c.y), __uint_as_float(c.z), __uint_as_float(c.w)};
+          float acc[4] = {0.f, 0.f, 0.f, 0.f};
+          if (!EXACT) {
+            const uint4 c = a[2];
+            acc[0] = __uint_as_float(c.x); acc[1] = __uint_as_float(c.y);
+            acc[2] = __uint_as_float(c.z); acc[3] = __uint_as_float(c.w);
+          }
 #pragma unroll
-          for (int k = 2 * QT - 1; k >= 0; --k)  // the smaller terms first
+          for (int k = EXACT ? 2 * NT - 1 : 1; k >= 0; --k)  // the smaller terms first
             mma_f16(acc, a[k].x, a[k].y, a[k].z, a[k].w, f[2 * (k & 1)], f[2 * (k & 1) + 1], acc);
+          if (EXACT && NT == 1) {
+            acc[0] += acc[2];
+            acc[1] += acc[3];
+          }
           const float2 sc = *reinterpret_cast<const float2*>(scales + y * kTile + n8 * 8 + 2 * t);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -742,14 +767,20 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
 // core kernel (d = 32 stays: its rows are half a swizzled operand row).
 constexpr int kChunkRows = 48;
 
+// Contexts of up to kWholeTiles tiles (in a batch of kWholeItems items or more,
+// of up to kWholeTilesBatch): a CTA per item and no join. Against ranges and a
+// join, d = 128, 16 + 4 heads (us): 512 keys 13 / 19, 1024 keys 17 / 20, 2048
+// keys 27 / 21; 64 sequences: 512 keys 15 / 29, 2048 keys 35 / 43.
+constexpr int kWholeTiles = 32, kWholeTilesBatch = 64, kWholeItems = 64;
+
 struct Plan {
-  bool chunk;
+  bool chunk, whole;
   int nt, row_tiles, ctas;
   long long items;
   size_t ml, total;  // workspace: offset behind the parts, bytes
 };
 
-Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int dtype) {
+Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int max_length, int dtype) {
   Plan pl{};
   const long long rows = (long long)nq * (Hq / c.Hk);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
@@ -765,7 +796,13 @@ Plan plan_of(const nys_kv4_cache_t& c, int B, int nq, int Hq, int dtype) {
   pl.nt = rows <= 8 ? 1 : 2;
   pl.row_tiles = (int)((rows + 15) / 16);
   pl.items = (long long)B * c.Hk * pl.row_tiles;
-  pl.ctas = plan_sms() * (dtype == NYS_BF16 && pl.nt == 1 ? kCtasPerSm : 2);
+  const int ctas[2][2] = {{c.d == 128 ? kCtas<float, 128, 1> : kCtas<float, 64, 1>,
+                           c.d == 128 ? kCtas<float, 128, 2> : kCtas<float, 64, 2>},
+                          {c.d == 128 ? kCtas<__nv_bfloat16, 128, 1> : kCtas<__nv_bfloat16, 64, 1>,
+                           c.d == 128 ? kCtas<__nv_bfloat16, 128, 2> : kCtas<__nv_bfloat16, 64, 2>}};
+  pl.ctas = plan_sms() * ctas[dtype == NYS_BF16][pl.nt - 1];
+  pl.whole = max_length <= (pl.items >= kWholeItems ? kWholeTilesBatch : kWholeTiles) * kTile;
+  if (pl.whole) return pl;
   pl.ml = up((size_t)pl.ctas * 2 * pl.nt * 8 * c.d * sizeof(float));
   pl.total = up(pl.ml + (size_t)pl.ctas * 2 * pl.nt * 8 * sizeof(float2));
   return pl;
@@ -780,7 +817,7 @@ int check_attn(const nys_kv4_cache_t* c, int B, int nq, int Hq, int max_length, 
   if ((long long)nq * (Hq / c->Hk) >= (1ll << 30)) return NYS_ERR_SHAPE;
   // the line of tiles (and the items) of the longest sequences allowed
   const long long length = std::min((long long)max_length, (long long)c->max_pages * c->page_size);
-  const Plan pl = plan_of(*c, B, nq, Hq, dtype);
+  const Plan pl = plan_of(*c, B, nq, Hq, max_length, dtype);
   const long long places = pl.chunk ? ChunkLine::places((int)((length + ChunkLine::TILE - 1) / ChunkLine::TILE))
                                     : SplitLine::places((int)((length + kTile - 1) / kTile));
   const long long units = pl.chunk ? pl.items * (ChunkLine::ROWS / 16) : pl.items;
@@ -821,10 +858,10 @@ int launch_split(const AttnParams& p, const Plan& pl, const void* q, void* out, 
   }
   {
     KernelScope scope("kv4_attn_split", st);
-    kv4_attn_split<T, D, NT><<<pl.ctas, kWarps * 32, smem, st>>>(p, static_cast<const T*>(q),
+    kv4_attn_split<T, D, NT><<<(unsigned)(pl.whole ? pl.items : pl.ctas), kWarps * 32, smem, st>>>(p, static_cast<const T*>(q),
                                                                 static_cast<T*>(out));
     const int rc = launch_status();
-    if (rc != NYS_OK) return rc;
+    if (rc != NYS_OK || pl.whole) return rc;
   }
   return launch_join<T, D, SplitLine>(p, out, NT * 8, st);
 }
@@ -841,7 +878,7 @@ extern "C" {
 size_t nystrom_kv4_attn_workspace_bytes(const nys_kv4_cache_t* cache, int B, int nq, int Hq,
                                         int max_length, int dtype) {
   if (check_attn(cache, B, nq, Hq, max_length, dtype) != NYS_OK) return 0;
-  return plan_of(*cache, B, nq, Hq, dtype).total;
+  return plan_of(*cache, B, nq, Hq, max_length, dtype).total;
 }
 
 int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
@@ -860,12 +897,12 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   if ((reinterpret_cast<uintptr_t>(lengths) | reinterpret_cast<uintptr_t>(q_counts)) & 3u)
     return NYS_ERR_ALIGN;
   if (workspace && (reinterpret_cast<uintptr_t>(workspace) & 255u)) return NYS_ERR_ALIGN;
-  const Plan pl = plan_of(*cache, B, nq, Hq, dtype);
+  const Plan pl = plan_of(*cache, B, nq, Hq, max_length, dtype);
   if (workspace && ws_bytes < pl.total) return NYS_ERR_NOMEM;
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
-  if (!workspace) {
+  if (!workspace && pl.total > 0) {
     rc = operator_workspace(dev, pl.total, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
@@ -887,6 +924,7 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   p.max_length = max_length;
   p.causal = causal;
   p.ctas = pl.ctas;
+  p.whole = pl.whole ? 1 : 0;
   p.scale_log2 = (scale == 0.f ? 1.f / std::sqrt((float)cache->d) : scale) * 1.4426950408889634f;
   if (pl.chunk) {
     rc = launch_kv4_chunk(p, cache->d, q, out, stream);

@@ -22,6 +22,7 @@ struct AttnParams {
   float2* part_ml;  // [CTAs][2][item rows]: their (maximum in log2 units, sum)
   int B, nq, rep, row_tiles, max_length, causal;
   int ctas;
+  int whole;          // an item per CTA, nothing is cut
   float scale_log2;  // scale * log2(e)
 };
 
@@ -122,6 +123,22 @@ struct Segment {
   __device__ __forceinline__ bool whole(int tile) const { return ntile == (len + tile - 1) / tile; }
 };
 
+// The rows of a segment of the sequence's item, from b and len.
+template <typename L>
+__device__ __forceinline__ void rows_of_segment(const AttnParams& p, int item, Segment& sg) {
+  sg.h = item / p.row_tiles;
+  sg.rt = item - sg.h * p.row_tiles;
+  sg.count = count_of(p, sg.b);
+  sg.rows = min(L::ROWS, sg.count * p.rep - sg.rt * L::ROWS);  // may be <= 0
+  sg.seen_min = sg.seen_max = sg.len;
+  if (p.causal) {
+    const int first = sg.len - sg.count + 1;  // keys the first query sees
+    sg.seen_min = max(0, first + sg.rt * L::ROWS / p.rep);
+    sg.seen_max = max(0, first + (sg.rt * L::ROWS + sg.rows - 1) / p.rep);
+  }
+  if (sg.rows <= 0) sg.seen_max = 0;
+}
+
 // Walks the segments of the range [pos, r1); base, b: as in Start.
 template <typename L>
 __device__ __forceinline__ bool next_segment(const AttnParams& p, int& pos, int r1, int& base, int& b,
@@ -146,21 +163,24 @@ __device__ __forceinline__ bool next_segment(const AttnParams& p, int& pos, int 
       if (pos >= r1) break;
     }
     sg.ntile = min(T_b - sg.tile0, r1 - pos);
-    sg.h = item / p.row_tiles;
-    sg.rt = item - sg.h * p.row_tiles;
-    sg.count = count_of(p, b);
-    sg.rows = min(L::ROWS, sg.count * p.rep - sg.rt * L::ROWS);  // may be <= 0
-    sg.seen_min = sg.seen_max = sg.len;
-    if (p.causal) {
-      const int first = sg.len - sg.count + 1;  // keys the first query sees
-      sg.seen_min = max(0, first + sg.rt * L::ROWS / p.rep);
-      sg.seen_max = max(0, first + (sg.rt * L::ROWS + sg.rows - 1) / p.rep);
-    }
-    if (sg.rows <= 0) sg.seen_max = 0;
+    rows_of_segment<L>(p, item, sg);
     pos += sg.ntile;
     return true;
   }
   return false;
+}
+
+// All of item `at` of the batch.
+template <typename L>
+__device__ __forceinline__ void whole_segment(const AttnParams& p, int at, Segment& sg) {
+  const int items = p.cache.Hk * p.row_tiles;
+  sg.b = at / items;
+  bool bad;
+  sg.len = length_of(p, sg.b, &bad);
+  sg.tile0 = 0;
+  sg.ntile = (sg.len + L::TILE - 1) / L::TILE;
+  rows_of_segment<L>(p, at - sg.b * items, sg);
+  if (bad && threadIdx.x == 0) report_index(p.status);
 }
 
 // Slot of a segment's part in its CTA: a range holds at most one item cut in
