@@ -318,6 +318,7 @@ _KV4_DESC = struct.Struct("=QQ5i4x")      # nys_kv4_cache_t
 _STRIDES = struct.Struct("=3q")           # nys_strides_t
 _NO_STRIDES = (0, 0, 0)
 _torch = None
+_np = None
 
 
 def _lazy_torch():
@@ -328,26 +329,37 @@ def _lazy_torch():
     return _torch
 
 
-def _heads(name, t, dtype=None, shape=None):
-    """(batch, head, token) strides of a [B, H, n, d] view on the current
-    device. An axis with one entry has no stride."""
+def _check_first(name, t):
+    """(strides, dtype code, device index) of a call's first heads."""
     torch = _torch or _lazy_torch()
-    if not t.is_cuda or t.dim() != 4:
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        code = NYS_BF16
+    elif dtype is torch.float32:
+        code = NYS_FP32
+    else:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor [B, H, n, d]")
+    device = torch._C._cuda_getDevice()
+    return _heads(name, t, dtype, None, device), code, device
+
+
+def _heads(name, t, dtype, shape, device):
+    """(batch, head, token) strides of a [B, H, n, d] view of the given type and
+    shape on the current device. An axis with one entry has no stride."""
     s, n = t.stride(), t.shape
-    if s[3] != 1:
-        raise ValueError(f"{name}'s channels must be contiguous")
+    if len(s) != 4 or s[3] != 1:
+        raise ValueError(f"{name} must be [B, H, n, d] with contiguous channels")
     if shape is not None and n != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(n)}")
-    if dtype is None:
-        dtype = t.dtype
-        if dtype != torch.bfloat16 and dtype != torch.float32:
-            raise ValueError(f"{name} must be float32 or bfloat16")
-    elif t.dtype != dtype:
+    if t.dtype is not dtype:
         raise ValueError(f"{name} must be {dtype} like the other heads")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{name} is on {t.device}, which is not the current device")
-    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    if 1 in n:
+        return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+    return s[:3]
 
 
 def _flat(name, t, dtype, shape, device):
@@ -355,7 +367,7 @@ def _flat(name, t, dtype, shape, device):
     index, or None."""
     if t is None:
         return None
-    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on device {device}")
     return t.data_ptr()
 
@@ -388,27 +400,31 @@ def _scratch(nbytes, workspace, device, stream):
 def _rope_args(names, tensors, inv_freq, positions, sections, norm, eps, pairing):
     """Packed descriptor, frequencies as bytes, address of the positions and
     device of a call on (q, k, q_out or gq, k_out or gk[, dq, dk])."""
+    global _np
     q, k = tensors[0], tensors[1]
-    qs = _heads(names[0], q)
-    torch, dtype, shape = _torch, q.dtype, q.shape
+    qs, code, device = _check_first(names[0], q)
+    dtype, shape = q.dtype, q.shape
     B, Hq, n, d = shape
     if k is None:
-        strides = [x for i in range(0, len(tensors), 2)
-                   for x in (qs if i == 0 else _heads(names[i], tensors[i], dtype, shape)) + _NO_STRIDES]
-        Hk = 0
+        Hk, kshape = 0, None
     else:
-        ks = _heads(names[1], k, dtype)
         kshape = k.shape
+        if len(kshape) != 4 or kshape[0] != B or kshape[2] != n or kshape[3] != d:
+            raise ValueError(f"k must have shape [{B}, Hk, {n}, {d}], not {tuple(kshape)}")
         Hk = kshape[1]
-        if kshape[0] != B or kshape[2] != n or kshape[3] != d:
-            raise ValueError(f"k must have shape {(B, Hk, n, d)}, not {tuple(kshape)}")
-        strides = [*qs, *ks]
-        for i in range(2, len(tensors)):
-            strides += _heads(names[i], tensors[i], dtype, kshape if i % 2 else shape)
+    strides = list(qs)
+    for i in range(1, len(tensors)):
+        if i & 1 == 0:
+            strides += _heads(names[i], tensors[i], dtype, shape, device)
+        elif k is None:
+            strides += _NO_STRIDES
+        else:
+            strides += _heads(names[i], tensors[i], dtype, kshape, device)
     if len(tensors) == 4:
         strides += _NO_STRIDES * 2
-    import numpy as np
-    freq = np.asarray(inv_freq, dtype=np.float64)
+    if _np is None:
+        import numpy as _np
+    freq = _np.asarray(inv_freq, dtype=_np.float64)
     if freq.ndim != 1 or len(freq) > 64:
         raise ValueError("inv_freq must be one-dimensional, at most 64 long")
     half = len(freq)
@@ -416,10 +432,9 @@ def _rope_args(names, tensors, inv_freq, positions, sections, norm, eps, pairing
     if not 1 <= axes <= 4:
         raise ValueError("one to four axes")
     sec = (half, 0, 0, 0) if sections is None else (*sections, *(0,) * (4 - axes))
-    desc = _ROPE_DESC.pack(B, n, Hq, Hk, d, 2 * half, axes, *sec, pairing, 1 if norm else 0,
-                           NYS_BF16 if dtype == torch.bfloat16 else NYS_FP32, eps, *strides)
-    device = q.get_device()
-    return desc, freq.tobytes(), _flat("positions", positions, torch.int32, (axes, B, n), device), device
+    desc = _ROPE_DESC.pack(B, n, Hq, Hk, d, 2 * half, axes, *sec, pairing, 1 if norm else 0, code, eps, *strides)
+    pos = None if positions is None else _flat("positions", positions, _torch.int32, (axes, B, n), device)
+    return desc, freq.tobytes(), pos, device
 
 
 def nystrom_qk_norm_rope_fwd(q, k, q_out, k_out, positions, inv_freq, q_weight=None, k_weight=None, *,
@@ -501,16 +516,14 @@ class NystromKv4Cache:
 
 
 def _kv4_io(cache, k, v, starts, counts):
-    n, dev, B = k.shape[2], cache.device, cache.B
-    shape = (B, cache.Hk, n, cache.d)
-    ks = _heads("k", k, None, shape)
-    vs = _heads("v", v, k.dtype, shape)
-    if k.get_device() != dev:
-        raise ValueError("k and v must be on the cache's device")
+    ks, code, dev = _check_first("k", k)
+    shape, dtype, B = k.shape, k.dtype, cache.B
+    if dev != cache.device or shape[0] != B or shape[1] != cache.Hk or shape[3] != cache.d:
+        raise ValueError(f"k must be [{B}, {cache.Hk}, n, {cache.d}] on the cache's device, not {tuple(shape)}")
+    vs = _heads("v", v, dtype, shape, dev)
     i32 = _torch.int32
     return (k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks), _STRIDES.pack(*vs),
-            _flat("starts", starts, i32, (B,), dev), _flat("counts", counts, i32, (B,), dev),
-            B, n, NYS_BF16 if k.dtype == _torch.bfloat16 else NYS_FP32)
+            _flat("starts", starts, i32, (B,), dev), _flat("counts", counts, i32, (B,), dev), B, shape[2], code)
 
 
 def nystrom_kv4_write(cache, k, v, starts=None, counts=None, stream=None):
@@ -542,14 +555,13 @@ def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, caus
     lib = _lib or load_library()
     if scale == 0:
         raise ValueError("scale must not be zero (None: 1/sqrt(d))")
-    dev = cache.device
-    qs = _heads("q", q)
-    shape, dtype = q.shape, q.dtype
+    qs, dt, dev = _check_first("q", q)
+    shape = q.shape
     B, Hq, nq, d = shape
-    if B != cache.B or d != cache.d or q.get_device() != dev:
+    if B != cache.B or d != cache.d or dev != cache.device:
         raise ValueError("q must be [B, Hq, nq, d] with the cache's B and d, on its device")
-    os_ = _heads("out", out, dtype, shape)
-    dt, i32 = (NYS_BF16 if dtype == _torch.bfloat16 else NYS_FP32), _torch.int32
+    os_ = _heads("out", out, q.dtype, shape, dev)
+    i32 = _torch.int32
     need = lib.nystrom_kv4_attn_workspace_bytes(cache.desc, B, nq, Hq, max_length, dt)
     ws, nbytes, keep = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_kv4_attn_fwd(

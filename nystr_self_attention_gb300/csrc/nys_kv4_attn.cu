@@ -106,9 +106,10 @@ __device__ __forceinline__ void store4(__nv_bfloat16* p, const float (&v)[4]) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
 }
 
-// CTAs per SM, by the registers a variant needs.
+// CTAs per SM, by the registers a variant needs (fp32 with 16 rows, d = 64: three
+// would fit but measured 27 us against 23, 5 drafted tokens over 4095 keys).
 template <typename T, int D, int NT>
-constexpr int kCtas = sizeof(T) == 2 ? (NT == 1 ? 4 : D == 128 ? 2 : 3) : (D == 128 ? 2 : 3);
+constexpr int kCtas = sizeof(T) == 2 ? (NT == 1 ? 4 : D == 128 ? 2 : 3) : (D == 128 || NT == 2 ? 2 : 3);
 
 template <int D>
 constexpr int ring_bytes() { return kWarps * kStages * 2 * block_bytes(D); }
@@ -632,21 +633,25 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
 // of sequences without keys. A CTA takes consecutive items, a warp a row. It
 // is launched while the split kernel runs (which items were cut follows from
 // the lengths alone) and waits for it before it reads a part.
+// Warps of a joining CTA: one for every other row, or for four rows at once.
+template <typename L>
+constexpr int kJoinWarps = L::ROWS == 16 ? 8 : 4;
+
 template <typename T, int D, typename L>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kJoinWarps<L> * 32)
 kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows,
               int items_per_cta, int n_items) {
   constexpr int SUB = L::ROWS / 16;  // a unit of work: 16 rows of an item
   // channels per lane; rows of a warp and their parts in flight: an item of few
   // rows has many parts, one of many rows a few
   constexpr int V = D / 32, AT_ONCE = SUB > 1 ? 4 : 1, AHEAD = SUB > 1 ? 2 : 8;
-  __shared__ int warp_sums[2][kWarps];
+  __shared__ int warp_sums[2][kJoinWarps<L>];
   const int per_b = p.cache.Hk * p.row_tiles * SUB, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int i0 = blockIdx.x * items_per_cta, i1 = min(n_items, i0 + items_per_cta);
   int b = i0 / per_b;
   int before = 0, all = 0;
 #pragma unroll 1
-  for (int j = tid; j < p.B; j += kWarps * 32) {
+  for (int j = tid; j < p.B; j += kJoinWarps<L> * 32) {
     const int n = L::places(L::tiles(p, j));
     all += n;
     if (j < b) before += n;
@@ -663,7 +668,7 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
   __syncthreads();
   before = all = 0;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
+  for (int w = 0; w < kJoinWarps<L>; ++w) {
     before += warp_sums[0][w];
     all += warp_sums[1][w];
   }
@@ -687,7 +692,7 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
     const int rows = min(L::ROWS, count_of(p, b) * p.rep - rt * L::ROWS);
     const int end = min(rows, sub * 16 + 16);
 #pragma unroll 1
-    for (int r0 = sub * 16 + warp * AT_ONCE; r0 < end; r0 += kWarps * AT_ONCE) {
+    for (int r0 = sub * 16 + warp * AT_ONCE; r0 < end; r0 += kJoinWarps<L> * AT_ONCE) {
       float top[AT_ONCE], sum[AT_ONCE], acc[AT_ONCE][V];
 #pragma unroll
       for (int u = 0; u < AT_ONCE; ++u) {
@@ -837,7 +842,7 @@ int launch_join(const AttnParams& p, void* out, int part_rows, cudaStream_t st) 
   const long long most = 8ll * plan_sms();
   const int per = (int)((units + most - 1) / most);
   cfg.gridDim = dim3((unsigned)((units + per - 1) / per));
-  cfg.blockDim = dim3(kWarps * 32);
+  cfg.blockDim = dim3(kJoinWarps<L> * 32);
   cfg.stream = st;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
