@@ -18,8 +18,8 @@
 // takes p from. A 4-bit field u = code + 8 becomes fp16 by masking alone (as a
 // subnormal it is u 2^-24, in the upper half of a byte u 2^-20; the queries
 // carry the factors and are scaled to the top of fp16's range), its offset 8 is
-// the product's starting value. (fp32: fields less 8, times two fp16 terms of
-// the query. The fields are e4m3 numbers as they lie, too, but the e4m3 form of
+// the product's starting value. (fp32: fields less 8, as normal numbers, times
+// two fp16 terms of the query. The fields are e4m3 numbers as they lie, too, but the e4m3 form of
 // the instruction took 11 instructions more a product: 62 us against 57 on the
 // case below.) V's fields are masked out as bf16 subnormals
 // and brought to (u - 8) 2^-6 by one fused multiply-add per pair.
@@ -346,13 +346,13 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
       const int e = top > 0.f ? (int)(__float_as_uint(top) >> 23) - 127 : 13;
       const float up = __uint_as_float((uint32_t)(127 + 13 - e) << 23) * (p.scale_log2 < 0.f ? -1.f : 1.f);
       const float down = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
-      rf[hr] = !finite ? NAN : down * 0x1p24f * (tiny ? 0x1p-80f : 1.f);
+      rf[hr] = !finite ? NAN : down * (EXACT ? 0x1p9f : 0x1p24f) * (tiny ? 0x1p-80f : 1.f);
       float sum = 0.f;
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        // odd fields sit four bits higher
+        // bf16: odd fields sit four bits higher
         const float v = finite ? (tiny ? x[j] * 0x1p80f : x[j]) * up : 0.f;
-        x[j] = (j & 1) ? v * 0.0625f : v;
+        x[j] = !EXACT && (j & 1) ? v * 0.0625f : v;
         sum += round_half(x[j]) * ((j & 1) ? 16.f : 1.f);
       }
       if (!EXACT) {
@@ -467,12 +467,15 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
         for (int n8 = 0; n8 < 4; ++n8) {
           uint32_t f[4] = {w[n8][y] & 0x000f000fu, w[n8][y] & 0x00f000f0u, (w[n8][y] >> 8) & 0x000f000fu,
                            (w[n8][y] >> 8) & 0x00f000f0u};
-          if (EXACT) {  // fields less 8, exact in subnormals too
+          if (EXACT) {
+            // To (u - 8) 2^-9, normal numbers: with subnormal operands the unit
+            // keeps fewer bits of a sum. Relative error of 5 tokens over 4095
+            // keys: 1.0e-6 that way, 1.5e-7 this way.
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const uint32_t eight = (j & 1) ? 0x00800080u : 0x00080008u;
-              const __half2 v = __hsub2(reinterpret_cast<const __half2&>(f[j]),
-                                        reinterpret_cast<const __half2&>(eight));
+              const uint32_t up = (j & 1) ? 0x68006800u : 0x78007800u, o = 0xa400a400u;  // 2^11, 2^15; -2^-6
+              const __half2 v = __hfma2(reinterpret_cast<const __half2&>(f[j]), reinterpret_cast<const __half2&>(up),
+                                        reinterpret_cast<const __half2&>(o));
               f[j] = reinterpret_cast<const uint32_t&>(v);
             }
           }
@@ -612,9 +615,9 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
                 mma_bf16_acc(O[2 * y + 1][nt], v[0][2], v[0][3], v[1][2], v[1][3], b0, b1);
               } else {
                 // The matrix units cut their sums off towards zero, so a long
-                // chain of them drifts: 16 keys, the smallest terms first, then
-                // an ordinary sum. Relative error of a result, 5 tokens over
-                // 4095 keys: 1.1e-6 as one chain, 4e-7 this way.
+                // chain of them drifts (half a step of 2^-24 per product, all of
+                // one sign): 16 keys, the smallest terms first, then an ordinary
+                // sum.
                 uint32_t b[3][2];
 #pragma unroll
                 for (int pt = 0; pt < 3; ++pt) {
