@@ -380,6 +380,7 @@ qk_norm_rope_back(const __grid_constant__ RopeParams p, const T* q, const T* k, 
   __shared__ float sums[kThreads / 32][LP][9];
   if (threadIdx.x < p.half) freq[threadIdx.x] = p.freq[threadIdx.x];
   __syncthreads();
+  cudaTriggerProgrammaticLaunchCompletion();
   constexpr int UNROLL = kAhead<T>;
   const bool keys = (int)blockIdx.y >= q_chunks;  // CTA-uniform
   const nys_strides_t &xs = keys ? p.ki : p.qi, &gs = keys ? p.ko : p.qo, &ds = keys ? p.dk : p.dq;
@@ -498,9 +499,11 @@ qk_norm_rope_back(const __grid_constant__ RopeParams p, const T* q, const T* k, 
 
 // dw[c] = sum over CTAs of part, 32 channels per CTA in 32 row slices: fixed
 // order. CTAs y = 0: q's rows [0, q_ctas) of part, y = 1: k's behind them.
+// Set up while the kernel that writes part still runs.
 __global__ void __launch_bounds__(1024)
-qk_weight_grad(const float* __restrict__ part, float* dqw, float* dkw, int d, int q_ctas, int k_ctas) {
+qk_weight_grad(const float* part, float* dqw, float* dkw, int d, int q_ctas, int k_ctas) {
   __shared__ float s[32][33];
+  cudaGridDependencySynchronize();
   float* dst = blockIdx.y ? dkw : dqw;
   if (!dst) return;
   const float* rows = part + (blockIdx.y ? (size_t)q_ctas * d : 0);
@@ -774,8 +777,17 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* a, const void* q, const void* 
   });
   if (rc != NYS_OK || !sums) return rc;
   KernelScope scope("qk_weight_grad", stream);
-  qk_weight_grad<<<dim3((a->d + 31) / 32, a->Hk > 0 ? 2 : 1), 1024, 0, stream>>>(
-      part, dq_weight, dk_weight, a->d, g.x * g.q_chunks, g.x * (g.y - g.q_chunks));
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a->d + 31) / 32, a->Hk > 0 ? 2 : 1);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, qk_weight_grad, static_cast<const float*>(part), dq_weight, dk_weight, a->d,
+                     g.x * g.q_chunks, g.x * (g.y - g.q_chunks));
   return launch_status();
 }
 
