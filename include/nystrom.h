@@ -416,8 +416,8 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* p, const void* q, const void* 
  * memory held, and no operator lets them into a result.
  * block_table: device int32 [B][max_pages]. Sequences may share pages that
  * are only read. Shape rules: num_pages, max_pages, Hk >= 1; page_size a
- * multiple of 16 in 16 .. 4096; d in {32, 64, 128}; max_pages * page_size <
- * 2^31.
+ * multiple of 16 in 16 .. 4096; d in {32, 64, 128}; max_pages * page_size <=
+ * 2^31 - 2^16.
  */
 typedef struct {
   void* data;
@@ -454,8 +454,8 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * nystrom_kv4_attn_fwd - attention of nq new queries of each sequence over its
  * cached keys and values:
  *   out = softmax(q K^T * scale) V
- * q, out [B, Hq, nq, d] in `dtype`, any strides; query head h reads cache head
- * h / (Hq/Hk). lengths: device int32 [B], the tokens of each sequence in the
+ * q, out [B, Hq, nq, d] in `dtype`, any strides (out may be q); query head h
+ * reads cache head h / (Hq/Hk). lengths: device int32 [B], the tokens of each sequence in the
  * cache (the new ones included). q_counts: device int32 [B], the real queries
  * of each sequence (NULL: nq); rows of out behind them are left as they were.
  * causal = 1: query i of c sees keys 0 .. length - c + i; causal = 0: all
@@ -471,8 +471,11 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * span more than 2^8. For NYS_FP32 queries and probabilities enter as sums of
  * 16-bit terms that keep at least 22 and 24 bits.
  * Shape rules: B, nq, Hk >= 1, Hq a multiple of Hk, Hq <= 65535, B <= 65535,
- * max_length >= 0, nq * (Hq/Hk) < 2^30 (else NYS_ERR_SHAPE); scale finite
- * (else NYS_ERR_ARG).
+ * max_length >= 0, nq * (Hq/Hk) < 2^30, and the key tiles that all items could
+ * have (32 keys x 16 query rows per cache head; more than 48 rows in bf16: 128 x
+ * 256) below 2^31 (else NYS_ERR_SHAPE); scale finite (else NYS_ERR_ARG).
+ * Magnitudes: probabilities are kept up to 2^8 above 1, so cached values beyond
+ * 2^100 may give infinities.
  * workspace: device, 256-byte aligned, ws_bytes >=
  * nystrom_kv4_attn_workspace_bytes(...) (which may be 0), not shared with a
  * call that may run at the same time. NULL uses the library's cached

@@ -492,9 +492,10 @@ def nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d) -> int:
 class NystromKv4Cache:
     """A 4-bit key/value cache over the caller's memory (format: see
     include/nystrom.h). data: uint8 CUDA tensor, a whole number of pages;
-    block_table: int32 [B, max_pages], sequence b's pages in order."""
+    block_table: int32 [B, max_pages], sequence b's pages in order. Both are
+    kept; new pages are entered into the same tensor."""
 
-    __slots__ = ("data", "block_table", "B", "Hk", "d", "device", "desc")
+    __slots__ = ("_data", "_block_table", "B", "Hk", "d", "device", "desc")
 
     def __init__(self, data, block_table, page_size, Hk, d):
         torch = _torch or _lazy_torch()
@@ -509,10 +510,18 @@ class NystromKv4Cache:
         if (block_table.dtype != torch.int32 or block_table.dim() != 2
                 or block_table.get_device() != data.get_device() or not block_table.is_contiguous()):
             raise ValueError("block_table must be a contiguous int32 tensor [B, max_pages] beside the data")
-        self.data, self.block_table = data, block_table
+        self._data, self._block_table = data, block_table
         self.B, max_pages = block_table.shape
         self.Hk, self.d, self.device = Hk, d, data.get_device()
         self.desc = _KV4_DESC.pack(data.data_ptr(), block_table.data_ptr(), pages, max_pages, page_size, Hk, d)
+
+    @property
+    def data(self):
+        return self._data
+
+    @property
+    def block_table(self):
+        return self._block_table
 
 
 def _kv4_io(cache, k, v, starts, counts):

@@ -25,7 +25,8 @@ int check_cache(const nys_kv4_cache_t* c) {
   if (c->num_pages < 1 || c->max_pages < 1 || c->Hk < 1 || c->Hk > 65535) return NYS_ERR_SHAPE;
   if (c->page_size < 16 || c->page_size > 4096 || c->page_size % 16) return NYS_ERR_SHAPE;
   if (c->d != 32 && c->d != 64 && c->d != 128) return NYS_ERR_SHAPE;
-  if ((long long)c->max_pages * c->page_size >= (1ll << 31)) return NYS_ERR_SHAPE;
+  // tiles and windows of pages past the last one keep 32-bit key indexes
+  if ((long long)c->max_pages * c->page_size > (1ll << 31) - 65536) return NYS_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(c->data) & 15u) return NYS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(c->block_table) & 3u) return NYS_ERR_ALIGN;
   return NYS_OK;

@@ -180,3 +180,25 @@ def test_well_formed_calls_need_the_gpu(N):
     assert rope(N, True, dqw=256) == N.NYS_ERR_UNSUPPORTED
     assert io(N, False, cache(N)) == N.NYS_ERR_UNSUPPORTED
     assert attn(N) == N.NYS_ERR_UNSUPPORTED
+
+
+def test_packed_descriptors_are_the_structures(N):
+    """The binding packs them by hand: the same bytes as the C layouts."""
+    from nystr_self_attention_gb300 import _binding as b
+    s = [N.NysStrides(100 + 3 * i, 101 + 3 * i, 102 + 3 * i) for i in range(6)]
+    rope = N.NysQkRope(1, 2, 3, 4, 5, 6, 7, (ctypes.c_int * 4)(8, 9, 10, 11), 12, 13, 14, 0.5, *s)
+    packed = b._ROPE_DESC.pack(1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 11, 12, 13, 14, 0.5, *range(100, 118))
+    assert bytes(rope) == packed
+    cache = b.NysKv4Cache(256, 512, 1, 2, 3, 4, 5)
+    assert bytes(cache) == b._KV4_DESC.pack(256, 512, 1, 2, 3, 4, 5)
+    assert bytes(s[0]) == b._STRIDES.pack(100, 101, 102)
+
+
+@pytest.mark.parametrize("max_pages,page,code", [(524272, 4096, None), (524273, 4096, E_SHAPE),
+                                                 (134213632, 16, None), (134213633, 16, E_SHAPE)])
+def test_positions_stay_clear_of_32_bits(N, max_pages, page, code):
+    """max_pages * page_size up to 2^31 - 2^16: key indexes of a tile past the
+    last one still fit."""
+    c = cache(N, max_pages=max_pages, page=page)
+    got = io(N, False, c, k=264)  # past the shape check only the alignment is wrong
+    assert got == (E_ALIGN if code is None else code)

@@ -465,3 +465,106 @@ def test_norm_write_attend_and_read_back_into_nystrom_attention():
     assert N.nystrom_get_status() == N.NYS_OK
     ref = R.nystrom_attention(host(q), host(K), host(V), np.zeros((Hk, 1)), 16, 6)
     assert np.abs(host(y) - ref).max() <= 2e-2 * np.abs(ref).max()
+
+
+RAGGED_CHUNKS = {
+    # B, Hq, Hk, d, page, nq, lens, counts: several items, cut and whole, of one and two groups of rows
+    "two_groups": (3, 8, 2, 128, 64, 70, [700, 130, 71], [70, 40, 70]),
+    "more_queries_than_tokens": (2, 4, 1, 128, 16, 90, [30, 257], [90, 90]),
+    "odd_heads": (2, 7, 1, 64, 32, 45, [385, 128], [45, 8]),
+    "some_without_queries": (5, 4, 4, 64, 16, 60, [1, 0, 128, 129, 300], [60, 60, 0, 1, 33]),
+    "one_long_many_short": (9, 2, 1, 128, 16, 130, [2600] + [5] * 8, [130] + [3] * 8),
+}
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", RAGGED_CHUNKS)
+def test_ragged_chunks(name, causal):
+    import nystr_self_attention_gb300 as N
+    B, Hq, Hk, d, page, nq, lens, counts = RAGGED_CHUNKS[name]
+    c = Both(B, Hk, d, page, -(-max(lens) // page))
+    c.fill(lens)
+    q = heads(c.rng.standard_normal((B, Hq, nq, d)), "bf16", "bnhd")
+    out = run_attn(c, q, lens, nq, counts, causal=causal)
+    assert N.nystrom_get_status() == N.NYS_OK
+    check(out, q, c, lens, "bf16", counts, causal=causal, name=name)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rep", [1, 12])
+def test_many_ragged_sequences_share_the_line(rep, dtype):
+    """Lengths from none to thousands, far fewer tokens than max_length allows:
+    ranges that end in, on and between items."""
+    import nystr_self_attention_gb300 as N
+    lens = [0, 3000, 31, 32, 33, 0, 0, 1, 640, 1999, 5, 64, 900, 0, 127, 2, 2304, 16, 17, 0]
+    c = Both(20, 3, 64, 16, 188)
+    c.fill(lens, dtype)
+    q = heads(c.rng.standard_normal((20, 3 * rep, 1, 64)), dtype, "bnhd")
+    out = run_attn(c, q, lens, 1, max_length=3008)
+    assert N.nystrom_get_status() == N.NYS_OK
+    check(out, q, c, lens, dtype)
+
+
+@pytest.mark.parametrize("B,Hk,lens,limits", [
+    (1, 2, [1024], [1024, 1025]), (2, 2, [1025, 1023], [1025, 4000]),
+    (16, 4, [2048, 2047, 1, 0] * 4, [2048, 2049]), (1, 1, [0], [0, 5000]),
+])
+def test_both_ways_of_planning_agree_with_the_oracle(B, Hk, lens, limits):
+    """Limits on both sides of where a CTA per item gives way to ranges."""
+    c = Both(B, Hk, 64, 64, max(1, -(-max(lens) // 64)))
+    c.fill(lens)
+    q = heads(c.rng.standard_normal((B, 2 * Hk, 1, 64)), "bf16", "bnhd")
+    for limit in limits:
+        check(run_attn(c, q, lens, 1, max_length=limit), q, c, lens, "bf16", name=f"limit {limit}")
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_no_tokens_at_all(nq):
+    c = Both(2, 2, 64, 16, 4)
+    q = heads(c.rng.standard_normal((2, 4, nq, 64)), "bf16", "bnhd")
+    assert (run_attn(c, q, [0, 0], nq, max_length=0) == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 100])
+def test_result_over_the_queries(nq, dtype):
+    """out may be q: whole items and items that several CTAs share."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    lens = [1800, 40]
+    c = Both(2, 2, 64, 32, 57)
+    c.fill(lens, dtype)
+    q = heads(c.rng.standard_normal((2, 6, nq, 64)), dtype, "bnhd")
+    apart = run_attn(c, q, lens, nq)
+    N.nystrom_kv4_attn_fwd(c.dev, q, q, i32(lens), 1800)
+    assert torch.equal(apart, q)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_read_of_any_bytes(d, dtype):
+    """Memory that nothing was written to, so every kind of scale: subnormal,
+    infinite, NaN. A code times a scale has at most 12 bits: one rounding."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    n = 16 * 24
+    c = Both(2, 2, d, 64, 6)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    k, v = (torch.empty(2, n, 2, d, dtype=t, device="cuda").transpose(1, 2) for _ in range(2))
+    N.nystrom_kv4_read(c.dev, k, v)
+    for b in range(2):
+        toks = [c.ref.token(b, i) for i in range(n)]
+        for got, kind in ((k, 0), (v, 1)):
+            with np.errstate(over="ignore", invalid="ignore"):
+                want = torch.from_numpy(np.stack([x[kind] for x in toks], 1)).to(torch.float32).to(t)
+            assert torch.equal(torch.nan_to_num(got[b].cpu().float(), nan=1.5),
+                               torch.nan_to_num(want.float(), nan=1.5))
+
+
+def test_a_cache_keeps_its_memory():
+    """Its tensors cannot be swapped under the addresses that it hands out."""
+    c = Both(1, 1, 32, 16, 2)
+    for name in ("data", "block_table"):
+        with pytest.raises(AttributeError):
+            setattr(c.dev, name, c.data)
+    assert c.dev.data is c.data and c.dev.block_table is c.dtable
