@@ -18,16 +18,18 @@
 // takes p from. A 4-bit field u = code + 8 becomes fp16 by masking alone (as a
 // subnormal it is u 2^-24, in the upper half of a byte u 2^-20; the queries
 // carry the factors and are scaled to the top of fp16's range), its offset 8 is
-// the product's starting value. (fp32: fields less 8, as normal numbers, times
-// two fp16 terms of the query. The fields are e4m3 numbers as they lie, too, but the e4m3 form of
-// the instruction took 11 instructions more a product: 62 us against 57 on the
-// case below.) V's fields are masked out as bf16 subnormals
-// and brought to (u - 8) 2^-6 by one fused multiply-add per pair.
+// the product's starting value. V's fields are masked out as bf16 subnormals
+// and brought to (u - 8) 2^-6 by one fused multiply-add per pair. fp32: fields
+// less 8, as normal numbers, times two fp16 terms of the query, and three bf16
+// terms of a probability. (The fields are e4m3 numbers as they lie, too, but the
+// e4m3 form of the instruction took 11 instructions more a product: 62 us
+// against 57 on the case below.)
 //
 // One token over 8 ragged sequences of up to 32768, 32 + 8 heads, d = 128 (203
-// MB): 50 us, the join included 58; four times as long 172 us (5.0 TB/s). What
-// bounds it is the unpacking: per 16 keys and head about 310 instructions of a
-// warp, 120 of them on the integer pipe.
+// MB): 61 us a call, 52 of them here, 3.3 TB/s; four times as long 172 us (5.0
+// TB/s). What bounds it is the unpacking: per 16 keys and head about 310
+// instructions of a warp, 120 of them on the integer pipe (42 % busy, HBM 48 %);
+// short calls: the launch, the queries and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -651,14 +653,18 @@ kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T*
   }
 }
 
-// Adds up the parts of items that several CTAs shared, and writes the zeros
-// of sequences without keys. A CTA takes consecutive items, a warp a row. It
-// is launched while the split kernel runs (which items were cut follows from
-// the lengths alone) and waits for it before it reads a part.
-// Warps of a joining CTA: one for every other row, or for four rows at once.
+// Warps of a joining CTA: one for every other row, or for four rows at once
+// (16-row items, 5 fp32 tokens over 16 sequences of up to 4095: 4 warps 5 us, 8
+// warps 3 us).
 template <typename L>
 constexpr int kJoinWarps = L::ROWS == 16 ? 8 : 4;
 
+// Adds up the parts of items that several CTAs shared, and writes the zeros
+// of sequences without keys. A CTA takes consecutive items, a warp a row. It
+// is launched while the split kernel runs (which items were cut follows from
+// the lengths alone) and waits for it before it reads a part. Its time is the
+// chain of loads: 5 us behind 8 long sequences, 11 (40 MB of parts in L2) behind
+// the chunk kernel's 128 items of 256 rows.
 template <typename T, int D, typename L>
 __global__ void __launch_bounds__(kJoinWarps<L> * 32)
 kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int part_rows,
@@ -791,7 +797,10 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
 // --------------------------------------------------------------------- host
 
 // bf16 calls with more query rows per cache head than this go to the tensor
-// core kernel (d = 32 stays: its rows are half a swizzled operand row).
+// core kernel (d = 32 stays: its rows are half a swizzled operand row). 8 ragged
+// sequences of up to 4096 / 32768 keys, 8 cache heads, d = 128, here against
+// there (us): 32 rows 33 / 140 against 37 / 192, 64 rows 51 / 262 against 38 /
+// 193, 128 rows of 4096 keys 85 against 41.
 constexpr int kChunkRows = 48;
 
 // Contexts of up to kWholeTiles tiles (in a batch of kWholeItems items or more,

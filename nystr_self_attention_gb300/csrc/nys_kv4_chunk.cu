@@ -28,6 +28,13 @@
 // the order of the 4-bit fields: the queries' channels are permuted to match,
 // and the output's columns are put right when they are written.
 //
+// 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 195 us
+// here, 205 with the join, 615 TFLOP/s (over 16384 tokens 690). Tensor cores 31 %
+// busy, HBM 1 %: a tile of a group is a chain of its softmax (about 900
+// instructions of a warp, 3100 cycles) and the two products (1100), of which the
+// other group fills a part. Halves of 64 keys with the next scores under way
+// shortened the chain but doubled its handshakes: 244 us.
+//
 // Every wait is bounded; one that runs out sets the status word, all roles wind
 // down, and tensor memory is freed.
 #include <cuda_bf16.h>
