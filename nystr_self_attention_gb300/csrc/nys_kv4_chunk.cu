@@ -79,6 +79,7 @@ struct Shared {
   int warp_sums[kThreads / 32];
   uint32_t tmem;
   int abort;
+  int turn;  // whether a group has the tensor cores
 };
 
 // The code is kept short where it can be (plain bounded spins, loops over
@@ -98,6 +99,16 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status,
                                           volatile int* abort_flag) {
   return __all_sync(0xffffffffu, wait_or_fail(bar, parity, status, abort_flag));
+}
+
+// A group's products, those of a tile's values and of the next tile's keys, run
+// in one go: with both groups' interleaved, both would wait for all of them and
+// then share the issue slots for their softmax. This orders time, not data: a
+// thread that has waited long goes ahead.
+__device__ __forceinline__ void take_turn(int* turn) {
+#pragma unroll 1
+  for (int i = 0; i < 4096 && atomicCAS(turn, 0, 1) != 0; ++i) {
+  }
 }
 
 __device__ __forceinline__ uint32_t half2_mul(uint32_t a, uint32_t b) {
@@ -362,9 +373,11 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   uint32_t n = 0, n_s = 0;  // tiles of the CTA; of this group
   // One thread of the group: S of tile t (slot k), once its keys are there; and
   // P V of tile t. A segment without a second group frees the slots for both.
+  auto keys_there = [&](uint32_t t) {
+    return wait_or_fail(&sh.k_full[t % kSlots], (t / kSlots) & 1u, p.status, abort_flag);
+  };
   auto issue_scores = [&](uint32_t t, int groups) {
     const int slot = t % kSlots;
-    if (!wait_or_fail(&sh.k_full[slot], (t / kSlots) & 1u, p.status, abort_flag)) return;
     tc_fence_after_sync();
     const uint64_t a0 = smem_desc(smem_u32(qs), 16, 1024, SW_128B);
     const uint64_t b0 = smem_desc(smem_u32(k_s + slot * tile_bytes<D>()), 16, 1024, SW_128B);
@@ -449,7 +462,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       fence_async_smem();
       tc_fence_before_sync();  // the previous segment's output has been read
       if (group_failed(g, !ok)) return;
-      if (leader) issue_scores(n, groups);
+      if (leader && keys_there(n)) issue_scores(n, groups);
       __syncwarp();
 
 #pragma unroll 1
@@ -573,10 +586,13 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
         tc_fence_before_sync();
         if (group_failed(g, false)) return;
         if (leader) {
+          // the next keys first: their slot may be waiting for the other group
+          const bool more = i + 1 < tiles && keys_there(n + 1);
+          take_turn(&sh.turn);
           issue_values(n, i == 0, groups);
           // S is this tile's P until its product is done
-          if (i + 1 < tiles && wait_or_fail(&sh.pv_done[g], n_s & 1u, p.status, abort_flag))
-            issue_scores(n + 1, groups);
+          if (more && wait_or_fail(&sh.pv_done[g], n_s & 1u, p.status, abort_flag)) issue_scores(n + 1, groups);
+          atomicExch(&sh.turn, 0);
         }
         __syncwarp();
       }
@@ -656,6 +672,7 @@ kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __rest
     }
     mbar_init(&sh.fin, 2);
     sh.abort = 0;
+    sh.turn = 0;
     fence_barrier_init();
   }
   cudaTriggerProgrammaticLaunchCompletion();
