@@ -65,7 +65,7 @@ struct TileInfo {
   float k2e[4];       // keys' factor / 2^10
   float ev[4];        // log2 of the values' factor
   float vinv[4];      // its inverse
-  uint32_t wide[4];   // p and V of these keys are bf16
+  alignas(16) uint32_t wide[4];  // p and V of these keys are bf16
   uint32_t have[4];   // which of the 32 tokens exist
   uint32_t odd[4];    // some value scale is infinite or NaN:
   uint32_t odd_of[4][4];  // [32 tokens][group]: which ones
@@ -371,12 +371,16 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   const uint32_t id_s = idesc_f16(128, 128), id_v = idesc_f16(128, D, true);
   const uint32_t id_w = idesc_bf16(128, D, false, true);
   uint32_t n = 0, n_s = 0;  // tiles of the CTA; of this group
-  // One thread of the group: S of tile t (slot k), once its keys are there; and
-  // P V of tile t. A segment without a second group frees the slots for both.
+  // One thread of the group: S of tile t, once its keys are there; P V of tile
+  // t; and a slot of it that the group is done with (a segment without a second
+  // group frees it for both).
   auto keys_there = [&](uint32_t t) {
     return wait_or_fail(&sh.k_full[t % kSlots], (t / kSlots) & 1u, p.status, abort_flag);
   };
-  auto issue_scores = [&](uint32_t t, int groups) {
+  auto release = [&](uint64_t* empty, uint32_t t, int groups) {
+    for (int k = groups; k < 3; ++k) mbar_arrive(&empty[t % kSlots]);
+  };
+  auto issue_scores = [&](uint32_t t) {
     const int slot = t % kSlots;
     tc_fence_after_sync();
     const uint64_t a0 = smem_desc(smem_u32(qs), 16, 1024, SW_128B);
@@ -387,19 +391,18 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       mma_bf16(tmem + 128 * g, a0 + off, b0 + off, id_s, kk > 0);
     }
     mma_commit(&sh.s_full[g]);
-    for (int k = groups; k < 3; ++k) mma_commit(&sh.k_empty[slot]);
   };
-  auto issue_values = [&](uint32_t t, bool first, int groups) {
+  auto issue_values = [&](uint32_t t, bool first) {
     const int slot = t % kSlots;
-    tc_fence_after_sync();
     const uint64_t v0 = smem_desc(smem_u32(v_s + slot * tile_bytes<D>()), 16384, 1024, SW_128B);
-    const TileInfo& info = sh.info[t % kInfo];
+    const uint4 wide = *reinterpret_cast<const uint4*>(sh.info[t % kInfo].wide);
+    const uint32_t id[4] = {wide.x ? id_w : id_v, wide.y ? id_w : id_v, wide.z ? id_w : id_v, wide.w ? id_w : id_v};
+    tc_fence_after_sync();
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)  // 16 keys: 2 KB of V, 8 columns of P
       mma_bf16_tA(tmem + 256 + g * D, tmem + 128 * g + kk * 8, v0 + (uint64_t)(kk * 128),
-                  info.wide[kk >> 1] ? id_w : id_v, (!first || kk > 0) ? 1u : 0u);
+                  id[kk >> 1], (!first || kk > 0) ? 1u : 0u);
     mma_commit(&sh.pv_done[g]);
-    for (int k = groups; k < 3; ++k) mma_commit(&sh.v_empty[slot]);
   };
   const bool leader = lr == 0;
   bool ok = true;
@@ -462,7 +465,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       fence_async_smem();
       tc_fence_before_sync();  // the previous segment's output has been read
       if (group_failed(g, !ok)) return;
-      if (leader && keys_there(n)) issue_scores(n, groups);
+      if (leader && keys_there(n)) issue_scores(n);
       __syncwarp();
 
 #pragma unroll 1
@@ -475,6 +478,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
           return;
         }
         tc_fence_after_sync();
+        if (leader) release(sh.k_empty, n, groups);
         const TileInfo& info = sh.info[n % kInfo];
         // tokens of 32-key chunk c that this row sees
         auto visible = [&](int c) {
@@ -586,12 +590,21 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
         tc_fence_before_sync();
         if (group_failed(g, false)) return;
         if (leader) {
-          // the next keys first: their slot may be waiting for the other group
-          const bool more = i + 1 < tiles && keys_there(n + 1);
           take_turn(&sh.turn);
-          issue_values(n, i == 0, groups);
-          // S is this tile's P until its product is done
-          if (more && wait_or_fail(&sh.pv_done[g], n_s & 1u, p.status, abort_flag)) issue_scores(n + 1, groups);
+          issue_values(n, i == 0);
+          if (i + 1 < tiles) {
+            bool there = mbar_test(&sh.k_full[(n + 1) % kSlots], ((n + 1) / kSlots) & 1u);
+            // S is this tile's P until its product is done
+            if (wait_or_fail(&sh.pv_done[g], n_s & 1u, p.status, abort_flag)) {
+              if (!there) {  // their slot may be waiting for the other group
+                atomicExch(&sh.turn, 0);
+                there = keys_there(n + 1);
+                take_turn(&sh.turn);
+              }
+              if (there) issue_scores(n + 1);
+              release(sh.v_empty, n, groups);
+            }
+          }
           atomicExch(&sh.turn, 0);
         }
         __syncwarp();
@@ -599,6 +612,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       ok = warp_wait(&sh.pv_done[g], (n_s - 1) & 1u, p.status, abort_flag);
       if (!ok) continue;  // to where the group meets next
       tc_fence_after_sync();
+      if (leader) release(sh.v_empty, n - 1, groups);
     }
     // ---- the row's output: columns back in channels' order
     const bool whole = sg.whole(L::TILE);
