@@ -137,6 +137,34 @@ __device__ __forceinline__ uint32_t fields_exact(const float (&x)[8], float s, f
   return w;
 }
 
+// The first guesses alone, two at a time, where all of them are clear of a
+// border: x * (1/s) is off by less than 2^-19, so a remainder of at most (1/2 -
+// 2^-17) s says that the guess is right (one warp in 250 has another). s is not
+// tiny here: |x / s| < 7.5. A chunk of 8 x 1021 tokens x 8 heads, d = 64: written
+// in 12 us by fields_exact, 8 us this way.
+__device__ __forceinline__ bool fields_clear(const float (&x)[8], float s, float inv, uint32_t& fields) {
+  constexpr float M = 12582920.f;
+  float t[8], worst = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    unsigned long long v, e;
+    asm("{\n\t.reg .b64 x, i, s, n, m, q;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 i, {%4, %4};\n\t"
+        "mov.b64 s, {%5, %5};\n\tmov.b64 m, {%6, %6};\n\tmov.b64 n, {%7, %7};\n\t"
+        "fma.rn.f32x2 %0, x, i, m;\n\tsub.rn.f32x2 q, n, %0;\n\tfma.rn.f32x2 %1, q, s, x;\n\t}"
+        : "=&l"(v), "=l"(e)
+        : "f"(x[i]), "f"(x[i + 1]), "f"(inv), "f"(s), "f"(M), "f"(M));
+    const float2 two = reinterpret_cast<const float2&>(v), rest = reinterpret_cast<const float2&>(e);
+    t[i] = two.x;
+    t[i + 1] = two.y;
+    worst = fmaxf(worst, fmaxf(fabsf(rest.x), fabsf(rest.y)));
+  }
+  uint32_t w = 0;
+#pragma unroll
+  for (int i = 7; i >= 0; --i) w = w * 16u + __float_as_uint(t[i]);
+  fields = w - 0x4B400000u * 0x11111111u;
+  return worst <= s * (0.5f - 0x1p-17f);
+}
+
 // 1/x to within a step or two of fp32, for normal x and 1/x.
 __device__ __forceinline__ float reciprocal(float x) {
   float y;
@@ -163,7 +191,9 @@ __device__ __forceinline__ uint32_t quantise(const Raw8<T>& raw, uint16_t& scale
   raw.widen(x);
   if (s >= 0x1p-100f) {
     const float inv = reciprocal(s);
-    return sizeof(T) == 2 ? fields_bf16(x, inv) : fields_exact(x, s, inv);
+    if (sizeof(T) == 2) return fields_bf16(x, inv);
+    uint32_t fields;
+    return fields_clear(x, s, inv, fields) ? fields : fields_exact(x, s, inv);
   }
   // tiny scales: 1/s may be out of range, a subnormal s may be short of bits
 #pragma unroll
