@@ -26,7 +26,7 @@
 // against 57 on the case below.)
 //
 // One token over 8 ragged sequences of up to 32768, 32 + 8 heads, d = 128 (203
-// MB): 61 us a call, 52 of them here, 3.3 TB/s; four times as long 172 us (5.0
+// MB): 61 us a call, 52 of them here, 3.3 TB/s; four times as long 190 us (4.3
 // TB/s). What bounds it is the unpacking: per 16 keys and head about 310
 // instructions of a warp, 120 of them on the integer pipe (42 % busy, HBM 48 %);
 // short calls: the launch, the queries and the join.

@@ -28,12 +28,15 @@
 // the order of the 4-bit fields: the queries' channels are permuted to match,
 // and the output's columns are put right when they are written.
 //
-// 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 195 us
-// here, 205 with the join, 615 TFLOP/s (over 16384 tokens 690). Tensor cores 31 %
-// busy, HBM 1 %: a tile of a group is a chain of its softmax (about 900
-// instructions of a warp, 3100 cycles) and the two products (1100), of which the
-// other group fills a part. Halves of 64 keys with the next scores under way
-// shortened the chain but doubled its handshakes: 244 us.
+// 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 172 us
+// here, 185 with the join, 680 TFLOP/s (over 16384 tokens 318 here, 790). Tensor
+// cores 34 % busy, HBM 1 %. Clock stamps: a tile of a group is a chain of 5900
+// cycles - softmax 2600 (about 900 instructions of a warp), the products 1700
+// (100 per issued instruction, the pipe's own time is 68), their handshakes and
+// the last one's end 1300 -, of which the other group's softmax and products
+// fill the gaps. Not kept: halves of 64 keys with the next scores under way (a
+// shorter chain, twice the handshakes: 244 us against 196 then); two threads per
+// row in 24 warps (191 against 176: exponentials and conversions share pipes).
 //
 // Every wait is bounded; one that runs out sets the status word, all roles wind
 // down, and tensor memory is freed.
