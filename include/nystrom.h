@@ -417,7 +417,7 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* p, const void* q, const void* 
  * block_table: device int32 [B][max_pages]. Sequences may share pages that
  * are only read. Shape rules: num_pages, max_pages, Hk >= 1; page_size a
  * multiple of 16 in 16 .. 4096; d in {32, 64, 128}; max_pages * page_size <=
- * 2^31 - 2^16.
+ * 2^31 - 2^16; nystrom_kv4_cache_bytes(...) <= 2^47.
  */
 typedef struct {
   void* data;

@@ -28,6 +28,9 @@ int check_cache(const nys_kv4_cache_t* c) {
   if (c->d != 32 && c->d != 64 && c->d != 128) return NYS_ERR_SHAPE;
   // tiles and windows of pages past the last one keep 32-bit key indexes
   if ((long long)c->max_pages * c->page_size > (1ll << 31) - 65536) return NYS_ERR_SHAPE;
+  // the pool's size and the addresses in it stay far from 64 bits
+  if ((long long)c->num_pages * c->Hk > (1ll << 47) / ((long long)(c->page_size / kBlock) * block_bytes(c->d)))
+    return NYS_ERR_SHAPE;
   if (reinterpret_cast<uintptr_t>(c->data) & 15u) return NYS_ERR_ALIGN;
   if (reinterpret_cast<uintptr_t>(c->block_table) & 3u) return NYS_ERR_ALIGN;
   return NYS_OK;

@@ -202,3 +202,12 @@ def test_positions_stay_clear_of_32_bits(N, max_pages, page, code):
     c = cache(N, max_pages=max_pages, page=page)
     got = io(N, False, c, k=264)  # past the shape check only the alignment is wrong
     assert got == (E_ALIGN if code is None else code)
+
+
+def test_pools_past_any_memory_are_refused(N):
+    big = 2 ** 31 - 1
+    assert N.nystrom_kv4_cache_bytes(big, 4096, 65535, 128) == 0
+    assert io(N, False, cache(N, pages=big, Hk=65535, page=4096)) == E_SHAPE
+    pages = 2 ** 47 // (65535 * 256 * 18 * 128)
+    assert N.nystrom_kv4_cache_bytes(pages, 4096, 65535, 128) == pages * 65535 * 256 * 18 * 128
+    assert N.nystrom_kv4_cache_bytes(pages + 1, 4096, 65535, 128) == 0

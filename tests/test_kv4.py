@@ -553,7 +553,8 @@ def test_read_of_any_bytes(d, dtype):
     k, v = (torch.empty(2, n, 2, d, dtype=t, device="cuda").transpose(1, 2) for _ in range(2))
     N.nystrom_kv4_read(c.dev, k, v)
     for b in range(2):
-        toks = [c.ref.token(b, i) for i in range(n)]
+        with np.errstate(invalid="ignore"):
+            toks = [c.ref.token(b, i) for i in range(n)]
         for got, kind in ((k, 0), (v, 1)):
             with np.errstate(over="ignore", invalid="ignore"):
                 want = torch.from_numpy(np.stack([x[kind] for x in toks], 1)).to(torch.float32).to(t)
