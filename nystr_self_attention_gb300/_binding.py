@@ -378,10 +378,14 @@ def _raw_stream(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
+_default_scratch = {}  # device index: workspace of calls on its default stream
+
+
 def _scratch(nbytes, workspace, device, stream):
     """(address, bytes, tensor to keep until the launch) of a call's workspace:
-    the caller's, or memory of torch's allocator that belongs to the call's
-    stream, so that it is reused only behind the call."""
+    the caller's; on the default stream one that its calls share (they run one
+    after another, and it cannot be captured); else memory of torch's allocator
+    that belongs to the call's stream, so that it is reused only behind the call."""
     torch = _torch
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
@@ -389,10 +393,15 @@ def _scratch(nbytes, workspace, device, stream):
         return workspace.data_ptr(), workspace.numel() * workspace.element_size(), workspace
     if nbytes == 0:
         return None, 0, None
-    if stream is None:
+    raw, current = _raw_stream(stream, device), torch._C._cuda_getCurrentRawStream(device)
+    if raw == 0 == current:
+        t = _default_scratch.get(device)
+        if t is None or t.numel() < nbytes:
+            t = _default_scratch[device] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+    elif raw == current:
         t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     else:
-        with torch.cuda.stream(torch.cuda.ExternalStream(_raw_stream(stream, device))):
+        with torch.cuda.stream(torch.cuda.ExternalStream(raw)):
             t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     return t.data_ptr(), nbytes, t
 

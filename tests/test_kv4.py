@@ -569,3 +569,37 @@ def test_a_cache_keeps_its_memory():
         with pytest.raises(AttributeError):
             setattr(c.dev, name, c.data)
     assert c.dev.data is c.data and c.dev.block_table is c.dtable
+
+
+def test_workspaces_of_calls_one_after_another_and_side_by_side():
+    """Calls of growing and shrinking needs on the default stream, whose
+    workspace they share, with others on a second stream meanwhile."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    cases, side = [], torch.cuda.Stream()
+    for i, (B, Hq, nq, n, dtype) in enumerate([(1, 8, 1, 1500, "f32"), (4, 8, 90, 1500, "bf16"),
+                                               (2, 16, 2, 1200, "bf16"), (3, 8, 3, 1400, "f32")]):
+        c = Both(B, 4, 64, 64, 24, seed=i)
+        k, v = (heads(c.rng.standard_normal((B, 4, n, 64)), dtype, "bnhd") for _ in range(2))
+        N.nystrom_kv4_write(c.dev, k, v)
+        q = heads(c.rng.standard_normal((B, Hq, nq, 64)), dtype, "bnhd")
+        lens = [n - 7 * b for b in range(B)]
+        need = N.nystrom_kv4_attn_workspace_bytes(c.dev, B, nq, Hq, n, N.NYS_BF16 if dtype == "bf16" else N.NYS_FP32)
+        assert need > 0
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        cases.append((c, q, i32(lens), n, run_attn(c, q, lens, nq, max_length=n, workspace=ws)))
+    torch.cuda.synchronize()
+    assert torch.cuda.current_stream().cuda_stream == 0
+    for _ in range(5):
+        outs = []
+        for j, (c, q, lens, n, want) in enumerate(cases):
+            o = torch.empty_like(q)
+            N.nystrom_kv4_attn_fwd(c.dev, q, o, lens, n)
+            c2, q2, lens2, n2, want2 = cases[-1 - j]
+            p = torch.empty_like(q2)
+            with torch.cuda.stream(side):
+                N.nystrom_kv4_attn_fwd(c2.dev, q2, p, lens2, n2)
+            outs += [(o, want), (p, want2)]
+        torch.cuda.synchronize()
+        for got, want in outs:
+            assert torch.equal(got, want)
