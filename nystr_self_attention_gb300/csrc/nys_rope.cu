@@ -16,9 +16,9 @@
 // its top two bits pick the quadrant and what is left, at most an eighth of a
 // turn, goes to the sine and cosine.
 //
-// Forward, 2 x 32768 tokens, 16 + 16 heads, d = 128, bf16 (1.07 GB): 167 us, 6.4
+// Forward, 2 x 32768 tokens, 16 + 16 heads, d = 128, bf16 (1.07 GB): 165 us, 6.5
 // TB/s where a copy reaches 6.8; fp32 pairs over three axes, 8 x 8190 tokens, 8 +
-// 8 heads, d = 64 (537 MB): 90 us, 6.0 TB/s. Backward, 8 x 8192 tokens, 8 + 8
+// 8 heads, d = 64 (537 MB): 88 us, 6.1 TB/s. Backward, 8 x 8192 tokens, 8 + 8
 // heads, d = 64, bf16 (403 MB): 77 us with the weights' sums, 5.2 TB/s; with 128
 // registers a thread only 16 warps fit an SM, and between loads and stores they
 // issue 2.4 instructions a cycle: latency and issue bound it together.
@@ -351,8 +351,10 @@ __device__ __forceinline__ void walk_forward(const T* x, T* y, long long xs, lon
 template <typename T>
 constexpr int kAhead = sizeof(T) == 2 ? 4 : 2;
 
+// Four CTAs per SM: 8 x 8190 tokens, 8 + 8 heads, d = 64, fp32 / bf16 86 / 47.5 us;
+// with the registers of three 88 / 49.6, though a few are spilled around the loop.
 template <typename T, int LP, int MODE>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 qk_norm_rope(const __grid_constant__ RopeParams p, const T* q, const T* k, T* qo, T* ko) {
   __shared__ unsigned long long freq[kMaxPairs];
   if (threadIdx.x < p.half) freq[threadIdx.x] = p.freq[threadIdx.x];
