@@ -60,7 +60,7 @@ constexpr int kInfo = 4;   // tiles whose facts are kept
 constexpr float kRebase = 8.0f;
 constexpr int kNarrow = 8;  // value scales of 32 tokens within 2^8: fp16
 constexpr uint64_t kWaitNs = 2000000000ull;
-constexpr int kSpins = 1 << 20;  // waits of up to 20 us each: a bound, never met
+constexpr int kSpins = 1 << 20;  // waits of up to 20 us each
 
 // What a tile's softmax has to know, per 32 tokens: the powers of two of keys
 // and values, and the tokens that must not enter a sum as they are.
@@ -375,14 +375,14 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   const uint32_t id_w = idesc_bf16(128, D, false, true);
   uint32_t n = 0, n_s = 0;  // tiles of the CTA; of this group
   // One thread of the group: S of tile t, once its keys are there; P V of tile
-  // t; and a slot of it that the group is done with (a segment without a second
-  // group frees it for both).
+  // t; and a slot of it that the group is done with. Both groups pass every tile
+  // of the CTA in order, one without rows in the segment too: a slot is filled
+  // anew only behind both, so nobody is ever more than one use of a slot away
+  // from anybody else, which is as far as the barriers' one bit of phase tells.
   auto keys_there = [&](uint32_t t) {
     return wait_or_fail(&sh.k_full[t % kSlots], (t / kSlots) & 1u, p.status, abort_flag);
   };
-  auto release = [&](uint64_t* empty, uint32_t t, int groups) {
-    for (int k = groups; k < 3; ++k) mbar_arrive(&empty[t % kSlots]);
-  };
+  auto release = [&](uint64_t* empty, uint32_t t) { mbar_arrive(&empty[t % kSlots]); };
   auto issue_scores = [&](uint32_t t) {
     const int slot = t % kSlots;
     tc_fence_after_sync();
@@ -412,7 +412,18 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   Segment sg;
   while (next_segment<L>(p, pos, r1, base, b, sg)) {
     const int tiles = max(0, tiles_seen(sg));
-    if (g >= groups_of(sg)) {
+    if (g >= groups_of(sg)) {  // no rows here: pass the tiles
+      if (leader) {
+#pragma unroll 1
+        for (uint32_t t = n; ok && t < n + tiles; ++t) {
+          ok = keys_there(t);
+          if (!ok) break;
+          release(sh.k_empty, t);
+          ok = wait_or_fail(&sh.v_full[t % kSlots], (t / kSlots) & 1u, p.status, abort_flag);
+          if (ok) release(sh.v_empty, t);
+        }
+      }
+      __syncwarp();
       n += tiles;
       continue;
     }
@@ -464,7 +475,6 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
             make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]),
                        pack_half2(v[3], v[7]));
       }
-      const int groups = groups_of(sg);
       fence_async_smem();
       tc_fence_before_sync();  // the previous segment's output has been read
       if (group_failed(g, !ok)) return;
@@ -481,7 +491,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
           return;
         }
         tc_fence_after_sync();
-        if (leader) release(sh.k_empty, n, groups);
+        if (leader) release(sh.k_empty, n);
         const TileInfo& info = sh.info[n % kInfo];
         // tokens of 32-key chunk c that this row sees
         auto visible = [&](int c) {
@@ -605,7 +615,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
                 take_turn(&sh.turn);
               }
               if (there) issue_scores(n + 1);
-              release(sh.v_empty, n, groups);
+              release(sh.v_empty, n);
             }
           }
           atomicExch(&sh.turn, 0);
@@ -615,7 +625,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       ok = warp_wait(&sh.pv_done[g], (n_s - 1) & 1u, p.status, abort_flag);
       if (!ok) continue;  // to where the group meets next
       tc_fence_after_sync();
-      if (leader) release(sh.v_empty, n - 1, groups);
+      if (leader) release(sh.v_empty, n - 1);
     }
     // ---- the row's output: columns back in channels' order
     const bool whole = sg.whole(L::TILE);
