@@ -7,6 +7,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+import threading
 
 NYS_FP32, NYS_BF16 = 0, 1
 NYS_OK, NYS_ERR_ARG, NYS_ERR_SHAPE, NYS_ERR_ALIGN = 0, -1, -2, -3
@@ -378,14 +379,23 @@ def _raw_stream(stream, device):
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
-_default_scratch = {}  # device index: workspace of calls on its default stream
+class _Scratch(threading.local):
+    """by_device: device index: workspace of this thread's calls on its default stream."""
+
+    def __init__(self):
+        self.by_device = {}
+
+
+_default_scratch = _Scratch()
 
 
 def _scratch(nbytes, workspace, device, stream):
     """(address, bytes, tensor to keep until the launch) of a call's workspace:
-    the caller's; on the default stream one that its calls share (they run one
-    after another, and it cannot be captured); else memory of torch's allocator
-    that belongs to the call's stream, so that it is reused only behind the call."""
+    the caller's; on the default stream one that this thread's calls share (the
+    kernels of one run behind those of another, and it cannot be captured; two
+    threads' calls could enqueue theirs in between each other); else memory of
+    torch's allocator that belongs to the call's stream, so that it is reused only
+    behind the call."""
     torch = _torch
     if workspace is not None:
         if workspace.get_device() != device or not workspace.is_contiguous():
@@ -395,9 +405,10 @@ def _scratch(nbytes, workspace, device, stream):
         return None, 0, None
     raw, current = _raw_stream(stream, device), torch._C._cuda_getCurrentRawStream(device)
     if raw == 0 == current:
-        t = _default_scratch.get(device)
+        kept = _default_scratch.by_device
+        t = kept.get(device)
         if t is None or t.numel() < nbytes:
-            t = _default_scratch[device] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
+            t = kept[device] = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     elif raw == current:
         t = torch.empty(nbytes, dtype=torch.uint8, device="cuda")
     else:
