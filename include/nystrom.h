@@ -44,7 +44,11 @@
  *  - Thread safety: calls may come from several host threads; the cached
  *    workspace of nystrom_attn_fwd is shared per device, so concurrent calls
  *    on different streams of one device must use nystrom_attn_fwd_ws with
- *    their own workspaces.
+ *    their own workspaces. The same holds for the cached workspace that
+ *    nystrom_qk_norm_rope_bwd and nystrom_kv4_attn_fwd use where none is given:
+ *    they are two kernels with the workspace between them, which no other
+ *    thread's call of theirs separates, but on another stream they may run at
+ *    the same time.
  */
 #ifndef NYSTROM_H_
 #define NYSTROM_H_

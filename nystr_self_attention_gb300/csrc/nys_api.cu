@@ -117,8 +117,10 @@ struct DeviceCache {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* last_ws = nullptr;  // status word of the most recent call
-  // the operators around a cached attention layer: their cached workspace
-  // and their status word (operator_workspace, operator_status)
+  // the operators around a cached attention layer: their cached workspace, held
+  // by one call at a time, and their status word (operator_workspace,
+  // operator_status)
+  std::mutex op_mu;
   void* op_ws = nullptr;
   size_t op_ws_bytes = 0;
   int* op_status = nullptr;
@@ -185,7 +187,8 @@ namespace {
 __device__ int g_op_status;
 }  // namespace
 
-int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out) {
+int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out,
+                       std::unique_lock<std::mutex>* held) {
   // a graph would keep the buffer's address past the next growth
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
@@ -193,7 +196,7 @@ int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out) {
     return NYS_ERR_ARG;
   }
   if (capturing != cudaStreamCaptureStatusNone) return NYS_ERR_ARG;
-  std::lock_guard<std::mutex> lk(g_dev[dev].mu);
+  *held = std::unique_lock<std::mutex>(g_dev[dev].op_mu);
   const int rc = ensure_buffer(&g_dev[dev].op_ws, &g_dev[dev].op_ws_bytes, bytes, stream);
   if (rc == NYS_OK) *out = g_dev[dev].op_ws;
   return rc;

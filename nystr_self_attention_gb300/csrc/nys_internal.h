@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cstddef>
 #include <cstdint>
+#include <mutex>
 #include <string>
 
 #include "nystrom.h"
@@ -99,8 +100,11 @@ int begin_call(char* ws, const Layout& L, cudaStream_t stream, int dev, bool cle
 void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc);
 // The cached workspace of the operators around a cached attention layer, in a
 // buffer of its own (nystrom_get_status reads the other one's first word).
-// NYS_ERR_ARG while `stream` is being captured.
-int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out);
+// NYS_ERR_ARG while `stream` is being captured. *held keeps other threads from
+// it: the caller holds on until all its kernels are enqueued, so that no other
+// call's come in between.
+int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out,
+                       std::unique_lock<std::mutex>* held);
 // Device address of those operators' status word on device `dev` (current):
 // zero until a kernel sets it, cleared when nystrom_get_status reports it.
 int operator_status(int dev, int** out);

@@ -938,8 +938,9 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
+  std::unique_lock<std::mutex> held;
   if (!workspace && pl.total > 0) {
-    rc = operator_workspace(dev, pl.total, stream, &workspace);
+    rc = operator_workspace(dev, pl.total, stream, &workspace, &held);
     if (rc != NYS_OK) return rc;
   }
   AttnParams p{};

@@ -775,8 +775,9 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* a, const void* q, const void* 
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
+  std::unique_lock<std::mutex> held;
   if (sums && !workspace) {
-    rc = operator_workspace(dev, need, stream, &workspace);
+    rc = operator_workspace(dev, need, stream, &workspace, &held);
     if (rc != NYS_OK) return rc;
   }
   const Grid g = grid_of(*a, true);

@@ -67,7 +67,8 @@ def calls_of(kind):
     if kind == "attention":
         return attention_call(1, 1, 8, 2, 2000, 1, torch.bfloat16), attention_call(2, 2, 4, 4, 1500, 3, torch.float32)
     if kind == "chunks":
-        return attention_call(3, 1, 8, 1, 3000, 30, torch.bfloat16), attention_call(4, 1, 4, 1, 2500, 50, torch.bfloat16)
+        return (attention_call(3, 1, 8, 1, 3000, 30, torch.bfloat16),
+                attention_call(4, 1, 4, 1, 2500, 50, torch.bfloat16))
     return gradient_call(5, 300, torch.float32), gradient_call(6, 700, torch.bfloat16)
 
 
@@ -155,3 +156,26 @@ def test_workspaces_of_threads_are_apart(kind, monkeypatch):
     assert not errors, errors
     (a,), (b,) = seen.values()
     assert a[0] and b[0] and (a[0] + a[1] <= b[0] or b[0] + b[1] <= a[0])
+
+
+@pytest.mark.parametrize("kind", ["attention", "chunks", "gradients"])
+def test_threads_with_the_librarys_workspace(kind, monkeypatch):
+    """The same through the C entries with no workspace given, on one stream."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    from nystr_self_attention_gb300 import _binding
+    name = "nystrom_qk_norm_rope_bwd" if kind == "gradients" else "nystrom_kv4_attn_fwd"
+    real = _binding.load_library()
+    fn = getattr(real, name)
+
+    class Library:
+        def __getattr__(self, attr):
+            if attr != name:
+                return getattr(real, attr)
+            return lambda *args: fn(*args[:-3], None, 0, args[-1])
+
+    calls = calls_of(kind)
+    torch.cuda.synchronize()
+    monkeypatch.setattr(_binding, "_lib", Library())
+    assert differing(calls) == [0, 0]
+    assert N.nystrom_get_status() == N.NYS_OK
