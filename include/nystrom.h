@@ -472,7 +472,11 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * enter the product with V as bf16; with more than 48 query rows per cache
  * head (nq * Hq/Hk, d in {64, 128}) they, and codes times scales, enter as
  * fp16 scaled by powers of two, or as bf16 where the value scales of 32 tokens
- * span more than 2^8. For NYS_FP32 queries and probabilities enter as sums of
+ * span more than 2^8. Queries enter the scores as fp16 scaled by a power of two
+ * per row, which loses nothing of channels down to 2^-26 of the row's largest. In
+ * the calls of more rows keys lose nothing down to 2^-29 of the largest key scale
+ * among the same 32 tokens; a smaller one is off by at most 2^-37 of that scale.
+ * For NYS_FP32 queries and probabilities enter as sums of
  * 16-bit terms that keep at least 22 and 24 bits.
  * Shape rules: B, nq, Hk >= 1, Hq a multiple of Hk, Hq <= 65535, B <= 65535,
  * max_length >= 0, nq * (Hq/Hk) < 2^30, and the key tiles that all items could

@@ -16,12 +16,14 @@
 // Warps 8-11 (K) and 12-15 (V): unpack 32 keys each of every tile into swizzled
 // fp16 operands.
 //
-// fp16 operands: code * scale has 12 bits and is rounded to 11 (bf16 would keep
-// 8, which alone would cost as much as rounding the result does). fp16's range
-// is met by powers of two: a query row is scaled to 2^13 .. 2^14, the keys and
-// the values of each 32 tokens by their largest scale; the factors come back
-// in the exponent of p (keys: f, values: added to it, and taken out of the sum
-// again), so each 32 tokens and each row have their own. Where the value scales
+// fp16 operands: code * scale has 11 bits, as fp16 does (bf16 would keep 8, which
+// alone would cost as much as rounding the result does). fp16's range is met by
+// powers of two: a query row is scaled to 2^13 .. 2^14, the keys and the values
+// of each 32 tokens by their largest scale; the factors come back in the exponent
+// of p (keys: f, values: added to it, and taken out of the sum again), so each 32
+// tokens and each row have their own. Keys use all of fp16's range, so that those
+// of scales up to 2^29 below the largest of their 32 tokens are exact: a score
+// is as if its operands were fp32 ones. Where the value scales
 // of 32 tokens span more than 2^8, fp16 would lose the small ones: those keys'
 // p and V are bf16 (the instruction's types are chosen per 16 keys) and carry no
 // factor. The unpacking keeps
@@ -65,7 +67,7 @@ constexpr int kSpins = 1 << 20;  // waits of up to 20 us each
 // What a tile's softmax has to know, per 32 tokens: the powers of two of keys
 // and values, and the tokens that must not enter a sum as they are.
 struct TileInfo {
-  float k2e[4];       // keys' factor / 2^10
+  float k2e[4];       // keys' factor, times 2^12
   float ev[4];        // log2 of the values' factor
   float vinv[4];      // its inverse
   alignas(16) uint32_t wide[4];  // p and V of these keys are bf16
@@ -136,6 +138,18 @@ __device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t a) {
   const uint32_t off = half2_mul(a, 0x80088008u);  // a * -8 * 2^-24
   return make_uint4(half2_fma(w & 0x000f000fu, a, off), half2_fma(w & 0x00f000f0u, up, off),
                     half2_fma((w >> 8) & 0x000f000fu, a, off), half2_fma((w >> 8) & 0x00f000f0u, up, off));
+}
+
+// Eight fields u of w to (u - 8) a, exactly: 1024 + u or, four bits up, 1024 +
+// 16 u by putting the field into the mantissa of 1024, brought to u - 8, times a.
+// A code of up to 7 times an 8-bit scale has 11 bits, as many as fp16.
+__device__ __forceinline__ uint4 unpack8_exact(uint32_t w, uint32_t a) {
+  auto one = [&](uint32_t u_less_8) { return half2_mul(u_less_8, a); };
+  const uint32_t k = 0x64006400u, sixteenth = 0x2c002c00u;  // 1024, 1/16
+  return make_uint4(one(half2_fma((w & 0x000f000fu) | k, 0x3c003c00u, 0xe408e408u)),  // less 1032
+                    one(half2_fma((w & 0x00f000f0u) | k, sixteenth, 0xd480d480u)),    // less 72
+                    one(half2_fma(((w >> 8) & 0x000f000fu) | k, 0x3c003c00u, 0xe408e408u)),
+                    one(half2_fma(((w >> 8) & 0x00f000f0u) | k, sixteenth, 0xd480d480u)));
 }
 
 // The same as bf16 (u - 8) a, a in bf16: u 2^-133 or u 2^-129 to (u - 8) 2^-6,
@@ -270,7 +284,7 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
       const bool wide = !KEYS && biased > (int)__reduce_min_sync(0xffffffffu, (unsigned)low) + kNarrow;
       top = max(biased - 127, -100);
       const bool any_odd = __any_sync(0xffffffffu, odd);
-      const float factor = __uint_as_float((uint32_t)(127 + 14 - top) << 23);
+      const float factor = __uint_as_float((uint32_t)(127 + (KEYS ? 12 : 14) - top) << 23);
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < N; ++j) {
@@ -317,7 +331,7 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
           for (int g = 0; g < G; ++g) {
             const uint32_t chunk = (uint32_t)((g & 1) * 4 + (lane >> 3)) ^ (row & 7u);
             *reinterpret_cast<uint4*>(dst + (g >> 1) * 16384 + row * 128 + (chunk << 4)) =
-                unpack8(w[g], a[g] * 0x10001u);
+                unpack8_exact(w[g], a[g] * 0x10001u);
           }
         } else {
           // tokens 2t, 2t + 1 of the half block, pairs of groups
@@ -459,7 +473,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       if (p.scale_log2 < 0.f) up = -up;
       // units of a score, less the keys' power of two
       float rf = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
-      rf = !finite ? NAN : rf * 0x1p10f * (tiny ? 0x1p-80f : 1.f);
+      rf = !finite ? NAN : rf * 0x1p-12f * (tiny ? 0x1p-80f : 1.f);
 #pragma unroll 8
       for (int k = 0; k < D / 8; ++k) {
         const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
