@@ -472,7 +472,9 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * enter the product with V as bf16; with more than 48 query rows per cache
  * head (nq * Hq/Hk, d in {64, 128}) they, and codes times scales, enter as
  * fp16 scaled by powers of two, or as bf16 where the value scales of 32 tokens
- * span more than 2^8. Queries enter the scores as fp16 scaled by a power of two
+ * span more than 2^29. With x the largest, over a row's keys, of the probability
+ * times the largest value scale of its 32 tokens, a probability there keeps fp16's
+ * 11 bits down to 2^-25 x and is off by at most 2^-36 x below. Queries enter the scores as fp16 scaled by a power of two
  * per row, which loses nothing of channels down to 2^-26 of the row's largest. In
  * the calls of more rows keys lose nothing down to 2^-29 of the largest key scale
  * among the same 32 tokens; a smaller one is off by at most 2^-37 of that scale.
@@ -482,8 +484,9 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * max_length >= 0, nq * (Hq/Hk) < 2^30, and the key tiles that all items could
  * have (32 keys x 16 query rows per cache head; more than 48 rows in bf16: 128 x
  * 256) below 2^31 (else NYS_ERR_SHAPE); scale finite (else NYS_ERR_ARG).
- * Magnitudes: probabilities are kept up to 2^8 above 1, so cached values beyond
- * 2^100 may give infinities.
+ * Magnitudes: in calls of few rows probabilities are kept up to 2^8 above 1, so
+ * cached values beyond 2^100 may give infinities; in those of more rows scales
+ * below 2^-97 lose bits.
  * workspace: device, 256-byte aligned, ws_bytes >=
  * nystrom_kv4_attn_workspace_bytes(...) (which may be 0), not shared with a
  * call that may run at the same time. NULL uses the library's cached

@@ -9,7 +9,7 @@
 //   S_g = Q_g K^T           tcgen05, both operands in shared memory
 //   p = 2^(S f - M)         thread = query row, S from tensor memory; P (fp16)
 //                           overwrites S; the running maximum moves when it
-//                           grows by more than 2^8 (O_g is rescaled then)
+//                           grows by more than 2^4 (O_g is rescaled then)
 //   O_g += P V              tcgen05, P from tensor memory, V channels innermost
 // Warps 0-3, 4-7: the groups' softmax; one thread of a group issues its products
 // (P V of a tile, then S of the next), so that nobody else has to be woken.
@@ -21,14 +21,13 @@
 // powers of two: a query row is scaled to 2^13 .. 2^14, the keys and the values
 // of each 32 tokens by their largest scale; the factors come back in the exponent
 // of p (keys: f, values: added to it, and taken out of the sum again), so each 32
-// tokens and each row have their own. Keys use all of fp16's range, so that those
-// of scales up to 2^29 below the largest of their 32 tokens are exact: a score
-// is as if its operands were fp32 ones. Where the value scales
-// of 32 tokens span more than 2^8, fp16 would lose the small ones: those keys'
-// p and V are bf16 (the instruction's types are chosen per 16 keys) and carry no
-// factor. The unpacking keeps
-// the order of the 4-bit fields: the queries' channels are permuted to match,
-// and the output's columns are put right when they are written.
+// tokens and each row have their own. Keys and values use all of fp16's range, so
+// that those of scales up to 2^29 below the largest of their 32 tokens are exact:
+// a score is as if its operands were fp32 ones, and what is rounded is p. Where
+// the value scales of 32 tokens span more than that, those keys' p and V are bf16
+// (the instruction's types are chosen per 16 keys). The unpacking keeps the order
+// of the 4-bit fields: the queries' channels are permuted to match, and the
+// output's columns are put right when they are written.
 //
 // 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 172 us
 // here, 185 with the join, 680 TFLOP/s (over 16384 tokens 318 here, 790). Tensor
@@ -59,8 +58,12 @@ using L = ChunkLine;
 constexpr int kThreads = 16 * 32;
 constexpr int kSlots = 2;  // K tiles and V tiles in shared memory
 constexpr int kInfo = 4;   // tiles whose facts are kept
-constexpr float kRebase = 8.0f;
-constexpr int kNarrow = 8;  // value scales of 32 tokens within 2^8: fp16
+// p is at most 2^(kLift + kRebase), close to fp16's largest number: full 11 bits
+// for keys down to 2^-25 of the row's largest p, 2^-36 of that the least that is
+// seen. (The running maximum moves when it grows by more than 2^kRebase.)
+constexpr float kRebase = 4.0f, kLift = 11.0f;
+constexpr int kNarrow = 29;  // value scales of 32 tokens within 2^29: fp16
+constexpr int kLeast = -68;  // the least power of two of 32 tokens' scales: keeps 1 / factor, times p, in range
 constexpr uint64_t kWaitNs = 2000000000ull;
 constexpr int kSpins = 1 << 20;  // waits of up to 20 us each
 
@@ -131,19 +134,10 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
   return r;
 }
 
-// Eight fields u of w to (u - 8) a 2^-24, a in pairs for the fields in the low
-// and high halves: fields as fp16 subnormals u 2^-24 or, four bits up, u 2^-20.
-__device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t a) {
-  const uint32_t up = half2_mul(a, 0x2c002c00u);   // a 2^-4
-  const uint32_t off = half2_mul(a, 0x80088008u);  // a * -8 * 2^-24
-  return make_uint4(half2_fma(w & 0x000f000fu, a, off), half2_fma(w & 0x00f000f0u, up, off),
-                    half2_fma((w >> 8) & 0x000f000fu, a, off), half2_fma((w >> 8) & 0x00f000f0u, up, off));
-}
-
 // Eight fields u of w to (u - 8) a, exactly: 1024 + u or, four bits up, 1024 +
 // 16 u by putting the field into the mantissa of 1024, brought to u - 8, times a.
 // A code of up to 7 times an 8-bit scale has 11 bits, as many as fp16.
-__device__ __forceinline__ uint4 unpack8_exact(uint32_t w, uint32_t a) {
+__device__ __forceinline__ uint4 unpack8(uint32_t w, uint32_t a) {
   auto one = [&](uint32_t u_less_8) { return half2_mul(u_less_8, a); };
   const uint32_t k = 0x64006400u, sixteenth = 0x2c002c00u;  // 1024, 1/16
   return make_uint4(one(half2_fma((w & 0x000f000fu) | k, 0x3c003c00u, 0xe408e408u)),  // less 1032
@@ -282,15 +276,15 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
       }
       const int biased = (int)__reduce_max_sync(0xffffffffu, (unsigned)top);
       const bool wide = !KEYS && biased > (int)__reduce_min_sync(0xffffffffu, (unsigned)low) + kNarrow;
-      top = max(biased - 127, -100);
+      top = max(biased - 127, kLeast);
       const bool any_odd = __any_sync(0xffffffffu, odd);
-      const float factor = __uint_as_float((uint32_t)(127 + (KEYS ? 12 : 14) - top) << 23);
+      const float factor = __uint_as_float((uint32_t)(127 + 12 - top) << 23);
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < N; ++j) {
         const bool drop = !KEYS && (bits[j] >> 23 & 255u) == 255u;  // told to the softmax below
-        const __half a = __float2half_rn(drop ? 0.f : __uint_as_float(bits[j]) * factor);
-        stage[(tok + j) * G + y] = wide ? __ushort_as_half(drop ? 0 : bits[j] >> 16) : a;
+        const float a = drop ? 0.f : __uint_as_float(bits[j]) * factor;
+        stage[(tok + j) * G + y] = wide ? __ushort_as_half(__float_as_uint(a) >> 16) : __float2half_rn(a);
       }
       // the facts of tile n - kInfo are no longer needed: the products that
       // freed this slot came after its softmax
@@ -302,8 +296,8 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
           info.k2e[part] = __uint_as_float((uint32_t)(127 + top) << 23);
           info.have[part] = now_have;
         } else {
-          info.ev[part] = wide ? 0.f : (float)(10 + top);
-          info.vinv[part] = wide ? 1.f : exp2f((float)(-10 - top));
+          info.ev[part] = (float)(top - 12);
+          info.vinv[part] = exp2f((float)(12 - top));
           info.wide[part] = wide ? 1u : 0u;
           info.odd[part] = any_odd ? 1u : 0u;
         }
@@ -331,7 +325,7 @@ __device__ __forceinline__ void unpack_tiles(const AttnParams& p, Shared& sh, ui
           for (int g = 0; g < G; ++g) {
             const uint32_t chunk = (uint32_t)((g & 1) * 4 + (lane >> 3)) ^ (row & 7u);
             *reinterpret_cast<uint4*>(dst + (g >> 1) * 16384 + row * 128 + (chunk << 4)) =
-                unpack8_exact(w[g], a[g] * 0x10001u);
+                unpack8(w[g], a[g] * 0x10001u);
           }
         } else {
           // tokens 2t, 2t + 1 of the half block, pairs of groups
@@ -547,7 +541,7 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
             l *= alpha;
             m = cand;
           }
-          const float ref = m == -INFINITY ? 0.f : m;
+          const float ref = m == -INFINITY ? 0.f : m - kLift;
 #pragma unroll 1
           for (int pr = 0; pr < 2; ++pr) {
             if (pr) {

@@ -102,3 +102,53 @@ def test_queries_of_small_keys_beside_large_ones(nq, span):
     N.nystrom_kv4_write(cache, x * size, v.float())
     N.nystrom_kv4_read(cache, back, torch.empty_like(x))
     attend(q.to(torch.bfloat16), cache, back.double(), v, n, name=f"span {span}")
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("span", [4, 6, 8, 9, 12, 20, 28, 40])
+@pytest.mark.parametrize("nq", ROWS)
+def test_value_sizes_between_groups_of_channels(nq, span, d):
+    import torch
+    size = torch.ones(d, device="cuda")
+    size[32:] = 2.0 ** -span
+    cache, k, v, g = filled(2, 2, d, 64, [700, 700], seed=span, v_size=size)
+    q = torch.randn(2, 2, nq, d, generator=g, device="cuda").to(torch.bfloat16)
+    attend(q, cache, k, v, 700, name=f"span {span}")
+
+
+@pytest.mark.parametrize("span", [6, 12, 18, 24])
+@pytest.mark.parametrize("nq", ROWS)
+def test_values_of_blocks_far_apart(nq, span):
+    """32 tokens whose first channels' values are 2^span larger and whose others
+    are zero: there the rest of the context has the word alone."""
+    import torch
+    d, n = 128, 900
+    size = torch.ones(n, d, device="cuda")
+    size[96:128, :32] = 2.0 ** span
+    size[96:128, 32:] = 0
+    cache, k, v, g = filled(2, 2, d, 64, [n, n], seed=span, v_size=size)
+    q = torch.randn(2, 2, nq, d, generator=g, device="cuda").to(torch.bfloat16)
+    attend(q, cache, k, v, n, name=f"span {span}")
+
+
+@pytest.mark.parametrize("tail", [65536, 3000])
+@pytest.mark.parametrize("bits", [8.0, 16.3, 20.0, 22.9, 25.1])
+@pytest.mark.parametrize("own", [0.0, 2.0 ** -20, 2.0 ** -7])
+@pytest.mark.parametrize("nq", ROWS)
+def test_a_dominant_key_and_a_long_even_tail(nq, own, bits, tail):
+    """One key 2^bits above all others, which weigh alike; its values are near
+    zero, so that the tail's mean is most of the result."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    d, n = 128, tail + 1
+    cache, k, v, g = filled(1, 1, d, 128, [n], seed=int(bits))
+    at = n // 3
+    x = torch.zeros(1, 1, n, d, device="cuda")
+    x[:, :, at, :32] = 1
+    y = v.float() * 0.25 + 1
+    y[:, :, at] *= own
+    N.nystrom_kv4_write(cache, x, y)
+    N.nystrom_kv4_read(cache, x, y)
+    q = torch.randn(1, 1, nq, d, generator=g, device="cuda")
+    q[..., :32] = bits * np.log(2.0) * d ** 0.5 / 32
+    attend(q.to(torch.bfloat16), cache, x.double(), y.double(), n, causal=False, name=f"2^-{bits}")
