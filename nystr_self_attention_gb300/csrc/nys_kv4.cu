@@ -350,6 +350,7 @@ kv4_read(const __grid_constant__ IoParams p, T* __restrict__ k, T* __restrict__ 
   for (int e = lane; e < HALF / 16; e += 32)  // no block: scales of zero
     reinterpret_cast<uint4*>(im)[e] =
         src ? reinterpret_cast<const uint4*>(src + r.kind * HALF)[e] : make_uint4(0u, 0u, 0u, 0u);
+  const uint32_t none = src ? 0u : 0x88888888u;  // and codes of zero
   __syncwarp();
   const int unit = lane % LPR, t = unit & 3, y = unit >> 2;
   const nys_strides_t& st = r.kind ? p.vs : p.ks;
@@ -366,7 +367,7 @@ kv4_read(const __grid_constant__ IoParams p, T* __restrict__ k, T* __restrict__ 
       const uint8_t* at = im + value_at<D>(row, t, y);
       w = *reinterpret_cast<const uint16_t*>(at) | (uint32_t)*reinterpret_cast<const uint16_t*>(at + D / 2) << 16;
     }
-    decode8(w, scale, dst + row * st.token);
+    decode8(w | none, scale, dst + row * st.token);
   }
 }
 
