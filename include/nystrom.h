@@ -492,7 +492,9 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * call that may run at the same time. NULL uses the library's cached
  * workspace, which a stream under capture may not do (NYS_ERR_ARG).
  * nystrom_get_status reports NYS_ERR_INDEX and NYS_ERR_TIMEOUT of these cache
- * operators until they are read: they are not cleared by a later call.
+ * operators until they are read: they are not cleared by a later call. A first
+ * call of a process may be captured, of these operators and of the norm and
+ * rotation.
  */
 size_t nystrom_kv4_attn_workspace_bytes(const nys_kv4_cache_t* cache, int B, int nq, int Hq,
                                         int max_length, int dtype);

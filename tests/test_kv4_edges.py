@@ -42,3 +42,56 @@ def test_positions_without_a_page_read_as_plus_zero(d, dtype):
     for x in (k, v):
         for rows in (x[0, :, 14:], x[1, :, :32], x[2, :, :16]):
             assert (rows == 0).all() and not torch.signbit(rows.float()).any()
+
+
+FIRST = """
+import sys, numpy as np, torch
+import nystr_self_attention_gb300 as N
+which, rows = sys.argv[1], {"chunk": 70}.get(sys.argv[1], 1)
+B, Hk, d, n = 2, 2, 64, 100
+g = torch.Generator(device="cuda").manual_seed(1)
+data = torch.full((N.nystrom_kv4_cache_bytes(B * 4, 32, Hk, d),), 0x3F, dtype=torch.uint8, device="cuda")
+cache = N.NystromKv4Cache(data, torch.arange(B * 4, dtype=torch.int32, device="cuda").view(B, 4), 32, Hk, d)
+k, v = (torch.randn(B, Hk, n, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+q = torch.randn(B, 4, rows, d, generator=g, device="cuda").to(torch.bfloat16)
+a, b, dw = torch.zeros_like(k), torch.zeros_like(v), torch.zeros(2, d, device="cuda")
+out, lens = torch.zeros_like(q), torch.full((B,), n, dtype=torch.int32, device="cuda")
+inv = 10000.0 ** (-np.arange(32) / 32)
+call = {
+    "write": lambda: N.nystrom_kv4_write(cache, k, v),
+    "read": lambda: N.nystrom_kv4_read(cache, a, b),
+    "token": lambda: N.nystrom_kv4_attn_fwd(cache, q, out, lens, 128),
+    "split": lambda: N.nystrom_kv4_attn_fwd(cache, q, out, lens, 5000),
+    "chunk": lambda: N.nystrom_kv4_attn_fwd(cache, q, out, lens, 128),
+    "rope": lambda: N.nystrom_qk_norm_rope_fwd(k, v, a, b, None, inv),
+    "gradient": lambda: N.nystrom_qk_norm_rope_bwd(k, v, v, k, a, b, None, inv, None, None, dw[0], dw[1]),
+}[which]
+results = (data, out, a, b, dw)
+before = [t.clone() for t in results]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    call()
+graph.replay()
+replayed = [t.clone() for t in results]
+for t, t0 in zip(results, before):
+    t.copy_(t0)
+call()
+torch.cuda.synchronize()
+assert N.nystrom_get_status() == N.NYS_OK
+same = [torch.equal(x, y) for x, y in zip(replayed, results)]
+moved = any(not torch.equal(x, y) for x, y in zip(replayed, before))
+assert all(same) and moved, (same, moved)
+"""
+
+
+@pytest.mark.parametrize("which", ["write", "read", "token", "split", "chunk", "rope", "gradient"])
+def test_a_first_call_may_be_captured(which):
+    """In a process of its own, whose first call of the library's kernels is
+    inside a capture: replayed, it gives what an eager call gives."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST, which], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
