@@ -483,7 +483,7 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * Shape rules: B, nq, Hk >= 1, Hq a multiple of Hk, Hq <= 65535, B <= 65535,
  * max_length >= 0, nq * (Hq/Hk) < 2^30, and the key tiles that all items could
  * have (32 keys x 16 query rows per cache head; more than 48 rows in bf16: 128 x
- * 256) below 2^31 (else NYS_ERR_SHAPE); scale finite (else NYS_ERR_ARG).
+ * 256) below 2^31 (else NYS_ERR_SHAPE); scale * log2(e) finite (else NYS_ERR_ARG).
  * Magnitudes: in calls of few rows probabilities are kept up to 2^8 above 1, so
  * cached values beyond 2^100 may give infinities; in those of more rows scales
  * below 2^-97 lose bits.

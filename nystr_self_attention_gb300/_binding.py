@@ -318,6 +318,7 @@ _ROPE_DESC = struct.Struct("=14if4x18q")  # nys_qk_rope_t
 _KV4_DESC = struct.Struct("=QQ5i4x")      # nys_kv4_cache_t
 _STRIDES = struct.Struct("=3q")           # nys_strides_t
 _NO_STRIDES = (0, 0, 0)
+_INT_MAX = 2 ** 31 - 1  # ctypes cuts what is larger to an int's 32 bits
 _torch = None
 _np = None
 
@@ -506,6 +507,8 @@ def nystrom_qk_norm_rope_bwd(q, k, gq, gk, dq, dk, positions, inv_freq, q_weight
 
 
 def nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d) -> int:
+    if max(num_pages, page_size, Hk, d) > _INT_MAX:
+        return 0  # like other sizes that a call refuses
     return load_library().nystrom_kv4_cache_bytes(num_pages, page_size, Hk, d)
 
 
@@ -550,6 +553,8 @@ def _kv4_io(cache, k, v, starts, counts):
     if dev != cache.device or shape[0] != B or shape[1] != cache.Hk or shape[3] != cache.d:
         raise ValueError(f"k must be [{B}, {cache.Hk}, n, {cache.d}] on the cache's device, not {tuple(shape)}")
     vs = _heads("v", v, dtype, shape, dev)
+    if shape[2] > _INT_MAX:
+        raise ValueError(f"{shape[2]} tokens are more than a call takes")
     i32 = _torch.int32
     return (k.data_ptr(), v.data_ptr(), _STRIDES.pack(*ks), _STRIDES.pack(*vs),
             _flat("starts", starts, i32, (B,), dev), _flat("counts", counts, i32, (B,), dev), B, shape[2], code)
@@ -572,6 +577,8 @@ def nystrom_kv4_read(cache, k, v, starts=None, counts=None, stream=None):
 
 
 def nystrom_kv4_attn_workspace_bytes(cache, B, nq, Hq, max_length, dtype) -> int:
+    if max(B, nq, Hq, max_length) > _INT_MAX:
+        return 0  # like other sizes that a call refuses
     return load_library().nystrom_kv4_attn_workspace_bytes(cache.desc, B, nq, Hq, max_length, dtype)
 
 
@@ -582,13 +589,17 @@ def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, caus
     max_length: an upper bound of them; q_counts: int32 [B], real queries
     (None: nq); scale: None for 1/sqrt(d)."""
     lib = _lib or load_library()
-    if scale == 0:
-        raise ValueError("scale must not be zero (None: 1/sqrt(d))")
+    if scale is None:
+        scale = 0.0
+    elif ctypes.c_float(scale).value == 0.0:
+        raise ValueError("scale must not be zero in fp32 (None: 1/sqrt(d))")
     qs, dt, dev = _check_first("q", q)
     shape = q.shape
     B, Hq, nq, d = shape
     if B != cache.B or d != cache.d or dev != cache.device:
         raise ValueError("q must be [B, Hq, nq, d] with the cache's B and d, on its device")
+    if max(nq, Hq, max_length) > _INT_MAX or max_length < 0:
+        raise ValueError(f"sizes past 32 bits or below zero: {nq} queries, {Hq} heads, max_length {max_length}")
     os_ = _heads("out", out, q.dtype, shape, dev)
     i32 = _torch.int32
     need = lib.nystrom_kv4_attn_workspace_bytes(cache.desc, B, nq, Hq, max_length, dt)
@@ -596,7 +607,7 @@ def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, caus
     rc = lib.nystrom_kv4_attn_fwd(
         cache.desc, q.data_ptr(), out.data_ptr(), _STRIDES.pack(*qs), _STRIDES.pack(*os_),
         _flat("lengths", lengths, i32, (B,), dev), _flat("q_counts", q_counts, i32, (B,), dev), B, nq, Hq,
-        max_length, 1 if causal else 0, 0.0 if scale is None else scale, dt, ws, nbytes,
+        max_length, 1 if causal else 0, scale, dt, ws, nbytes,
         _raw_stream(stream, dev))
     del keep
     return rc if rc >= 0 else _check(rc, "nystrom_kv4_attn_fwd")

@@ -54,6 +54,7 @@ using SplitLine = Line<32, 16, 6, 4>;
 constexpr int kTile = SplitLine::TILE;
 constexpr float kRebase = 8.0f;  // move the running maximum when it grows by 2^8
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4]) {
@@ -923,7 +924,7 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
                          int max_length, int causal, float scale, int dtype, void* workspace,
                          size_t ws_bytes, nys_stream_t stream) {
   if (!q || !out || !q_strides || !out_strides || !lengths) return NYS_ERR_ARG;
-  if ((causal != 0 && causal != 1) || !std::isfinite(scale)) return NYS_ERR_ARG;
+  if ((causal != 0 && causal != 1) || !std::isfinite(scale * kLog2e)) return NYS_ERR_ARG;
   int rc = check_attn(cache, B, nq, Hq, max_length, dtype);
   if (rc != NYS_OK) return rc;
   if (!strides_ok(*q_strides) || !strides_ok(*out_strides) ||
@@ -962,7 +963,7 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   p.causal = causal;
   p.ctas = pl.ctas;
   p.whole = pl.whole ? 1 : 0;
-  p.scale_log2 = (scale == 0.f ? 1.f / std::sqrt((float)cache->d) : scale) * 1.4426950408889634f;
+  p.scale_log2 = (scale == 0.f ? 1.f / std::sqrt((float)cache->d) : scale) * kLog2e;
   if (pl.chunk) {
     rc = launch_kv4_chunk(p, cache->d, q, out, stream);
     if (rc != NYS_OK) return rc;

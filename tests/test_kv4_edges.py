@@ -95,3 +95,26 @@ def test_a_first_call_may_be_captured(which):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", FIRST, which], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+def test_sizes_and_scales_that_a_call_cannot_hold_are_refused():
+    """Not cut to 32 bits on their way, and a scale that vanishes in fp32 does
+    not turn into the default one."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    c = cache_of(1, 2, 64, 32, 2)
+    q, lens = torch.zeros(1, 4, 1, 64, device="cuda"), i32([40])
+    out = torch.full_like(q, 7.0)
+    for limit in (2 ** 32 + 40, 2 ** 31, -1, -2 ** 32 + 64):
+        with pytest.raises((ValueError, N.NystromError)):
+            N.nystrom_kv4_attn_fwd(c, q, out, lens, limit)
+    for scale in (0.0, 1e-50, -1e-60, float("nan"), float("inf"), 1e39, 3e38):
+        with pytest.raises((ValueError, N.NystromError)):
+            N.nystrom_kv4_attn_fwd(c, q, out, lens, 64, scale=scale)
+    many = torch.zeros(1, 2, 1, 64, device="cuda").expand(1, 2, 2 ** 32 + 3, 64)
+    with pytest.raises((ValueError, N.NystromError)):
+        N.nystrom_kv4_write(c, many, many)
+    torch.cuda.synchronize()
+    assert (out == 7.0).all() and N.nystrom_get_status() == N.NYS_OK
+    N.nystrom_kv4_attn_fwd(c, q, out, lens, 2 ** 31 - 1, scale=1e-30)
+    assert N.nystrom_get_status() == N.NYS_OK
