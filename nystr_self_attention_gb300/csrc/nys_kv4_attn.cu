@@ -134,9 +134,11 @@ constexpr int split_smem() {
 // times its scale is the sum of three bf16 terms.
 // The code is kept short (one copy of each step, masks as uniform branches):
 // a decoding step finds none of it in the instruction caches.
+// out may be q: an item's rows are read by its CTA before they are written, or,
+// where CTAs share it, by all of them before the join writes.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, kCtas<T, D, NT>)
-kv4_attn_split(const __grid_constant__ AttnParams p, const T* __restrict__ q, T* __restrict__ out) {
+kv4_attn_split(const __grid_constant__ AttnParams p, const T* q, T* out) {
   constexpr int G = D / 32, BB = block_bytes(D);
   constexpr bool EXACT = sizeof(T) == 4;
   constexpr int ENTRIES = kTable<T, NT>;

@@ -468,20 +468,24 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
       // units of a score, less the keys' power of two
       float rf = fabsf(p.scale_log2) * __uint_as_float((uint32_t)(127 + max(e - 13, -100)) << 23);
       rf = !finite ? NAN : rf * 0x1p-12f * (tiny ? 0x1p-80f : 1.f);
-#pragma unroll 8
-      for (int k = 0; k < D / 8; ++k) {
-        const uint4 x = live ? src[k] : make_uint4(0u, 0u, 0u, 0u);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        float v[8];
+#pragma unroll 1
+      for (int k0 = 0; k0 < D / 8; k0 += 8) {
+        uint4 x[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[2 * j] = finite ? __uint_as_float(w[j] << 16) * pre * up : 0.f;
-          v[2 * j + 1] = finite ? __uint_as_float(w[j] & 0xffff0000u) * pre * up : 0.f;
+        for (int j = 0; j < 8; ++j) x[j] = live ? src[k0 + j] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {  // k0 + c: group k / 4, quarter k % 4
+          const uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          float v[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            v[2 * j] = finite ? __uint_as_float(w[j] << 16) * pre * up : 0.f;
+            v[2 * j + 1] = finite ? __uint_as_float(w[j] & 0xffff0000u) * pre * up : 0.f;
+          }
+          *reinterpret_cast<uint4*>(qs + (k0 >> 3) * 16384 + lr * 128 + ((c ^ (lr & 7)) << 4)) =
+              make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]),
+                         pack_half2(v[3], v[7]));
         }
-        const uint32_t chunk = (uint32_t)(k & 7) ^ (lr & 7u);  // k: group k / 4, quarter k % 4
-        *reinterpret_cast<uint4*>(qs + (k >> 3) * 16384 + lr * 128 + (chunk << 4)) =
-            make_uint4(pack_half2(v[0], v[4]), pack_half2(v[1], v[5]), pack_half2(v[2], v[6]),
-                       pack_half2(v[3], v[7]));
       }
       fence_async_smem();
       tc_fence_before_sync();  // the previous segment's output has been read
@@ -683,10 +687,11 @@ __device__ __forceinline__ void softmax_rows(const AttnParams& p, Shared& sh, ui
   }
 }
 
+// out may be q: a row is read by its thread before it is written, or, where CTAs
+// share the item, by all of them before the join writes.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* __restrict__ q,
-               __nv_bfloat16* __restrict__ out) {
+kv4_attn_chunk(const __grid_constant__ AttnParams p, const __nv_bfloat16* q, __nv_bfloat16* out) {
   constexpr uint32_t TILE = tile_bytes<D>();
   extern __shared__ uint8_t smem_raw[];
   __shared__ Shared sh;

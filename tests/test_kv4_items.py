@@ -136,3 +136,24 @@ def test_items_of_one_and_two_groups_in_one_range(name, causal):
         outs.append(out)
     compare(outs[0], q, k, v, lens, counts, causal, name=name)
     assert torch.equal(outs[0], outs[1]), "two runs differ"
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["tails_of_88_rows", "mixed_counts"])
+@pytest.mark.parametrize("few", [False, True])
+def test_result_over_the_queries_of_many_items(name, few):
+    """out may be q where CTAs go from item to item; `few`: the kernel for calls
+    of few query rows as well."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    B, Hq, Hk, d, page, nq, lens, counts = CASES[name]
+    if few:
+        nq, counts = 5, [min(c, 5) for c in counts]
+    cache, _, _, g = filled(B, Hk, d, page, lens, seed=4)
+    q = torch.randn(B, nq, Hq, d, generator=g, device="cuda").to(torch.bfloat16).transpose(1, 2)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    apart = q.clone()
+    N.nystrom_kv4_attn_fwd(cache, q, apart, i32(lens), max(lens), i32(counts))
+    N.nystrom_kv4_attn_fwd(cache, q, q, i32(lens), max(lens), i32(counts))
+    assert N.nystrom_get_status() == N.NYS_OK
+    assert torch.equal(apart, q)
