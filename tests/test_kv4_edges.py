@@ -118,3 +118,43 @@ def test_sizes_and_scales_that_a_call_cannot_hold_are_refused():
     assert (out == 7.0).all() and N.nystrom_get_status() == N.NYS_OK
     N.nystrom_kv4_attn_fwd(c, q, out, lens, 2 ** 31 - 1, scale=1e-30)
     assert N.nystrom_get_status() == N.NYS_OK
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_offsets_past_32_bits(nq):
+    """Pages beyond 4 GiB of a pool and rows 2^31 elements and more apart: the
+    bits of the same call in compact memory."""
+    import numpy as np
+    import torch
+    import nystr_self_attention_gb300 as N
+    B, Hk, Hq, d, n, page = 3, 2, 4, 128, 200, 16
+    per = -(-n // page)
+    page_bytes = N.nystrom_kv4_cache_bytes(1, page, Hk, d)
+    pages = (5 << 30) // page_bytes
+    data = torch.empty(pages * page_bytes, dtype=torch.uint8, device="cuda")
+    far = N.NystromKv4Cache(data, (pages - 1 - 7 * torch.arange(B * per, device="cuda")).to(torch.int32).view(B, per),
+                            page, Hk, d)
+    near = cache_of(B, Hk, d, page, per)
+    apart = 2 ** 31 + 128  # elements between sequences
+    room = torch.empty(2 * apart + (1 << 22), dtype=torch.bfloat16, device="cuda")
+    at = 0
+
+    def wide(H, rows):
+        nonlocal at
+        t = room.as_strided((B, H, rows, d), (apart, rows * d, d, 1), at)
+        at += H * rows * d
+        return t.normal_()
+
+    k, v, q, out = wide(Hk, n), wide(Hk, n), wide(Hq, nq), wide(Hq, nq)
+    ck, cv, cq, cout = (t.contiguous() for t in (k, v, q, out))
+    inv = 10000.0 ** (-np.arange(64) / 64)
+    starts, lens = i32([0] * B), i32([n, n - 7, n - 100])
+    for cache, (a, b, x, y) in ((far, (k, v, q, out)), (near, (ck, cv, cq, cout))):
+        N.nystrom_qk_norm_rope_fwd(a, b, a, b, None, inv)
+        N.nystrom_kv4_write(cache, a, b, starts)
+        N.nystrom_kv4_attn_fwd(cache, x, y, lens, n)
+        N.nystrom_kv4_read(cache, a, b, i32([3, 0, 1]), i32([n - 3, n, n - 1]))
+        N.nystrom_qk_norm_rope_bwd(x, None, y, None, y, None, None, inv)
+    assert N.nystrom_get_status() == N.NYS_OK
+    for x, y in ((k, ck), (v, cv), (q, cq), (out, cout)):
+        assert torch.equal(x, y)
