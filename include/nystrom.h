@@ -324,7 +324,10 @@ int nystrom_plan_describe(int B, int H, int n, int d, int m, int iters,
  * three, so [B][H][n][d] (the layout of the forward pass) and [B][n][H][d]
  * (a projection's output, or a slice of a packed one) are both read and
  * written in place. Row addresses are 16-byte aligned (else NYS_ERR_ALIGN),
- * strides are not negative, and rows of an output do not overlap.
+ * strides are not negative, and rows of an output do not overlap one another or
+ * another output's. Where an output may be an input, it has the same address and
+ * strides; the same address with other strides, or of two outputs, is refused
+ * (NYS_ERR_ARG).
  */
 typedef struct { long long batch, head, token; } nys_strides_t;
 
@@ -361,8 +364,8 @@ typedef struct { long long batch, head, token; } nys_strides_t;
  *   dx = (w g - h mean(w g h)) / sqrt(mean(x^2) + eps),  dw = sum of g h
  * over all rows (norm = 0: dx = g). dq, dk in `dtype`, strides p->dq, p->dk;
  * dq may be gq and dk may be gk (same strides). dq_weight, dk_weight: device
- * float [d], overwritten; NULL if not wanted. The sums are fp32 in a fixed
- * order: the same call gives the same bits.
+ * float [d], overwritten, two arrays; NULL if not wanted. The sums are fp32 in a
+ * fixed order: the same call gives the same bits.
  * workspace: device, 256-byte aligned, ws_bytes >=
  * nystrom_qk_norm_rope_workspace_bytes(p); needed only when a weight gradient
  * is asked for. NULL uses the library's cached workspace, which a stream
@@ -458,9 +461,9 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * nystrom_kv4_attn_fwd - attention of nq new queries of each sequence over its
  * cached keys and values:
  *   out = softmax(q K^T * scale) V
- * q, out [B, Hq, nq, d] in `dtype`, any strides (out may be q); query head h
- * reads cache head h / (Hq/Hk). lengths: device int32 [B], the tokens of each sequence in the
- * cache (the new ones included). q_counts: device int32 [B], the real queries
+ * q, out [B, Hq, nq, d] in `dtype`, any strides (out may be q, with the same
+ * ones); query head h reads cache head h / (Hq/Hk). lengths: device int32 [B],
+ * the tokens of each sequence in the cache (the new ones included). q_counts: device int32 [B], the real queries
  * of each sequence (NULL: nq); rows of out behind them are left as they were.
  * causal = 1: query i of c sees keys 0 .. length - c + i; causal = 0: all
  * `length` keys. A query that sees no key gives zeros. max_length: an upper

@@ -95,6 +95,13 @@ int check_device(int* dev_out);  // current device, must be compute capability 1
 // Makes `ws` the workspace nystrom_get_status reads for this device and
 // clears its status word on `stream` (unless told not to).
 int begin_call(char* ws, const Layout& L, cudaStream_t stream, int dev, bool clear_status = true);
+// Whether an output at the address of an input has its rows in the same places
+// (an axis with one entry has no stride); at another address, true.
+inline bool apart_or_same_rows(const void* out, const nys_strides_t& os, const void* in,
+                               const nys_strides_t& is, int B, int H, int n) {
+  return out != in || ((B == 1 || os.batch == is.batch) && (H == 1 || os.head == is.head) &&
+                       (n == 1 || os.token == is.token));
+}
 // The library's cached workspace of this device, grown to `bytes` (NULL and
 // *rc < 0 on failure).
 void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc);

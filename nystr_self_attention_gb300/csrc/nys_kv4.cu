@@ -461,6 +461,7 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v, const nys_s
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
+  if (k == v) return NYS_ERR_ARG;
   IoParams p{};
   rc = io_params(*cache, *k_strides, *v_strides, starts, counts, B, n, dev, &p);
   if (rc != NYS_OK) return rc;

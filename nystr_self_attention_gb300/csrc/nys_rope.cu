@@ -723,6 +723,10 @@ int nystrom_qk_norm_rope_fwd(const nys_qk_rope_t* a, const void* q, const void* 
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
+  if (!apart_or_same_rows(q_out, a->q_out, q, a->q, a->B, a->Hq, a->n)) return NYS_ERR_ARG;
+  if (a->Hk > 0 && (!apart_or_same_rows(k_out, a->k_out, k, a->k, a->B, a->Hk, a->n) || q_out == k_out ||
+                    q_out == k || k_out == q))
+    return NYS_ERR_ARG;
   const Grid g = grid_of(*a, false);
   const RopeParams p = params_of(*a, q_weight, k_weight, positions, inv_freq_host, g.heads_per_chunk);
   return dispatch(*a, [&](auto type, auto lp, auto mode) {
@@ -775,6 +779,11 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* a, const void* q, const void* 
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
+  if (!apart_or_same_rows(dq, a->dq, gq, a->q_out, a->B, a->Hq, a->n)) return NYS_ERR_ARG;
+  if (a->Hk > 0 && (!apart_or_same_rows(dk, a->dk, gk, a->k_out, a->B, a->Hk, a->n) || dq == dk || dq == gk ||
+                    dk == gq))
+    return NYS_ERR_ARG;
+  if (dq_weight && dq_weight == dk_weight) return NYS_ERR_ARG;
   std::unique_lock<std::mutex> held;
   if (sums && !workspace) {
     rc = operator_workspace(dev, need, stream, &workspace, &held);
