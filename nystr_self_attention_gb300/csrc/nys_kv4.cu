@@ -11,7 +11,7 @@
 // never read and rewritten, so its other tokens are not touched.
 //
 // Written and read back, 2 x 32765 tokens x 16 heads, d = 128, bf16 (1.2 GB):
-// 196 us, 6.1 TB/s where a copy reaches 6.8. Short calls are one wave of CTAs and
+// 180 to 205 us on several cards, 5.9 to 6.7 TB/s where a copy reaches 6.8. Short calls are one wave of CTAs and
 // bound by its chain of loads: 8 x 1021 tokens x 8 heads, d = 64, fp32: 21 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -27,9 +27,10 @@
 //
 // One token over 8 ragged sequences of up to 32768, 32 + 8 heads, d = 128 (203
 // MB): 61 us a call, 52 of them here, 3.3 TB/s; four times as long 190 us (4.3
-// TB/s). What bounds it is the unpacking: per 16 keys and head about 310
-// instructions of a warp, 120 of them on the integer pipe (42 % busy, HBM 48 %);
-// short calls: the launch, the queries and the join.
+// TB/s). No unit is full (issue 51 %, HBM 48 %, integer pipe 42 %): 16 warps per
+// SM, as many as the registers allow, wait for the results of about 310
+// instructions per 16 keys and head, most of them unpacking; short calls: the
+// launch, the queries and the join.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -801,9 +802,9 @@ kv4_attn_join(const __grid_constant__ AttnParams p, T* __restrict__ out, int par
 
 // bf16 calls with more query rows per cache head than this go to the tensor
 // core kernel (d = 32 stays: its rows are half a swizzled operand row). 8 ragged
-// sequences of up to 4096 / 32768 keys, 8 cache heads, d = 128, here against
-// there (us): 32 rows 33 / 140 against 37 / 192, 64 rows 51 / 262 against 38 /
-// 193, 128 rows of 4096 keys 85 against 41.
+// sequences of up to 4096 / 32768 keys, 8 cache heads, d = 128, a call here
+// against there (us): 32 rows 37 / 145 against 41 / 201, 48 rows 46 / 207 against
+// 41 / 201, 64 rows 54 / 268 against 41 / 203, 128 rows 89 / 510 against 46 / 207.
 constexpr int kChunkRows = 48;
 
 // Contexts of up to kWholeTiles tiles (in a batch of kWholeItems items or more,

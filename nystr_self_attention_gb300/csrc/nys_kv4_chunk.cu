@@ -29,9 +29,9 @@
 // of the 4-bit fields: the queries' channels are permuted to match, and the
 // output's columns are put right when they are written.
 //
-// 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 172 us
-// here, 185 with the join, 680 TFLOP/s (over 16384 tokens 318 here, 790). Tensor
-// cores 34 % busy, HBM 1 %. Clock stamps: a tile of a group is a chain of 5900
+// 1000 queries x 16 + 4 heads over 8192 tokens of 2 sequences, d = 128: 174 us
+// here, 187 with the join, 672 TFLOP/s (over 16384 tokens 322 here, 335, 775).
+// Tensor cores 33 % busy, HBM 1 %. Clock stamps: a tile of a group is a chain of 5900
 // cycles - softmax 2600 (about 900 instructions of a warp), the products 1700
 // (100 per issued instruction, the pipe's own time is 68), their handshakes and
 // the last one's end 1300 -, of which the other group's softmax and products

@@ -19,8 +19,8 @@
 // Forward, 2 x 32768 tokens, 16 + 16 heads, d = 128, bf16 (1.07 GB): 165 us, 6.5
 // TB/s where a copy reaches 6.8; fp32 pairs over three axes, 8 x 8190 tokens, 8 +
 // 8 heads, d = 64 (537 MB): 88 us, 6.1 TB/s. Backward, 8 x 8192 tokens, 8 + 8
-// heads, d = 64, bf16 (403 MB): 77 us with the weights' sums, 5.2 TB/s; with 128
-// registers a thread only 16 warps fit an SM, and between loads and stores they
+// heads, d = 64, bf16 (403 MB): 77 us with the weights' sums, 5.2 TB/s (fp32, 805
+// MB: 122 us, 6.6 TB/s); with 128 registers a thread only 16 warps fit an SM, and between loads and stores they
 // issue 2.4 instructions a cycle: latency and issue bound it together.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
