@@ -488,8 +488,10 @@ int nystrom_kv4_read(const nys_kv4_cache_t* cache, void* k, void* v,
  * have (32 keys x 16 query rows per cache head; more than 48 rows in bf16: 128 x
  * 256) below 2^31 (else NYS_ERR_SHAPE); scale * log2(e) finite (else NYS_ERR_ARG).
  * Magnitudes: in calls of few rows probabilities are kept up to 2^8 above 1, so
- * cached values beyond 2^100 may give infinities; in those of more rows scales
- * below 2^-97 lose bits.
+ * cached values beyond 2^100 may give infinities, as may bf16 queries that times
+ * the scale go beyond 2^114. In calls of more rows scales below 2^-97 lose bits,
+ * and value scales of 2^58 and more have no common measure with those of 32
+ * tokens that are all below 2^-68 (or zero).
  * workspace: device, 256-byte aligned, ws_bytes >=
  * nystrom_kv4_attn_workspace_bytes(...) (which may be 0), not shared with a
  * call that may run at the same time. NULL uses the library's cached

@@ -158,3 +158,65 @@ def test_offsets_past_32_bits(nq):
     assert N.nystrom_get_status() == N.NYS_OK
     for x, y in ((k, ck), (v, cv), (q, cq), (out, cout)):
         assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("nq", [1, 60])
+def test_a_query_with_nan_or_infinity_spoils_its_own_row_alone(nq, dtype):
+    import torch
+    import nystr_self_attention_gb300 as N
+    B, Hk, Hq, d, n = 2, 2, 4, 128, 3000
+    c = cache_of(B, Hk, d, 64, 47)
+    t = torch.bfloat16 if dtype == "bf16" else torch.float32
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k, v = (torch.randn(B, Hk, n, d, generator=g, device="cuda").to(t) for _ in range(2))
+    N.nystrom_kv4_write(c, k, v)
+    q = torch.randn(B, Hq, nq, d, generator=g, device="cuda").to(t)
+    lens = i32([n, nq // 2])  # the second sequence's first queries see nothing
+    want, out = torch.empty_like(q), torch.empty_like(q)
+    N.nystrom_kv4_attn_fwd(c, q, want, lens, n)
+    bad = torch.zeros(B, Hq, nq, dtype=torch.bool, device="cuda")
+    for h, i, x in ((0, 0, float("nan")), (1, nq // 2, float("inf")), (3, nq - 1, -float("inf"))):
+        q[:, h, i, 5 * h] = x
+        bad[:, h, i] = True
+    N.nystrom_kv4_attn_fwd(c, q, out, lens, n)
+    assert N.nystrom_get_status() == N.NYS_OK
+    sees = torch.arange(nq, device="cuda")[None] >= (nq - lens[:, None])  # [B, nq]
+    sees = sees[:, None].expand(B, Hq, nq)
+    assert torch.isnan(out[bad & sees]).all() and (out[~sees] == 0).all()
+    assert torch.equal(out[~bad], want[~bad]) and torch.isfinite(want).all()
+
+
+@pytest.mark.parametrize("nq", [1, 60])
+def test_two_graphs_replayed_side_by_side(nq):
+    """Captured one after the other, replayed at once on two streams: each has
+    a workspace of its own."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    B, Hk, Hq, d, n = 3, 2, 8, 128, 3000
+    runs = []
+    for seed in range(2):
+        c = cache_of(B, Hk, d, 64, 47)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        k, v = (torch.randn(B, Hk, n, d, generator=g, device="cuda") for _ in range(2))
+        N.nystrom_kv4_write(c, k, v)
+        q = torch.randn(B, Hq, nq, d, generator=g, device="cuda").to(torch.bfloat16)
+        out, lens = torch.empty_like(q), i32([n, n - 700 * (seed + 1), 5])
+        N.nystrom_kv4_attn_fwd(c, q, out, lens, n)
+        want = out.clone()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for _ in range(4):
+                N.nystrom_kv4_attn_fwd(c, q, out, lens, n)
+        runs.append((graph, torch.cuda.Stream(), out, want, (c, q, lens)))
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for _, _, out, _, _ in runs:
+            out.fill_(9.0)
+        torch.cuda.synchronize()
+        for graph, stream, _, _, _ in runs:
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(out, want) for _, _, out, want, _ in runs)
+    assert N.nystrom_get_status() == N.NYS_OK
