@@ -152,3 +152,30 @@ def test_a_dominant_key_and_a_long_even_tail(nq, own, bits, tail):
     q = torch.randn(1, 1, nq, d, generator=g, device="cuda")
     q[..., :32] = bits * np.log(2.0) * d ** 0.5 / 32
     attend(q.to(torch.bfloat16), cache, x.double(), y.double(), n, causal=False, name=f"2^-{bits}")
+
+
+@pytest.mark.parametrize("n", [2, 3, 12, 30, 500])
+@pytest.mark.parametrize("nq", [20, 100])
+def test_weights_far_below_the_largest(nq, n):
+    """Scores tens apart: where the heaviest key's code is zero, a channel is the
+    sum of keys of far smaller weight. With more than 48 rows a weight times the
+    largest scale s of its 32 tokens is off by at most 2^-36 of the row's largest
+    such product x <= s, and an element is at most 8 s: n 2^-36 8 s beside the
+    bound, s at most twice (a power of two is kept) the largest |v| / 7."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    B, H, d = 4, 4, 128
+    cache, k, v, g = filled(B, H, d, 64, [n] * B, seed=n)
+    q = torch.randn(B, H, nq, d, generator=g, device="cuda").to(torch.bfloat16)
+    out, lens = torch.empty_like(q), torch.full((B,), n, dtype=torch.int32, device="cuda")
+    N.nystrom_kv4_attn_fwd(cache, q, out, lens, n, None, False, 0.3)
+    assert N.nystrom_get_status() == N.NYS_OK
+    scale, x = float(np.float32(0.3)), q.double()
+    s, reach = x @ k.transpose(2, 3) * scale, x.abs() @ k.abs().transpose(2, 3) * scale
+    p = torch.softmax(s, -1)
+    want, A = p @ v, p @ v.abs()
+    tol = A * U * (160 * reach.amax(-1, keepdim=True) + 160) * (1 + HB) + (A + want.abs()) * HB * (1 + 2 * HB)
+    if nq > 48:
+        tol += n * 2.0 ** -36 * 8 * 2 * v.abs().max() / 7
+    err = (out.double() - want).abs()
+    assert (err <= tol).all(), f"{(err / tol.clamp(min=1e-300)).max():.2f} of the bound"
