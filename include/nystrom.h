@@ -510,6 +510,153 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
                          size_t ws_bytes, nys_stream_t stream);
 
 /*
+ * Around the attention module in a Transformer layer: the residual's addition
+ * with the norm that follows it, projections in 8 bits, the gated feed-forward
+ * product. These operators take matrices: rows are tokens (or a weight's output
+ * channels), each a run of contiguous elements, `stride` elements apart, so a
+ * slice of a wider matrix is read and written in place. Addresses are 16-byte
+ * aligned and strides multiples of 16 bytes (else NYS_ERR_ALIGN); rows of an
+ * output do not overlap (a stride below the row's length, with more than one
+ * row, is NYS_ERR_ARG). Outputs overlap neither one another nor an input,
+ * except where an operator says so; one at the very address of another, or of
+ * an input it may not be, is refused (NYS_ERR_ARG).
+ */
+
+/*
+ * A matrix in 8 bits: `rows` rows of K e4m3 codes (4 exponent bits, 3 of
+ * mantissa, largest 448), and for each row and block of 128 consecutive channels
+ * (the last one of a row may be shorter) one scale, a power of two 2^(byte - 127)
+ * (byte 255: NaN). The matrix stands for code * scale. scales: device, 32-bit
+ * words [ceil(K/512)][rows], contiguous; byte j (from the low end) of word g of a
+ * row is the scale of its block 4 g + j (0 behind the last block).
+ * With a the largest magnitude of a block, its scale is the smallest power of two
+ * with a <= 448 * scale, at least 2^-127 (a block of zeros), and a code is the
+ * value over the scale, rounded to nearest, ties to even: nothing saturates, and
+ * a value is off by at most 2^-4 of itself, or by 2^-10 * scale below 2^-6 * scale.
+ * A block that holds an infinity or a NaN gets scale 255 and reads back as NaN.
+ * Shape rules (else NYS_ERR_SHAPE): rows, K >= 1, K % 16 == 0, K <= 2^20,
+ * rows < 2^31 - 2^10.
+ */
+typedef struct {
+  void* codes;  /* device, 16-byte aligned */
+  void* scales; /* device, 16-byte aligned, nystrom_q8_scales_bytes(rows, K) bytes */
+  int rows, K;
+  long long stride; /* bytes between rows of codes, a multiple of 16 */
+} nys_q8_t;
+size_t nystrom_q8_scales_bytes(int rows, int K);
+
+/*
+ * nystrom_q8_write - quantises x, [rows][K] in `dtype`, element (r, k) at
+ * x[r row_stride + k channel_stride]; one of the two strides is 1 (a weight kept
+ * as [K][rows], the order of nystrom_mha_fwd, is read as it lies), the other a
+ * multiple of 16 bytes. Where row_stride is 1 and channel_stride is not, rows
+ * must be a multiple of 8 (else NYS_ERR_SHAPE). block_rows: 1, or 128: the rows
+ * 128 i .. 128 i + 127 share one scale per block of channels (weights).
+ * nystrom_q8_read - the reverse: code * scale, rounded to `dtype`, to
+ * out[r stride + k].
+ */
+int nystrom_q8_write(const nys_q8_t* q, const void* x, long long row_stride,
+                     long long channel_stride, int block_rows, int dtype, nys_stream_t stream);
+int nystrom_q8_read(const nys_q8_t* q, void* out, long long stride, int dtype,
+                    nys_stream_t stream);
+
+/*
+ * nystrom_q8_matmul - out[t][n] = sum over k of A[t][k] W[n][k], the values that
+ * the two 8-bit matrices stand for: a [T][K], w [N][K], out [T][N] in `dtype`
+ * (row stride out_stride). Products are exact and summed in fp32 by the matrix
+ * units, which apply the scales; one rounding to dtype. a's K and w's are equal
+ * (else NYS_ERR_SHAPE); N a multiple of 8.
+ * workspace: device, 256-byte aligned, ws_bytes >= nystrom_q8_matmul_workspace_bytes
+ * (which may be 0), not shared with a call that may run at the same time. NULL
+ * uses the library's cached workspace, which a stream under capture may not do
+ * (NYS_ERR_ARG) where one is needed.
+ */
+size_t nystrom_q8_matmul_workspace_bytes(int T, int N, int K, int dtype);
+int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long out_stride,
+                      int dtype, void* workspace, size_t ws_bytes, nys_stream_t stream);
+
+/*
+ * nystrom_add_rms_norm_fwd - the residual's addition and the norm of the sum:
+ *   s = x + residual, rounded to dtype (residual NULL: s = x, sum NULL)
+ *   y = weight * s / sqrt(mean(s^2) + eps)
+ * x, residual, sum, y: [rows][d] in `dtype`, row strides p->x, p->residual,
+ * p->sum, p->y. weight: device float [d], or NULL for all ones. sum and y may each
+ * be x or residual (same address and stride). In place of y, y8: an 8-bit
+ * matrix of rows x d (see nys_q8_t), quantised from y in fp32; exactly one of y
+ * and y8 is given. sum may be NULL with a residual too: s is then not kept.
+ * Shape rules (else NYS_ERR_SHAPE): rows >= 1, d % 8 == 0 (16 with y8),
+ * 8 <= d <= 16384. NYS_ERR_ARG for a negative or non-finite eps.
+ *
+ * nystrom_add_rms_norm_bwd - its gradients: from s (stride p->sum), the gradient
+ * gy of y (stride p->y) and gs of s from elsewhere (stride p->gs; NULL: none),
+ * with r = 1 / sqrt(mean(s^2) + eps), h = r s:
+ *   dx = gs + r (weight gy - h mean(weight gy h)),   dweight = sum over rows of gy h
+ * dx [rows][d] in `dtype`, stride p->dx, is the gradient of x and of the residual
+ * alike; it may be gy or gs (same address and stride). dweight: device float
+ * [d], or NULL. Sums are fp32 in a fixed order: the same call gives the same
+ * bits. workspace: as above, nystrom_add_rms_norm_workspace_bytes(p), needed for
+ * dweight only.
+ */
+typedef struct {
+  int rows, d, dtype;
+  float eps;
+  long long x, residual, sum, y; /* row strides in elements */
+  long long gs, dx;              /* backward only */
+} nys_add_rms_norm_t;
+int nystrom_add_rms_norm_fwd(const nys_add_rms_norm_t* p, const void* x, const void* residual,
+                             const float* weight, void* sum, void* y, const nys_q8_t* y8,
+                             nys_stream_t stream);
+size_t nystrom_add_rms_norm_workspace_bytes(const nys_add_rms_norm_t* p);
+int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const void* gy,
+                             const void* gs, const float* weight, void* dx, float* dweight,
+                             void* workspace, size_t ws_bytes, nys_stream_t stream);
+
+/*
+ * nystrom_gated_ff_fwd - both projections of a gated feed-forward block, the
+ * activation and the product:
+ *   g = x W_gate, u = x W_up, h = act(g) * u
+ * x [T][d], h [T][f] in `dtype`, row strides p->x, p->h; weights in `dtype`:
+ * NYS_FF_IN_OUT: [d][f], NYS_FF_OUT_IN: [f][d], row stride p->w, both alike.
+ * gate, up: [T][f], row strides p->gate, p->up, receive g and u for the
+ * backward pass; both or neither (NULL).
+ * act: NYS_ACT_SILU g / (1 + e^-g); NYS_ACT_GELU g (1 + erf(g / sqrt 2)) / 2;
+ * NYS_ACT_GELU_TANH g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2;
+ * NYS_ACT_RELU max(g, 0).
+ *
+ * nystrom_gated_ff_bwd - its gradients, from x, the weights, the kept g and u,
+ * and the gradient gh of h (stride p->h):
+ *   dg = gh u act'(g), du = gh act(g)     (rounded to dtype; act'(0) = 0 for RELU)
+ *   dx = dg W_gate^T + du W_up^T, dW_gate = x^T dg, dW_up = x^T du
+ * dx: stride p->dx, NULL if not wanted; dw_gate, dw_up: the weights' layout, row
+ * stride p->dw, both or neither NULL.
+ *
+ * Sums are fp32 in the matrix units, in a fixed order; one rounding to dtype.
+ * NYS_FP32 operands enter the products as sums of three bfloat16 terms (24 bits;
+ * six of the nine products, all that matter at 2^-24), so an infinity gives NaN
+ * where a finite sum could not, values beyond 3.38e38 are infinite, and bits
+ * below 2^-133 are lost.
+ * Shape rules (else NYS_ERR_SHAPE): T, d, f >= 1, d % 8 == f % 8 == 0, d, f <= 2^20,
+ * T <= 2^30.
+ * workspace: as above (back: 0 forward, 1 backward).
+ */
+typedef enum { NYS_ACT_SILU = 0, NYS_ACT_GELU = 1, NYS_ACT_GELU_TANH = 2, NYS_ACT_RELU = 3 } nys_act_t;
+typedef enum { NYS_FF_IN_OUT = 0, NYS_FF_OUT_IN = 1 } nys_ff_layout_t;
+typedef struct {
+  int T, d, f;
+  int act, layout, dtype;
+  long long x, w, h, gate, up; /* row strides in elements */
+  long long dx, dw;            /* backward only */
+} nys_gated_ff_t;
+size_t nystrom_gated_ff_workspace_bytes(const nys_gated_ff_t* p, int back);
+int nystrom_gated_ff_fwd(const nys_gated_ff_t* p, const void* x, const void* w_gate,
+                         const void* w_up, void* h, void* gate, void* up, void* workspace,
+                         size_t ws_bytes, nys_stream_t stream);
+int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_gate,
+                         const void* w_up, const void* gate, const void* up, const void* gh,
+                         void* dx, void* dw_gate, void* dw_up, void* workspace, size_t ws_bytes,
+                         nys_stream_t stream);
+
+/*
  * nystrom_get_status - waits for `stream`, then returns and clears the
  * device-side status word of the most recent call on the current device
  * (NYS_OK, or NYS_ERR_TIMEOUT if a bounded wait inside a kernel ran out),

@@ -17,4 +17,9 @@ from ._binding import (  # noqa: F401
     NystromKv4Cache, nystrom_kv4_attn_fwd, nystrom_kv4_attn_workspace_bytes, nystrom_kv4_cache_bytes,
     nystrom_kv4_read, nystrom_kv4_write, nystrom_qk_norm_rope_bwd, nystrom_qk_norm_rope_fwd,
     nystrom_qk_norm_rope_workspace_bytes,
+    NYS_ACT_GELU, NYS_ACT_GELU_TANH, NYS_ACT_RELU, NYS_ACT_SILU, NYS_FF_IN_OUT, NYS_FF_OUT_IN,
+    NysAddRmsNorm, NysGatedFf, NysQ8, NystromQ8, nystrom_add_rms_norm_bwd, nystrom_add_rms_norm_fwd,
+    nystrom_add_rms_norm_workspace_bytes, nystrom_gated_ff_bwd, nystrom_gated_ff_fwd,
+    nystrom_gated_ff_workspace_bytes, nystrom_q8_matmul, nystrom_q8_matmul_workspace_bytes, nystrom_q8_read,
+    nystrom_q8_scales_bytes, nystrom_q8_write,
 )

@@ -16,6 +16,8 @@ NYS_ERR_INDEX = -8
 NYS_ROPE_HALVES, NYS_ROPE_PAIRS = 0, 1
 NYS_STAGE_Q_TILDE, NYS_STAGE_K_TILDE, NYS_STAGE_G, NYS_STAGE_A_S, NYS_STAGE_W, NYS_STAGE_Z = range(6)
 NYS_CONV_PER_HEAD, NYS_CONV_PER_CHANNEL = 0, 1
+NYS_ACT_SILU, NYS_ACT_GELU, NYS_ACT_GELU_TANH, NYS_ACT_RELU = range(4)
+NYS_FF_IN_OUT, NYS_FF_OUT_IN = 0, 1
 NYS_CSTAGE_ASSIGN, NYS_CSTAGE_CENTROIDS_PREV, NYS_CSTAGE_CENTROIDS, NYS_CSTAGE_G = range(4)
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libnystrom.so")
@@ -42,6 +44,23 @@ class NysKv4Cache(ctypes.Structure):
     """nys_kv4_cache_t."""
     _fields_ = [("data", _P), ("block_table", _P), ("num_pages", _I), ("max_pages", _I),
                 ("page_size", _I), ("Hk", _I), ("d", _I)]
+
+
+class NysQ8(ctypes.Structure):
+    """nys_q8_t."""
+    _fields_ = [("codes", _P), ("scales", _P), ("rows", _I), ("K", _I), ("stride", ctypes.c_longlong)]
+
+
+class NysAddRmsNorm(ctypes.Structure):
+    """nys_add_rms_norm_t."""
+    _fields_ = [("rows", _I), ("d", _I), ("dtype", _I), ("eps", ctypes.c_float)] + [
+        (n, ctypes.c_longlong) for n in ("x", "residual", "sum", "y", "gs", "dx")]
+
+
+class NysGatedFf(ctypes.Structure):
+    """nys_gated_ff_t."""
+    _fields_ = [(n, _I) for n in ("T", "d", "f", "act", "layout", "dtype")] + [
+        (n, ctypes.c_longlong) for n in ("x", "w", "h", "gate", "up", "dx", "dw")]
 
 
 _SIG = {
@@ -80,6 +99,17 @@ _SIG = {
                                   _P, ctypes.c_size_t, _P]),
     "nystrom_profile_read": (_I, [_I, ctypes.c_char_p, _I, ctypes.POINTER(ctypes.c_double),
                                   ctypes.POINTER(ctypes.c_longlong)]),
+    "nystrom_q8_scales_bytes": (ctypes.c_size_t, [_I, _I]),
+    "nystrom_q8_write": (_I, [_P, _P, ctypes.c_longlong, ctypes.c_longlong, _I, _I, _P]),
+    "nystrom_q8_read": (_I, [_P, _P, ctypes.c_longlong, _I, _P]),
+    "nystrom_q8_matmul_workspace_bytes": (ctypes.c_size_t, [_I, _I, _I, _I]),
+    "nystrom_q8_matmul": (_I, [_P, _P, _P, ctypes.c_longlong, _I, _P, ctypes.c_size_t, _P]),
+    "nystrom_add_rms_norm_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P]),
+    "nystrom_add_rms_norm_workspace_bytes": (ctypes.c_size_t, [_P]),
+    "nystrom_add_rms_norm_bwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "nystrom_gated_ff_workspace_bytes": (ctypes.c_size_t, [_P, _I]),
+    "nystrom_gated_ff_fwd": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P]),
+    "nystrom_gated_ff_bwd": (_I, [_P] * 11 + [ctypes.c_size_t, _P]),
 }
 
 
@@ -611,3 +641,282 @@ def nystrom_kv4_attn_fwd(cache, q, out, lengths, max_length, q_counts=None, caus
         _raw_stream(stream, dev))
     del keep
     return rc if rc >= 0 else _check(rc, "nystrom_kv4_attn_fwd")
+
+
+# ---------------------------------------------- around the attention module
+#
+# These take matrices: torch tensors [rows, width] whose rows are contiguous
+# runs any distance apart (a [B, n, D] tensor: its view(-1, D)).
+
+_Q8_DESC = struct.Struct("=QQiiq")      # nys_q8_t
+_NORM_DESC = struct.Struct("=3if6q")    # nys_add_rms_norm_t
+_FF_DESC = struct.Struct("=6i7q")       # nys_gated_ff_t
+
+
+def _first_matrix(name, t):
+    """(rows, width, row stride, dtype code, device index) of a call's first matrix."""
+    torch = _torch or _lazy_torch()
+    dtype = t.dtype
+    if dtype is torch.bfloat16:
+        code = NYS_BF16
+    elif dtype is torch.float32:
+        code = NYS_FP32
+    else:
+        raise ValueError(f"{name} must be float32 or bfloat16")
+    if not t.is_cuda or t.dim() != 2:
+        raise ValueError(f"{name} must be a CUDA tensor [rows, width]")
+    device = torch._C._cuda_getDevice()
+    rows, width = t.shape
+    if max(rows, width) > _INT_MAX:
+        raise ValueError(f"{name} has sizes past 32 bits: {tuple(t.shape)}")
+    return rows, width, _matrix(name, t, dtype, t.shape, device), code, device
+
+
+def _matrix(name, t, dtype, shape, device):
+    """Distance between the rows of a [rows, width] tensor of the given type,
+    shape and device."""
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    s = t.stride()
+    if s[1] != 1 and shape[1] > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return s[0] if shape[0] > 1 else shape[1]
+
+
+class NystromQ8:
+    """A matrix in 8 bits over the caller's memory (format: see
+    include/nystrom.h). codes: uint8 CUDA tensor [rows, K], rows contiguous;
+    scales: contiguous int32 [ceil(K / 512), rows]. Both are kept."""
+
+    __slots__ = ("_codes", "_scales", "rows", "K", "device", "desc")
+
+    def __init__(self, codes, scales):
+        torch = _torch or _lazy_torch()
+        if not codes.is_cuda or codes.dtype != torch.uint8 or codes.dim() != 2:
+            raise ValueError("codes must be a uint8 CUDA tensor [rows, K]")
+        rows, K = codes.shape
+        if codes.stride(1) != 1:
+            raise ValueError("codes must have contiguous rows")
+        if rows < 1 or K < 1 or K % 16 or max(rows, K) > _INT_MAX:
+            raise NystromError(NYS_ERR_SHAPE, "NystromQ8")
+        self.device = codes.get_device()
+        words = (-(-K // 512), rows)
+        at = _flat("scales", scales, torch.int32, words, self.device)
+        self._codes, self._scales, self.rows, self.K = codes, scales, rows, K
+        self.desc = _Q8_DESC.pack(codes.data_ptr(), at, rows, K, codes.stride(0) if rows > 1 else K)
+
+    @property
+    def codes(self):
+        return self._codes
+
+    @property
+    def scales(self):
+        return self._scales
+
+
+def _q8_here(name, q):
+    if not isinstance(q, NystromQ8):
+        raise ValueError(f"{name} must be a NystromQ8")
+    if q.device != _torch._C._cuda_getDevice():
+        raise ValueError(f"{name} is on device {q.device}, not on the current CUDA device")
+
+
+def nystrom_q8_scales_bytes(rows, K) -> int:
+    if max(rows, K) > _INT_MAX:
+        return 0  # like other sizes that a call refuses
+    return load_library().nystrom_q8_scales_bytes(rows, K)
+
+
+def nystrom_q8_write(q, x, block_rows=1, stream=None):
+    """Quantises x [rows, K] (contiguous rows, or the transpose of a [K, rows]
+    tensor) into q; block_rows: 1, or 128 rows that share a scale (weights)."""
+    lib = _lib or load_library()
+    torch = _torch or _lazy_torch()
+    _q8_here("q", q)
+    if not x.is_cuda or x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("x must be a float32 or bfloat16 CUDA tensor [rows, K]")
+    if x.shape != (q.rows, q.K) or x.get_device() != q.device:
+        raise ValueError(f"x must have shape {(q.rows, q.K)}, on q's device")
+    rs, cs = x.stride()
+    if q.rows == 1:
+        rs = q.K
+    if cs != 1 and rs != 1:
+        raise ValueError("x must have contiguous rows or columns")
+    rc = lib.nystrom_q8_write(q.desc, x.data_ptr(), rs, cs, block_rows,
+                              NYS_BF16 if x.dtype is torch.bfloat16 else NYS_FP32, _raw_stream(stream, q.device))
+    return rc if rc >= 0 else _check(rc, "nystrom_q8_write")
+
+
+def nystrom_q8_read(q, out, stream=None):
+    """The values that q stands for, to out [rows, K]."""
+    lib = _lib or load_library()
+    rows, K, stride, code, dev = _first_matrix("out", out)
+    _q8_here("q", q)
+    if (rows, K) != (q.rows, q.K):
+        raise ValueError(f"out must have shape {(q.rows, q.K)}, not {(rows, K)}")
+    rc = lib.nystrom_q8_read(q.desc, out.data_ptr(), stride, code, _raw_stream(stream, dev))
+    return rc if rc >= 0 else _check(rc, "nystrom_q8_read")
+
+
+def nystrom_q8_matmul_workspace_bytes(T, N, K, dtype) -> int:
+    if max(T, N, K) > _INT_MAX:
+        return 0
+    return load_library().nystrom_q8_matmul_workspace_bytes(T, N, K, dtype)
+
+
+def nystrom_q8_matmul(a, w, out, workspace=None, stream=None):
+    """out [T, N] = a w^T of the 8-bit matrices a [T, K] and w [N, K] (NystromQ8)."""
+    lib = _lib or load_library()
+    T, N, stride, code, dev = _first_matrix("out", out)
+    _q8_here("a", a)
+    _q8_here("w", w)
+    if (T, N) != (a.rows, w.rows):
+        raise ValueError(f"out must have shape {(a.rows, w.rows)}, not {(T, N)}")
+    need = lib.nystrom_q8_matmul_workspace_bytes(T, N, a.K, code)
+    ws, nbytes, keep = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_q8_matmul(a.desc, w.desc, out.data_ptr(), stride, code, ws, nbytes, _raw_stream(stream, dev))
+    del keep
+    return rc if rc >= 0 else _check(rc, "nystrom_q8_matmul")
+
+
+def nystrom_add_rms_norm_fwd(x, residual, weight, sum_out, y, eps=1e-6, stream=None):
+    """s = x + residual to sum_out (residual None: s = x; sum_out None: not
+    kept), y = weight s / sqrt(mean(s^2) + eps), rows of [rows, d] matrices.
+    y: a matrix like x, or a NystromQ8. weight: float32 [d], or None."""
+    lib = _lib or load_library()
+    rows, d, xs, code, dev = _first_matrix("x", x)
+    dtype, shape = x.dtype, x.shape
+    rs = 0 if residual is None else _matrix("residual", residual, dtype, shape, dev)
+    ss = 0 if sum_out is None else _matrix("sum_out", sum_out, dtype, shape, dev)
+    eight = isinstance(y, NystromQ8)
+    if eight:
+        _q8_here("y", y)
+        if (y.rows, y.K) != (rows, d):
+            raise ValueError(f"y must be {(rows, d)}, not {(y.rows, y.K)}")
+        ys = 0
+    else:
+        ys = _matrix("y", y, dtype, shape, dev)
+    rc = lib.nystrom_add_rms_norm_fwd(
+        _NORM_DESC.pack(rows, d, code, eps, xs, rs, ss, ys, 0, 0), x.data_ptr(),
+        None if residual is None else residual.data_ptr(), _flat("weight", weight, _torch.float32, (d,), dev),
+        None if sum_out is None else sum_out.data_ptr(), None if eight else y.data_ptr(),
+        y.desc if eight else None, _raw_stream(stream, dev))
+    return rc if rc >= 0 else _check(rc, "nystrom_add_rms_norm_fwd")
+
+
+def nystrom_add_rms_norm_workspace_bytes(desc) -> int:
+    """desc: NysAddRmsNorm."""
+    return load_library().nystrom_add_rms_norm_workspace_bytes(
+        ctypes.byref(desc) if isinstance(desc, NysAddRmsNorm) else desc)
+
+
+def nystrom_add_rms_norm_bwd(s, gy, gs, weight, dx, dweight=None, eps=1e-6, workspace=None, stream=None):
+    """Gradients of nystrom_add_rms_norm_fwd: from the sum s, the gradient gy of
+    y and gs of s (or None), to dx (x's and the residual's; may be gy or gs) and,
+    where given, dweight (float32 [d])."""
+    lib = _lib or load_library()
+    rows, d, ss, code, dev = _first_matrix("s", s)
+    dtype, shape, f32 = s.dtype, s.shape, _torch.float32
+    desc = _NORM_DESC.pack(rows, d, code, eps, 0, 0, ss, _matrix("gy", gy, dtype, shape, dev),
+                           0 if gs is None else _matrix("gs", gs, dtype, shape, dev),
+                           _matrix("dx", dx, dtype, shape, dev))
+    need = 0 if dweight is None else lib.nystrom_add_rms_norm_workspace_bytes(desc)
+    ws, nbytes, keep = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_add_rms_norm_bwd(
+        desc, s.data_ptr(), gy.data_ptr(), None if gs is None else gs.data_ptr(),
+        _flat("weight", weight, f32, (d,), dev), dx.data_ptr(), _flat("dweight", dweight, f32, (d,), dev),
+        ws, nbytes, _raw_stream(stream, dev))
+    del keep
+    return rc if rc >= 0 else _check(rc, "nystrom_add_rms_norm_bwd")
+
+
+def _weight(name, t, dtype, shape, device, like=None):
+    """(layout, distance between the stored rows) of a weight [d, f]: stored so,
+    or the transpose of a stored [f, d]; `like`: the layout it has to have."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {tuple(t.shape)}")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    s = t.stride()
+    if s[1] == 1:
+        layout, stride = NYS_FF_IN_OUT, s[0]
+    elif s[0] == 1:
+        layout, stride = NYS_FF_OUT_IN, s[1]
+    else:
+        raise ValueError(f"{name} must have contiguous rows or columns")
+    if like is not None and layout != like:
+        raise ValueError(f"{name} must be laid out like the other weights")
+    return layout, stride
+
+
+def _ff_args(x, w_gate, w_up):
+    T, d, xs, code, dev = _first_matrix("x", x)
+    dtype = x.dtype
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be [d, f]")
+    f = w_gate.shape[1]
+    layout, ws = _weight("w_gate", w_gate, dtype, (d, f), dev)
+    if _weight("w_up", w_up, dtype, (d, f), dev, layout)[1] != ws:
+        raise ValueError("w_up must have w_gate's strides")
+    if f > _INT_MAX:
+        raise ValueError(f"{f} features are more than a call takes")
+    return T, d, f, code, dev, dtype, layout, xs, ws
+
+
+def nystrom_gated_ff_workspace_bytes(desc, back) -> int:
+    """desc: NysGatedFf."""
+    return load_library().nystrom_gated_ff_workspace_bytes(
+        ctypes.byref(desc) if isinstance(desc, NysGatedFf) else desc, 1 if back else 0)
+
+
+def nystrom_gated_ff_fwd(x, w_gate, w_up, h, gate=None, up=None, activation=NYS_ACT_SILU, workspace=None,
+                         stream=None):
+    """h [T, f] = act(x w_gate) * (x w_up) of x [T, d] and weights [d, f] (stored
+    so, or transposes of [f, d]); gate, up: the two products, kept for the
+    backward pass, or None."""
+    lib = _lib or load_library()
+    T, d, f, code, dev, dtype, layout, xs, wst = _ff_args(x, w_gate, w_up)
+    keep = gate is not None or up is not None
+    if keep and (gate is None or up is None):
+        raise ValueError("gate and up: both or neither")
+    desc = _FF_DESC.pack(T, d, f, activation, layout, code, xs, wst, _matrix("h", h, dtype, (T, f), dev),
+                         _matrix("gate", gate, dtype, (T, f), dev) if keep else 0,
+                         _matrix("up", up, dtype, (T, f), dev) if keep else 0, 0, 0)
+    need = lib.nystrom_gated_ff_workspace_bytes(desc, 0)
+    ws, nbytes, kept = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_gated_ff_fwd(desc, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(),
+                                  gate.data_ptr() if keep else None, up.data_ptr() if keep else None, ws, nbytes,
+                                  _raw_stream(stream, dev))
+    del kept
+    return rc if rc >= 0 else _check(rc, "nystrom_gated_ff_fwd")
+
+
+def nystrom_gated_ff_bwd(x, w_gate, w_up, gate, up, gh, dx=None, dw_gate=None, dw_up=None,
+                         activation=NYS_ACT_SILU, workspace=None, stream=None):
+    """Gradients of nystrom_gated_ff_fwd from its inputs, the kept gate and up
+    and the gradient gh of h: dx [T, d] and dw_gate, dw_up (laid out like the
+    weights); dx, or both weights', may be None."""
+    lib = _lib or load_library()
+    T, d, f, code, dev, dtype, layout, xs, wst = _ff_args(x, w_gate, w_up)
+    dws = 0
+    if dw_gate is not None:
+        dws = _weight("dw_gate", dw_gate, dtype, (d, f), dev, layout)[1]
+    if (dw_gate is None) != (dw_up is None):
+        raise ValueError("dw_gate and dw_up: both or neither")
+    if dw_up is not None and _weight("dw_up", dw_up, dtype, (d, f), dev, layout)[1] != dws:
+        raise ValueError("dw_up must have dw_gate's strides")
+    desc = _FF_DESC.pack(T, d, f, activation, layout, code, xs, wst, _matrix("gh", gh, dtype, (T, f), dev),
+                         _matrix("gate", gate, dtype, (T, f), dev), _matrix("up", up, dtype, (T, f), dev),
+                         0 if dx is None else _matrix("dx", dx, dtype, (T, d), dev), dws)
+    need = lib.nystrom_gated_ff_workspace_bytes(desc, 1)
+    ws, nbytes, kept = _scratch(need, workspace, dev, stream)
+    rc = lib.nystrom_gated_ff_bwd(
+        desc, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(), gh.data_ptr(),
+        None if dx is None else dx.data_ptr(), None if dw_gate is None else dw_gate.data_ptr(),
+        None if dw_up is None else dw_up.data_ptr(), ws, nbytes, _raw_stream(stream, dev))
+    del kept
+    return rc if rc >= 0 else _check(rc, "nystrom_gated_ff_bwd")

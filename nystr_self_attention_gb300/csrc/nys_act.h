@@ -1,0 +1,67 @@
+// Activations of the gated feed-forward product and their derivatives.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "nystrom.h"
+
+namespace nys {
+namespace act {
+
+// FAST: special-function unit, relative error below 2^-20 (bf16 results).
+template <bool FAST>
+__device__ __forceinline__ float exponential(float x) {
+  return FAST ? __expf(x) : expf(x);
+}
+template <bool FAST>
+__device__ __forceinline__ float sigmoid(float x) {
+  const float e = 1.f + exponential<FAST>(-x);
+  return FAST ? __fdividef(1.f, e) : 1.f / e;
+}
+
+// tanh as 2 sigmoid(2 z) - 1: the factor (1 + tanh z) / 2 then loses no bits
+// where it is small. 2 sqrt(2/pi) = 1.5957691...
+constexpr float kTanh1 = 1.59576912160573f, kTanh3 = kTanh1 * 0.044715f;
+
+template <int ACT, bool FAST>
+__device__ __forceinline__ float value(float g) {
+  if (ACT == NYS_ACT_SILU) return g * sigmoid<FAST>(g);
+  if (ACT == NYS_ACT_GELU) return 0.5f * g * erfcf(-0.70710678118654752f * g);
+  if (ACT == NYS_ACT_GELU_TANH) return g * sigmoid<FAST>(g * fmaf(kTanh3, g * g, kTanh1));
+  return fmaxf(g, 0.f) + (g != g ? g : 0.f);  // NaN stays NaN
+}
+
+// act(g) and act'(g).
+template <int ACT, bool FAST>
+__device__ __forceinline__ void with_slope(float g, float& a, float& slope) {
+  if (ACT == NYS_ACT_SILU) {
+    const float s = sigmoid<FAST>(g);
+    a = g * s;
+    slope = s * fmaf(g, 1.f - s, 1.f);
+  } else if (ACT == NYS_ACT_GELU) {
+    const float p = 0.5f * erfcf(-0.70710678118654752f * g);
+    a = g * p;
+    slope = fmaf(0.39894228040143268f * g, exponential<FAST>(-0.5f * g * g), p);
+  } else if (ACT == NYS_ACT_GELU_TANH) {
+    const float s = sigmoid<FAST>(g * fmaf(kTanh3, g * g, kTanh1));
+    a = g * s;
+    slope = fmaf(g * s * (1.f - s), fmaf(3.f * kTanh3, g * g, kTanh1), s);
+  } else {
+    a = value<NYS_ACT_RELU, FAST>(g);
+    slope = g > 0.f ? 1.f : (g != g ? g : 0.f);
+  }
+}
+
+// f(std::integral_constant<int, ACT>) for a run-time choice.
+template <typename F>
+__host__ __device__ __forceinline__ auto by_act(int a, F&& f) {
+  switch (a) {
+    case NYS_ACT_SILU: return f(std::integral_constant<int, NYS_ACT_SILU>{});
+    case NYS_ACT_GELU: return f(std::integral_constant<int, NYS_ACT_GELU>{});
+    case NYS_ACT_GELU_TANH: return f(std::integral_constant<int, NYS_ACT_GELU_TANH>{});
+    default: return f(std::integral_constant<int, NYS_ACT_RELU>{});
+  }
+}
+
+}  // namespace act
+}  // namespace nys

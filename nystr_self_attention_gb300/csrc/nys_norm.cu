@@ -1,0 +1,517 @@
+// The residual's addition with the root-mean-square norm of the sum, output in
+// the input's type or in 8 bits, and its gradients (declared in
+// include/nystrom.h). All are bound by HBM: each element is read and written
+// once, with the row held in registers between its sum of squares and its
+// output.
+//
+// TPR threads share a row, V vectors of eight channels each; vector i of thread
+// t is channels 8 (i TPR + t), so 16 neighbouring threads hold the 128 channels
+// of one 8-bit block. A CTA holds several short rows or one long one and walks
+// rows with the grid's step; the weight stays in registers, and the next row's
+// loads are in flight while this one is summed.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <mutex>
+
+#include "nys_q8.h"
+
+namespace nys {
+namespace {
+
+using q8::kBlock;
+constexpr int kMaxD = 16384;
+
+struct NormParams {
+  long long x, r, s, y, gs, dx;  // row strides
+  int rows, d;
+  float eps, inv_d;
+  uint8_t *codes, *scales;
+};
+
+// Eight channels as they lie in memory.
+template <typename T>
+struct Vec;
+template <>
+struct Vec<float> {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const uint4*>(p)[0];
+    b = reinterpret_cast<const uint4*>(p)[1];
+  }
+  __device__ __forceinline__ void clear() { a = b = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+  }
+  __device__ __forceinline__ void narrow(const float (&v)[8]) {
+    a = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+    b = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+  }
+  __device__ __forceinline__ void store(float* p) const {
+    reinterpret_cast<uint4*>(p)[0] = a;
+    reinterpret_cast<uint4*>(p)[1] = b;
+  }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void clear() { a = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void widen(float (&v)[8]) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+  __device__ __forceinline__ void narrow(const float (&v)[8]) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w[i]) : "f"(v[2 * i + 1]), "f"(v[2 * i]));
+    a = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
+};
+
+// Sum of v over the TPR threads of a row, the same bits in each: shuffles, then
+// one slot per warp. The slots alternate between two sets, so one barrier per
+// sum is enough.
+template <int TPR, int N>
+__device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[N], int& phase) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
+  if (TPR == 32) return;
+  constexpr int W = TPR / 32;
+  const int warp = threadIdx.x >> 5, group = threadIdx.x / TPR;
+  float(*set)[N] = slots + phase * (blockDim.x / 32);
+  phase ^= 1;
+  if ((threadIdx.x & 31) == 0)
+#pragma unroll
+    for (int j = 0; j < N; ++j) set[warp][j] = v[j];
+  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < W; ++w) s += set[group * W + w][j];
+    v[j] = s;
+  }
+}
+
+constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+
+template <typename T, int TPR, int V, bool EIGHT>
+__global__ void __launch_bounds__(threads_of(TPR), (sizeof(T) == 4 || V > 2 ? 512 : 1024) / threads_of(TPR))
+add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restrict__ weight, T* sum, T* y) {
+  constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
+  __shared__ float slots[2 * THREADS / 32][1];
+  int phase = 0;
+  const int t = threadIdx.x % TPR;
+  const int step = gridDim.x * GROUPS;
+  int row = blockIdx.x * GROUPS + threadIdx.x / TPR;
+  Vec<T> nx[V], nr[V];
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (i * TPR + t);
+      nx[i].clear();
+      nr[i].clear();
+      if (r < p.rows && c < p.d) {
+        nx[i].load(x + r * p.x + c);
+        if (res) nr[i].load(res + r * p.r + c);
+      }
+    }
+  };
+  fetch(row);
+  float w[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = 8 * (i * TPR + t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[i][j] = c < p.d ? (weight ? weight[c + j] : 1.f) : 0.f;
+  }
+  // the threads of a row leave together: `row` is the group's
+  for (; row < p.rows; row += step) {
+    float s[V][8], total[1] = {0.f};
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      nx[i].widen(s[i]);
+      if (res) {
+        float r[8];
+        nr[i].widen(r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+        Vec<T> out;  // s is what is kept: rounded
+        out.narrow(s[i]);
+        out.widen(s[i]);
+        const int c = 8 * (i * TPR + t);
+        if (sum && c < p.d) out.store(sum + row * p.s + c);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) total[0] = fmaf(s[i][j], s[i][j], total[0]);
+    }
+    fetch(row < p.rows - step ? row + step : p.rows);
+    row_sums<TPR, 1>(total, slots, phase);
+    const float r = rsqrtf(fmaf(total[0], p.inv_d, p.eps));
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (i * TPR + t);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[i][j] *= r * w[i][j];
+      if (!EIGHT) {
+        Vec<T> out;
+        out.narrow(s[i]);
+        if (c < p.d) out.store(y + row * p.y + c);
+      } else {
+        uint32_t top = 0u;  // magnitudes compare as integers, NaN above infinity
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, c < p.d ? __float_as_uint(s[i][j]) & 0x7fffffffu : 0u);
+#pragma unroll
+        for (int o = 8; o > 0; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+        const uint32_t byte = q8::scale_byte(top);
+        const float inv = q8::inverse_scale(byte);
+        if (c < p.d) {
+          const uint2 codes = make_uint2(q8::encode4(s[i][0], s[i][1], s[i][2], s[i][3], inv),
+                                         q8::encode4(s[i][4], s[i][5], s[i][6], s[i][7], inv));
+          *reinterpret_cast<uint2*>(p.codes + row * p.y + c) = codes;
+          if ((t & 15) == 0)
+            q8::store_scale(p.scales, c / kBlock, (p.d + kBlock - 1) / kBlock, row, p.rows, byte);
+        }
+      }
+    }
+    if (row >= p.rows - step) break;  // the next index may pass 2^31
+  }
+}
+
+// part: [CTAs][d] sums of gy h over a CTA's rows, or null.
+template <typename T, int TPR, int V>
+__global__ void __launch_bounds__(threads_of(TPR), TPR > 512 ? 1 : 512 / threads_of(TPR))
+add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, const float* __restrict__ weight,
+                  T* dx, float* part) {
+  constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
+  // the weight in registers and the next row in flight as long as both fit
+  constexpr bool ROOMY = V * sizeof(T) <= 4;
+  __shared__ float slots[2 * THREADS / 32][2];
+  extern __shared__ float sums[];  // [GROUPS][d] where a CTA holds several rows
+  int phase = 0;
+  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  const int step = gridDim.x * GROUPS;
+  int row = blockIdx.x * GROUPS + group;
+  Vec<T> ns[V], ng[V], na[V];
+  auto fetch = [&](int r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (i * TPR + t);
+      ns[i].clear();
+      ng[i].clear();
+      na[i].clear();
+      if (r < p.rows && c < p.d) {
+        ns[i].load(s + r * p.s + c);
+        ng[i].load(gy + r * p.y + c);
+        if (gs) na[i].load(gs + r * p.gs + c);
+      }
+    }
+  };
+  auto load_weight = [&](int i, float (&w)[8]) {
+    const int c = 8 * (i * TPR + t);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] = c < p.d ? (weight ? weight[c + j] : 1.f) : 0.f;
+  };
+  fetch(row);
+  float kept[ROOMY ? V : 1][8], acc[V][8];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    if (ROOMY) load_weight(i, kept[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) acc[i][j] = 0.f;
+  }
+  for (; row < p.rows; row += step) {
+    Vec<T> xs[V], xg[V], xa[V];
+    float total[2] = {0.f, 0.f};  // s^2, weight gy s
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      xs[i] = ns[i];
+      xg[i] = ng[i];
+      xa[i] = na[i];
+      float a[8], g[8], w[8];
+      xs[i].widen(a);
+      xg[i].widen(g);
+      if (!ROOMY) load_weight(i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        total[0] = fmaf(a[j], a[j], total[0]);
+        total[1] = fmaf((ROOMY ? kept[ROOMY ? i : 0][j] : w[j]) * g[j], a[j], total[1]);
+      }
+    }
+    const int next = row < p.rows - step ? row + step : p.rows;
+    if (ROOMY) fetch(next);
+    row_sums<TPR, 2>(total, slots, phase);
+    const float r = rsqrtf(fmaf(total[0], p.inv_d, p.eps));
+    const float m = -r * r * total[1] * p.inv_d;  // -mean(weight gy h) r
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      float a[8], g[8], e[8], w[8];
+      xs[i].widen(a);
+      xg[i].widen(g);
+      xa[i].widen(e);
+      if (!ROOMY) load_weight(i, w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float h = a[j] * r;
+        acc[i][j] = fmaf(g[j], h, acc[i][j]);
+        e[j] = fmaf(r, (ROOMY ? kept[ROOMY ? i : 0][j] : w[j]) * g[j], fmaf(h, m, e[j]));
+      }
+      const int c = 8 * (i * TPR + t);
+      Vec<T> out;
+      out.narrow(e);
+      if (c < p.d) out.store(dx + row * p.dx + c);
+    }
+    if (!ROOMY) fetch(next);
+    if (next == p.rows) break;  // row + step may pass 2^31
+  }
+  if (!part) return;
+  float* dst = part + (size_t)blockIdx.x * p.d;
+  if constexpr (GROUPS == 1) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (i * TPR + t);
+      if (c < p.d)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dst[c + j] = acc[i][j];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = 8 * (i * TPR + t);
+      if (c < p.d)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sums[group * p.d + c + j] = acc[i][j];
+    }
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.d; c += THREADS) {
+      float v = 0.f;
+#pragma unroll
+      for (int g = 0; g < GROUPS; ++g) v += sums[g * p.d + c];
+      dst[c] = v;
+    }
+  }
+}
+
+// dw[c] = sum over the CTAs of part, 32 channels per CTA in 32 row slices: a
+// fixed order. Set up while the kernel that writes part still runs.
+__global__ void __launch_bounds__(1024)
+norm_weight_grad(const float* part, float* dw, int d, int ctas) {
+  __shared__ float s[32][33];
+  cudaGridDependencySynchronize();
+  const int lane = threadIdx.x & 31, slice = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  float v = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (int r = slice; r < ctas; r += 32) v += part[(size_t)r * d + c];
+  }
+  s[slice][lane] = v;
+  __syncthreads();
+  float x = s[lane][slice];  // warp `slice` sums channel `slice` of this CTA's 32
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if (lane == 0 && blockIdx.x * 32 + slice < d) dw[blockIdx.x * 32 + slice] = x;
+}
+
+int check_common(const nys_add_rms_norm_t* p) {
+  if (!p) return NYS_ERR_ARG;
+  if (p->dtype != NYS_FP32 && p->dtype != NYS_BF16) return NYS_ERR_ARG;
+  if (!(p->eps >= 0.f) || std::isinf(p->eps)) return NYS_ERR_ARG;
+  if (p->rows < 1 || p->d < 8 || p->d % 8 || p->d > kMaxD) return NYS_ERR_SHAPE;
+  return NYS_OK;
+}
+
+// f(TPR, V) for a row of d channels: two vectors per thread until a row has a
+// CTA of 512 threads to itself, then four.
+template <typename F>
+auto by_width(int d, F&& f) {
+  using std::integral_constant;
+  if (d <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (d <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
+  if (d <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
+  if (d <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
+  if (d <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
+  if (d <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
+  return f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+}
+
+// CTAs: one per group of rows until the GPU is full.
+int grid_of(int rows, int groups, int ctas_per_sm) {
+  const long long want = ((long long)rows + groups - 1) / groups, most = (long long)plan_sms() * ctas_per_sm;
+  return (int)(want < most ? want : most);
+}
+
+template <int TPR>
+int back_grid(int rows) {
+  constexpr int T = threads_of(TPR);
+  return grid_of(rows, T / TPR, 512 / T);
+}
+
+int back_ctas(const nys_add_rms_norm_t& a) {
+  return by_width(a.d, [&](auto tpr, auto) { return back_grid<decltype(tpr)::value>(a.rows); });
+}
+
+NormParams params_of(const nys_add_rms_norm_t& a) {
+  NormParams p{};
+  p.x = a.x;
+  p.r = a.residual;
+  p.s = a.sum;
+  p.y = a.y;
+  p.gs = a.gs;
+  p.dx = a.dx;
+  p.rows = a.rows;
+  p.d = a.d;
+  p.eps = a.eps;
+  p.inv_d = 1.f / (float)a.d;
+  return p;
+}
+
+template <typename T>
+int launch_fwd(const nys_add_rms_norm_t& a, const void* x, const void* res, const float* weight, void* sum,
+               void* y, const nys_q8_t* y8, cudaStream_t st) {
+  NormParams p = params_of(a);
+  if (y8) {
+    p.codes = static_cast<uint8_t*>(y8->codes);
+    p.scales = static_cast<uint8_t*>(y8->scales);
+    p.y = y8->stride;
+  }
+  return by_width(a.d, [&](auto tpr, auto v) {
+    constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
+    constexpr int per_sm = (sizeof(T) == 4 || V > 2 ? 512 : 1024) / THREADS;
+    const int grid = grid_of(a.rows, THREADS / TPR, per_sm);
+    auto go = [&](auto kernel) {
+      KernelScope scope("add_rms_norm", st);
+      kernel<<<grid, THREADS, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(res), weight,
+                                       static_cast<T*>(sum), static_cast<T*>(y));
+      return launch_status();
+    };
+    return y8 ? go(add_rms_norm<T, TPR, V, true>) : go(add_rms_norm<T, TPR, V, false>);
+  });
+}
+
+template <typename T>
+int launch_bwd(const nys_add_rms_norm_t& a, const void* s, const void* gy, const void* gs, const float* weight,
+               void* dx, float* part, cudaStream_t st) {
+  const NormParams p = params_of(a);
+  return by_width(a.d, [&](auto tpr, auto v) {
+    constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
+    constexpr int GROUPS = THREADS / TPR;
+    const size_t smem = GROUPS > 1 && part ? (size_t)GROUPS * a.d * sizeof(float) : 0;  // at most 16 KB
+    KernelScope scope("add_rms_norm_back", st);
+    add_rms_norm_back<T, TPR, V><<<back_grid<TPR>(a.rows), THREADS, smem, st>>>(
+        p, static_cast<const T*>(s), static_cast<const T*>(gy), static_cast<const T*>(gs), weight,
+        static_cast<T*>(dx), part);
+    return launch_status();
+  });
+}
+
+// The same address means the same rows: one stride, or one row.
+bool apart_or_same(const void* out, long long os, const void* in, long long is, int rows) {
+  return out != in || rows == 1 || os == is;
+}
+
+}  // namespace
+}  // namespace nys
+
+using namespace nys;
+
+extern "C" {
+
+int nystrom_add_rms_norm_fwd(const nys_add_rms_norm_t* p, const void* x, const void* residual,
+                             const float* weight, void* sum, void* y, const nys_q8_t* y8,
+                             nys_stream_t stream) {
+  int rc = check_common(p);
+  if (rc != NYS_OK) return rc;
+  if (!x || (y == nullptr) == (y8 == nullptr) || (sum && !residual)) return NYS_ERR_ARG;
+  auto rows = [&](const void* at, long long stride, bool out) {
+    return at ? q8::check_rows(at, stride, p->rows, p->d, p->dtype, out) : NYS_OK;
+  };
+  if ((rc = rows(x, p->x, false)) != NYS_OK || (rc = rows(residual, p->residual, false)) != NYS_OK ||
+      (rc = rows(sum, p->sum, true)) != NYS_OK || (rc = rows(y, p->y, true)) != NYS_OK)
+    return rc;
+  if (y8) {
+    if ((rc = q8::check_q8(y8, true)) != NYS_OK) return rc;
+    if (y8->rows != p->rows || y8->K != p->d) return NYS_ERR_SHAPE;
+    for (const void* other : {x, residual, static_cast<const void*>(sum), static_cast<const void*>(weight)})
+      if (other && (y8->codes == other || y8->scales == other)) return NYS_ERR_ARG;
+  }
+  if (reinterpret_cast<uintptr_t>(weight) & 3u) return NYS_ERR_ALIGN;
+  if (sum && sum == y) return NYS_ERR_ARG;
+  if ((sum && (!apart_or_same(sum, p->sum, x, p->x, p->rows) ||
+               !apart_or_same(sum, p->sum, residual, p->residual, p->rows))) ||
+      (y && (!apart_or_same(y, p->y, x, p->x, p->rows) ||
+             (residual && !apart_or_same(y, p->y, residual, p->residual, p->rows)))))
+    return NYS_ERR_ARG;
+  int dev = 0;
+  rc = check_device(&dev);
+  if (rc != NYS_OK) return rc;
+  return p->dtype == NYS_BF16 ? launch_fwd<__nv_bfloat16>(*p, x, residual, weight, sum, y, y8, stream)
+                              : launch_fwd<float>(*p, x, residual, weight, sum, y, y8, stream);
+}
+
+size_t nystrom_add_rms_norm_workspace_bytes(const nys_add_rms_norm_t* p) {
+  if (check_common(p) != NYS_OK) return 0;
+  return ((size_t)back_ctas(*p) * p->d * sizeof(float) + 255) & ~size_t(255);
+}
+
+int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const void* gy, const void* gs,
+                             const float* weight, void* dx, float* dweight, void* workspace,
+                             size_t ws_bytes, nys_stream_t stream) {
+  int rc = check_common(p);
+  if (rc != NYS_OK) return rc;
+  if (!s || !gy || !dx) return NYS_ERR_ARG;
+  auto rows = [&](const void* at, long long stride, bool out) {
+    return at ? q8::check_rows(at, stride, p->rows, p->d, p->dtype, out) : NYS_OK;
+  };
+  if ((rc = rows(s, p->sum, false)) != NYS_OK || (rc = rows(gy, p->y, false)) != NYS_OK ||
+      (rc = rows(gs, p->gs, false)) != NYS_OK || (rc = rows(dx, p->dx, true)) != NYS_OK)
+    return rc;
+  if ((reinterpret_cast<uintptr_t>(weight) | reinterpret_cast<uintptr_t>(dweight)) & 3u) return NYS_ERR_ALIGN;
+  if (dx == s || !apart_or_same(dx, p->dx, gy, p->y, p->rows) ||
+      (gs && !apart_or_same(dx, p->dx, gs, p->gs, p->rows)))
+    return NYS_ERR_ARG;
+  if (dweight && (dweight == weight || dweight == dx || dweight == s || dweight == gy || dweight == gs))
+    return NYS_ERR_ARG;
+  const size_t need = dweight ? nystrom_add_rms_norm_workspace_bytes(p) : 0;
+  if (dweight && workspace) {
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return NYS_ERR_ALIGN;
+    if (ws_bytes < need) return NYS_ERR_NOMEM;
+  }
+  int dev = 0;
+  rc = check_device(&dev);
+  if (rc != NYS_OK) return rc;
+  std::unique_lock<std::mutex> held;
+  if (dweight && !workspace) {
+    rc = operator_workspace(dev, need, stream, &workspace, &held);
+    if (rc != NYS_OK) return rc;
+  }
+  float* part = dweight ? static_cast<float*>(workspace) : nullptr;
+  rc = p->dtype == NYS_BF16 ? launch_bwd<__nv_bfloat16>(*p, s, gy, gs, weight, dx, part, stream)
+                            : launch_bwd<float>(*p, s, gy, gs, weight, dx, part, stream);
+  if (rc != NYS_OK || !dweight) return rc;
+  KernelScope scope("norm_weight_grad", stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((p->d + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, norm_weight_grad, static_cast<const float*>(part), dweight, p->d, back_ctas(*p));
+  return launch_status();
+}
+
+}  // extern "C"

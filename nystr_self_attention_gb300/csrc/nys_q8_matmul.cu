@@ -1,0 +1,137 @@
+// The product of two matrices in 8 bits (declared in include/nystrom.h):
+// out[t][n] = sum over k of A[t][k] W[n][k]. The scales are powers of two, so the
+// tensor cores' block-scaled form applies them exactly: one scale for four
+// instructions of 32 channels, its byte named by the instruction, words of four
+// blocks copied into TMEM as they are needed.
+//
+// Up to 128 tokens the weights are the 128-row operand and the tokens the short
+// one (nothing is padded to 128 rows, so the weights stream at HBM's pace), K
+// split so that every SM has an equal share; the partial sums are joined. More
+// tokens are the rows themselves, in tiles of 128 x 128.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
+
+#include "nys_gemm.h"
+#include "nys_q8.h"
+
+namespace nys {
+namespace {
+
+using namespace nys::gemm;
+
+struct Q8Plan {
+  bool turned;
+  int bn, splits, its_per_split;
+  size_t bytes;  // of partial sums
+};
+
+Q8Plan plan_of(int T, int N, int K) {
+  Q8Plan q{};
+  const int its = (K + 127) / 128;
+  q.turned = T <= 128;
+  q.bn = !q.turned ? 128 : T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
+  const long long tiles = q.turned ? (N + 127) / 128 : (long long)((T + 127) / 128) * ((N + 127) / 128);
+  q.splits = splits_of(tiles, its, q.turned ? 2 : 4, 16, q.bn / 16.0);
+  q.its_per_split = (its + q.splits - 1) / q.splits;
+  if (q.turned)
+    q.bytes = (size_t)q.splits * N * q.bn * 4;
+  else if (q.splits > 1)
+    q.bytes = (size_t)q.splits * T * N * 4;
+  q.bytes = (q.bytes + 255) & ~size_t(255);
+  return q;
+}
+
+int check_sizes(int T, int N, int K) {
+  if (T < 1 || N < 1 || N % 8 || K < 1) return NYS_ERR_SHAPE;
+  if ((long long)((T + 127) / 128) * ((N + 127) / 128) >= (1ll << 26)) return NYS_ERR_SHAPE;
+  return NYS_OK;
+}
+
+Matrix codes_of(const nys_q8_t& q) { return Matrix{q.codes, q.rows, q.K, q.stride, 1}; }
+
+}  // namespace
+}  // namespace nys
+
+using namespace nys;
+
+extern "C" {
+
+size_t nystrom_q8_matmul_workspace_bytes(int T, int N, int K, int dtype) {
+  if ((dtype != NYS_FP32 && dtype != NYS_BF16) || check_sizes(T, N, K) != NYS_OK || K % 16 || K > (1 << 20))
+    return 0;
+  return plan_of(T, N, K).bytes;
+}
+
+int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long out_stride, int dtype,
+                      void* workspace, size_t ws_bytes, nys_stream_t stream) {
+  int rc;
+  if ((rc = q8::check_q8(a, false)) != NYS_OK || (rc = q8::check_q8(w, false)) != NYS_OK) return rc;
+  if (!out || (dtype != NYS_FP32 && dtype != NYS_BF16)) return NYS_ERR_ARG;
+  if (a->K != w->K) return NYS_ERR_SHAPE;
+  const int T = a->rows, N = w->rows, K = a->K;
+  if ((rc = check_sizes(T, N, K)) != NYS_OK) return rc;
+  if ((rc = q8::check_rows(out, out_stride, T, N, dtype, true)) != NYS_OK) return rc;
+  if (out == a->codes || out == w->codes || out == a->scales || out == w->scales) return NYS_ERR_ARG;
+  const Q8Plan plan = plan_of(T, N, K);
+  if (plan.bytes && workspace) {
+    if (reinterpret_cast<uintptr_t>(workspace) & 255u) return NYS_ERR_ALIGN;
+    if (ws_bytes < plan.bytes) return NYS_ERR_NOMEM;
+  }
+  int dev = 0;
+  rc = check_device(&dev);
+  if (rc != NYS_OK) return rc;
+  std::unique_lock<std::mutex> held;
+  if (plan.bytes && !workspace) {
+    rc = operator_workspace(dev, plan.bytes, stream, &workspace, &held);
+    if (rc != NYS_OK) return rc;
+  }
+  const nys_q8_t &rows = plan.turned ? *w : *a, &cols = plan.turned ? *a : *w;
+  Params p{};
+  if ((rc = operator_status(dev, &p.status)) != NYS_OK) return rc;
+  p.m_tiles = (rows.rows + 127) / 128;
+  p.n_tiles = (cols.rows + plan.bn - 1) / plan.bn;
+  p.parts = p.pairs = 1;
+  p.splits = plan.splits;
+  p.k_blocks = p.its = (K + 127) / 128;
+  p.its_per_split = plan.its_per_split;
+  p.chunk = 8;
+  p.group = 8;
+  p.a_scales = static_cast<const uint32_t*>(rows.scales);
+  p.b_scales = static_cast<const uint32_t*>(cols.scales);
+  p.a_rows = rows.rows;
+  p.b_rows = cols.rows;
+  Maps maps{};
+  bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.bn);
+  const bool direct = !plan.turned && plan.splits == 1;
+  if (direct)
+    ok = ok && map_out(&maps.c[0], Matrix{out, T, N, out_stride, dtype == NYS_FP32 ? 4 : 2});
+  else if (plan.turned)
+    ok = ok && map_out(&maps.c[0], Matrix{workspace, N, plan.bn, plan.bn, 4, plan.splits, (long long)N * plan.bn},
+                       plan.bn == 16);
+  else
+    ok = ok && map_out(&maps.c[0], Matrix{workspace, T, N, N, 4, plan.splits, (long long)T * N});
+  if (!ok) return tensor_map_error(__FILE__, __LINE__);
+  maps.a[1] = maps.a[0];
+  maps.b[1] = maps.b[0];
+  const char* name = "q8_matmul";
+  if (plan.turned) {
+    switch (plan.bn) {
+      case 16: rc = launch<kMx8, false, false, 16, kPlain, float>(name, maps, p, stream); break;
+      case 32: rc = launch<kMx8, false, false, 32, kPlain, float>(name, maps, p, stream); break;
+      case 64: rc = launch<kMx8, false, false, 64, kPlain, float>(name, maps, p, stream); break;
+      default: rc = launch<kMx8, false, false, 128, kPlain, float>(name, maps, p, stream);
+    }
+  } else if (!direct || dtype == NYS_FP32) {
+    rc = launch<kMx8, false, false, 128, kPlain, float>(name, maps, p, stream);
+  } else {
+    rc = launch<kMx8, false, false, 128, kPlain, __nv_bfloat16>(name, maps, p, stream);
+  }
+  if (rc != NYS_OK || direct) return rc;
+  const Join j{static_cast<const float*>(workspace), plan.splits, T, N, plan.turned ? plan.bn : 0,
+               {out, nullptr}, {out_stride, 0}};
+  return join(j, 1, dtype, stream);
+}
+
+}  // extern "C"
