@@ -129,20 +129,19 @@ struct Product {
 Product product_of(long long M, long long N, long long k, int k_parts, int parts, int pairs, bool gated,
                    bool may_turn) {
   Product q{};
-  q.turned = may_turn && M <= 128;
-  // fp32 results are summed in registers, which hold 128 columns
-  q.bn = !q.turned ? (pairs > 1 ? 128 : 256) : M <= 16 ? 16 : M <= 32 ? 32 : M <= 64 ? 64 : 128;
+  q.turned = may_turn && M <= kMostTokens;
+  q.bn = q.turned ? columns_of((int)M) : 256;
   q.k_blocks = (int)((k + 63) / 64);
-  const int steps = q.k_blocks * k_parts;
+  const int steps = q.k_blocks * k_parts, rows = q.turned ? 128 : 256;
   q.its = steps * pairs;
-  q.m_tiles = (int)(((q.turned ? N : M) + 127) / 128);
+  q.m_tiles = (int)(((q.turned ? N : M) + rows - 1) / rows);
   // tiles of the split form; the gated one has half as many columns of each part
-  const int nt = q.turned ? 1 : (int)((N + q.bn - 1) / q.bn);
+  const int nt = q.turned ? 1 : (int)((N + 255) / 256);
   const long long tiles = (long long)q.m_tiles * nt * parts;
-  q.splits = splits_of(tiles, steps, 4, 16, q.bn / 16.0 / pairs);
+  q.splits = splits_of(tiles, q.turned ? 1 : 2, steps, 4, 16, q.bn / 16.0 / pairs);
   q.its_per_split = (steps + q.splits - 1) / q.splits * pairs;  // all pairs of a block
   const bool direct = !q.turned && q.splits == 1;
-  q.n_tiles = gated && direct ? (int)((N + q.bn / 2 - 1) / (q.bn / 2)) : nt;
+  q.n_tiles = gated && direct ? (int)((N + 127) / 128) : nt;
   if (q.turned)
     q.bytes = align256((size_t)q.splits * parts * N * q.bn * 4);
   else if (!direct)
@@ -238,25 +237,15 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
 }
 
 // The turned form: weights (k contiguous, or turned themselves) x tokens.
-int launch_turned(bool amn, const Product& q, const Maps& maps, const Params& p, cudaStream_t st) {
-  auto by_bn = [&](auto mn) -> int {
-    constexpr bool A = decltype(mn)::value;
-    switch (q.bn) {
-      case 16: return launch<kBf16, A, false, 16, kPlain, float>("gated_ff_tokens", maps, p, st);
-      case 32: return launch<kBf16, A, false, 32, kPlain, float>("gated_ff_tokens", maps, p, st);
-      case 64: return launch<kBf16, A, false, 64, kPlain, float>("gated_ff_tokens", maps, p, st);
-      default: return launch<kBf16, A, false, 128, kPlain, float>("gated_ff_tokens", maps, p, st);
-    }
-  };
-  return amn ? by_bn(std::true_type{}) : by_bn(std::false_type{});
+int launch_turned(const char* name, bool amn, const Product& q, const Maps& maps, const Params& p, cudaStream_t st) {
+  return amn ? launch_tokens<kBf16, true>(name, q.bn, maps, p, st) : launch_tokens<kBf16, false>(name, q.bn, maps, p, st);
 }
 
-// Results, or partial sums of split products, in rows.
+// Results, or (wide) fp32 results or partial sums, in rows.
 template <bool AMN, bool BMN>
-int launch_plain(const char* name, bool f32, bool parts, const Maps& maps, const Params& p, cudaStream_t st) {
-  if (f32) return launch<kBf16, AMN, BMN, 128, kPlain, float>(name, maps, p, st);
-  return parts ? launch<kBf16, AMN, BMN, 256, kPlain, float>(name, maps, p, st)
-               : launch<kBf16, AMN, BMN, 256, kPlain, __nv_bfloat16>(name, maps, p, st);
+int launch_plain(const char* name, bool wide, const Maps& maps, const Params& p, cudaStream_t st) {
+  return wide ? launch_pair<kBf16, AMN, BMN, kPlain, float>(name, maps, p, st)
+              : launch_pair<kBf16, AMN, BMN, kPlain, __nv_bfloat16>(name, maps, p, st);
 }
 
 // Operand of `rows` lines of `k`, or stored [k][rows] (mn), in one or three terms.
@@ -297,7 +286,7 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
     ok = map_k(&maps.a[0], xm, 128);
     maps.a[1] = maps.a[0];
     for (int i = 0; i < 2; ++i)
-      ok = ok && (io ? map_mn(&maps.b[i], w[i]) : map_k(&maps.b[i], w[i], direct ? q.bn / 2 : q.bn));
+      ok = ok && (io ? map_mn(&maps.b[i], w[i]) : map_k(&maps.b[i], w[i], 128));
     if (direct) {
       const int e = pl.f32 ? 4 : 2;
       ok = ok && map_out(&maps.c[0], Matrix{h, a.T, a.f, a.h, e});
@@ -311,16 +300,16 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
   }
   if (!ok) return tensor_map_error(__FILE__, __LINE__);
   if (q.turned) {
-    rc = launch_turned(io, q, maps, p, st);
+    rc = launch_turned("gated_ff_tokens", io, q, maps, p, st);
   } else if (!direct) {
-    rc = io ? launch_plain<false, true>("gated_ff_split", pl.f32, true, maps, p, st)
-            : launch_plain<false, false>("gated_ff_split", pl.f32, true, maps, p, st);
+    rc = io ? launch_plain<false, true>("gated_ff_split", true, maps, p, st)
+            : launch_plain<false, false>("gated_ff_split", true, maps, p, st);
   } else if (pl.f32) {
-    rc = io ? launch<kBf16, false, true, 128, kGated, float>("gated_ff", maps, p, st)
-            : launch<kBf16, false, false, 128, kGated, float>("gated_ff", maps, p, st);
+    rc = io ? launch_pair<kBf16, false, true, kGated, float>("gated_ff", maps, p, st)
+            : launch_pair<kBf16, false, false, kGated, float>("gated_ff", maps, p, st);
   } else {
-    rc = io ? launch<kBf16, false, true, 256, kGated, __nv_bfloat16>("gated_ff", maps, p, st)
-            : launch<kBf16, false, false, 256, kGated, __nv_bfloat16>("gated_ff", maps, p, st);
+    rc = io ? launch_pair<kBf16, false, true, kGated, __nv_bfloat16>("gated_ff", maps, p, st)
+            : launch_pair<kBf16, false, false, kGated, __nv_bfloat16>("gated_ff", maps, p, st);
   }
   if (rc != NYS_OK || direct) return rc;
   const JoinGated j{reinterpret_cast<const float*>(ws + pl.part), q.splits, a.T, a.f, q.turned ? q.bn : 0,
@@ -342,7 +331,7 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap &wm = q.turned ? maps.a[i] : maps.b[i], &gm = q.turned ? maps.b[i] : maps.a[i];
-    ok = ok && (io ? map_k(&wm, w[i], q.turned ? 128 : q.bn) : map_mn(&wm, w[i])) &&
+    ok = ok && (io ? map_k(&wm, w[i], 128) : map_mn(&wm, w[i])) &&
          map_k(&gm, g[i], q.turned ? q.bn : 128);
   }
   char* part = ws + pl.part;
@@ -356,10 +345,10 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
   int rc;
   const char* name = "gated_ff_dx";
   if (q.turned)
-    rc = launch_turned(!io, q, maps, p, st);
+    rc = launch_turned(name, !io, q, maps, p, st);
   else
-    rc = io ? launch_plain<false, false>(name, pl.f32, !direct, maps, p, st)
-            : launch_plain<false, true>(name, pl.f32, !direct, maps, p, st);
+    rc = io ? launch_plain<false, false>(name, pl.f32 || !direct, maps, p, st)
+            : launch_plain<false, true>(name, pl.f32 || !direct, maps, p, st);
   if (rc != NYS_OK || direct) return rc;
   const Join j{reinterpret_cast<const float*>(part), q.splits, a.T, a.d, q.turned ? q.bn : 0, {dx, nullptr}, {a.dx, 0}};
   return join(j, 1, a.dtype, st);
@@ -386,7 +375,7 @@ int weight_gradients(const nys_gated_ff_t& a, const Plan& pl, const void* x, voi
   if (!direct) ok = ok && map_out(&maps.c[0], Matrix{part, M, N, N, 4, 2 * q.splits, (long long)M * N});
   if (!ok) return tensor_map_error(__FILE__, __LINE__);
   const char* name = "gated_ff_dw";
-  const int rc = launch_plain<true, true>(name, pl.f32, !direct, maps, p, st);
+  const int rc = launch_plain<true, true>(name, pl.f32 || !direct, maps, p, st);
   if (rc != NYS_OK || direct) return rc;
   const Join j{reinterpret_cast<const float*>(part), q.splits, M, N, 0, {dwg, dwu}, {a.dw, a.dw}};
   return join(j, 2, a.dtype, st);

@@ -1,21 +1,25 @@
 // Matrix products on the tensor cores for the operators around the attention
 // module: D[m][n] = sum over k of A[m][k] B[n][k], accumulated in fp32 in TMEM.
 //
-// A persistent CTA works through output tiles of 128 x BN with one warp that
-// issues the TMA copies, one that issues the products, four that carry finished
-// tiles out, and (8-bit operands) one that lays the scales out. K advances 128
-// bytes per stage: 64 bf16 or 128 e4m3, four instructions. Two accumulators in
-// TMEM let a tile's products run while the previous one is carried out.
-//
-// The matrix units cut sums off towards zero: 120 instructions in a row leave
-// 2e-6 of a result, too much for fp32. Kernels with fp32 results of up to 128
-// columns therefore sum a few K blocks at a time in TMEM and add those sums in
-// registers, rounding to nearest.
+// Two kernels, both persistent: a warp issues the TMA copies, one the products,
+// and others carry finished tiles out while the next ones run; K advances 128
+// bytes per stage, 64 bf16 or 128 e4m3, four instructions.
+//   gemm_pair: tiles of 256 x 256 by a cluster of two CTAs. Each holds half of A's
+//     rows and half of B's in shared memory and the instruction reads both CTAs'
+//     halves of B, so a CTA fetches 32 KB per stage where a tile of its own would
+//     take 48 (and 96 bytes a cycle instead of 64 out of shared memory).
+//   gemm_tokens: tiles of 128 rows x up to 128 columns by one CTA, for products
+//     with few columns (tokens) whose other operand (weights) has to stream.
 //
 // Either operand may lie with its k contiguous (rows of 128 bytes, 128-byte
 // swizzle) or with its m or n contiguous ("MN-major": boxes of 64 elements x 64
 // k), so a weight and the transposed factors of its gradient are read as they
 // lie. Coordinates past a matrix's end read zeros and are not stored.
+//
+// The matrix units cut sums off towards zero: 120 instructions in a row leave
+// 2e-6 of a result, too much for fp32. Kernels with fp32 results therefore sum a
+// few K blocks at a time in TMEM and add those sums in registers, rounding to
+// nearest (relative error 1e-7).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -91,6 +95,24 @@ __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int
   return false;
 }
 
+// The same for a whole warp, whose lanes go on together. A phase that is over
+// takes one test.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, int* status, volatile int* abort_flag) {
+  if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
+  return __all_sync(0xffffffffu, wait_or_fail(bar, parity, status, abort_flag));
+}
+// True in one lane of a converged warp. The warps that issue copies and products
+// run their loops whole and elect a lane around the instructions: in a branch on
+// the lane's number the compiler has to move every operand of such an instruction
+// to the uniform registers one lane at a time, and a stage's four products took
+// longer to issue than to run.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p)::"memory");
+  return p != 0;
+}
+
 // The scales of 128 rows of an operand, 512 bytes in shared memory, to four
 // columns of TMEM (repeated for each quarter of the lanes).
 __device__ __forceinline__ void copy_scales(uint32_t tmem, const uint8_t* smem) {
@@ -114,33 +136,18 @@ __device__ __forceinline__ uint32_t idesc_mx8(int M, int N, uint32_t id) {
          (static_cast<uint32_t>(M >> 4) << 24) | (id << 29);
 }
 
-// Places of a kernel's shared memory.
-template <int KIND, int BN>
-struct Layout {
-  static constexpr int kA = 128 * 128, kB = BN * 128, kStage = kA + kB;
-  static constexpr int kStaging = 4 * 2 * 4096;  // two boxes per warp that carries out
-  static constexpr int kScales = KIND == kMx8 ? 2 * (512 + (BN + 127) / 128 * 512) : 0;
-  static constexpr int kBars = 512;
-  static constexpr int kFree = 232448 - 1024 - kStaging - kScales - kBars;
-  static constexpr int kStages = kFree / kStage < 12 ? kFree / kStage : 12;
-  static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBars;
-  static constexpr int kScaleCol = 2 * BN;  // TMEM column of the scales: two slots of 4 + 8
-  static constexpr int kCols = 2 * BN + (KIND == kMx8 ? 32 : 0);
-  static constexpr int kAlloc = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
-  static_assert(kCols <= 512, "TMEM columns");
-  static constexpr int kThreads = KIND == kMx8 ? 224 : 192;
-};
-
+// Barriers and the like at the end of a kernel's shared memory.
 struct Bars {
   uint64_t full[12], empty[12], acc_full[2], acc_empty[2], sf_full[2], sf_empty[2], fin;
   uint32_t tmem;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512, "barriers");
+constexpr int kBarBytes = 512;
+static_assert(sizeof(Bars) <= kBarBytes, "barriers");
+constexpr int kSmem = 232448;  // of a CTA
 
-// 32 columns of a lane's row as fp32 to a box in shared memory whose rows are
-// 128 bytes, 16-byte pieces in the 128-byte swizzle; `half`: of bf16, which 64
-// bytes.
+// 32 columns of a lane's row to a box in shared memory whose rows are 128 bytes,
+// 16-byte pieces in the 128-byte swizzle; `half`: of bf16, which 64 bytes.
 __device__ __forceinline__ void stage32(uint8_t* box, int lane, int, const float (&v)[32], float) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
@@ -154,29 +161,22 @@ __device__ __forceinline__ void stage32(uint8_t* box, int lane, int half, const 
         make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
                    pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
 }
-__device__ __forceinline__ void load_columns(uint32_t taddr, float (&v)[32]) {
-  uint32_t r[32];
-  tmem_ld32(taddr, r);
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
-}
-__device__ __forceinline__ void load_columns(uint32_t taddr, float (&v)[16]) {
-  uint32_t r[16];
-  tmem_ld16(taddr, r);
-  tmem_ld_wait();
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
-}
+// 32 or 16 columns of a lane's row; the values hold after tmem_ld_wait().
+__device__ __forceinline__ void start_columns(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
+__device__ __forceinline__ void start_columns(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
-// A warp's two boxes in turn, each to memory by one TMA store.
+// A warp's boxes in turn, each to memory by one TMA store.
+template <int BOXES>
 struct Staging {
   uint8_t* base;
   int lane, turn;
-  __device__ __forceinline__ uint8_t* take() {  // the box of two stores ago has left
-    if (lane == 0) bulk_wait_read1();
+  __device__ __forceinline__ uint8_t* take() {  // the box of BOXES stores ago has left
+    if (lane == 0) {
+      if (BOXES == 1) bulk_wait_read0();
+      else bulk_wait_read1();
+    }
     __syncwarp();
-    uint8_t* box = base + (turn & 1) * 4096;
+    uint8_t* box = base + (BOXES == 1 ? 0 : (turn & 1) * 4096);
     ++turn;
     return box;
   }
@@ -190,16 +190,413 @@ struct Staging {
   }
 };
 
-template <int KIND, bool AMN, bool BMN, int BN, int EPI, typename OutT>
-__global__ void __launch_bounds__(Layout<KIND, BN>::kThreads, 1)
-gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
-  using L = Layout<KIND, BN>;
+// The terms of pair 0 .. 5 of fp32 operands, small products first: (2,0) (0,2)
+// (1,1) (1,0) (0,1) (0,0).
+__device__ __forceinline__ int term_of_a(const Params& p, int pair) {
+  return p.pairs == 1 ? 0 : (0x001102 >> (4 * pair)) & 15;
+}
+__device__ __forceinline__ int term_of_b(const Params& p, int pair) {
+  return p.pairs == 1 ? 0 : (0x010120 >> (4 * pair)) & 15;
+}
+// Where a tile's first step lies.
+struct Step {
+  int pair, kb, kpart;
+  __device__ __forceinline__ Step(const Params& p, int it) {
+    pair = it % p.pairs;
+    kb = it / p.pairs;
+    kpart = kb / p.k_blocks;
+    kb -= kpart * p.k_blocks;
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    if (++pair == p.pairs) {
+      pair = 0;
+      if (++kb == p.k_blocks) kb = 0, ++kpart;
+    }
+  }
+};
+__device__ __forceinline__ int map_of(int by, const Tile& tile, const Step& s) {
+  return by == kByPart ? tile.part : by == kByKPart ? s.kpart : 0;
+}
+
+// Scale words (four K blocks) of 128 rows from r0 on, as the copy to TMEM takes
+// them: rows lane, lane + 32, + 64, + 96 side by side.
+__device__ __forceinline__ uint4 scale_words(const uint32_t* words, int rows, int group, int r0, int lane) {
+  const uint32_t* at = words + (size_t)group * rows;
+  auto one = [&](int r) { return r < rows ? at[r] : 0u; };
+  return make_uint4(one(r0 + lane), one(r0 + lane + 32), one(r0 + lane + 64), one(r0 + lane + 96));
+}
+
+// ------------------------------------------------------ two CTAs per tile
+
+template <int KIND, typename OutT>
+struct PairLayout {
+  static constexpr int kA = 128 * 128, kStage = 2 * kA;  // a CTA's halves of A and B
+  static constexpr int kStages = 5;
+  static constexpr int kBoxes = KIND == kMx8 ? 1 : 2;
+  static constexpr int kStaging = 8 * kBoxes * 4096;
+  static constexpr int kScales = KIND == kMx8 ? 2 * (512 + 1024) : 0;
+  static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
+  static_assert(kBytes <= kSmem, "shared memory");
+  // TMEM: two accumulators, or one and two slots of scales
+  static constexpr int kAccs = KIND == kMx8 ? 1 : 2, kScaleCol = 256;
+  static constexpr int kFirst = KIND == kMx8 ? 3 : 2;  // warps that carry out
+  static constexpr int kThreads = (kFirst + 8) * 32;
+};
+
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// Address of the first CTA's copy of a shared variable.
+__device__ __forceinline__ uint32_t in_first(const void* p) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
+  return a;
+}
+__device__ __forceinline__ void arrive_in_first(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+}
+// Copy to this CTA's shared memory that reports to the first CTA's barrier.
+__device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma_bf16(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t more) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(more)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma_mx8(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t a_scale,
+                                             uint32_t b_scale, uint32_t more) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(a_scale), "r"(b_scale), "r"(more)
+      : "memory");
+}
+__device__ __forceinline__ void pair_copy_scales(uint32_t tmem, const uint8_t* smem) {
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem),
+               "l"(smem_desc(smem_u32(smem), 0, 128, SW_NONE))
+               : "memory");
+}
+// Arrives on both CTAs' copies of bar when the products issued so far are done.
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+// Tiles of 256 rows x 256 columns; EPI kGated: the columns are 128 of the gate
+// (B of the first CTA) and the same 128 of the other projection (B of the
+// second), and the result has 128.
+template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<KIND, OutT>::kThreads, 1)
+gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using L = PairLayout<KIND, OutT>;
+  constexpr int S = L::kStages, kAccs = L::kAccs;
+  constexpr bool kSum = sizeof(OutT) == 4;  // sums move to registers
+  constexpr int kBox = 128 / sizeof(OutT);  // columns stored at a time
+  extern __shared__ uint8_t raw[];
+  uint8_t* sm = align1024(raw);
+  uint8_t* staging = sm + S * L::kStage;
+  uint8_t* scales = staging + L::kStaging;
+  Bars& bars = *reinterpret_cast<Bars*>(scales + L::kScales);
+  volatile int* abort_flag = &bars.abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_rank(), pairs = gridDim.x / 2;
+  const int tiles = p.m_tiles * p.n_tiles * p.parts * p.splits;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.acc_full[i], 1);
+      mbar_init(&bars.acc_empty[i], 16);
+      mbar_init(&bars.sf_full[i], 2);
+      mbar_init(&bars.sf_empty[i], 1);
+    }
+    mbar_init(&bars.fin, 1);
+    bars.abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars.tmem))
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers and TMEM are there
+  tc_fence_after_sync();
+  // all CTAs of the grid run at once: a join behind it may take its place
+  cudaTriggerProgrammaticLaunchCompletion();
+  const uint32_t tmem = bars.tmem;
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- copies
+    if (elect_one()) {
+      for (int i = 0; i < 2; ++i) {
+        tma_prefetch(&maps.a[i]);
+        tma_prefetch(&maps.b[i]);
+      }
+    }
+    uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
+    bool ok = true;
+    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_of(p, t);
+      const int m0 = tile.m * 256 + rank * 128;
+      const int n0 = EPI == kGated ? tile.n * 128 : tile.n * 256 + rank * 128;
+      Step s(p, tile.it0);
+      for (int it = tile.it0; it < tile.it1; ++it, ++n, s.next(p)) {
+        if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
+          uint8_t* a = sm + st * L::kStage;
+          uint8_t* b = a + L::kA;
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * L::kStage);
+          const uint32_t bar = in_first(&bars.full[st]);
+          const int k = s.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, s.pair), pb = term_of_b(p, s.pair);
+          const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, s)];
+          const CUtensorMap* bm = &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, s)];
+          if (AMN) {
+            pair_load_3d(a, am, bar, m0, k, pa);
+            pair_load_3d(a + 8192, am, bar, m0 + 64, k, pa);
+          } else {
+            pair_load_3d(a, am, bar, k, m0, pa);
+          }
+          if (BMN) {
+            pair_load_3d(b, bm, bar, n0, k, pb);
+            pair_load_3d(b + 8192, bm, bar, n0 + 64, k, pb);
+          } else {
+            pair_load_3d(b, bm, bar, k, n0, pb);
+          }
+        }
+        __syncwarp();
+        if (++st == S) st = 0, ++round;
+      }
+    }
+    // nothing may land in shared memory behind the kernel's end (the first
+    // CTA's barriers count both CTAs' copies)
+    if (rank == 0)
+      for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&bars.full[i % S], (i / S) & 1, nullptr, kWaitNs);
+  } else if (warp == 1) {
+    // ------------------------------------------------------------ products
+    if (rank == 0) {
+      const uint32_t idesc = idesc_bf16(256, 256, AMN, BMN);
+      const uint32_t first_stage = smem_u32(sm);
+      const uint64_t a0 = AMN ? smem_desc(first_stage, 8192, 1024, SW_128B) : smem_desc(first_stage, 16, 1024, SW_128B);
+      const uint64_t b0 = BMN ? smem_desc(first_stage + L::kA, 8192, 1024, SW_128B)
+                              : smem_desc(first_stage + L::kA, 16, 1024, SW_128B);
+      uint32_t st = 0, phase = 0, nc = 0, ns = 0;
+      bool ok = true;
+      for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
+        const Tile tile = tile_of(p, t);
+        uint32_t d = 0;
+        int left = 0;  // steps of this accumulator
+        for (int it = tile.it0; it < tile.it1; ++it) {
+          const bool first = left == 0;
+          if (first) {
+            left = kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
+            d = tmem + (nc % kAccs) * 256;
+            if (nc >= kAccs && !warp_wait(&bars.acc_empty[nc % kAccs], (nc / kAccs - 1) & 1, p.status, abort_flag)) {
+              ok = false;
+              break;
+            }
+          }
+          const uint32_t slot = ns & 1, sf = tmem + L::kScaleCol + slot * 16;
+          const bool new_scales = KIND == kMx8 && (it == tile.it0 || (it & 3) == 0);
+          if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / 2) & 1, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          if (!warp_wait(&bars.full[st], phase, p.status, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          const bool last_scales = KIND == kMx8 && (it + 1 == tile.it1 || (it & 3) == 3);
+          --left;
+          if (elect_one()) {
+            if (new_scales) {
+              const uint8_t* from = scales + slot * (L::kScales / 2);
+#pragma unroll
+              for (int i = 0; i < 3; ++i) pair_copy_scales(sf + 4 * i, from + 512 * i);
+            }
+            const uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + (BMN ? kk * 128 : kk * 2);
+              const uint32_t more = !first || kk > 0;
+              if (KIND == kMx8)
+                pair_mma_mx8(d, ak, bk, idesc_mx8(256, 256, it & 3), sf, sf + 4, more);
+              else
+                pair_mma_bf16(d, ak, bk, idesc, more);
+            }
+            pair_commit(&bars.empty[st]);
+            if (last_scales) pair_commit(&bars.sf_empty[slot]);
+            if (left == 0) pair_commit(&bars.acc_full[nc % kAccs]);
+          }
+          __syncwarp();
+          if (last_scales) ++ns;
+          if (left == 0) ++nc;
+          if (++st == S) st = 0, phase ^= 1;
+        }
+      }
+      // no product may be in flight when TMEM is freed
+      if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         smem_u32(&bars.fin))
+                     : "memory");
+      __syncwarp();
+      mbar_wait(&bars.fin, 0, nullptr, kWaitNs);
+    }
+  } else if (warp >= L::kFirst) {
+    // ------------------------------------------------------- finished tiles
+    // Two warps for each quarter of the lanes, 128 columns each.
+    const int quarter = warp & 3, half = (warp - L::kFirst) / 4;
+    Staging<L::kBoxes> out{staging + (warp - L::kFirst) * L::kBoxes * 4096, lane, 0};
+    uint32_t nc = 0;  // accumulators taken
+    bool ok = true;
+    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_of(p, t);
+      float f[4][32];  // a lane's row: 128 columns, or 64 of each projection
+      if (kSum) {
+#pragma unroll
+        for (int i = 0; i < 128; ++i) f[i / 32][i % 32] = 0.f;
+      }
+#pragma unroll 1
+      for (int it = tile.it0; it < tile.it1;) {
+        const int acc = nc % kAccs;
+        if (!__all_sync(0xffffffffu, wait_or_fail(&bars.acc_full[acc], (nc / kAccs) & 1, p.status, abort_flag))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const uint32_t d = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
+        auto column = [&](int i) { return EPI == kGated ? (i & 1) * 32 + half * 64 + (i >> 1) * 128 : half * 128 + 32 * i; };
+        if constexpr (!kSum) {
+          uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(f);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(d + column(i), r[i]);
+          tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint32_t r[16];
+            tmem_ld16(d + column(i / 2) + 16 * (i & 1), r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) f[i / 2][16 * (i & 1) + j] += __uint_as_float(r[j]);
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) arrive_in_first(&bars.acc_empty[acc]);
+        ++nc;
+        it += kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
+      }
+      if (!ok) break;
+      const int y = tile.m * 256 + rank * 128 + quarter * 32;
+      auto send = [&](const CUtensorMap* map, int first, int columns, int x, int z) {
+#pragma unroll
+        for (int c = 0; c < columns; c += kBox) {
+          uint8_t* box = out.take();
+#pragma unroll
+          for (int h = 0; h < kBox / 32; ++h) stage32(box, lane, h, f[first + c / 32 + h], OutT{});
+          out.send(map, box, x + c, y, z);
+        }
+      };
+      if constexpr (EPI == kPlain) {
+        send(&maps.c[p.c_by_part ? tile.part : 0], 0, 128, tile.n * 256 + half * 128,
+             p.c_by_part ? 0 : tile.split * p.parts + tile.part);
+      } else {
+        const int x = tile.n * 128 + half * 64;
+        if (p.keep) {
+          send(&maps.c[1], 0, 64, x, 0);
+          send(&maps.c[2], 2, 64, x, 0);
+        }
+        act::by_act(p.act, [&](auto a) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              f[i][j] = act::value<decltype(a)::value, sizeof(OutT) == 2>(f[i][j]) * f[i + 2][j];
+        });
+        send(&maps.c[0], 0, 64, x, 0);
+      }
+    }
+    if (lane == 0) bulk_wait0();
+  } else if (KIND == kMx8) {
+    // -------------------------------------------------------------- scales
+    // Of this CTA's rows of A and of all 256 columns, which both CTAs need.
+    uint32_t ns = 0;
+    bool ok = true;
+    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
+      const Tile tile = tile_of(p, t);
+      for (int g = tile.it0 >> 2; g <= (tile.it1 - 1) >> 2; ++g, ++ns) {
+        const uint32_t slot = ns & 1;
+        uint4 w[3];
+        w[0] = scale_words(p.a_scales, p.a_rows, g, tile.m * 256 + rank * 128, lane);
+        w[1] = scale_words(p.b_scales, p.b_rows, g, tile.n * 256, lane);
+        w[2] = scale_words(p.b_scales, p.b_rows, g, tile.n * 256 + 128, lane);
+        if (ns >= 2 &&
+            !__all_sync(0xffffffffu, wait_or_fail(&bars.sf_empty[slot], (ns / 2 - 1) & 1, p.status, abort_flag))) {
+          ok = false;
+          break;
+        }
+        uint4* to = reinterpret_cast<uint4*>(scales + slot * (L::kScales / 2));
+#pragma unroll
+        for (int i = 0; i < 3; ++i) to[32 * i + lane] = w[i];
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_in_first(&bars.sf_full[slot]);
+      }
+    }
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  cluster_sync();  // neither CTA's products read the other's memory any more
+  if (warp == 1) asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+}
+
+// ------------------------------------------------------- one CTA per tile
+
+template <int KIND, int BN>
+struct TokensLayout {
+  static constexpr int kA = 128 * 128, kB = BN * 128, kStage = kA + kB;
+  static constexpr int kStaging = 4 * 2 * 4096;  // two boxes per warp that carries out
+  static constexpr int kScales = KIND == kMx8 ? 2 * (512 + 512) : 0;
+  static constexpr int kFree = kSmem - 1024 - kStaging - kScales - kBarBytes;
+  static constexpr int kStages = kFree / kStage < 12 ? kFree / kStage : 12;
+  static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
+  static constexpr int kScaleCol = 2 * BN;  // TMEM column of the scales: two slots of 4 + 4
+  static constexpr int kCols = 2 * BN + (KIND == kMx8 ? 32 : 0);
+  static constexpr int kAlloc = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
+  static constexpr int kThreads = KIND == kMx8 ? 224 : 192;
+};
+
+// Tiles of 128 rows (weights) x BN columns (tokens), fp32 partial sums.
+template <int KIND, bool AMN, int BN>
+__global__ void __launch_bounds__(TokensLayout<KIND, BN>::kThreads, 1)
+gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
+  using L = TokensLayout<KIND, BN>;
   constexpr int S = L::kStages;
-  constexpr int kHalfN = EPI == kGated ? BN / 2 : BN;  // columns of the output per tile
-  constexpr bool kSum = sizeof(OutT) == 4 && BN <= 128;  // sums move to registers
-  constexpr int kW = BN < 32 ? BN : 32;                  // columns read from TMEM at a time
-  constexpr int kBox = 128 / sizeof(OutT);               // columns stored at a time
-  static_assert(BN >= 32 || (kSum && EPI == kPlain), "16 columns are partial sums");
+  constexpr int kW = BN < 32 ? BN : 32;  // columns read from TMEM at a time
   extern __shared__ uint8_t raw[];
   uint8_t* sm = align1024(raw);
   uint8_t* staging = sm + S * L::kStage;
@@ -234,115 +631,87 @@ gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 
   if (warp == 0) {
     // -------------------------------------------------------------- copies
-    if (lane == 0) {
+    if (elect_one()) {
       for (int i = 0; i < 2; ++i) {
         tma_prefetch(&maps.a[i]);
         tma_prefetch(&maps.b[i]);
       }
-      uint32_t n = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile tile = tile_of(p, t);
-        int pair = tile.it0 % p.pairs, kb = tile.it0 / p.pairs, kpart = 0;
-        while (kb >= p.k_blocks) kb -= p.k_blocks, ++kpart;
-        for (int it = tile.it0; it < tile.it1; ++it, ++n) {
-          const int st = n % S;
-          if (n >= S && !wait_or_fail(&bars.empty[st], (n / S - 1) & 1, p.status, abort_flag)) {
-            ok = false;
-            break;
-          }
+    }
+    uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile tile = tile_of(p, t);
+      Step s(p, tile.it0);
+      for (int it = tile.it0; it < tile.it1; ++it, ++n, s.next(p)) {
+        if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           uint8_t* a = sm + st * L::kStage;
-          uint8_t* b = a + L::kA;
           uint64_t* bar = &bars.full[st];
           mbar_arrive_expect_tx(bar, L::kStage);
-          // the terms of pair 0 .. 5, small products first: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0)
-          const int pa = p.pairs == 1 ? 0 : (0x001102 >> (4 * pair)) & 15;
-          const int pb = p.pairs == 1 ? 0 : (0x010120 >> (4 * pair)) & 15;
-          const int k = kb * (KIND == kMx8 ? 128 : 64);
-          const CUtensorMap* am = &maps.a[p.a_by == kByPart ? tile.part : p.a_by == kByKPart ? kpart : 0];
-          const CUtensorMap* bm = &maps.b[p.b_by == kByPart ? tile.part : p.b_by == kByKPart ? kpart : 0];
+          const int k = s.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, s.pair);
+          const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, s)];
           if (AMN) {
             tma_load_3d(a, am, bar, tile.m * 128, k, pa);
             tma_load_3d(a + 8192, am, bar, tile.m * 128 + 64, k, pa);
           } else {
             tma_load_3d(a, am, bar, k, tile.m * 128, pa);
           }
-          if (EPI == kGated) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint8_t* bh = b + h * (BN / 2) * 128;
-              if (BMN) {
-                for (int i = 0; i < BN / 128; ++i)
-                  tma_load_3d(bh + i * 8192, &maps.b[h], bar, tile.n * kHalfN + 64 * i, k, pb);
-              } else {
-                tma_load_3d(bh, &maps.b[h], bar, k, tile.n * kHalfN, pb);
-              }
-            }
-          } else if (BMN) {
-            for (int i = 0; i < BN / 64; ++i)
-              tma_load_3d(b + i * 8192, bm, bar, tile.n * BN + 64 * i, k, pb);
-          } else {
-            tma_load_3d(b, bm, bar, k, tile.n * BN, pb);
-          }
-          if (++pair == p.pairs) {
-            pair = 0;
-            if (++kb == p.k_blocks) kb = 0, ++kpart;
-          }
+          tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, s)], bar, k, tile.n * BN, term_of_b(p, s.pair));
         }
+        __syncwarp();
+        if (++st == S) st = 0, ++round;
       }
-      // nothing may land in shared memory behind the kernel's end
-      for (uint32_t i = n > S ? n - S : 0; i < n; ++i)
-        mbar_wait(&bars.full[i % S], (i / S) & 1, nullptr, kWaitNs);
     }
+    // nothing may land in shared memory behind the kernel's end
+    for (uint32_t i = n > S ? n - S : 0; i < n; ++i) mbar_wait(&bars.full[i % S], (i / S) & 1, nullptr, kWaitNs);
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
-    if (lane == 0) {
-      const uint32_t idesc = idesc_bf16(128, BN, AMN, BMN);
-      uint32_t n = 0, nc = 0, ns = 0;
-      bool ok = true;
-      for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-        const Tile tile = tile_of(p, t);
-        uint32_t d = 0;
-        int left = 0;  // steps of this accumulator
-        for (int it = tile.it0; it < tile.it1; ++it, ++n) {
-          const int st = n % S;
-          const bool first = left == 0;
-          if (first) {
-            left = kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
-            d = tmem + (nc & 1) * BN;
-            if (nc >= 2 && !wait_or_fail(&bars.acc_empty[nc & 1], (nc / 2 - 1) & 1, p.status, abort_flag)) {
-              ok = false;
-              break;
-            }
-            tc_fence_after_sync();
-          }
-          uint32_t sf = 0;
-          if (KIND == kMx8) {
-            const uint32_t slot = ns & 1;
-            sf = tmem + L::kScaleCol + slot * 16;
-            if (it == tile.it0 || (it & 3) == 0) {
-              if (!wait_or_fail(&bars.sf_full[slot], (ns / 2) & 1, p.status, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              const uint8_t* from = scales + slot * (L::kScales / 2);
-              copy_scales(sf, from);
-#pragma unroll
-              for (int i = 0; i < (BN + 127) / 128; ++i) copy_scales(sf + 4 + 4 * i, from + 512 + 512 * i);
-            }
-          }
-          if (!wait_or_fail(&bars.full[st], (n / S) & 1, p.status, abort_flag)) {
+    const uint32_t idesc = idesc_bf16(128, BN, AMN, false);
+    const uint32_t first_stage = smem_u32(sm);
+    const uint64_t a0 = AMN ? smem_desc(first_stage, 8192, 1024, SW_128B) : smem_desc(first_stage, 16, 1024, SW_128B);
+    const uint64_t b0 = smem_desc(first_stage + L::kA, 16, 1024, SW_128B);
+    uint32_t st = 0, phase = 0, nc = 0, ns = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
+      const Tile tile = tile_of(p, t);
+      uint32_t d = 0;
+      int left = 0;  // steps of this accumulator
+      for (int it = tile.it0; it < tile.it1; ++it) {
+        const bool first = left == 0;
+        if (first) {
+          left = min(p.chunk, tile.it1 - it);
+          d = tmem + (nc & 1) * BN;
+          if (nc >= 2 && !warp_wait(&bars.acc_empty[nc & 1], (nc / 2 - 1) & 1, p.status, abort_flag)) {
             ok = false;
             break;
           }
-          tc_fence_after_sync();
-          const uint32_t a = smem_u32(sm + st * L::kStage), b = a + L::kA;
-          const uint64_t ad = AMN ? smem_desc(a, 8192, 1024, SW_128B) : smem_desc(a, 16, 1024, SW_128B);
-          const uint64_t bd = BMN ? smem_desc(b, 8192, 1024, SW_128B) : smem_desc(b, 16, 1024, SW_128B);
+        }
+        const uint32_t slot = ns & 1, sf = tmem + L::kScaleCol + slot * 16;
+        const bool new_scales = KIND == kMx8 && (it == tile.it0 || (it & 3) == 0);
+        if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / 2) & 1, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        if (!warp_wait(&bars.full[st], phase, p.status, abort_flag)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after_sync();
+        const bool last_scales = KIND == kMx8 && (it + 1 == tile.it1 || (it & 3) == 3);
+        --left;
+        if (elect_one()) {
+          if (new_scales) {
+            const uint8_t* from = scales + slot * (L::kScales / 2);
+            copy_scales(sf, from);
+            copy_scales(sf + 4, from + 512);
+          }
+          const uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
 #pragma unroll
           for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + (BMN ? kk * 128 : kk * 2);
+            const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + kk * 2;
             const uint32_t more = !first || kk > 0;
             if (KIND == kMx8)
               mma_mx8(d, ak, bk, idesc_mx8(128, BN, it & 3), sf, sf + 4, more);
@@ -350,160 +719,88 @@ gemm_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
               mma_bf16(d, ak, bk, idesc, more);
           }
           mma_commit(&bars.empty[st]);
-          if (KIND == kMx8 && (it + 1 == tile.it1 || (it & 3) == 3)) {
-            mma_commit(&bars.sf_empty[ns & 1]);
-            ++ns;
-          }
-          if (--left == 0) {
-            mma_commit(&bars.acc_full[nc & 1]);
-            ++nc;
-          }
+          if (last_scales) mma_commit(&bars.sf_empty[slot]);
+          if (left == 0) mma_commit(&bars.acc_full[nc & 1]);
         }
+        __syncwarp();
+        if (last_scales) ++ns;
+        if (left == 0) ++nc;
+        if (++st == S) st = 0, phase ^= 1;
       }
-      // no product may be in flight when TMEM is freed
-      mma_commit(&bars.fin);
-      mbar_wait(&bars.fin, 0, nullptr, kWaitNs);
     }
+    // no product may be in flight when TMEM is freed
+    if (elect_one()) mma_commit(&bars.fin);
+    __syncwarp();
+    mbar_wait(&bars.fin, 0, nullptr, kWaitNs);
   } else if (warp < 6) {
     // ------------------------------------------------------- finished tiles
     const int quarter = warp & 3;
-    Staging out{staging + (warp - 2) * 8192, lane, 0};
+    Staging<2> out{staging + (warp - 2) * 8192, lane, 0};
     uint32_t nc = 0;  // accumulators taken
-    auto ready = [&] {
-      if (!__all_sync(0xffffffffu, wait_or_fail(&bars.acc_full[nc & 1], (nc / 2) & 1, p.status, abort_flag)))
-        return false;
-      tc_fence_after_sync();
-      return true;
-    };
-    auto release = [&] {  // the accumulator has been read
-      tc_fence_before_sync();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&bars.acc_empty[nc & 1]);
-      ++nc;
-    };
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const Tile tile = tile_of(p, t);
-      const uint32_t lanes = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int y = tile.m * 128 + quarter * 32, z = p.c_by_part ? 0 : tile.split * p.parts + tile.part;
-      const CUtensorMap* cm = &maps.c[p.c_by_part ? tile.part : 0];
-      float sum[kSum ? BN / kW : 1][kW];  // a lane's row
-      if constexpr (kSum) {
-        for (int it = tile.it0; it < tile.it1; it += min(p.chunk, tile.it1 - it)) {
-          if (!ready()) {
-            ok = false;
-            break;
-          }
-          const uint32_t d = lanes + (nc & 1) * BN;
+      float sum[BN / kW][kW];  // a lane's row
 #pragma unroll
-          for (int c = 0; c < BN / kW; ++c) {
-            float v[kW];
-            load_columns(d + c * kW, v);
-#pragma unroll
-            for (int i = 0; i < kW; ++i) sum[c][i] = it == tile.it0 ? v[i] : sum[c][i] + v[i];
-          }
-          release();
+      for (int i = 0; i < BN; ++i) sum[i / kW][i % kW] = 0.f;
+#pragma unroll 1
+      for (int it = tile.it0; it < tile.it1; it += min(p.chunk, tile.it1 - it)) {
+        if (!__all_sync(0xffffffffu, wait_or_fail(&bars.acc_full[nc & 1], (nc / 2) & 1, p.status, abort_flag))) {
+          ok = false;
+          break;
         }
-        if (!ok) break;
-      } else if (!ready()) {
-        break;
+        tc_fence_after_sync();
+        const uint32_t d = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + (nc & 1) * BN;
+#pragma unroll
+        for (int c = 0; c < BN / kW; ++c) {
+          uint32_t r[kW];
+          start_columns(d + c * kW, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kW; ++i) sum[c][i] += __uint_as_float(r[i]);
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.acc_empty[nc & 1]);
+        ++nc;
       }
-      const uint32_t d = lanes + (nc & 1) * BN;
-      // 32 columns c .. of the tile
-      auto columns = [&](int c, float(&v)[kW]) {
-        if constexpr (kSum) {
-#pragma unroll
-          for (int i = 0; i < kW; ++i) v[i] = sum[c / kW][i];
-        } else {
-          load_columns(d + c, v);
-        }
-      };
+      if (!ok) break;
+      const int y = tile.m * 128 + quarter * 32, z = tile.split * p.parts + tile.part;
       if constexpr (BN < 32) {
         uint8_t* box = out.take();  // rows of 64 bytes
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<float4*>(box + sw64_offset(lane, c * 16)) =
               make_float4(sum[0][4 * c], sum[0][4 * c + 1], sum[0][4 * c + 2], sum[0][4 * c + 3]);
-        out.send(cm, box, tile.n * BN, y, z);
-      } else if constexpr (EPI == kPlain) {
-#pragma unroll kSum ? BN / kBox : 1
-        for (int c = 0; c < BN; c += kBox) {
-          uint8_t* box = out.take();
-#pragma unroll
-          for (int h = 0; h < kBox / 32; ++h) {
-            float v[32];
-            columns(c + 32 * h, v);
-            stage32(box, lane, h, v, OutT{});
-          }
-          if (!kSum && c + kBox == BN) release();
-          out.send(cm, box, tile.n * BN + c, y, z);
-        }
+        out.send(&maps.c[0], box, tile.n * BN, y, z);
       } else {
-        constexpr int kH = kBox / 32;
-        constexpr bool kFast = sizeof(OutT) == 2;
-#pragma unroll kSum ? kHalfN / kBox : 1
-        for (int c = 0; c < kHalfN; c += kBox) {
-          float g[kH][32], u[kH][32];
 #pragma unroll
-          for (int h = 0; h < kH; ++h) {
-            columns(c + 32 * h, g[h]);
-            columns(kHalfN + c + 32 * h, u[h]);
-          }
-          if (!kSum && c + kBox == kHalfN) release();
-          const int x = tile.n * kHalfN + c;
-          if (p.keep) {
-            uint8_t* box = out.take();
-#pragma unroll
-            for (int h = 0; h < kH; ++h) stage32(box, lane, h, g[h], OutT{});
-            out.send(&maps.c[1], box, x, y, 0);
-            box = out.take();
-#pragma unroll
-            for (int h = 0; h < kH; ++h) stage32(box, lane, h, u[h], OutT{});
-            out.send(&maps.c[2], box, x, y, 0);
-          }
-          act::by_act(p.act, [&](auto a) {
-#pragma unroll
-            for (int h = 0; h < kH; ++h)
-#pragma unroll
-              for (int i = 0; i < 32; ++i) g[h][i] = act::value<decltype(a)::value, kFast>(g[h][i]) * u[h][i];
-          });
+        for (int c = 0; c < BN / 32; ++c) {
           uint8_t* box = out.take();
-#pragma unroll
-          for (int h = 0; h < kH; ++h) stage32(box, lane, h, g[h], OutT{});
-          out.send(&maps.c[0], box, x, y, 0);
+          stage32(box, lane, 0, sum[c], 0.f);
+          out.send(&maps.c[0], box, tile.n * BN + 32 * c, y, z);
         }
       }
     }
     if (lane == 0) bulk_wait0();
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
-    // Words of four K blocks: rows lane, lane + 32, + 64, + 96 side by side.
     uint32_t ns = 0;
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const Tile tile = tile_of(p, t);
       for (int g = tile.it0 >> 2; g <= (tile.it1 - 1) >> 2; ++g, ++ns) {
         const uint32_t slot = ns & 1;
-        uint4 w[1 + (BN + 127) / 128];
-        auto four = [&](const uint32_t* s, int rows, int r0) {
-          const uint32_t* at = s + (size_t)g * rows;
-          auto one = [&](int r) { return r < rows ? at[r] : 0u; };
-          return make_uint4(one(r0 + lane), one(r0 + lane + 32), one(r0 + lane + 64), one(r0 + lane + 96));
-        };
-        w[0] = four(p.a_scales, p.a_rows, tile.m * 128);
-#pragma unroll
-        for (int i = 0; i < (BN + 127) / 128; ++i)
-          w[1 + i] = four(p.b_scales, p.b_rows, tile.n * BN + 128 * i);
-        if (ns >= 2) {
-          const bool free = wait_or_fail(&bars.sf_empty[slot], (ns / 2 - 1) & 1, p.status, abort_flag);
-          if (!__all_sync(0xffffffffu, free)) {
-            ok = false;
-            break;
-          }
+        const uint4 wa = scale_words(p.a_scales, p.a_rows, g, tile.m * 128, lane);
+        const uint4 wb = scale_words(p.b_scales, p.b_rows, g, tile.n * BN, lane);
+        if (ns >= 2 &&
+            !__all_sync(0xffffffffu, wait_or_fail(&bars.sf_empty[slot], (ns / 2 - 1) & 1, p.status, abort_flag))) {
+          ok = false;
+          break;
         }
         uint4* to = reinterpret_cast<uint4*>(scales + slot * (L::kScales / 2));
-#pragma unroll
-        for (int i = 0; i < 1 + (BN + 127) / 128; ++i) to[32 * i + lane] = w[i];
+        to[lane] = wa;
+        to[32 + lane] = wb;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.sf_full[slot]);
@@ -571,26 +868,46 @@ struct JoinGated {
 };
 int join_gated(const JoinGated& j, int act, int dtype, cudaStream_t st);
 
-template <int KIND, bool AMN, bool BMN, int BN, int EPI, typename OutT>
-int launch(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {
-  using L = Layout<KIND, BN>;
-  auto kernel = gemm_kernel<KIND, AMN, BMN, BN, EPI, OutT>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kBytes) != cudaSuccess)
+template <typename Kernel>
+int start(const char* name, Kernel kernel, int ctas_per_tile, int threads, int bytes, const Maps& maps,
+          const Params& p, cudaStream_t st) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
   const long long tiles = (long long)p.m_tiles * p.n_tiles * p.parts * p.splits;
   if (tiles >= (1ll << 31) - 1024) return NYS_ERR_SHAPE;
-  const int sms = plan_sms();
-  if (p.chunk < 1) return NYS_ERR_ARG;
+  const int most = plan_sms() / ctas_per_tile;
   KernelScope scope(name, st);
-  kernel<<<tiles < sms ? (int)tiles : sms, L::kThreads, L::kBytes, st>>>(maps, p);
+  kernel<<<(tiles < most ? (int)tiles : most) * ctas_per_tile, threads, bytes, st>>>(maps, p);
   return launch_status();
 }
+template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
+int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {
+  using L = PairLayout<KIND, OutT>;
+  return start(name, gemm_pair<KIND, AMN, BMN, EPI, OutT>, 2, L::kThreads, L::kBytes, maps, p, st);
+}
+template <int KIND, bool AMN>
+int launch_tokens(const char* name, int bn, const Maps& maps, const Params& p, cudaStream_t st) {
+  auto go = [&](auto n) {
+    constexpr int BN = decltype(n)::value;
+    using L = TokensLayout<KIND, BN>;
+    return start(name, gemm_tokens<KIND, AMN, BN>, 1, L::kThreads, L::kBytes, maps, p, st);
+  };
+  using std::integral_constant;
+  switch (bn) {
+    case 16: return go(integral_constant<int, 16>{});
+    case 32: return go(integral_constant<int, 32>{});
+    case 64: return go(integral_constant<int, 64>{});
+    default: return go(integral_constant<int, 128>{});
+  }
+}
+constexpr int kMostTokens = 128;  // of gemm_tokens
+inline int columns_of(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
 
 // Ranges of K that fill the SMs: as many as leave the last round of tiles
 // fullest, each at least `least` steps long, one where the tiles alone give
 // whole rounds. More ranges cost partial sums, taken as `cost` steps each.
-inline int splits_of(long long tiles, int its, int least, int most, double cost) {
-  const int sms = plan_sms();
+inline int splits_of(long long tiles, int ctas_per_tile, int its, int least, int most, double cost) {
+  const int sms = plan_sms() / ctas_per_tile;
   int best = 1;
   double best_time = 1e30;
   for (int s = 1; s <= most && (s == 1 || its / s >= least); ++s) {

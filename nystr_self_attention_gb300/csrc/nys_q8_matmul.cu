@@ -7,7 +7,7 @@
 // Up to 128 tokens the weights are the 128-row operand and the tokens the short
 // one (nothing is padded to 128 rows, so the weights stream at HBM's pace), K
 // split so that every SM has an equal share; the partial sums are joined. More
-// tokens are the rows themselves, in tiles of 128 x 128.
+// tokens are the rows themselves, in tiles of 256 x 256 by two CTAs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -30,10 +30,10 @@ struct Q8Plan {
 Q8Plan plan_of(int T, int N, int K) {
   Q8Plan q{};
   const int its = (K + 127) / 128;
-  q.turned = T <= 128;
-  q.bn = !q.turned ? 128 : T <= 16 ? 16 : T <= 32 ? 32 : T <= 64 ? 64 : 128;
-  const long long tiles = q.turned ? (N + 127) / 128 : (long long)((T + 127) / 128) * ((N + 127) / 128);
-  q.splits = splits_of(tiles, its, q.turned ? 2 : 4, 16, q.bn / 16.0);
+  q.turned = T <= kMostTokens;
+  q.bn = q.turned ? columns_of(T) : 256;
+  const long long tiles = q.turned ? (N + 127) / 128 : (long long)((T + 255) / 256) * ((N + 255) / 256);
+  q.splits = splits_of(tiles, q.turned ? 1 : 2, its, q.turned ? 2 : 4, 16, q.bn / 16.0);
   q.its_per_split = (its + q.splits - 1) / q.splits;
   if (q.turned)
     q.bytes = (size_t)q.splits * N * q.bn * 4;
@@ -90,7 +90,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   const nys_q8_t &rows = plan.turned ? *w : *a, &cols = plan.turned ? *a : *w;
   Params p{};
   if ((rc = operator_status(dev, &p.status)) != NYS_OK) return rc;
-  p.m_tiles = (rows.rows + 127) / 128;
+  p.m_tiles = plan.turned ? (rows.rows + 127) / 128 : (rows.rows + 255) / 256;
   p.n_tiles = (cols.rows + plan.bn - 1) / plan.bn;
   p.parts = p.pairs = 1;
   p.splits = plan.splits;
@@ -103,7 +103,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   p.a_rows = rows.rows;
   p.b_rows = cols.rows;
   Maps maps{};
-  bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.bn);
+  bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.turned ? plan.bn : 128);
   const bool direct = !plan.turned && plan.splits == 1;
   if (direct)
     ok = ok && map_out(&maps.c[0], Matrix{out, T, N, out_stride, dtype == NYS_FP32 ? 4 : 2});
@@ -116,18 +116,12 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   maps.a[1] = maps.a[0];
   maps.b[1] = maps.b[0];
   const char* name = "q8_matmul";
-  if (plan.turned) {
-    switch (plan.bn) {
-      case 16: rc = launch<kMx8, false, false, 16, kPlain, float>(name, maps, p, stream); break;
-      case 32: rc = launch<kMx8, false, false, 32, kPlain, float>(name, maps, p, stream); break;
-      case 64: rc = launch<kMx8, false, false, 64, kPlain, float>(name, maps, p, stream); break;
-      default: rc = launch<kMx8, false, false, 128, kPlain, float>(name, maps, p, stream);
-    }
-  } else if (!direct || dtype == NYS_FP32) {
-    rc = launch<kMx8, false, false, 128, kPlain, float>(name, maps, p, stream);
-  } else {
-    rc = launch<kMx8, false, false, 128, kPlain, __nv_bfloat16>(name, maps, p, stream);
-  }
+  if (plan.turned)
+    rc = launch_tokens<kMx8, false>(name, plan.bn, maps, p, stream);
+  else if (!direct || dtype == NYS_FP32)
+    rc = launch_pair<kMx8, false, false, kPlain, float>(name, maps, p, stream);
+  else
+    rc = launch_pair<kMx8, false, false, kPlain, __nv_bfloat16>(name, maps, p, stream);
   if (rc != NYS_OK || direct) return rc;
   const Join j{static_cast<const float*>(workspace), plan.splits, T, N, plan.turned ? plan.bn : 0,
                {out, nullptr}, {out_stride, 0}};
