@@ -130,18 +130,18 @@ Product product_of(long long M, long long N, long long k, int k_parts, int parts
                    bool may_turn) {
   Product q{};
   q.turned = may_turn && M <= kMostTokens;
-  q.bn = q.turned ? columns_of((int)M) : 256;
   q.k_blocks = (int)((k + 63) / 64);
-  const int steps = q.k_blocks * k_parts, rows = q.turned ? 128 : 256;
+  const int steps = q.k_blocks * k_parts;
   q.its = steps * pairs;
-  q.m_tiles = (int)(((q.turned ? N : M) + rows - 1) / rows);
-  // tiles of the split form; the gated one has half as many columns of each part
-  const int nt = q.turned ? 1 : (int)((N + 255) / 256);
-  const long long tiles = (long long)q.m_tiles * nt * parts;
-  q.splits = splits_of(tiles, q.turned ? 1 : 2, steps, 4, 16, q.bn / 16.0 / pairs);
-  q.its_per_split = (steps + q.splits - 1) / q.splits * pairs;  // all pairs of a block
+  const Cut cut = q.turned ? cut_tokens((N + 127) / 128 * parts, N * parts, columns_of((int)M), steps, 1, pairs, pairs > 1 ? 1 : 4)
+                           : cut_pair(M, N, steps, 1, pairs, parts, 256, gated ? 64 : 32, gated, pairs > 1 ? 1 : 4);
+  q.bn = cut.bn;
+  q.splits = cut.splits;
+  const bool fused = gated && !q.turned && q.splits == 1;  // a tile has bn / 2 columns of each part
+  q.m_tiles = (int)(q.turned ? (N + 127) / 128 : (M + 255) / 256);
+  q.n_tiles = q.turned ? 1 : (int)((N + q.bn / (fused ? 2 : 1) - 1) / (q.bn / (fused ? 2 : 1)));
+  q.its_per_split = range_of(steps, q.splits, 1) * pairs;  // all pairs of a block
   const bool direct = !q.turned && q.splits == 1;
-  q.n_tiles = gated && direct ? (int)((N + 127) / 128) : nt;
   if (q.turned)
     q.bytes = align256((size_t)q.splits * parts * N * q.bn * 4);
   else if (!direct)
@@ -228,7 +228,8 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
   p.its = q.its;
   p.its_per_split = q.its_per_split;
   p.pairs = pairs;
-  p.chunk = pairs > 1 ? pairs : q.its;  // fp32: the six products of a K block
+  p.bn = q.bn;
+  p.chunk = pairs > 1 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
   p.a_by = a_by;
   p.b_by = b_by;
   p.group = 8;
@@ -280,13 +281,13 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
   if (q.turned) {
     for (int i = 0; i < 2; ++i) ok = ok && (io ? map_mn(&maps.a[i], w[i]) : map_k(&maps.a[i], w[i], 128));
     ok = ok && map_k(&maps.b[0], xm, q.bn) &&
-         map_out(&maps.c[0], Matrix{ws + pl.part, a.f, q.bn, q.bn, 4, 2 * q.splits, (long long)a.f * q.bn}, q.bn == 16);
+         map_out(&maps.c[0], Matrix{ws + pl.part, a.f, q.bn, q.bn, 4, 2 * q.splits, (long long)a.f * q.bn}, q.bn == 16 ? 16 : 32);
     maps.b[1] = maps.b[0];
   } else {
     ok = map_k(&maps.a[0], xm, 128);
     maps.a[1] = maps.a[0];
     for (int i = 0; i < 2; ++i)
-      ok = ok && (io ? map_mn(&maps.b[i], w[i]) : map_k(&maps.b[i], w[i], 128));
+      ok = ok && (io ? map_mn(&maps.b[i], w[i]) : map_k(&maps.b[i], w[i], q.bn / 2));
     if (direct) {
       const int e = pl.f32 ? 4 : 2;
       ok = ok && map_out(&maps.c[0], Matrix{h, a.T, a.f, a.h, e});
@@ -331,14 +332,14 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap &wm = q.turned ? maps.a[i] : maps.b[i], &gm = q.turned ? maps.b[i] : maps.a[i];
-    ok = ok && (io ? map_k(&wm, w[i], 128) : map_mn(&wm, w[i])) &&
+    ok = ok && (io ? map_k(&wm, w[i], q.turned ? 128 : q.bn / 2) : map_mn(&wm, w[i])) &&
          map_k(&gm, g[i], q.turned ? q.bn : 128);
   }
   char* part = ws + pl.part;
   if (direct)
     ok = ok && map_out(&maps.c[0], Matrix{dx, a.T, a.d, a.dx, pl.f32 ? 4 : 2});
   else if (q.turned)
-    ok = ok && map_out(&maps.c[0], Matrix{part, a.d, q.bn, q.bn, 4, q.splits, (long long)a.d * q.bn}, q.bn == 16);
+    ok = ok && map_out(&maps.c[0], Matrix{part, a.d, q.bn, q.bn, 4, q.splits, (long long)a.d * q.bn}, q.bn == 16 ? 16 : 32);
   else
     ok = ok && map_out(&maps.c[0], Matrix{part, a.T, a.d, a.d, 4, q.splits, (long long)a.T * a.d});
   if (!ok) return tensor_map_error(__FILE__, __LINE__);

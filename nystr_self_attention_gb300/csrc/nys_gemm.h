@@ -2,11 +2,13 @@
 // module: D[m][n] = sum over k of A[m][k] B[n][k], accumulated in fp32 in TMEM.
 //
 // Two kernels, both persistent: a warp issues the TMA copies, one the products,
-// and others carry finished tiles out while the next ones run; K advances 128
-// bytes per stage, 64 bf16 or 128 e4m3, four instructions.
+// and others carry finished tiles out while the next ones run. A step of K is 128
+// bytes, 64 bf16 or 128 e4m3, four instructions; a stage holds two steps, since a
+// wait and a commit cost the issuing warp some 150 cycles (with one step per stage
+// it took 650 cycles a step, where the tensor cores need 450 to 512).
 //   gemm_pair: tiles of 256 x 256 by a cluster of two CTAs. Each holds half of A's
 //     rows and half of B's in shared memory and the instruction reads both CTAs'
-//     halves of B, so a CTA fetches 32 KB per stage where a tile of its own would
+//     halves of B, so a CTA fetches 32 KB per step where a tile of its own would
 //     take 48 (and 96 bytes a cycle instead of 64 out of shared memory).
 //   gemm_tokens: tiles of 128 rows x up to 128 columns by one CTA, for products
 //     with few columns (tokens) whose other operand (weights) has to stream.
@@ -54,7 +56,8 @@ struct Params {
   int splits;            // ranges of its; each writes a plane of fp32 partial sums
   int k_blocks;          // 128-byte blocks of one K part
   int its, its_per_split;  // K parts x k_blocks x pairs
-  int chunk;             // steps summed in TMEM before the sum moves to registers (fp32 results)
+  int bn;                // columns of a tile (gemm_pair)
+  int chunk;             // steps (even) summed in TMEM before the sum moves to registers (fp32 results)
   int pairs;             // 1, or 6 pairs of the three terms of fp32 operands
   int a_by, b_by;        // By
   int c_by_part;         // results of part i to c[i]; else to plane split * parts + part of c[0]
@@ -138,26 +141,27 @@ __device__ __forceinline__ uint32_t idesc_mx8(int M, int N, uint32_t id) {
 
 // Barriers and the like at the end of a kernel's shared memory.
 struct Bars {
-  uint64_t full[12], empty[12], acc_full[2], acc_empty[2], sf_full[2], sf_empty[2], fin;
+  uint64_t full[12], empty[12], acc_full[2], acc_empty[2], sf_full[4], sf_empty[4], fin;
   uint32_t tmem;
   int abort;
 };
 constexpr int kBarBytes = 512;
 static_assert(sizeof(Bars) <= kBarBytes, "barriers");
 constexpr int kSmem = 232448;  // of a CTA
+constexpr int kSlots = 4;      // scale words of four K blocks each on their way
 
-// 32 columns of a lane's row to a box in shared memory whose rows are 128 bytes,
-// 16-byte pieces in the 128-byte swizzle; `half`: of bf16, which 64 bytes.
-__device__ __forceinline__ void stage32(uint8_t* box, int lane, int, const float (&v)[32], float) {
+// 32 columns of a lane's row to a box in shared memory: rows of 128 bytes (fp32)
+// or 64 (bf16), 16-byte pieces in the swizzle of that width.
+__device__ __forceinline__ void stage32(uint8_t* box, int lane, const float (&v)[32], float) {
 #pragma unroll
   for (int c = 0; c < 8; ++c)
-    *reinterpret_cast<float4*>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) =
+    *reinterpret_cast<float4*>(box + sw128_offset(lane, c * 16)) =
         make_float4(v[4 * c], v[4 * c + 1], v[4 * c + 2], v[4 * c + 3]);
 }
-__device__ __forceinline__ void stage32(uint8_t* box, int lane, int half, const float (&v)[32], __nv_bfloat16) {
+__device__ __forceinline__ void stage32(uint8_t* box, int lane, const float (&v)[32], __nv_bfloat16) {
 #pragma unroll
   for (int c = 0; c < 4; ++c)
-    *reinterpret_cast<uint4*>(box + lane * 128 + (((c + 4 * half) ^ (lane & 7)) << 4)) =
+    *reinterpret_cast<uint4*>(box + sw64_offset(lane, c * 16)) =
         make_uint4(pack_bf16x2(v[8 * c], v[8 * c + 1]), pack_bf16x2(v[8 * c + 2], v[8 * c + 3]),
                    pack_bf16x2(v[8 * c + 4], v[8 * c + 5]), pack_bf16x2(v[8 * c + 6], v[8 * c + 7]));
 }
@@ -165,8 +169,8 @@ __device__ __forceinline__ void stage32(uint8_t* box, int lane, int half, const 
 __device__ __forceinline__ void start_columns(uint32_t taddr, uint32_t (&r)[32]) { tmem_ld32(taddr, r); }
 __device__ __forceinline__ void start_columns(uint32_t taddr, uint32_t (&r)[16]) { tmem_ld16(taddr, r); }
 
-// A warp's boxes in turn, each to memory by one TMA store.
-template <int BOXES>
+// A warp's boxes (one or two) in turn, each to memory by one TMA store.
+template <int BYTES, int BOXES>
 struct Staging {
   uint8_t* base;
   int lane, turn;
@@ -176,7 +180,7 @@ struct Staging {
       else bulk_wait_read1();
     }
     __syncwarp();
-    uint8_t* box = base + (BOXES == 1 ? 0 : (turn & 1) * 4096);
+    uint8_t* box = base + (BOXES == 1 ? 0 : (turn & 1) * BYTES);
     ++turn;
     return box;
   }
@@ -219,26 +223,76 @@ __device__ __forceinline__ int map_of(int by, const Tile& tile, const Step& s) {
 }
 
 // Scale words (four K blocks) of 128 rows from r0 on, as the copy to TMEM takes
-// them: rows lane, lane + 32, + 64, + 96 side by side.
+// them: rows lane, lane + 32, + 64, + 96 side by side. Rows past the end get zeros.
 __device__ __forceinline__ uint4 scale_words(const uint32_t* words, int rows, int group, int r0, int lane) {
   const uint32_t* at = words + (size_t)group * rows;
   auto one = [&](int r) { return r < rows ? at[r] : 0u; };
   return make_uint4(one(r0 + lane), one(r0 + lane + 32), one(r0 + lane + 64), one(r0 + lane + 96));
 }
 
+// The groups of four K blocks of a CTA's tiles, in order.
+struct ScaleWalk {
+  Tile tile;
+  int t, step, tiles, group;
+  bool more;
+  __device__ __forceinline__ ScaleWalk(const Params& p, int first, int step_, int tiles_)
+      : t(first), step(step_), tiles(tiles_), more(first < tiles_) {
+    if (more) enter(p);
+  }
+  __device__ __forceinline__ void enter(const Params& p) {
+    tile = tile_of(p, t);
+    group = tile.it0 >> 2;
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    if (++group <= (tile.it1 - 1) >> 2) return;
+    t += step;
+    more = t < tiles;
+    if (more) enter(p);
+  }
+};
+
+// The scale warp's loop: load(walk, w) reads a group's words, hand_over(slot)
+// says that they are in shared memory. A group is loaded right behind the hand-over
+// of the one before it and not sooner: the fence waits for every load that is on
+// its way (2000 cycles, where four steps of products take 1800).
+template <int N, typename Load, typename Hand>
+__device__ __forceinline__ void scale_loop(const Params& p, Bars& bars, uint8_t* scales, int first, int step,
+                                           int tiles, Load load, Hand hand_over) {
+  const int lane = threadIdx.x & 31;
+  ScaleWalk at(p, first, step, tiles);
+  uint4 w[N];
+  if (at.more) load(at, w);
+#pragma unroll 1
+  for (uint32_t ns = 0; at.more; ++ns) {
+    const uint32_t slot = ns % kSlots;
+    if (ns >= kSlots && !warp_wait(&bars.sf_empty[slot], (ns / kSlots - 1) & 1, p.status, &bars.abort)) return;
+    uint4* to = reinterpret_cast<uint4*>(scales + slot * N * 512);
+#pragma unroll
+    for (int i = 0; i < N; ++i) to[32 * i + lane] = w[i];
+    fence_async_smem();
+    __syncwarp();
+    if (lane == 0) hand_over(slot);
+    at.next(p);
+    if (at.more) load(at, w);
+  }
+}
+
 // ------------------------------------------------------ two CTAs per tile
 
 template <int KIND, typename OutT>
 struct PairLayout {
-  static constexpr int kA = 128 * 128, kStage = 2 * kA;  // a CTA's halves of A and B
-  static constexpr int kStages = 5;
-  static constexpr int kBoxes = KIND == kMx8 ? 1 : 2;
-  static constexpr int kStaging = 8 * kBoxes * 4096;
-  static constexpr int kScales = KIND == kMx8 ? 2 * (512 + 1024) : 0;
+  // 8-bit tiles leave TMEM columns for the scales beside two accumulators
+  static constexpr int kCols = KIND == kMx8 ? 224 : 256;           // most columns of a tile
+  static constexpr int kA = 128 * 128, kB = kCols / 2 * 128;       // a CTA's halves of A and B
+  static constexpr int kStep = kA + kB, kStage = 2 * kStep;
+  static constexpr int kBox = 32 * 32 * sizeof(OutT), kBoxes = sizeof(OutT) == 4 ? 1 : 2;
+  static constexpr int kStaging = 8 * kBoxes * kBox;
+  static constexpr int kScaleSlot = 512 + 1024, kScales = KIND == kMx8 ? kSlots * kScaleSlot : 0;
+  static constexpr int kStages = (kSmem - 1024 - kStaging - kScales - kBarBytes) / kStage;
+  static_assert(kStages >= 3, "shared memory");
   static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
-  static_assert(kBytes <= kSmem, "shared memory");
-  // TMEM: two accumulators, or one and two slots of scales
-  static constexpr int kAccs = KIND == kMx8 ? 1 : 2, kScaleCol = 256;
+  static constexpr int kScaleCol = 2 * kCols, kScaleCols = 12;  // TMEM columns of the scales, of a slot
+  static_assert(KIND != kMx8 || kScaleCol + kSlots * kScaleCols <= 512, "TMEM columns");
   static constexpr int kFirst = KIND == kMx8 ? 3 : 2;  // warps that carry out
   static constexpr int kThreads = (kFirst + 8) * 32;
 };
@@ -257,8 +311,11 @@ __device__ __forceinline__ uint32_t in_first(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
+// What the arrival orders are this CTA's own accesses (its TMEM has been read, its
+// scales stand in its shared memory, both fenced), so the release is of CTA scope:
+// one of cluster scope takes 1500 cycles.
 __device__ __forceinline__ void arrive_in_first(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+  asm volatile("mbarrier.arrive.release.cta.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
 }
 // Copy to this CTA's shared memory that reports to the first CTA's barrier.
 __device__ __forceinline__ void pair_load_3d(void* dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z) {
@@ -297,16 +354,15 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       : "memory");
 }
 
-// Tiles of 256 rows x 256 columns; EPI kGated: the columns are 128 of the gate
-// (B of the first CTA) and the same 128 of the other projection (B of the
-// second), and the result has 128.
+// Tiles of 256 rows x p.bn columns, a multiple of 32; EPI kGated: half of them are
+// the gate's (B of the first CTA), half the same columns of the other projection
+// (B of the second), bn is a multiple of 64, and the result has bn / 2.
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<KIND, OutT>::kThreads, 1)
 gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using L = PairLayout<KIND, OutT>;
-  constexpr int S = L::kStages, kAccs = L::kAccs;
+  constexpr int S = L::kStages;
   constexpr bool kSum = sizeof(OutT) == 4;  // sums move to registers
-  constexpr int kBox = 128 / sizeof(OutT);  // columns stored at a time
   extern __shared__ uint8_t raw[];
   uint8_t* sm = align1024(raw);
   uint8_t* staging = sm + S * L::kStage;
@@ -325,6 +381,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], 16);
+    }
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars.sf_full[i], 2);
       mbar_init(&bars.sf_empty[i], 1);
     }
@@ -354,39 +412,47 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
       }
     }
     uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
+    const int lines = p.bn / 2, blocks = (lines + 63) / 64;  // of this CTA's half of B
+    const uint32_t bytes = 2 * (L::kA + (BMN ? blocks * 64 : lines) * 128);  // of both CTAs, a step
     bool ok = true;
     for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
       const Tile tile = tile_of(p, t);
       const int m0 = tile.m * 256 + rank * 128;
-      const int n0 = EPI == kGated ? tile.n * 128 : tile.n * 256 + rank * 128;
+      const int n0 = EPI == kGated ? tile.n * lines : tile.n * p.bn + rank * lines;
       Step s(p, tile.it0);
-      for (int it = tile.it0; it < tile.it1; ++it, ++n, s.next(p)) {
+      for (int it = tile.it0; it < tile.it1; it += 2, ++n) {
         if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
+        const int count = min(2, tile.it1 - it);
         if (elect_one()) {
-          uint8_t* a = sm + st * L::kStage;
-          uint8_t* b = a + L::kA;
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], 2 * L::kStage);
+          if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], count * bytes);
           const uint32_t bar = in_first(&bars.full[st]);
-          const int k = s.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, s.pair), pb = term_of_b(p, s.pair);
-          const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, s)];
-          const CUtensorMap* bm = &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, s)];
-          if (AMN) {
-            pair_load_3d(a, am, bar, m0, k, pa);
-            pair_load_3d(a + 8192, am, bar, m0 + 64, k, pa);
-          } else {
-            pair_load_3d(a, am, bar, k, m0, pa);
-          }
-          if (BMN) {
-            pair_load_3d(b, bm, bar, n0, k, pb);
-            pair_load_3d(b + 8192, bm, bar, n0 + 64, k, pb);
-          } else {
-            pair_load_3d(b, bm, bar, k, n0, pb);
+          Step at = s;
+          for (int j = 0; j < count; ++j, at.next(p)) {
+            uint8_t* a = sm + st * L::kStage + j * L::kStep;
+            uint8_t* b = a + L::kA;
+            const int k = at.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, at.pair), pb = term_of_b(p, at.pair);
+            const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, at)];
+            const CUtensorMap* bm = &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, at)];
+            if (AMN) {
+              pair_load_3d(a, am, bar, m0, k, pa);
+              pair_load_3d(a + 8192, am, bar, m0 + 64, k, pa);
+            } else {
+              pair_load_3d(a, am, bar, k, m0, pa);
+            }
+            if (BMN) {
+              pair_load_3d(b, bm, bar, n0, k, pb);
+              if (blocks > 1) pair_load_3d(b + 8192, bm, bar, n0 + 64, k, pb);
+            } else {
+              pair_load_3d(b, bm, bar, k, n0, pb);
+            }
           }
         }
         __syncwarp();
+        s.next(p);
+        s.next(p);
         if (++st == S) st = 0, ++round;
       }
     }
@@ -397,7 +463,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   } else if (warp == 1) {
     // ------------------------------------------------------------ products
     if (rank == 0) {
-      const uint32_t idesc = idesc_bf16(256, 256, AMN, BMN);
+      const uint32_t idesc = idesc_bf16(256, p.bn, AMN, BMN);
       const uint32_t first_stage = smem_u32(sm);
       const uint64_t a0 = AMN ? smem_desc(first_stage, 8192, 1024, SW_128B) : smem_desc(first_stage, 16, 1024, SW_128B);
       const uint64_t b0 = BMN ? smem_desc(first_stage + L::kA, 8192, 1024, SW_128B)
@@ -408,19 +474,19 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
         const Tile tile = tile_of(p, t);
         uint32_t d = 0;
         int left = 0;  // steps of this accumulator
-        for (int it = tile.it0; it < tile.it1; ++it) {
+        for (int it = tile.it0; it < tile.it1; it += 2) {
           const bool first = left == 0;
           if (first) {
             left = kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
-            d = tmem + (nc % kAccs) * 256;
-            if (nc >= kAccs && !warp_wait(&bars.acc_empty[nc % kAccs], (nc / kAccs - 1) & 1, p.status, abort_flag)) {
+            d = tmem + (nc & 1) * L::kCols;
+            if (nc >= 2 && !warp_wait(&bars.acc_empty[nc & 1], (nc / 2 - 1) & 1, p.status, abort_flag)) {
               ok = false;
               break;
             }
           }
-          const uint32_t slot = ns & 1, sf = tmem + L::kScaleCol + slot * 16;
-          const bool new_scales = KIND == kMx8 && (it == tile.it0 || (it & 3) == 0);
-          if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / 2) & 1, p.status, abort_flag)) {
+          const uint32_t slot = ns % kSlots, sf = tmem + L::kScaleCol + slot * L::kScaleCols;
+          const bool new_scales = KIND == kMx8 && (it & 3) == 0;
+          if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / kSlots) & 1, p.status, abort_flag)) {
             ok = false;
             break;
           }
@@ -429,27 +495,31 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
             break;
           }
           tc_fence_after_sync();
-          const bool last_scales = KIND == kMx8 && (it + 1 == tile.it1 || (it & 3) == 3);
-          --left;
+          const int count = min(2, tile.it1 - it);
+          const bool last_scales = KIND == kMx8 && (it + 2 >= tile.it1 || (it & 3) == 2);
+          left -= count;
           if (elect_one()) {
             if (new_scales) {
-              const uint8_t* from = scales + slot * (L::kScales / 2);
+              const uint8_t* from = scales + slot * L::kScaleSlot;
 #pragma unroll
               for (int i = 0; i < 3; ++i) pair_copy_scales(sf + 4 * i, from + 512 * i);
             }
-            const uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
+            uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
+            for (int j = 0; j < count; ++j, ad += L::kStep / 16, bd += L::kStep / 16) {
+              const uint32_t id = KIND == kMx8 ? idesc_mx8(256, p.bn, (it + j) & 3) : idesc;
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk) {
-              const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + (BMN ? kk * 128 : kk * 2);
-              const uint32_t more = !first || kk > 0;
-              if (KIND == kMx8)
-                pair_mma_mx8(d, ak, bk, idesc_mx8(256, 256, it & 3), sf, sf + 4, more);
-              else
-                pair_mma_bf16(d, ak, bk, idesc, more);
+              for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + (BMN ? kk * 128 : kk * 2);
+                const uint32_t more = !first || j > 0 || kk > 0;
+                if (KIND == kMx8)
+                  pair_mma_mx8(d, ak, bk, id, sf, sf + 4, more);
+                else
+                  pair_mma_bf16(d, ak, bk, id, more);
+              }
             }
             pair_commit(&bars.empty[st]);
             if (last_scales) pair_commit(&bars.sf_empty[slot]);
-            if (left == 0) pair_commit(&bars.acc_full[nc % kAccs]);
+            if (left == 0) pair_commit(&bars.acc_full[nc & 1]);
           }
           __syncwarp();
           if (last_scales) ++ns;
@@ -467,68 +537,73 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     }
   } else if (warp >= L::kFirst) {
     // ------------------------------------------------------- finished tiles
-    // Two warps for each quarter of the lanes, 128 columns each.
+    // Two warps for each quarter of the lanes, which take 32 columns of the
+    // result in turn: the plain form up to four times, the gated one twice.
     const int quarter = warp & 3, half = (warp - L::kFirst) / 4;
-    Staging<L::kBoxes> out{staging + (warp - L::kFirst) * L::kBoxes * 4096, lane, 0};
+    const int width = EPI == kGated ? p.bn / 2 : p.bn;  // columns of the result
+    constexpr int kTurns = EPI == kGated ? 2 : 4;
+    Staging<L::kBox, L::kBoxes> out{staging + (warp - L::kFirst) * L::kBoxes * L::kBox, lane, 0};
     uint32_t nc = 0;  // accumulators taken
     bool ok = true;
     for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
       const Tile tile = tile_of(p, t);
-      float f[4][32];  // a lane's row: 128 columns, or 64 of each projection
+      float f[4][32];  // a lane's row: columns of the result, or of g (0, 1) and u (2, 3)
       if (kSum) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) f[i / 32][i % 32] = 0.f;
       }
 #pragma unroll 1
       for (int it = tile.it0; it < tile.it1;) {
-        const int acc = nc % kAccs;
-        if (!__all_sync(0xffffffffu, wait_or_fail(&bars.acc_full[acc], (nc / kAccs) & 1, p.status, abort_flag))) {
+        if (!warp_wait(&bars.acc_full[nc & 1], (nc / 2) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
         tc_fence_after_sync();
-        const uint32_t d = tmem + acc * 256 + (static_cast<uint32_t>(quarter * 32) << 16);
-        auto column = [&](int i) { return EPI == kGated ? (i & 1) * 32 + half * 64 + (i >> 1) * 128 : half * 128 + 32 * i; };
-        if constexpr (!kSum) {
-          uint32_t(&r)[4][32] = reinterpret_cast<uint32_t(&)[4][32]>(f);
+        const uint32_t d = tmem + (nc & 1) * L::kCols + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(d + column(i), r[i]);
-          tmem_ld_wait();
-        } else {
+        for (int i = 0; i < 4; ++i) {
+          const int c = (2 * (i % kTurns) + half) * 32;  // of the result
+          if (c >= width) continue;
+          const uint32_t at = d + c + (i >= kTurns ? width : 0);
+          if constexpr (!kSum) {
+            tmem_ld32(at, reinterpret_cast<uint32_t(&)[4][32]>(f)[i]);
+          } else {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint32_t r[16];
-            tmem_ld16(d + column(i / 2) + 16 * (i & 1), r);
-            tmem_ld_wait();
+            for (int h = 0; h < 2; ++h) {
+              uint32_t r[16];
+              tmem_ld16(at + 16 * h, r);
+              tmem_ld_wait();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) f[i / 2][16 * (i & 1) + j] += __uint_as_float(r[j]);
+              for (int j = 0; j < 16; ++j) f[i][16 * h + j] += __uint_as_float(r[j]);
+            }
           }
         }
+        if (!kSum) tmem_ld_wait();
         tc_fence_before_sync();
         __syncwarp();
-        if (lane == 0) arrive_in_first(&bars.acc_empty[acc]);
+        if (lane == 0) arrive_in_first(&bars.acc_empty[nc & 1]);
         ++nc;
         it += kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
       }
       if (!ok) break;
-      const int y = tile.m * 256 + rank * 128 + quarter * 32;
-      auto send = [&](const CUtensorMap* map, int first, int columns, int x, int z) {
+      const int y = tile.m * 256 + rank * 128 + quarter * 32, x = tile.n * width;
+      const int z = EPI == kGated || p.c_by_part ? 0 : tile.split * p.parts + tile.part;
+      auto send = [&](const CUtensorMap* map, int first) {
 #pragma unroll
-        for (int c = 0; c < columns; c += kBox) {
+        for (int i = 0; i < kTurns; ++i) {
+          const int c = (2 * i + half) * 32;
+          if (c >= width) break;
           uint8_t* box = out.take();
-#pragma unroll
-          for (int h = 0; h < kBox / 32; ++h) stage32(box, lane, h, f[first + c / 32 + h], OutT{});
+          stage32(box, lane, f[first + i], OutT{});
           out.send(map, box, x + c, y, z);
         }
       };
       if constexpr (EPI == kPlain) {
-        send(&maps.c[p.c_by_part ? tile.part : 0], 0, 128, tile.n * 256 + half * 128,
-             p.c_by_part ? 0 : tile.split * p.parts + tile.part);
+        send(&maps.c[p.c_by_part ? tile.part : 0], 0);
       } else {
-        const int x = tile.n * 128 + half * 64;
         if (p.keep) {
-          send(&maps.c[1], 0, 64, x, 0);
-          send(&maps.c[2], 2, 64, x, 0);
+          send(&maps.c[1], 0);
+          send(&maps.c[2], 2);
         }
         act::by_act(p.act, [&](auto a) {
 #pragma unroll
@@ -537,36 +612,21 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
             for (int j = 0; j < 32; ++j)
               f[i][j] = act::value<decltype(a)::value, sizeof(OutT) == 2>(f[i][j]) * f[i + 2][j];
         });
-        send(&maps.c[0], 0, 64, x, 0);
+        send(&maps.c[0], 0);
       }
     }
     if (lane == 0) bulk_wait0();
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
-    // Of this CTA's rows of A and of all 256 columns, which both CTAs need.
-    uint32_t ns = 0;
-    bool ok = true;
-    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_of(p, t);
-      for (int g = tile.it0 >> 2; g <= (tile.it1 - 1) >> 2; ++g, ++ns) {
-        const uint32_t slot = ns & 1;
-        uint4 w[3];
-        w[0] = scale_words(p.a_scales, p.a_rows, g, tile.m * 256 + rank * 128, lane);
-        w[1] = scale_words(p.b_scales, p.b_rows, g, tile.n * 256, lane);
-        w[2] = scale_words(p.b_scales, p.b_rows, g, tile.n * 256 + 128, lane);
-        if (ns >= 2 &&
-            !__all_sync(0xffffffffu, wait_or_fail(&bars.sf_empty[slot], (ns / 2 - 1) & 1, p.status, abort_flag))) {
-          ok = false;
-          break;
-        }
-        uint4* to = reinterpret_cast<uint4*>(scales + slot * (L::kScales / 2));
-#pragma unroll
-        for (int i = 0; i < 3; ++i) to[32 * i + lane] = w[i];
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_in_first(&bars.sf_full[slot]);
-      }
-    }
+    // Of this CTA's rows of A and of all columns, which both CTAs need.
+    scale_loop<3>(
+        p, bars, scales, blockIdx.x / 2, pairs, tiles,
+        [&](const ScaleWalk& at, uint4(&w)[3]) {
+          w[0] = scale_words(p.a_scales, p.a_rows, at.group, at.tile.m * 256 + rank * 128, lane);
+          w[1] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * p.bn, lane);
+          w[2] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * p.bn + 128, lane);
+        },
+        [&](uint32_t slot) { arrive_in_first(&bars.sf_full[slot]); });
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -578,14 +638,14 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
 
 template <int KIND, int BN>
 struct TokensLayout {
-  static constexpr int kA = 128 * 128, kB = BN * 128, kStage = kA + kB;
+  static constexpr int kA = 128 * 128, kB = BN * 128, kStep = kA + kB, kStage = 2 * kStep;
   static constexpr int kStaging = 4 * 2 * 4096;  // two boxes per warp that carries out
-  static constexpr int kScales = KIND == kMx8 ? 2 * (512 + 512) : 0;
+  static constexpr int kScaleSlot = 512 + 512, kScales = KIND == kMx8 ? kSlots * kScaleSlot : 0;
   static constexpr int kFree = kSmem - 1024 - kStaging - kScales - kBarBytes;
   static constexpr int kStages = kFree / kStage < 12 ? kFree / kStage : 12;
   static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
-  static constexpr int kScaleCol = 2 * BN;  // TMEM column of the scales: two slots of 4 + 4
-  static constexpr int kCols = 2 * BN + (KIND == kMx8 ? 32 : 0);
+  static constexpr int kScaleCol = 2 * BN, kScaleCols = 8;  // TMEM columns of a slot's scales
+  static constexpr int kCols = 2 * BN + (KIND == kMx8 ? kSlots * kScaleCols : 0);
   static constexpr int kAlloc = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : kCols <= 256 ? 256 : 512;
   static constexpr int kThreads = KIND == kMx8 ? 224 : 192;
 };
@@ -614,6 +674,8 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.acc_full[i], 1);
       mbar_init(&bars.acc_empty[i], 4);
+    }
+    for (int i = 0; i < kSlots; ++i) {
       mbar_init(&bars.sf_full[i], 1);
       mbar_init(&bars.sf_empty[i], 1);
     }
@@ -642,26 +704,32 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const Tile tile = tile_of(p, t);
       Step s(p, tile.it0);
-      for (int it = tile.it0; it < tile.it1; ++it, ++n, s.next(p)) {
+      for (int it = tile.it0; it < tile.it1; it += 2, ++n) {
         if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
+        const int count = min(2, tile.it1 - it);
         if (elect_one()) {
-          uint8_t* a = sm + st * L::kStage;
           uint64_t* bar = &bars.full[st];
-          mbar_arrive_expect_tx(bar, L::kStage);
-          const int k = s.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, s.pair);
-          const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, s)];
-          if (AMN) {
-            tma_load_3d(a, am, bar, tile.m * 128, k, pa);
-            tma_load_3d(a + 8192, am, bar, tile.m * 128 + 64, k, pa);
-          } else {
-            tma_load_3d(a, am, bar, k, tile.m * 128, pa);
+          mbar_arrive_expect_tx(bar, count * L::kStep);
+          Step at = s;
+          for (int j = 0; j < count; ++j, at.next(p)) {
+            uint8_t* a = sm + st * L::kStage + j * L::kStep;
+            const int k = at.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, at.pair);
+            const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, at)];
+            if (AMN) {
+              tma_load_3d(a, am, bar, tile.m * 128, k, pa);
+              tma_load_3d(a + 8192, am, bar, tile.m * 128 + 64, k, pa);
+            } else {
+              tma_load_3d(a, am, bar, k, tile.m * 128, pa);
+            }
+            tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, at)], bar, k, tile.n * BN, term_of_b(p, at.pair));
           }
-          tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, s)], bar, k, tile.n * BN, term_of_b(p, s.pair));
         }
         __syncwarp();
+        s.next(p);
+        s.next(p);
         if (++st == S) st = 0, ++round;
       }
     }
@@ -679,7 +747,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
       const Tile tile = tile_of(p, t);
       uint32_t d = 0;
       int left = 0;  // steps of this accumulator
-      for (int it = tile.it0; it < tile.it1; ++it) {
+      for (int it = tile.it0; it < tile.it1; it += 2) {
         const bool first = left == 0;
         if (first) {
           left = min(p.chunk, tile.it1 - it);
@@ -689,9 +757,9 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
             break;
           }
         }
-        const uint32_t slot = ns & 1, sf = tmem + L::kScaleCol + slot * 16;
-        const bool new_scales = KIND == kMx8 && (it == tile.it0 || (it & 3) == 0);
-        if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / 2) & 1, p.status, abort_flag)) {
+        const uint32_t slot = ns % kSlots, sf = tmem + L::kScaleCol + slot * L::kScaleCols;
+        const bool new_scales = KIND == kMx8 && (it & 3) == 0;
+        if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / kSlots) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
@@ -700,23 +768,27 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
           break;
         }
         tc_fence_after_sync();
-        const bool last_scales = KIND == kMx8 && (it + 1 == tile.it1 || (it & 3) == 3);
-        --left;
+        const int count = min(2, tile.it1 - it);
+        const bool last_scales = KIND == kMx8 && (it + 2 >= tile.it1 || (it & 3) == 2);
+        left -= count;
         if (elect_one()) {
           if (new_scales) {
-            const uint8_t* from = scales + slot * (L::kScales / 2);
+            const uint8_t* from = scales + slot * L::kScaleSlot;
             copy_scales(sf, from);
             copy_scales(sf + 4, from + 512);
           }
-          const uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
+          uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
+          for (int j = 0; j < count; ++j, ad += L::kStep / 16, bd += L::kStep / 16) {
+            const uint32_t id = KIND == kMx8 ? idesc_mx8(128, BN, (it + j) & 3) : idesc;
 #pragma unroll
-          for (int kk = 0; kk < 4; ++kk) {
-            const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + kk * 2;
-            const uint32_t more = !first || kk > 0;
-            if (KIND == kMx8)
-              mma_mx8(d, ak, bk, idesc_mx8(128, BN, it & 3), sf, sf + 4, more);
-            else
-              mma_bf16(d, ak, bk, idesc, more);
+            for (int kk = 0; kk < 4; ++kk) {
+              const uint64_t ak = ad + (AMN ? kk * 128 : kk * 2), bk = bd + kk * 2;
+              const uint32_t more = !first || j > 0 || kk > 0;
+              if (KIND == kMx8)
+                mma_mx8(d, ak, bk, id, sf, sf + 4, more);
+              else
+                mma_bf16(d, ak, bk, id, more);
+            }
           }
           mma_commit(&bars.empty[st]);
           if (last_scales) mma_commit(&bars.sf_empty[slot]);
@@ -735,7 +807,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
   } else if (warp < 6) {
     // ------------------------------------------------------- finished tiles
     const int quarter = warp & 3;
-    Staging<2> out{staging + (warp - 2) * 8192, lane, 0};
+    Staging<4096, 2> out{staging + (warp - 2) * 8192, lane, 0};
     uint32_t nc = 0;  // accumulators taken
     bool ok = true;
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
@@ -777,7 +849,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) {
           uint8_t* box = out.take();
-          stage32(box, lane, 0, sum[c], 0.f);
+          stage32(box, lane, sum[c], 0.f);
           out.send(&maps.c[0], box, tile.n * BN + 32 * c, y, z);
         }
       }
@@ -785,27 +857,13 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     if (lane == 0) bulk_wait0();
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
-    uint32_t ns = 0;
-    bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_of(p, t);
-      for (int g = tile.it0 >> 2; g <= (tile.it1 - 1) >> 2; ++g, ++ns) {
-        const uint32_t slot = ns & 1;
-        const uint4 wa = scale_words(p.a_scales, p.a_rows, g, tile.m * 128, lane);
-        const uint4 wb = scale_words(p.b_scales, p.b_rows, g, tile.n * BN, lane);
-        if (ns >= 2 &&
-            !__all_sync(0xffffffffu, wait_or_fail(&bars.sf_empty[slot], (ns / 2 - 1) & 1, p.status, abort_flag))) {
-          ok = false;
-          break;
-        }
-        uint4* to = reinterpret_cast<uint4*>(scales + slot * (L::kScales / 2));
-        to[lane] = wa;
-        to[32 + lane] = wb;
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars.sf_full[slot]);
-      }
-    }
+    scale_loop<2>(
+        p, bars, scales, blockIdx.x, gridDim.x, tiles,
+        [&](const ScaleWalk& at, uint4(&w)[2]) {
+          w[0] = scale_words(p.a_scales, p.a_rows, at.group, at.tile.m * 128, lane);
+          w[1] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * BN, lane);
+        },
+        [&](uint32_t slot) { mbar_arrive(&bars.sf_full[slot]); });
   }
   tc_fence_before_sync();
   __syncthreads();
@@ -842,10 +900,10 @@ inline bool map_k(CUtensorMap* map, const Matrix& x, int lines) {
 }
 // ... or stored [k][m or n].
 inline bool map_mn(CUtensorMap* map, const Matrix& x) { return make_map(map, x, 64, 64, CU_TENSOR_MAP_SWIZZLE_128B); }
-// Results in boxes of 32 rows x 128 bytes, or x 64 where a row has no more.
-inline bool map_out(CUtensorMap* map, const Matrix& x, bool narrow = false) {
-  return make_map(map, x, (narrow ? 64 : 128) / x.esize, 32,
-                  narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
+// Results in boxes of 32 rows x 32 columns, or x 16 of fp32.
+inline bool map_out(CUtensorMap* map, const Matrix& x, int columns = 32) {
+  return make_map(map, x, columns, 32,
+                  columns * x.esize == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
 // Sums of the partial planes of a split product (nys_join.cu): part holds
@@ -903,19 +961,48 @@ int launch_tokens(const char* name, int bn, const Maps& maps, const Params& p, c
 constexpr int kMostTokens = 128;  // of gemm_tokens
 inline int columns_of(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
 
-// Ranges of K that fill the SMs: as many as leave the last round of tiles
-// fullest, each at least `least` steps long, one where the tiles alone give
-// whole rounds. More ranges cost partial sums, taken as `cost` steps each.
-inline int splits_of(long long tiles, int ctas_per_tile, int its, int least, int most, double cost) {
-  const int sms = plan_sms() / ctas_per_tile;
-  int best = 1;
+// How a product is cut: columns of a tile (gemm_pair; gemm_tokens has its own) and
+// ranges of K, whose partial sums are joined. The time of a choice is counted in
+// steps of a full tile (0.3 us; `pairs` of them for a K block of fp32): rounds of tiles over the CTAs times a tile's steps,
+// two more for its start and end, and for more than one range the join (ten
+// steps' time to begin, then its bytes, write and read, at 5 TB/s).
+struct Cut {
+  int bn, splits;
+};
+// Steps of each of s ranges, a multiple of `unit` (8-bit operands: four, whose
+// scales come in one word).
+inline int range_of(int steps, int s, int unit) { return ((steps + s - 1) / s + unit - 1) / unit * unit; }
+inline Cut cut_tokens(long long row_tiles, long long rows, int bn, int steps, int unit, int pairs, int least) {
+  const int sms = plan_sms();
+  Cut best{bn, 1};
   double best_time = 1e30;
-  for (int s = 1; s <= most && (s == 1 || its / s >= least); ++s) {
-    const int per = (its + s - 1) / s;
-    if ((its + per - 1) / per != s) continue;  // no empty range
-    const double rounds = (double)((tiles * s + sms - 1) / sms);
-    const double time = rounds * (per + (s > 1 ? cost : 0.0)) + (s > 1 ? 2 * cost : 0.0);
-    if (time < best_time * 0.999) best_time = time, best = s;
+  for (int s = 1; s <= 16 && (s == 1 || steps / s >= least); ++s) {
+    const int per = range_of(steps, s, unit);
+    if ((steps + per - 1) / per != s) continue;  // no empty range
+    const double rounds = (double)((row_tiles * s + sms - 1) / sms);
+    // 16 KB of the weights a step, and the partial sums in and out
+    const double time = rounds * (per * (double)pairs + 1.0) + (double)s * rows * bn * 8.0 / (16384.0 * sms);
+    if (time < best_time * 0.999) best_time = time, best.splits = s;
+  }
+  return best;
+}
+inline Cut cut_pair(long long M, long long N, int steps, int unit, int pairs, int parts, int most_bn, int bn_step, bool gated,
+                    int least) {
+  const int clusters = plan_sms() / 2;
+  Cut best{most_bn, 1};
+  double best_time = 1e30;
+  for (int bn = most_bn; bn >= 128; bn -= bn_step) {
+    for (int s = 1; s <= 16 && (s == 1 || steps / s >= least); ++s) {
+      const int per = range_of(steps, s, unit);
+      if ((steps + per - 1) / per != s) continue;
+      // the gated form computes both parts in one tile, unless K is split
+      const int columns = gated && s == 1 ? bn / 2 : bn, of = gated && s == 1 ? 1 : parts;
+      const long long tiles = ((M + 255) / 256) * ((N + columns - 1) / columns) * of * s;
+      const double rounds = (double)((tiles + clusters - 1) / clusters);
+      double time = rounds * (per * (double)pairs * (bn + 8.0) / 264.0 + 2.0);
+      if (s > 1) time += 10.0 + (double)s * parts * M * N * 8.0 / 1.5e6;
+      if (time < best_time * 0.999) best_time = time, best = Cut{bn, s};
+    }
   }
   return best;
 }

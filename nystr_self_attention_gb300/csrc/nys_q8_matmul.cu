@@ -7,7 +7,7 @@
 // Up to 128 tokens the weights are the 128-row operand and the tokens the short
 // one (nothing is padded to 128 rows, so the weights stream at HBM's pace), K
 // split so that every SM has an equal share; the partial sums are joined. More
-// tokens are the rows themselves, in tiles of 256 x 256 by two CTAs.
+// tokens are the rows themselves, in tiles of 256 x up to 224 by two CTAs.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -31,10 +31,11 @@ Q8Plan plan_of(int T, int N, int K) {
   Q8Plan q{};
   const int its = (K + 127) / 128;
   q.turned = T <= kMostTokens;
-  q.bn = q.turned ? columns_of(T) : 256;
-  const long long tiles = q.turned ? (N + 127) / 128 : (long long)((T + 255) / 256) * ((N + 255) / 256);
-  q.splits = splits_of(tiles, q.turned ? 1 : 2, its, q.turned ? 2 : 4, 16, q.bn / 16.0);
-  q.its_per_split = (its + q.splits - 1) / q.splits;
+  const Cut cut = q.turned ? cut_tokens((N + 127) / 128, N, columns_of(T), its, 4, 1, 2)
+                           : cut_pair(T, N, its, 4, 1, 1, 224, 32, false, 4);
+  q.bn = cut.bn;
+  q.splits = cut.splits;
+  q.its_per_split = range_of(its, q.splits, 4);
   if (q.turned)
     q.bytes = (size_t)q.splits * N * q.bn * 4;
   else if (q.splits > 1)
@@ -96,6 +97,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   p.splits = plan.splits;
   p.k_blocks = p.its = (K + 127) / 128;
   p.its_per_split = plan.its_per_split;
+  p.bn = plan.bn;
   p.chunk = 8;
   p.group = 8;
   p.a_scales = static_cast<const uint32_t*>(rows.scales);
@@ -103,13 +105,13 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   p.a_rows = rows.rows;
   p.b_rows = cols.rows;
   Maps maps{};
-  bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.turned ? plan.bn : 128);
+  bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.turned ? plan.bn : plan.bn / 2);
   const bool direct = !plan.turned && plan.splits == 1;
   if (direct)
     ok = ok && map_out(&maps.c[0], Matrix{out, T, N, out_stride, dtype == NYS_FP32 ? 4 : 2});
   else if (plan.turned)
     ok = ok && map_out(&maps.c[0], Matrix{workspace, N, plan.bn, plan.bn, 4, plan.splits, (long long)N * plan.bn},
-                       plan.bn == 16);
+                       plan.bn == 16 ? 16 : 32);
   else
     ok = ok && map_out(&maps.c[0], Matrix{workspace, T, N, N, 4, plan.splits, (long long)T * N});
   if (!ok) return tensor_map_error(__FILE__, __LINE__);
