@@ -3,9 +3,10 @@
 //
 // Two kernels, both persistent: a warp issues the TMA copies, one the products,
 // and others carry finished tiles out while the next ones run. A step of K is 128
-// bytes, 64 bf16 or 128 e4m3, four instructions; a stage holds two steps, since a
-// wait and a commit cost the issuing warp some 150 cycles (with one step per stage
-// it took 650 cycles a step, where the tensor cores need 450 to 512).
+// bytes, 64 bf16 or 128 e4m3, four instructions. A stage is a step of bf16 (two:
+// 670,000 against 700,000 cycles for a gradient of the input) or two steps of 8
+// bits, whose products are issued with their scales (one: 690,000 cycles for 65536
+// x 4096 x 2048, two: 620,000).
 //   gemm_pair: tiles of 256 x 256 by a cluster of two CTAs. Each holds half of A's
 //     rows and half of B's in shared memory and the instruction reads both CTAs'
 //     halves of B, so a CTA fetches 32 KB per step where a tile of its own would
@@ -284,7 +285,7 @@ struct PairLayout {
   // 8-bit tiles leave TMEM columns for the scales beside two accumulators
   static constexpr int kCols = KIND == kMx8 ? 224 : 256;           // most columns of a tile
   static constexpr int kA = 128 * 128, kB = kCols / 2 * 128;       // a CTA's halves of A and B
-  static constexpr int kStep = kA + kB, kStage = 2 * kStep;
+  static constexpr int kStep = kA + kB, kSteps = KIND == kMx8 ? 2 : 1, kStage = kSteps * kStep;
   static constexpr int kBox = 32 * 32 * sizeof(OutT), kBoxes = sizeof(OutT) == 4 ? 1 : 2;
   static constexpr int kStaging = 8 * kBoxes * kBox;
   static constexpr int kScaleSlot = 512 + 1024, kScales = KIND == kMx8 ? kSlots * kScaleSlot : 0;
@@ -293,7 +294,7 @@ struct PairLayout {
   static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
   static constexpr int kScaleCol = 2 * kCols, kScaleCols = 12;  // TMEM columns of the scales, of a slot
   static_assert(KIND != kMx8 || kScaleCol + kSlots * kScaleCols <= 512, "TMEM columns");
-  static constexpr int kFirst = KIND == kMx8 ? 3 : 2;  // warps that carry out
+  static constexpr int kFirst = KIND == kMx8 ? 4 : 3;  // warps that carry out
   static constexpr int kThreads = (kFirst + 8) * 32;
 };
 
@@ -403,56 +404,52 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t tmem = bars.tmem;
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 2) {
     // -------------------------------------------------------------- copies
+    // A's by one warp, B's by another: up to four copies a step take one as long
+    // to issue as the products take to run (16384 tokens, 2048 -> 5632: forward
+    // 761,000 cycles, gradients of the weights 779,000; with two 726,000, 747,000).
+    const bool first = warp == 0;
     if (elect_one()) {
-      for (int i = 0; i < 2; ++i) {
-        tma_prefetch(&maps.a[i]);
-        tma_prefetch(&maps.b[i]);
-      }
+      for (int i = 0; i < 2; ++i) tma_prefetch(first ? &maps.a[i] : &maps.b[i]);
     }
-    uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
+    uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, stages filled
     const int lines = p.bn / 2, blocks = (lines + 63) / 64;  // of this CTA's half of B
     const uint32_t bytes = 2 * (L::kA + (BMN ? blocks * 64 : lines) * 128);  // of both CTAs, a step
+    const int half = !first && blocks == 1 ? 0 : 1;  // a second box of 64 (MN-major)
     bool ok = true;
     for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
       const Tile tile = tile_of(p, t);
-      const int m0 = tile.m * 256 + rank * 128;
-      const int n0 = EPI == kGated ? tile.n * lines : tile.n * p.bn + rank * lines;
+      // rows of A, or of B (columns of the result)
+      const int r0 = first            ? tile.m * 256 + rank * 128
+                     : EPI == kGated ? tile.n * lines
+                                     : tile.n * p.bn + rank * lines;
       Step s(p, tile.it0);
-      for (int it = tile.it0; it < tile.it1; it += 2, ++n) {
+      for (int it = tile.it0; it < tile.it1; it += L::kSteps, ++n) {
         if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
-        const int count = min(2, tile.it1 - it);
+        const int count = min(L::kSteps, tile.it1 - it);
         if (elect_one()) {
-          if (rank == 0) mbar_arrive_expect_tx(&bars.full[st], count * bytes);
+          if (first && rank == 0) mbar_arrive_expect_tx(&bars.full[st], count * bytes);
           const uint32_t bar = in_first(&bars.full[st]);
           Step at = s;
           for (int j = 0; j < count; ++j, at.next(p)) {
-            uint8_t* a = sm + st * L::kStage + j * L::kStep;
-            uint8_t* b = a + L::kA;
-            const int k = at.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, at.pair), pb = term_of_b(p, at.pair);
-            const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, at)];
-            const CUtensorMap* bm = &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, at)];
-            if (AMN) {
-              pair_load_3d(a, am, bar, m0, k, pa);
-              pair_load_3d(a + 8192, am, bar, m0 + 64, k, pa);
+            uint8_t* to = sm + st * L::kStage + j * L::kStep + (first ? 0 : L::kA);
+            const int k = at.kb * (KIND == kMx8 ? 128 : 64), z = first ? term_of_a(p, at.pair) : term_of_b(p, at.pair);
+            const CUtensorMap* map = first ? &maps.a[map_of(p.a_by, tile, at)]
+                                           : &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, at)];
+            if (first ? AMN : BMN) {
+              pair_load_3d(to, map, bar, r0, k, z);
+              if (half) pair_load_3d(to + 8192, map, bar, r0 + 64, k, z);
             } else {
-              pair_load_3d(a, am, bar, k, m0, pa);
-            }
-            if (BMN) {
-              pair_load_3d(b, bm, bar, n0, k, pb);
-              if (blocks > 1) pair_load_3d(b + 8192, bm, bar, n0 + 64, k, pb);
-            } else {
-              pair_load_3d(b, bm, bar, k, n0, pb);
+              pair_load_3d(to, map, bar, k, r0, z);
             }
           }
         }
         __syncwarp();
-        s.next(p);
-        s.next(p);
+        for (int j = 0; j < L::kSteps; ++j) s.next(p);
         if (++st == S) st = 0, ++round;
       }
     }
@@ -474,7 +471,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
         const Tile tile = tile_of(p, t);
         uint32_t d = 0;
         int left = 0;  // steps of this accumulator
-        for (int it = tile.it0; it < tile.it1; it += 2) {
+        for (int it = tile.it0; it < tile.it1; it += L::kSteps) {
           const bool first = left == 0;
           if (first) {
             left = kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
@@ -495,8 +492,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
             break;
           }
           tc_fence_after_sync();
-          const int count = min(2, tile.it1 - it);
-          const bool last_scales = KIND == kMx8 && (it + 2 >= tile.it1 || (it & 3) == 2);
+          const int count = min(L::kSteps, tile.it1 - it);
+          const bool last_scales = KIND == kMx8 && (it + L::kSteps >= tile.it1 || ((it + L::kSteps) & 3) == 0);
           left -= count;
           if (elect_one()) {
             if (new_scales) {
@@ -638,7 +635,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
 
 template <int KIND, int BN>
 struct TokensLayout {
-  static constexpr int kA = 128 * 128, kB = BN * 128, kStep = kA + kB, kStage = 2 * kStep;
+  static constexpr int kA = 128 * 128, kB = BN * 128, kStep = kA + kB, kSteps = 2, kStage = kSteps * kStep;
   static constexpr int kStaging = 4 * 2 * 4096;  // two boxes per warp that carries out
   static constexpr int kScaleSlot = 512 + 512, kScales = KIND == kMx8 ? kSlots * kScaleSlot : 0;
   static constexpr int kFree = kSmem - 1024 - kStaging - kScales - kBarBytes;
@@ -704,12 +701,12 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
       const Tile tile = tile_of(p, t);
       Step s(p, tile.it0);
-      for (int it = tile.it0; it < tile.it1; it += 2, ++n) {
+      for (int it = tile.it0; it < tile.it1; it += L::kSteps, ++n) {
         if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
           ok = false;
           break;
         }
-        const int count = min(2, tile.it1 - it);
+        const int count = min(L::kSteps, tile.it1 - it);
         if (elect_one()) {
           uint64_t* bar = &bars.full[st];
           mbar_arrive_expect_tx(bar, count * L::kStep);
@@ -728,8 +725,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
           }
         }
         __syncwarp();
-        s.next(p);
-        s.next(p);
+        for (int j = 0; j < L::kSteps; ++j) s.next(p);
         if (++st == S) st = 0, ++round;
       }
     }
@@ -747,7 +743,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
       const Tile tile = tile_of(p, t);
       uint32_t d = 0;
       int left = 0;  // steps of this accumulator
-      for (int it = tile.it0; it < tile.it1; it += 2) {
+      for (int it = tile.it0; it < tile.it1; it += L::kSteps) {
         const bool first = left == 0;
         if (first) {
           left = min(p.chunk, tile.it1 - it);
@@ -768,8 +764,8 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
           break;
         }
         tc_fence_after_sync();
-        const int count = min(2, tile.it1 - it);
-        const bool last_scales = KIND == kMx8 && (it + 2 >= tile.it1 || (it & 3) == 2);
+        const int count = min(L::kSteps, tile.it1 - it);
+        const bool last_scales = KIND == kMx8 && (it + L::kSteps >= tile.it1 || ((it + L::kSteps) & 3) == 0);
         left -= count;
         if (elect_one()) {
           if (new_scales) {
