@@ -123,6 +123,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 struct Product {
   bool turned;  // D is the result's transpose: its N are the 128-row operand's rows
   int bn, splits, its, its_per_split, k_blocks, m_tiles, n_tiles;
+  Line line;     // turned
   size_t bytes;  // of partial sums
 };
 
@@ -133,19 +134,23 @@ Product product_of(long long M, long long N, long long k, int k_parts, int parts
   q.k_blocks = (int)((k + 63) / 64);
   const int steps = q.k_blocks * k_parts;
   q.its = steps * pairs;
-  const Cut cut = q.turned ? cut_tokens((N + 127) / 128 * parts, N * parts, columns_of((int)M), steps, 1, pairs, pairs > 1 ? 1 : 4)
-                           : cut_pair(M, N, steps, 1, pairs, parts, 256, gated ? 64 : 32, gated, pairs > 1 ? 1 : 4);
+  if (q.turned) {
+    q.bn = columns_of((int)M);
+    q.line = line_of(N, q.its, parts, pairs > 1 ? pairs : 2, q.bn);
+    q.splits = most_planes(q.line);
+    q.m_tiles = q.line.m_tiles;
+    q.n_tiles = 1;
+    q.bytes = align256((size_t)q.splits * parts * N * q.bn * 4);
+    return q;
+  }
+  const Cut cut = cut_pair(M, N, steps, 1, pairs, parts, 256, gated ? 64 : 32, gated, pairs > 1 ? 1 : 4);
   q.bn = cut.bn;
   q.splits = cut.splits;
-  const bool fused = gated && !q.turned && q.splits == 1;  // a tile has bn / 2 columns of each part
-  q.m_tiles = (int)(q.turned ? (N + 127) / 128 : (M + 255) / 256);
-  q.n_tiles = q.turned ? 1 : (int)((N + q.bn / (fused ? 2 : 1) - 1) / (q.bn / (fused ? 2 : 1)));
   q.its_per_split = range_of(steps, q.splits, 1) * pairs;  // all pairs of a block
-  const bool direct = !q.turned && q.splits == 1;
-  if (q.turned)
-    q.bytes = align256((size_t)q.splits * parts * N * q.bn * 4);
-  else if (!direct)
-    q.bytes = align256((size_t)q.splits * parts * M * N * 4);
+  const int width = gated && q.splits == 1 ? q.bn / 2 : q.bn;  // of each part
+  q.m_tiles = (int)((M + 255) / 256);
+  q.n_tiles = (int)((N + width - 1) / width);
+  if (q.splits > 1) q.bytes = align256((size_t)q.splits * parts * M * N * 4);
   return q;
 }
 
@@ -229,6 +234,8 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
   p.its_per_split = q.its_per_split;
   p.pairs = pairs;
   p.bn = q.bn;
+  p.unit = pairs > 1 ? pairs : 2;
+  p.units = q.line.units;
   p.chunk = pairs > 1 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
   p.a_by = a_by;
   p.b_by = b_by;
@@ -239,7 +246,8 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
 
 // The turned form: weights (k contiguous, or turned themselves) x tokens.
 int launch_turned(const char* name, bool amn, const Product& q, const Maps& maps, const Params& p, cudaStream_t st) {
-  return amn ? launch_tokens<kBf16, true>(name, q.bn, maps, p, st) : launch_tokens<kBf16, false>(name, q.bn, maps, p, st);
+  return amn ? launch_tokens<kBf16, true>(name, q.bn, q.line.ctas, maps, p, st)
+             : launch_tokens<kBf16, false>(name, q.bn, q.line.ctas, maps, p, st);
 }
 
 // Results, or (wide) fp32 results or partial sums, in rows.
@@ -313,8 +321,7 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
             : launch_pair<kBf16, false, false, kGated, __nv_bfloat16>("gated_ff", maps, p, st);
   }
   if (rc != NYS_OK || direct) return rc;
-  const JoinGated j{reinterpret_cast<const float*>(ws + pl.part), q.splits, a.T, a.f, q.turned ? q.bn : 0,
-                    h, gate, up, a.h, a.gate, a.up};
+  const JoinGated j{reinterpret_cast<const float*>(ws + pl.part), q.splits, a.T, a.f, q.line, h, gate, up, a.h, a.gate, a.up};
   return join_gated(j, a.act, a.dtype, st);
 }
 
@@ -351,7 +358,7 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
     rc = io ? launch_plain<false, false>(name, pl.f32 || !direct, maps, p, st)
             : launch_plain<false, true>(name, pl.f32 || !direct, maps, p, st);
   if (rc != NYS_OK || direct) return rc;
-  const Join j{reinterpret_cast<const float*>(part), q.splits, a.T, a.d, q.turned ? q.bn : 0, {dx, nullptr}, {a.dx, 0}};
+  const Join j{reinterpret_cast<const float*>(part), q.splits, a.T, a.d, q.line, {dx, nullptr}, {a.dx, 0}};
   return join(j, 1, a.dtype, st);
 }
 
@@ -378,7 +385,7 @@ int weight_gradients(const nys_gated_ff_t& a, const Plan& pl, const void* x, voi
   const char* name = "gated_ff_dw";
   const int rc = launch_plain<true, true>(name, pl.f32 || !direct, maps, p, st);
   if (rc != NYS_OK || direct) return rc;
-  const Join j{reinterpret_cast<const float*>(part), q.splits, M, N, 0, {dwg, dwu}, {a.dw, a.dw}};
+  const Join j{reinterpret_cast<const float*>(part), q.splits, M, N, q.line, {dwg, dwu}, {a.dw, a.dw}};
   return join(j, 2, a.dtype, st);
 }
 

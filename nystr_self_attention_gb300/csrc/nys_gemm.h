@@ -12,7 +12,8 @@
 //     halves of B, so a CTA fetches 32 KB per step where a tile of its own would
 //     take 48 (and 96 bytes a cycle instead of 64 out of shared memory).
 //   gemm_tokens: tiles of 128 rows x up to 128 columns by one CTA, for products
-//     with few columns (tokens) whose other operand (weights) has to stream.
+//     with few columns (tokens) whose other operand (weights) has to stream: the
+//     CTAs divide its K steps evenly, whatever the number of tiles.
 //
 // Either operand may lie with its k contiguous (rows of 128 bytes, 128-byte
 // swizzle) or with its m or n contiguous ("MN-major": boxes of 64 elements x 64
@@ -54,7 +55,8 @@ struct Maps {
 struct Params {
   int m_tiles, n_tiles;  // of one part
   int parts;             // products side by side in one launch (a[part], b[part], plane of c)
-  int splits;            // ranges of its; each writes a plane of fp32 partial sums
+  int splits;            // ranges of its; each writes a plane of fp32 partial sums (gemm_pair)
+  int unit, units;       // gemm_tokens: steps that stay together, and how many of them a tile has
   int k_blocks;          // 128-byte blocks of one K part
   int its, its_per_split;  // K parts x k_blocks x pairs
   int bn;                // columns of a tile (gemm_pair)
@@ -90,6 +92,59 @@ __device__ __forceinline__ Tile tile_of(const Params& p, int t) {
   r.it1 = min(p.its, r.it0 + p.its_per_split);
   return r;
 }
+
+// gemm_pair's walk: every so-manyth tile.
+struct GridWalk {
+  Tile tile;
+  int t, step, tiles;
+  bool more;
+  __device__ __forceinline__ explicit GridWalk(const Params& p)
+      : t(blockIdx.x / 2), step(gridDim.x / 2), tiles(p.m_tiles * p.n_tiles * p.parts * p.splits) {
+    enter(p);
+  }
+  __device__ __forceinline__ void enter(const Params& p) {
+    more = t < tiles;
+    if (more) tile = tile_of(p, t);
+  }
+  __device__ __forceinline__ void next(const Params& p) {
+    t += step;
+    enter(p);
+  }
+};
+
+// gemm_tokens' walk: the units of all tiles form one line, which the CTAs divide
+// evenly, so a CTA has the end of a tile, whole ones and the start of another. A
+// tile's n-th CTA writes plane n of the partial sums.
+__host__ __device__ __forceinline__ long long line_start(long long line, int ctas, int cta) {
+  return line * cta / ctas;
+}
+__host__ __device__ __forceinline__ int line_cta(long long line, int ctas, long long unit) {
+  return (int)(((unit + 1) * ctas - 1) / line);
+}
+struct LineWalk {
+  Tile tile;
+  long long u, end, line;
+  bool more;
+  __device__ __forceinline__ explicit LineWalk(const Params& p) : line((long long)p.m_tiles * p.parts * p.units) {
+    u = line_start(line, gridDim.x, blockIdx.x);
+    end = line_start(line, gridDim.x, blockIdx.x + 1);
+    enter(p);
+  }
+  __device__ __forceinline__ void enter(const Params& p) {
+    more = u < end;
+    if (!more) return;
+    const int t = (int)(u / p.units), r = (int)(u - (long long)t * p.units);
+    const int n = (int)min((long long)(p.units - r), end - u);
+    tile.part = t / p.m_tiles;
+    tile.m = t - tile.part * p.m_tiles;
+    tile.n = 0;
+    tile.split = (int)blockIdx.x - line_cta(line, gridDim.x, (long long)t * p.units);
+    tile.it0 = r * p.unit;
+    tile.it1 = min(p.its, (r + n) * p.unit);
+    u += n;
+  }
+  __device__ __forceinline__ void next(const Params& p) { enter(p); }
+};
 
 __device__ __forceinline__ bool wait_or_fail(uint64_t* bar, uint32_t parity, int* status,
                                              volatile int* abort_flag) {
@@ -232,23 +287,15 @@ __device__ __forceinline__ uint4 scale_words(const uint32_t* words, int rows, in
 }
 
 // The groups of four K blocks of a CTA's tiles, in order.
+template <typename Walk>
 struct ScaleWalk {
-  Tile tile;
-  int t, step, tiles, group;
-  bool more;
-  __device__ __forceinline__ ScaleWalk(const Params& p, int first, int step_, int tiles_)
-      : t(first), step(step_), tiles(tiles_), more(first < tiles_) {
-    if (more) enter(p);
-  }
-  __device__ __forceinline__ void enter(const Params& p) {
-    tile = tile_of(p, t);
-    group = tile.it0 >> 2;
-  }
+  Walk walk;
+  int group;
+  __device__ __forceinline__ explicit ScaleWalk(const Params& p) : walk(p), group(walk.tile.it0 >> 2) {}
   __device__ __forceinline__ void next(const Params& p) {
-    if (++group <= (tile.it1 - 1) >> 2) return;
-    t += step;
-    more = t < tiles;
-    if (more) enter(p);
+    if (++group <= (walk.tile.it1 - 1) >> 2) return;
+    walk.next(p);
+    group = walk.tile.it0 >> 2;
   }
 };
 
@@ -256,15 +303,14 @@ struct ScaleWalk {
 // says that they are in shared memory. A group is loaded right behind the hand-over
 // of the one before it and not sooner: the fence waits for every load that is on
 // its way (2000 cycles, where four steps of products take 1800).
-template <int N, typename Load, typename Hand>
-__device__ __forceinline__ void scale_loop(const Params& p, Bars& bars, uint8_t* scales, int first, int step,
-                                           int tiles, Load load, Hand hand_over) {
+template <int N, typename Walk, typename Load, typename Hand>
+__device__ __forceinline__ void scale_loop(const Params& p, Bars& bars, uint8_t* scales, Load load, Hand hand_over) {
   const int lane = threadIdx.x & 31;
-  ScaleWalk at(p, first, step, tiles);
+  ScaleWalk<Walk> at(p);
   uint4 w[N];
-  if (at.more) load(at, w);
+  if (at.walk.more) load(at.walk.tile, at.group, w);
 #pragma unroll 1
-  for (uint32_t ns = 0; at.more; ++ns) {
+  for (uint32_t ns = 0; at.walk.more; ++ns) {
     const uint32_t slot = ns % kSlots;
     if (ns >= kSlots && !warp_wait(&bars.sf_empty[slot], (ns / kSlots - 1) & 1, p.status, &bars.abort)) return;
     uint4* to = reinterpret_cast<uint4*>(scales + slot * N * 512);
@@ -274,7 +320,7 @@ __device__ __forceinline__ void scale_loop(const Params& p, Bars& bars, uint8_t*
     __syncwarp();
     if (lane == 0) hand_over(slot);
     at.next(p);
-    if (at.more) load(at, w);
+    if (at.walk.more) load(at.walk.tile, at.group, w);
   }
 }
 
@@ -371,8 +417,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   Bars& bars = *reinterpret_cast<Bars*>(scales + L::kScales);
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)cluster_rank(), pairs = gridDim.x / 2;
-  const int tiles = p.m_tiles * p.n_tiles * p.parts * p.splits;
+  const int rank = (int)cluster_rank();
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -418,8 +463,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     const uint32_t bytes = 2 * (L::kA + (BMN ? blocks * 64 : lines) * 128);  // of both CTAs, a step
     const int half = !first && blocks == 1 ? 0 : 1;  // a second box of 64 (MN-major)
     bool ok = true;
-    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_of(p, t);
+    for (GridWalk walk(p); ok && walk.more; walk.next(p)) {
+      const Tile& tile = walk.tile;
       // rows of A, or of B (columns of the result)
       const int r0 = first            ? tile.m * 256 + rank * 128
                      : EPI == kGated ? tile.n * lines
@@ -467,8 +512,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
                               : smem_desc(first_stage + L::kA, 16, 1024, SW_128B);
       uint32_t st = 0, phase = 0, nc = 0, ns = 0;
       bool ok = true;
-      for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
-        const Tile tile = tile_of(p, t);
+      for (GridWalk walk(p); ok && walk.more; walk.next(p)) {
+        const Tile& tile = walk.tile;
         uint32_t d = 0;
         int left = 0;  // steps of this accumulator
         for (int it = tile.it0; it < tile.it1; it += L::kSteps) {
@@ -542,8 +587,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     Staging<L::kBox, L::kBoxes> out{staging + (warp - L::kFirst) * L::kBoxes * L::kBox, lane, 0};
     uint32_t nc = 0;  // accumulators taken
     bool ok = true;
-    for (int t = blockIdx.x / 2; ok && t < tiles; t += pairs) {
-      const Tile tile = tile_of(p, t);
+    for (GridWalk walk(p); ok && walk.more; walk.next(p)) {
+      const Tile& tile = walk.tile;
       float f[4][32];  // a lane's row: columns of the result, or of g (0, 1) and u (2, 3)
       if (kSum) {
 #pragma unroll
@@ -616,12 +661,12 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
     // Of this CTA's rows of A and of all columns, which both CTAs need.
-    scale_loop<3>(
-        p, bars, scales, blockIdx.x / 2, pairs, tiles,
-        [&](const ScaleWalk& at, uint4(&w)[3]) {
-          w[0] = scale_words(p.a_scales, p.a_rows, at.group, at.tile.m * 256 + rank * 128, lane);
-          w[1] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * p.bn, lane);
-          w[2] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * p.bn + 128, lane);
+    scale_loop<3, GridWalk>(
+        p, bars, scales,
+        [&](const Tile& tile, int group, uint4(&w)[3]) {
+          w[0] = scale_words(p.a_scales, p.a_rows, group, tile.m * 256 + rank * 128, lane);
+          w[1] = scale_words(p.b_scales, p.b_rows, group, tile.n * p.bn, lane);
+          w[2] = scale_words(p.b_scales, p.b_rows, group, tile.n * p.bn + 128, lane);
         },
         [&](uint32_t slot) { arrive_in_first(&bars.sf_full[slot]); });
   }
@@ -661,7 +706,6 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
   Bars& bars = *reinterpret_cast<Bars*>(scales + L::kScales);
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int tiles = p.m_tiles * p.n_tiles * p.parts * p.splits;
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
@@ -698,8 +742,8 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     }
     uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_of(p, t);
+    for (LineWalk walk(p); ok && walk.more; walk.next(p)) {
+      const Tile& tile = walk.tile;
       Step s(p, tile.it0);
       for (int it = tile.it0; it < tile.it1; it += L::kSteps, ++n) {
         if (round > 0 && !warp_wait(&bars.empty[st], (round - 1) & 1, p.status, abort_flag)) {
@@ -721,7 +765,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
             } else {
               tma_load_3d(a, am, bar, k, tile.m * 128, pa);
             }
-            tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, at)], bar, k, tile.n * BN, term_of_b(p, at.pair));
+            tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, at)], bar, k, 0, term_of_b(p, at.pair));
           }
         }
         __syncwarp();
@@ -739,8 +783,8 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     const uint64_t b0 = smem_desc(first_stage + L::kA, 16, 1024, SW_128B);
     uint32_t st = 0, phase = 0, nc = 0, ns = 0;
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_of(p, t);
+    for (LineWalk walk(p); ok && walk.more; walk.next(p)) {
+      const Tile& tile = walk.tile;
       uint32_t d = 0;
       int left = 0;  // steps of this accumulator
       for (int it = tile.it0; it < tile.it1; it += L::kSteps) {
@@ -754,7 +798,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
           }
         }
         const uint32_t slot = ns % kSlots, sf = tmem + L::kScaleCol + slot * L::kScaleCols;
-        const bool new_scales = KIND == kMx8 && (it & 3) == 0;
+        const bool new_scales = KIND == kMx8 && (it == tile.it0 || (it & 3) == 0);
         if (new_scales && !warp_wait(&bars.sf_full[slot], (ns / kSlots) & 1, p.status, abort_flag)) {
           ok = false;
           break;
@@ -806,8 +850,8 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     Staging<4096, 2> out{staging + (warp - 2) * 8192, lane, 0};
     uint32_t nc = 0;  // accumulators taken
     bool ok = true;
-    for (int t = blockIdx.x; ok && t < tiles; t += gridDim.x) {
-      const Tile tile = tile_of(p, t);
+    for (LineWalk walk(p); ok && walk.more; walk.next(p)) {
+      const Tile& tile = walk.tile;
       float sum[BN / kW][kW];  // a lane's row
 #pragma unroll
       for (int i = 0; i < BN; ++i) sum[i / kW][i % kW] = 0.f;
@@ -840,24 +884,24 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
         for (int c = 0; c < 4; ++c)
           *reinterpret_cast<float4*>(box + sw64_offset(lane, c * 16)) =
               make_float4(sum[0][4 * c], sum[0][4 * c + 1], sum[0][4 * c + 2], sum[0][4 * c + 3]);
-        out.send(&maps.c[0], box, tile.n * BN, y, z);
+        out.send(&maps.c[0], box, 0, y, z);
       } else {
 #pragma unroll
         for (int c = 0; c < BN / 32; ++c) {
           uint8_t* box = out.take();
           stage32(box, lane, sum[c], 0.f);
-          out.send(&maps.c[0], box, tile.n * BN + 32 * c, y, z);
+          out.send(&maps.c[0], box, 32 * c, y, z);
         }
       }
     }
     if (lane == 0) bulk_wait0();
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
-    scale_loop<2>(
-        p, bars, scales, blockIdx.x, gridDim.x, tiles,
-        [&](const ScaleWalk& at, uint4(&w)[2]) {
-          w[0] = scale_words(p.a_scales, p.a_rows, at.group, at.tile.m * 128, lane);
-          w[1] = scale_words(p.b_scales, p.b_rows, at.group, at.tile.n * BN, lane);
+    scale_loop<2, LineWalk>(
+        p, bars, scales,
+        [&](const Tile& tile, int group, uint4(&w)[2]) {
+          w[0] = scale_words(p.a_scales, p.a_rows, group, tile.m * 128, lane);
+          w[1] = scale_words(p.b_scales, p.b_rows, group, 0, lane);
         },
         [&](uint32_t slot) { mbar_arrive(&bars.sf_full[slot]); });
   }
@@ -903,12 +947,22 @@ inline bool map_out(CUtensorMap* map, const Matrix& x, int columns = 32) {
 }
 
 // Sums of the partial planes of a split product (nys_join.cu): part holds
-// `splits` x `parts` planes of fp32, plane split * parts + part, each [M][N]
-// (rows of a result) or, turned, [N][width] (a result's columns, its rows
-// side by side). Results in dtype; set up while the product still runs.
+// planes of fp32, plane split * parts + part, each [M][N] (rows of a result) or,
+// of gemm_tokens, [N][width] (a result's columns, its rows side by side).
+// Results in dtype; set up while the product still runs.
+struct Line {  // gemm_tokens' division: a tile of 128 columns has the planes of its CTAs
+  int width;   // 0: not turned
+  int m_tiles, units, ctas;
+  long long line;
+  __host__ __device__ __forceinline__ int planes(int part, int column) const {
+    const long long u = ((long long)part * m_tiles + column / 128) * units;
+    return line_cta(line, ctas, u + units - 1) - line_cta(line, ctas, u) + 1;
+  }
+};
 struct Join {
   const float* part;
-  int splits, M, N, width;  // width: 0, or of turned planes
+  int splits, M, N;
+  Line line;
   void* out[2];             // [M][N] of part 0, 1
   long long stride[2];
 };
@@ -916,35 +970,37 @@ int join(const Join& j, int parts, int dtype, cudaStream_t st);
 // part 0: g, part 1: u; h = act(g) u, and g, u where gate, up are set.
 struct JoinGated {
   const float* part;
-  int splits, M, N, width;
+  int splits, M, N;
+  Line line;
   void *h, *gate, *up;
   long long h_stride, gate_stride, up_stride;
 };
 int join_gated(const JoinGated& j, int act, int dtype, cudaStream_t st);
 
 template <typename Kernel>
-int start(const char* name, Kernel kernel, int ctas_per_tile, int threads, int bytes, const Maps& maps,
-          const Params& p, cudaStream_t st) {
+int start(const char* name, Kernel kernel, int grid, int threads, int bytes, const Maps& maps, const Params& p,
+          cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
-  const long long tiles = (long long)p.m_tiles * p.n_tiles * p.parts * p.splits;
-  if (tiles >= (1ll << 31) - 1024) return NYS_ERR_SHAPE;
-  const int most = plan_sms() / ctas_per_tile;
   KernelScope scope(name, st);
-  kernel<<<(tiles < most ? (int)tiles : most) * ctas_per_tile, threads, bytes, st>>>(maps, p);
+  kernel<<<grid, threads, bytes, st>>>(maps, p);
   return launch_status();
 }
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {
   using L = PairLayout<KIND, OutT>;
-  return start(name, gemm_pair<KIND, AMN, BMN, EPI, OutT>, 2, L::kThreads, L::kBytes, maps, p, st);
+  const long long tiles = (long long)p.m_tiles * p.n_tiles * p.parts * p.splits;
+  if (tiles >= (1ll << 31) - 1024) return NYS_ERR_SHAPE;
+  const int most = plan_sms() / 2;
+  return start(name, gemm_pair<KIND, AMN, BMN, EPI, OutT>, 2 * (tiles < most ? (int)tiles : most), L::kThreads,
+               L::kBytes, maps, p, st);
 }
 template <int KIND, bool AMN>
-int launch_tokens(const char* name, int bn, const Maps& maps, const Params& p, cudaStream_t st) {
+int launch_tokens(const char* name, int bn, int ctas, const Maps& maps, const Params& p, cudaStream_t st) {
   auto go = [&](auto n) {
     constexpr int BN = decltype(n)::value;
     using L = TokensLayout<KIND, BN>;
-    return start(name, gemm_tokens<KIND, AMN, BN>, 1, L::kThreads, L::kBytes, maps, p, st);
+    return start(name, gemm_tokens<KIND, AMN, BN>, ctas, L::kThreads, L::kBytes, maps, p, st);
   };
   using std::integral_constant;
   switch (bn) {
@@ -957,8 +1013,7 @@ int launch_tokens(const char* name, int bn, const Maps& maps, const Params& p, c
 constexpr int kMostTokens = 128;  // of gemm_tokens
 inline int columns_of(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
 
-// How a product is cut: columns of a tile (gemm_pair; gemm_tokens has its own) and
-// ranges of K, whose partial sums are joined. The time of a choice is counted in
+// How gemm_pair's product is cut: columns of a tile and ranges of K, whose partial sums are joined. The time of a choice is counted in
 // steps of a full tile (0.3 us; `pairs` of them for a K block of fp32): rounds of tiles over the CTAs times a tile's steps,
 // two more for its start and end, and for more than one range the join (ten
 // steps' time to begin, then its bytes, write and read, at 5 TB/s).
@@ -968,19 +1023,25 @@ struct Cut {
 // Steps of each of s ranges, a multiple of `unit` (8-bit operands: four, whose
 // scales come in one word).
 inline int range_of(int steps, int s, int unit) { return ((steps + s - 1) / s + unit - 1) / unit * unit; }
-inline Cut cut_tokens(long long row_tiles, long long rows, int bn, int steps, int unit, int pairs, int least) {
-  const int sms = plan_sms();
-  Cut best{bn, 1};
-  double best_time = 1e30;
-  for (int s = 1; s <= 16 && (s == 1 || steps / s >= least); ++s) {
-    const int per = range_of(steps, s, unit);
-    if ((steps + per - 1) / per != s) continue;  // no empty range
-    const double rounds = (double)((row_tiles * s + sms - 1) / sms);
-    // 16 KB of the weights a step, and the partial sums in and out
-    const double time = rounds * (per * (double)pairs + 1.0) + (double)s * rows * bn * 8.0 / (16384.0 * sms);
-    if (time < best_time * 0.999) best_time = time, best.splits = s;
-  }
-  return best;
+
+// gemm_tokens: the line of `parts` x N / 128 tiles in units of two steps (fp32: the
+// six products of a K block) over the SMs; a CTA has three units at least, so that
+// its partial sums stay few beside its weights.
+inline Line line_of(long long N, int its, int parts, int unit, int width) {
+  Line l{};
+  l.width = width;
+  l.m_tiles = (int)((N + 127) / 128);
+  l.units = (its + unit - 1) / unit;
+  l.line = (long long)l.m_tiles * parts * l.units;
+  const long long most = l.line / 3 > 0 ? l.line / 3 : 1;
+  l.ctas = (int)(most < plan_sms() ? most : plan_sms());
+  return l;
+}
+// Planes that a tile may have: as many CTAs as its units can touch.
+inline int most_planes(const Line& l) {
+  const long long least = l.line / l.ctas;  // units of a CTA
+  const long long n = (l.units + least - 2) / least + 1;
+  return (int)(n < l.ctas ? n : l.ctas);
 }
 inline Cut cut_pair(long long M, long long N, int steps, int unit, int pairs, int parts, int most_bn, int bn_step, bool gated,
                     int least) {

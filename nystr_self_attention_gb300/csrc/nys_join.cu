@@ -47,12 +47,13 @@ join_turned(const Join j) {
   cudaGridDependencySynchronize();
   const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32;
   const int n = n0 + threadIdx.x / 8, m = m0 + (threadIdx.x & 7) * 4;
-  const long long plane = (long long)j.N * j.width;
+  const long long plane = (long long)j.N * j.line.width;
   float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
   if (n < j.N && m < j.M) {
-    const float* at = j.part + (long long)n * j.width + m;
+    const float* at = j.part + (long long)n * j.line.width + m;
+    const int planes = j.line.planes(0, n0);
 #pragma unroll 8
-    for (int s = 0; s < j.splits; ++s) add(v, *reinterpret_cast<const float4*>(at + s * plane));
+    for (int s = 0; s < planes; ++s) add(v, *reinterpret_cast<const float4*>(at + s * plane));
   }
   const int q = (threadIdx.x & 7) * 4;
   tile[q][threadIdx.x / 8] = v.x, tile[q + 1][threadIdx.x / 8] = v.y;
@@ -100,15 +101,15 @@ join_gated_turned(const JoinGated j, int act) {
   cudaGridDependencySynchronize();
   const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32;
   const int n = n0 + threadIdx.x / 8, m = m0 + (threadIdx.x & 7) * 4;
-  const long long plane = (long long)j.N * j.width;
+  const long long plane = (long long)j.N * j.line.width;
   float4 g = make_float4(0.f, 0.f, 0.f, 0.f), u = g;
   if (n < j.N && m < j.M) {
-    const float* at = j.part + (long long)n * j.width + m;
+    const float* at = j.part + (long long)n * j.line.width + m;
+    const int of_g = j.line.planes(0, n0), of_u = j.line.planes(1, n0);
 #pragma unroll 4
-    for (int s = 0; s < j.splits; ++s) {
-      add(g, *reinterpret_cast<const float4*>(at + 2 * s * plane));
-      add(u, *reinterpret_cast<const float4*>(at + (2 * s + 1) * plane));
-    }
+    for (int s = 0; s < of_g; ++s) add(g, *reinterpret_cast<const float4*>(at + 2 * s * plane));
+#pragma unroll 4
+    for (int s = 0; s < of_u; ++s) add(u, *reinterpret_cast<const float4*>(at + (2 * s + 1) * plane));
   }
   const int q = (threadIdx.x & 7) * 4, f = threadIdx.x / 8;
   gs[q][f] = g.x, gs[q + 1][f] = g.y, gs[q + 2][f] = g.z, gs[q + 3][f] = g.w;
@@ -148,7 +149,7 @@ int start(const char* name, K kernel, dim3 grid, cudaStream_t st, Args... args) 
 
 int join(const Join& j, int parts, int dtype, cudaStream_t st) {
   const bool bf16 = dtype == NYS_BF16;
-  if (j.width) {
+  if (j.line.width) {
     const dim3 grid((j.N + 31) / 32, (j.M + 31) / 32);
     return bf16 ? start("product_join", join_turned<__nv_bfloat16>, grid, st, j)
                 : start("product_join", join_turned<float>, grid, st, j);
@@ -161,7 +162,7 @@ int join(const Join& j, int parts, int dtype, cudaStream_t st) {
 
 int join_gated(const JoinGated& j, int act, int dtype, cudaStream_t st) {
   const bool bf16 = dtype == NYS_BF16;
-  if (j.width) {
+  if (j.line.width) {
     const dim3 grid((j.N + 31) / 32, (j.M + 31) / 32);
     return bf16 ? start("gated_join", join_gated_turned<__nv_bfloat16>, grid, st, j, act)
                 : start("gated_join", join_gated_turned<float>, grid, st, j, act);

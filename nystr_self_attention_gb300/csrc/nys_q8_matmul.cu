@@ -24,6 +24,7 @@ using namespace nys::gemm;
 struct Q8Plan {
   bool turned;
   int bn, splits, its_per_split;
+  Line line;
   size_t bytes;  // of partial sums
 };
 
@@ -31,15 +32,18 @@ Q8Plan plan_of(int T, int N, int K) {
   Q8Plan q{};
   const int its = (K + 127) / 128;
   q.turned = T <= kMostTokens;
-  const Cut cut = q.turned ? cut_tokens((N + 127) / 128, N, columns_of(T), its, 4, 1, 2)
-                           : cut_pair(T, N, its, 4, 1, 1, 224, 32, false, 4);
-  q.bn = cut.bn;
-  q.splits = cut.splits;
-  q.its_per_split = range_of(its, q.splits, 4);
-  if (q.turned)
+  if (q.turned) {
+    q.bn = columns_of(T);
+    q.line = line_of(N, its, 1, 2, q.bn);
+    q.splits = most_planes(q.line);
     q.bytes = (size_t)q.splits * N * q.bn * 4;
-  else if (q.splits > 1)
-    q.bytes = (size_t)q.splits * T * N * 4;
+  } else {
+    const Cut cut = cut_pair(T, N, its, 4, 1, 1, 224, 32, false, 4);
+    q.bn = cut.bn;
+    q.splits = cut.splits;
+    q.its_per_split = range_of(its, q.splits, 4);
+    if (q.splits > 1) q.bytes = (size_t)q.splits * T * N * 4;
+  }
   q.bytes = (q.bytes + 255) & ~size_t(255);
   return q;
 }
@@ -92,9 +96,11 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   Params p{};
   if ((rc = operator_status(dev, &p.status)) != NYS_OK) return rc;
   p.m_tiles = plan.turned ? (rows.rows + 127) / 128 : (rows.rows + 255) / 256;
-  p.n_tiles = (cols.rows + plan.bn - 1) / plan.bn;
+  p.n_tiles = plan.turned ? 1 : (cols.rows + plan.bn - 1) / plan.bn;
   p.parts = p.pairs = 1;
   p.splits = plan.splits;
+  p.unit = 2;
+  p.units = plan.line.units;
   p.k_blocks = p.its = (K + 127) / 128;
   p.its_per_split = plan.its_per_split;
   p.bn = plan.bn;
@@ -119,14 +125,14 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   maps.b[1] = maps.b[0];
   const char* name = "q8_matmul";
   if (plan.turned)
-    rc = launch_tokens<kMx8, false>(name, plan.bn, maps, p, stream);
+    rc = launch_tokens<kMx8, false>(name, plan.bn, plan.line.ctas, maps, p, stream);
   else if (!direct || dtype == NYS_FP32)
     rc = launch_pair<kMx8, false, false, kPlain, float>(name, maps, p, stream);
   else
     rc = launch_pair<kMx8, false, false, kPlain, __nv_bfloat16>(name, maps, p, stream);
   if (rc != NYS_OK || direct) return rc;
-  const Join j{static_cast<const float*>(workspace), plan.splits, T, N, plan.turned ? plan.bn : 0,
-               {out, nullptr}, {out_stride, 0}};
+  const Join j{static_cast<const float*>(workspace), plan.splits, T, N, plan.line, {out, nullptr},
+               {out_stride, 0}};
   return join(j, 1, dtype, stream);
 }
 
