@@ -4,8 +4,8 @@
 // once, with the row held in registers between its sum of squares and its
 // output.
 //
-// TPR threads share a row, V vectors of eight channels each; vector i of thread
-// t is channels 8 (i TPR + t), so 16 neighbouring threads hold the 128 channels
+// TPR threads share a row (or as many as it needs, where it has a CTA to itself), V
+// vectors of eight channels each; vector i of thread t is channels 8 (i TPR + t), so 16 neighbouring threads hold the 128 channels
 // of one 8-bit block. A CTA holds several short rows or one long one and walks
 // rows with the grid's step; the weight stays in registers, and the next row's
 // loads are in flight while this one is summed.
@@ -81,6 +81,7 @@ struct Vec<__nv_bfloat16> {
 // Sum of v over the TPR threads of a row, the same bits in each: shuffles, then
 // one slot per warp. The slots alternate between two sets, so one barrier per
 // sum is enough.
+// A group that has its CTA to itself (TPR >= 256) may have fewer threads than TPR.
 template <int TPR, int N>
 __device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[N], int& phase) {
 #pragma unroll
@@ -88,44 +89,55 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[N], int& 
 #pragma unroll
     for (int j = 0; j < N; ++j) v[j] += __shfl_xor_sync(0xffffffffu, v[j], o);
   if (TPR == 32) return;
-  constexpr int W = TPR / 32;
-  const int warp = threadIdx.x >> 5, group = threadIdx.x / TPR;
+  const int W = TPR >= 256 ? blockDim.x / 32 : TPR / 32;
+  const int warp = threadIdx.x >> 5, group = TPR >= 256 ? 0 : threadIdx.x / TPR;
   float(*set)[N] = slots + phase * (blockDim.x / 32);
   phase ^= 1;
   if ((threadIdx.x & 31) == 0)
 #pragma unroll
     for (int j = 0; j < N; ++j) set[warp][j] = v[j];
-  asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
+  if (TPR >= 256)
+    __syncthreads();  // the CTA is the group
+  else
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     float s = 0.f;
 #pragma unroll
-    for (int w = 0; w < W; ++w) s += set[group * W + w][j];
+    for (int w = 0; w < TPR / 32; ++w)
+      if (TPR < 256 || w < W) s += set[group * W + w][j];
     v[j] = s;
   }
 }
 
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
+// Threads per SM that the registers are cut for.
+template <typename T, int TPR, bool RES>
+constexpr int fwd_threads() {
+  return TPR == 1024 ? 1024 : sizeof(T) == 4 && RES ? 1024 : 1536;
+}
+constexpr int kBwdThreads = 512;
 
-template <typename T, int TPR, int V, bool EIGHT>
-__global__ void __launch_bounds__(threads_of(TPR), (sizeof(T) == 4 || V > 2 ? 512 : 1024) / threads_of(TPR))
+
+template <typename T, int TPR, int V, bool EIGHT, bool RES>
+__global__ void __launch_bounds__(threads_of(TPR), fwd_threads<T, TPR, RES>() / threads_of(TPR))
 add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restrict__ weight, T* sum, T* y) {
   constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
   __shared__ float slots[2 * THREADS / 32][1];
   int phase = 0;
-  const int t = threadIdx.x % TPR;
+  const int across = GROUPS == 1 ? blockDim.x : TPR, t = threadIdx.x % TPR;  // threads of a row
   const int step = gridDim.x * GROUPS;
   int row = blockIdx.x * GROUPS + threadIdx.x / TPR;
   Vec<T> nx[V], nr[V];
   auto fetch = [&](int r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
       nx[i].clear();
-      nr[i].clear();
+      if (RES) nr[i].clear();
       if (r < p.rows && c < p.d) {
         nx[i].load(x + r * p.x + c);
-        if (res) nr[i].load(res + r * p.r + c);
+        if (RES) nr[i].load(res + r * p.r + c);
       }
     }
   };
@@ -133,7 +145,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
   float w[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
-    const int c = 8 * (i * TPR + t);
+    const int c = 8 * (i * across + t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[i][j] = c < p.d ? (weight ? weight[c + j] : 1.f) : 0.f;
   }
@@ -143,7 +155,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       nx[i].widen(s[i]);
-      if (res) {
+      if (RES) {
         float r[8];
         nr[i].widen(r);
 #pragma unroll
@@ -151,7 +163,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
         Vec<T> out;  // s is what is kept: rounded
         out.narrow(s[i]);
         out.widen(s[i]);
-        const int c = 8 * (i * TPR + t);
+        const int c = 8 * (i * across + t);
         if (sum && c < p.d) out.store(sum + row * p.s + c);
       }
 #pragma unroll
@@ -162,7 +174,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
     const float r = rsqrtf(fmaf(total[0], p.inv_d, p.eps));
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
 #pragma unroll
       for (int j = 0; j < 8; ++j) s[i][j] *= r * w[i][j];
       if (!EIGHT) {
@@ -192,7 +204,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
 
 // part: [CTAs][d] sums of gy h over a CTA's rows, or null.
 template <typename T, int TPR, int V>
-__global__ void __launch_bounds__(threads_of(TPR), TPR > 512 ? 1 : 512 / threads_of(TPR))
+__global__ void __launch_bounds__(threads_of(TPR), kBwdThreads / threads_of(TPR))
 add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, const float* __restrict__ weight,
                   T* dx, float* part) {
   constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
@@ -201,14 +213,15 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
   __shared__ float slots[2 * THREADS / 32][2];
   extern __shared__ float sums[];  // [GROUPS][d] where a CTA holds several rows
   int phase = 0;
-  const int t = threadIdx.x % TPR, group = threadIdx.x / TPR;
+  cudaTriggerProgrammaticLaunchCompletion();
+  const int across = GROUPS == 1 ? blockDim.x : TPR, t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int step = gridDim.x * GROUPS;
   int row = blockIdx.x * GROUPS + group;
   Vec<T> ns[V], ng[V], na[V];
   auto fetch = [&](int r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
       ns[i].clear();
       ng[i].clear();
       na[i].clear();
@@ -220,7 +233,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
     }
   };
   auto load_weight = [&](int i, float (&w)[8]) {
-    const int c = 8 * (i * TPR + t);
+    const int c = 8 * (i * across + t);
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = c < p.d ? (weight ? weight[c + j] : 1.f) : 0.f;
   };
@@ -268,7 +281,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
         acc[i][j] = fmaf(g[j], h, acc[i][j]);
         e[j] = fmaf(r, (ROOMY ? kept[ROOMY ? i : 0][j] : w[j]) * g[j], fmaf(h, m, e[j]));
       }
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
       Vec<T> out;
       out.narrow(e);
       if (c < p.d) out.store(dx + row * p.dx + c);
@@ -281,7 +294,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
   if constexpr (GROUPS == 1) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
       if (c < p.d)
 #pragma unroll
         for (int j = 0; j < 8; ++j) dst[c + j] = acc[i][j];
@@ -289,7 +302,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
   } else {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int c = 8 * (i * TPR + t);
+      const int c = 8 * (i * across + t);
       if (c < p.d)
 #pragma unroll
         for (int j = 0; j < 8; ++j) sums[group * p.d + c + j] = acc[i][j];
@@ -332,34 +345,41 @@ int check_common(const nys_add_rms_norm_t* p) {
   return NYS_OK;
 }
 
-// f(TPR, V) for a row of d channels: two vectors per thread until a row has a
-// CTA of 512 threads to itself, then four.
-template <typename F>
+// f(TPR, V) for a row of d channels: one vector per thread until a row has 1024
+// threads; backward (MORE), whose threads also carry the weight's sums, two until
+// it has 512. Forward to 8 bits, 65536 x 2048: 160 us with two, 149 with one;
+// backward, 16384 x 4096: 91 us with two, 95 with one.
+template <bool MORE, typename F>
 auto by_width(int d, F&& f) {
   using std::integral_constant;
-  if (d <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
-  if (d <= 512) return f(integral_constant<int, 32>{}, integral_constant<int, 2>{});
-  if (d <= 1024) return f(integral_constant<int, 64>{}, integral_constant<int, 2>{});
-  if (d <= 2048) return f(integral_constant<int, 128>{}, integral_constant<int, 2>{});
-  if (d <= 4096) return f(integral_constant<int, 256>{}, integral_constant<int, 2>{});
-  if (d <= 8192) return f(integral_constant<int, 512>{}, integral_constant<int, 2>{});
-  return f(integral_constant<int, 512>{}, integral_constant<int, 4>{});
+  constexpr int V = MORE ? 2 : 1;
+  const int units = (d + 8 * V - 1) / (8 * V);
+  if (MORE && d <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 1>{});
+  if (units <= 32) return f(integral_constant<int, 32>{}, integral_constant<int, V>{});
+  if (units <= 64) return f(integral_constant<int, 64>{}, integral_constant<int, V>{});
+  if (units <= 128) return f(integral_constant<int, 128>{}, integral_constant<int, V>{});
+  if (units <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, V>{});
+  if (units <= 512) return f(integral_constant<int, 512>{}, integral_constant<int, V>{});
+  return f(integral_constant<int, MORE ? 512 : 1024>{}, integral_constant<int, MORE ? 4 : 2>{});
 }
-
 // CTAs: one per group of rows until the GPU is full.
 int grid_of(int rows, int groups, int ctas_per_sm) {
   const long long want = ((long long)rows + groups - 1) / groups, most = (long long)plan_sms() * ctas_per_sm;
   return (int)(want < most ? want : most);
 }
 
-template <int TPR>
-int back_grid(int rows) {
-  constexpr int T = threads_of(TPR);
-  return grid_of(rows, T / TPR, 512 / T);
+// Threads of a CTA: as many warps as a row has vectors for, where it has one row.
+template <int TPR, int V>
+int cta_threads(int d) {
+  return TPR < 256 ? 256 : ((d + 8 * V - 1) / (8 * V) + 31) / 32 * 32;
+}
+template <int TPR, int V>
+int back_grid(const nys_add_rms_norm_t& a) {
+  return grid_of(a.rows, threads_of(TPR) / TPR, kBwdThreads / cta_threads<TPR, V>(a.d));
 }
 
 int back_ctas(const nys_add_rms_norm_t& a) {
-  return by_width(a.d, [&](auto tpr, auto) { return back_grid<decltype(tpr)::value>(a.rows); });
+  return by_width<true>(a.d, [&](auto tpr, auto v) { return back_grid<decltype(tpr)::value, decltype(v)::value>(a); });
 }
 
 NormParams params_of(const nys_add_rms_norm_t& a) {
@@ -386,17 +406,20 @@ int launch_fwd(const nys_add_rms_norm_t& a, const void* x, const void* res, cons
     p.scales = static_cast<uint8_t*>(y8->scales);
     p.y = y8->stride;
   }
-  return by_width(a.d, [&](auto tpr, auto v) {
+  return by_width<false>(a.d, [&](auto tpr, auto v) {
     constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
-    constexpr int per_sm = (sizeof(T) == 4 || V > 2 ? 512 : 1024) / THREADS;
-    const int grid = grid_of(a.rows, THREADS / TPR, per_sm);
-    auto go = [&](auto kernel) {
+    const int threads = cta_threads<TPR, V>(a.d);
+    auto go = [&](auto kernel, int per_sm) {
+      const int grid = grid_of(a.rows, THREADS / TPR, per_sm / threads);
       KernelScope scope("add_rms_norm", st);
-      kernel<<<grid, THREADS, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(res), weight,
+      kernel<<<grid, threads, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(res), weight,
                                        static_cast<T*>(sum), static_cast<T*>(y));
       return launch_status();
     };
-    return y8 ? go(add_rms_norm<T, TPR, V, true>) : go(add_rms_norm<T, TPR, V, false>);
+    constexpr int with = fwd_threads<T, TPR, true>(), without = fwd_threads<T, TPR, false>();
+    if (res)
+      return y8 ? go(add_rms_norm<T, TPR, V, true, true>, with) : go(add_rms_norm<T, TPR, V, false, true>, with);
+    return y8 ? go(add_rms_norm<T, TPR, V, true, false>, without) : go(add_rms_norm<T, TPR, V, false, false>, without);
   });
 }
 
@@ -404,12 +427,12 @@ template <typename T>
 int launch_bwd(const nys_add_rms_norm_t& a, const void* s, const void* gy, const void* gs, const float* weight,
                void* dx, float* part, cudaStream_t st) {
   const NormParams p = params_of(a);
-  return by_width(a.d, [&](auto tpr, auto v) {
+  return by_width<true>(a.d, [&](auto tpr, auto v) {
     constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
     constexpr int GROUPS = THREADS / TPR;
     const size_t smem = GROUPS > 1 && part ? (size_t)GROUPS * a.d * sizeof(float) : 0;  // at most 16 KB
     KernelScope scope("add_rms_norm_back", st);
-    add_rms_norm_back<T, TPR, V><<<back_grid<TPR>(a.rows), THREADS, smem, st>>>(
+    add_rms_norm_back<T, TPR, V><<<back_grid<TPR, V>(a), cta_threads<TPR, V>(a.d), smem, st>>>(
         p, static_cast<const T*>(s), static_cast<const T*>(gy), static_cast<const T*>(gs), weight,
         static_cast<T*>(dx), part);
     return launch_status();
