@@ -663,28 +663,32 @@ def _first_matrix(name, t):
         code = NYS_FP32
     else:
         raise ValueError(f"{name} must be float32 or bfloat16")
-    if not t.is_cuda or t.dim() != 2:
+    shape = t.shape
+    if not t.is_cuda or len(shape) != 2:
         raise ValueError(f"{name} must be a CUDA tensor [rows, width]")
     device = torch._C._cuda_getDevice()
-    rows, width = t.shape
-    if max(rows, width) > _INT_MAX:
-        raise ValueError(f"{name} has sizes past 32 bits: {tuple(t.shape)}")
-    return rows, width, _matrix(name, t, dtype, t.shape, device), code, device
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
+    rows, width = shape
+    if rows > _INT_MAX or width > _INT_MAX:
+        raise ValueError(f"{name} has sizes past 32 bits: {tuple(shape)}")
+    stride, one = t.stride()
+    if one != 1 and width > 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return rows, width, stride if rows > 1 else width, code, device
 
 
 def _matrix(name, t, dtype, shape, device):
     """Distance between the rows of a [rows, width] tensor of the given type,
     shape and device."""
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
-    if t.dtype is not dtype:
-        raise ValueError(f"{name} must be {dtype}")
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype} of shape {tuple(shape)}, not {t.dtype} of {tuple(t.shape)}")
     if t.get_device() != device:
         raise ValueError(f"{name} is on {t.device}, not on the current CUDA device")
-    s = t.stride()
-    if s[1] != 1 and shape[1] > 1:
+    stride, one = t.stride()
+    if one != 1 and shape[1] > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return s[0] if shape[0] > 1 else shape[1]
+    return stride if shape[0] > 1 else shape[1]
 
 
 class NystromQ8:
@@ -696,18 +700,19 @@ class NystromQ8:
 
     def __init__(self, codes, scales):
         torch = _torch or _lazy_torch()
-        if not codes.is_cuda or codes.dtype != torch.uint8 or codes.dim() != 2:
+        shape = codes.shape
+        if not codes.is_cuda or codes.dtype is not torch.uint8 or len(shape) != 2:
             raise ValueError("codes must be a uint8 CUDA tensor [rows, K]")
-        rows, K = codes.shape
-        if codes.stride(1) != 1:
+        rows, K = shape
+        stride, one = codes.stride()
+        if one != 1:
             raise ValueError("codes must have contiguous rows")
-        if rows < 1 or K < 1 or K % 16 or max(rows, K) > _INT_MAX:
+        if rows < 1 or K < 1 or K % 16 or rows > _INT_MAX or K > _INT_MAX:
             raise NystromError(NYS_ERR_SHAPE, "NystromQ8")
         self.device = codes.get_device()
-        words = (-(-K // 512), rows)
-        at = _flat("scales", scales, torch.int32, words, self.device)
+        at = _flat("scales", scales, torch.int32, (-(-K // 512), rows), self.device)
         self._codes, self._scales, self.rows, self.K = codes, scales, rows, K
-        self.desc = _Q8_DESC.pack(codes.data_ptr(), at, rows, K, codes.stride(0) if rows > 1 else K)
+        self.desc = _Q8_DESC.pack(codes.data_ptr(), at, rows, K, stride if rows > 1 else K)
 
     @property
     def codes(self):
@@ -718,10 +723,10 @@ class NystromQ8:
         return self._scales
 
 
-def _q8_here(name, q):
+def _q8_here(name, q, device):
     if not isinstance(q, NystromQ8):
         raise ValueError(f"{name} must be a NystromQ8")
-    if q.device != _torch._C._cuda_getDevice():
+    if q.device != device:
         raise ValueError(f"{name} is on device {q.device}, not on the current CUDA device")
 
 
@@ -736,7 +741,7 @@ def nystrom_q8_write(q, x, block_rows=1, stream=None):
     tensor) into q; block_rows: 1, or 128 rows that share a scale (weights)."""
     lib = _lib or load_library()
     torch = _torch or _lazy_torch()
-    _q8_here("q", q)
+    _q8_here("q", q, torch._C._cuda_getDevice())
     if not x.is_cuda or x.dim() != 2 or x.dtype not in (torch.float32, torch.bfloat16):
         raise ValueError("x must be a float32 or bfloat16 CUDA tensor [rows, K]")
     if x.shape != (q.rows, q.K) or x.get_device() != q.device:
@@ -755,7 +760,7 @@ def nystrom_q8_read(q, out, stream=None):
     """The values that q stands for, to out [rows, K]."""
     lib = _lib or load_library()
     rows, K, stride, code, dev = _first_matrix("out", out)
-    _q8_here("q", q)
+    _q8_here("q", q, dev)
     if (rows, K) != (q.rows, q.K):
         raise ValueError(f"out must have shape {(q.rows, q.K)}, not {(rows, K)}")
     rc = lib.nystrom_q8_read(q.desc, out.data_ptr(), stride, code, _raw_stream(stream, dev))
@@ -768,15 +773,30 @@ def nystrom_q8_matmul_workspace_bytes(T, N, K, dtype) -> int:
     return load_library().nystrom_q8_matmul_workspace_bytes(T, N, K, dtype)
 
 
+_needs = {}  # workspace bytes by call, sizes and device (its SMs): a dictionary takes a fifth of the query
+
+
+def _need(query, key):
+    n = _needs.get(key)
+    if n is None:
+        n = query()
+        if n:  # 0 may mean a refused call, which the key does not tell
+            if len(_needs) > 4096:
+                _needs.clear()
+            _needs[key] = n
+    return n
+
+
 def nystrom_q8_matmul(a, w, out, workspace=None, stream=None):
     """out [T, N] = a w^T of the 8-bit matrices a [T, K] and w [N, K] (NystromQ8)."""
     lib = _lib or load_library()
     T, N, stride, code, dev = _first_matrix("out", out)
-    _q8_here("a", a)
-    _q8_here("w", w)
+    _q8_here("a", a, dev)
+    _q8_here("w", w, dev)
     if (T, N) != (a.rows, w.rows):
         raise ValueError(f"out must have shape {(a.rows, w.rows)}, not {(T, N)}")
-    need = lib.nystrom_q8_matmul_workspace_bytes(T, N, a.K, code)
+    K = a.K
+    need = _need(lambda: lib.nystrom_q8_matmul_workspace_bytes(T, N, K, code), ("q8", T, N, K, code, dev))
     ws, nbytes, keep = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_q8_matmul(a.desc, w.desc, out.data_ptr(), stride, code, ws, nbytes, _raw_stream(stream, dev))
     del keep
@@ -794,7 +814,7 @@ def nystrom_add_rms_norm_fwd(x, residual, weight, sum_out, y, eps=1e-6, stream=N
     ss = 0 if sum_out is None else _matrix("sum_out", sum_out, dtype, shape, dev)
     eight = isinstance(y, NystromQ8)
     if eight:
-        _q8_here("y", y)
+        _q8_here("y", y, dev)
         if (y.rows, y.K) != (rows, d):
             raise ValueError(f"y must be {(rows, d)}, not {(y.rows, y.K)}")
         ys = 0
@@ -886,7 +906,7 @@ def nystrom_gated_ff_fwd(x, w_gate, w_up, h, gate=None, up=None, activation=NYS_
     desc = _FF_DESC.pack(T, d, f, activation, layout, code, xs, wst, _matrix("h", h, dtype, (T, f), dev),
                          _matrix("gate", gate, dtype, (T, f), dev) if keep else 0,
                          _matrix("up", up, dtype, (T, f), dev) if keep else 0, 0, 0)
-    need = lib.nystrom_gated_ff_workspace_bytes(desc, 0)
+    need = _need(lambda: lib.nystrom_gated_ff_workspace_bytes(desc, 0), ("ff", T, d, f, layout, code, dev))
     ws, nbytes, kept = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_gated_ff_fwd(desc, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), h.data_ptr(),
                                   gate.data_ptr() if keep else None, up.data_ptr() if keep else None, ws, nbytes,
@@ -912,7 +932,7 @@ def nystrom_gated_ff_bwd(x, w_gate, w_up, gate, up, gh, dx=None, dw_gate=None, d
     desc = _FF_DESC.pack(T, d, f, activation, layout, code, xs, wst, _matrix("gh", gh, dtype, (T, f), dev),
                          _matrix("gate", gate, dtype, (T, f), dev), _matrix("up", up, dtype, (T, f), dev),
                          0 if dx is None else _matrix("dx", dx, dtype, (T, d), dev), dws)
-    need = lib.nystrom_gated_ff_workspace_bytes(desc, 1)
+    need = _need(lambda: lib.nystrom_gated_ff_workspace_bytes(desc, 1), ("ffb", T, d, f, layout, code, dev))
     ws, nbytes, kept = _scratch(need, workspace, dev, stream)
     rc = lib.nystrom_gated_ff_bwd(
         desc, x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), gate.data_ptr(), up.data_ptr(), gh.data_ptr(),

@@ -62,18 +62,37 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
   }
 }
 
-// x [rows][cols] -> terms [3][rows][cols]. Eight elements per thread.
-__global__ void __launch_bounds__(256)
-split_terms(const float* __restrict__ x, long long stride, __nv_bfloat16* __restrict__ terms, long long rows,
-            int cols) {
-  const int units = cols / 8;
-  const long long e = (long long)blockIdx.x * 256 + threadIdx.x, r = e / units;
-  if (r >= rows) return;
+// Matrices to split: x [rows][cols] -> terms [3][rows][cols], eight elements per
+// thread, each matrix by a range of a launch's CTAs.
+struct Splits {
+  struct One {
+    const float* x;
+    __nv_bfloat16* terms;
+    long long stride, rows;
+    int cols;
+    unsigned end;  // CTAs up to and with this matrix's
+  } one[3];
+  int count;
+  void add(const void* x, long long stride, void* terms, long long rows, int cols) {
+    const unsigned start = ctas();
+    one[count++] = One{static_cast<const float*>(x), static_cast<__nv_bfloat16*>(terms), stride, rows, cols,
+                       start + (unsigned)((rows * (cols / 8) + 255) / 256)};
+  }
+  unsigned ctas() const { return count ? one[count - 1].end : 0u; }
+};
+__device__ __forceinline__ void split_matrix(const Splits& p, unsigned cta) {
+  int i = 0;
+  while (cta >= p.one[i].end) ++i;
+  const Splits::One& m = p.one[i];
+  const int units = m.cols / 8;
+  const long long e = (long long)(cta - (i ? p.one[i - 1].end : 0u)) * 256 + threadIdx.x, r = e / units;
+  if (r >= m.rows) return;
   const int c = (int)(e - r * units) * 8;
   float v[8];
-  load8(x + r * stride + c, v);
-  store_terms(terms + r * cols + c, rows * cols, v);
+  load8(m.x + r * m.stride + c, v);
+  store_terms(m.terms + r * m.cols + c, m.rows * m.cols, v);
 }
+__global__ void __launch_bounds__(256) split_terms(const __grid_constant__ Splits p) { split_matrix(p, blockIdx.x); }
 
 // ------------------------------------------------------- dg and du
 
@@ -81,13 +100,18 @@ struct GradParams {
   long long g, u, h;  // row strides
   long long T;
   int f;
+  unsigned ctas;  // those behind split the matrices of `more`
 };
 
 // dg, du [T][f]; of fp32 as terms [3][T][f]. Eight elements per thread.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
-gated_ff_back(const GradParams p, const T* __restrict__ gate, const T* __restrict__ up, const T* __restrict__ gh,
+gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Splits more, const T* __restrict__ gate, const T* __restrict__ up, const T* __restrict__ gh,
               __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du) {
+  if (sizeof(T) == 4 && blockIdx.x >= p.ctas) {
+    split_matrix(more, blockIdx.x - p.ctas);
+    return;
+  }
   const int units = p.f / 8;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x, r = e / units;
   if (r >= p.T) return;
@@ -215,14 +239,6 @@ int check_common(const nys_gated_ff_t* p) {
 
 // ----------------------------------------------------------------- launches
 
-int split(const void* x, long long stride, void* terms, long long rows, int cols, cudaStream_t st) {
-  const long long ctas = (rows * (cols / 8) + 255) / 256;
-  KernelScope scope("split_terms", st);
-  split_terms<<<(unsigned)ctas, 256, 0, st>>>(static_cast<const float*>(x), stride,
-                                              static_cast<__nv_bfloat16*>(terms), rows, cols);
-  return launch_status();
-}
-
 Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int* status) {
   Params p{};
   p.m_tiles = q.m_tiles;
@@ -268,10 +284,13 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
   int rc;
   if (pl.f32) {
     const int wr = io ? a.d : a.f, wc = io ? a.f : a.d;
-    if ((rc = split(x, a.x, ws + pl.x, a.T, a.d, st)) != NYS_OK ||
-        (rc = split(wg, a.w, ws + pl.wg, wr, wc, st)) != NYS_OK ||
-        (rc = split(wu, a.w, ws + pl.wu, wr, wc, st)) != NYS_OK)
-      return rc;
+    Splits m{};
+    m.add(x, a.x, ws + pl.x, a.T, a.d);
+    m.add(wg, a.w, ws + pl.wg, wr, wc);
+    m.add(wu, a.w, ws + pl.wu, wr, wc);
+    KernelScope scope("split_terms", st);
+    split_terms<<<m.ctas(), 256, 0, st>>>(m);
+    if ((rc = launch_status()) != NYS_OK) return rc;
     x = ws + pl.x;
     wg = ws + pl.wg;
     wu = ws + pl.wu;
@@ -390,14 +409,13 @@ int weight_gradients(const nys_gated_ff_t& a, const Plan& pl, const void* x, voi
 }
 
 template <typename T>
-int launch_grads(const nys_gated_ff_t& a, const Plan& pl, const void* gate, const void* up, const void* gh, char* ws,
-                 cudaStream_t st) {
-  const GradParams p{a.gate, a.up, a.h, a.T, a.f};
-  const long long ctas = ((long long)a.T * (a.f / 8) + 255) / 256;
+int launch_grads(const nys_gated_ff_t& a, const Plan& pl, const void* gate, const void* up, const void* gh,
+                 const Splits& more, char* ws, cudaStream_t st) {
+  const GradParams p{a.gate, a.up, a.h, a.T, a.f, (unsigned)(((long long)a.T * (a.f / 8) + 255) / 256)};
   KernelScope scope("gated_ff_back", st);
   act::by_act(a.act, [&](auto k) {
-    gated_ff_back<T, decltype(k)::value><<<(unsigned)ctas, 256, 0, st>>>(
-        p, static_cast<const T*>(gate), static_cast<const T*>(up), static_cast<const T*>(gh),
+    gated_ff_back<T, decltype(k)::value><<<p.ctas + more.ctas(), 256, 0, st>>>(
+        p, more, static_cast<const T*>(gate), static_cast<const T*>(up), static_cast<const T*>(gh),
         reinterpret_cast<__nv_bfloat16*>(ws + pl.dg), reinterpret_cast<__nv_bfloat16*>(ws + pl.du));
   });
   return launch_status();
@@ -494,21 +512,21 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
   int* status = nullptr;
   if ((rc = operator_status(dev, &status)) != NYS_OK) return rc;
   char* ws = static_cast<char*>(workspace);
-  rc = pl.f32 ? launch_grads<float>(*p, pl, gate, up, gh, ws, stream)
-              : launch_grads<__nv_bfloat16>(*p, pl, gate, up, gh, ws, stream);
-  if (rc != NYS_OK) return rc;
   const void *xs = x, *wg = w_gate, *wu = w_up;
+  Splits more{};
   if (pl.f32 && want_dw) {
-    if ((rc = split(x, p->x, ws + pl.x, p->T, p->d, stream)) != NYS_OK) return rc;
+    more.add(x, p->x, ws + pl.x, p->T, p->d);
     xs = ws + pl.x;
   }
   if (pl.f32 && dx) {
-    if ((rc = split(w_gate, p->w, ws + pl.wg, wr, wc, stream)) != NYS_OK ||
-        (rc = split(w_up, p->w, ws + pl.wu, wr, wc, stream)) != NYS_OK)
-      return rc;
+    more.add(w_gate, p->w, ws + pl.wg, wr, wc);
+    more.add(w_up, p->w, ws + pl.wu, wr, wc);
     wg = ws + pl.wg;
     wu = ws + pl.wu;
   }
+  rc = pl.f32 ? launch_grads<float>(*p, pl, gate, up, gh, more, ws, stream)
+              : launch_grads<__nv_bfloat16>(*p, pl, gate, up, gh, more, ws, stream);
+  if (rc != NYS_OK) return rc;
   if (dx && (rc = input_gradient(*p, pl, wg, wu, dx, ws, status, stream)) != NYS_OK) return rc;
   return want_dw ? weight_gradients(*p, pl, xs, dw_gate, dw_up, ws, status, stream) : NYS_OK;
 }
