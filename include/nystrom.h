@@ -517,7 +517,7 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
  * slice of a wider matrix is read and written in place. Addresses are 16-byte
  * aligned and strides multiples of 16 bytes (else NYS_ERR_ALIGN); rows of an
  * output do not overlap (a stride below the row's length, with more than one
- * row, is NYS_ERR_ARG). Outputs overlap neither one another nor an input,
+ * row, is NYS_ERR_ARG; the stride of a single row does not matter). Outputs overlap neither one another nor an input,
  * except where an operator says so; one at the very address of another, or of
  * an input it may not be, is refused (NYS_ERR_ARG).
  */
@@ -539,7 +539,7 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
  */
 typedef struct {
   void* codes;  /* device, 16-byte aligned */
-  void* scales; /* device, 16-byte aligned, nystrom_q8_scales_bytes(rows, K) bytes */
+  void* scales; /* device, 4-byte aligned, nystrom_q8_scales_bytes(rows, K) bytes */
   int rows, K;
   long long stride; /* bytes between rows of codes, a multiple of 16 */
 } nys_q8_t;

@@ -92,7 +92,11 @@ __device__ __forceinline__ void split_matrix(const Splits& p, unsigned cta) {
   load8(m.x + r * m.stride + c, v);
   store_terms(m.terms + r * m.cols + c, m.rows * m.cols, v);
 }
-__global__ void __launch_bounds__(256) split_terms(const __grid_constant__ Splits p) { split_matrix(p, blockIdx.x); }
+__global__ void __launch_bounds__(256) split_terms(const __grid_constant__ Splits p) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
+  split_matrix(p, blockIdx.x);
+}
 
 // ------------------------------------------------------- dg and du
 
@@ -108,6 +112,8 @@ template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
 gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Splits more, const T* __restrict__ gate, const T* __restrict__ up, const T* __restrict__ gh,
               __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   if (sizeof(T) == 4 && blockIdx.x >= p.ctas) {
     split_matrix(more, blockIdx.x - p.ctas);
     return;
@@ -232,7 +238,7 @@ int check_common(const nys_gated_ff_t* p) {
   const long long T = p->T, d = p->d, f = p->f, most = 1ll << 44;
   if (T * d >= most || T * f >= most || (T / 128 + 1) * (f / 128 + 1) >= (1ll << 26) ||
       (T / 128 + 1) * (d / 128 + 1) >= (1ll << 26) || (d / 128 + 1) * (f / 128 + 1) >= (1ll << 25) ||
-      (T / 8) * f >= (1ll << 38) || (T / 8) * d >= (1ll << 38))
+      (T / 8) * f >= (1ll << 37) || (T / 8) * d >= (1ll << 37))
     return NYS_ERR_SHAPE;
   return NYS_OK;
 }
@@ -288,9 +294,7 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
     m.add(x, a.x, ws + pl.x, a.T, a.d);
     m.add(wg, a.w, ws + pl.wg, wr, wc);
     m.add(wu, a.w, ws + pl.wu, wr, wc);
-    KernelScope scope("split_terms", st);
-    split_terms<<<m.ctas(), 256, 0, st>>>(m);
-    if ((rc = launch_status()) != NYS_OK) return rc;
+    if ((rc = launch_behind("split_terms", split_terms, dim3(m.ctas()), dim3(256), 0, st, m)) != NYS_OK) return rc;
     x = ws + pl.x;
     wg = ws + pl.wg;
     wu = ws + pl.wu;
@@ -412,13 +416,12 @@ template <typename T>
 int launch_grads(const nys_gated_ff_t& a, const Plan& pl, const void* gate, const void* up, const void* gh,
                  const Splits& more, char* ws, cudaStream_t st) {
   const GradParams p{a.gate, a.up, a.h, a.T, a.f, (unsigned)(((long long)a.T * (a.f / 8) + 255) / 256)};
-  KernelScope scope("gated_ff_back", st);
-  act::by_act(a.act, [&](auto k) {
-    gated_ff_back<T, decltype(k)::value><<<p.ctas + more.ctas(), 256, 0, st>>>(
-        p, more, static_cast<const T*>(gate), static_cast<const T*>(up), static_cast<const T*>(gh),
-        reinterpret_cast<__nv_bfloat16*>(ws + pl.dg), reinterpret_cast<__nv_bfloat16*>(ws + pl.du));
+  return act::by_act(a.act, [&](auto k) {
+    return launch_behind("gated_ff_back", gated_ff_back<T, decltype(k)::value>, dim3(p.ctas + more.ctas()), dim3(256),
+                         0, st, p, more, static_cast<const T*>(gate), static_cast<const T*>(up),
+                         static_cast<const T*>(gh), reinterpret_cast<__nv_bfloat16*>(ws + pl.dg),
+                         reinterpret_cast<__nv_bfloat16*>(ws + pl.du));
   });
-  return launch_status();
 }
 
 // Whether an address is any of the others.
@@ -461,8 +464,7 @@ int nystrom_gated_ff_fwd(const nys_gated_ff_t* p, const void* x, const void* w_g
     if (ws_bytes < pl.total) return NYS_ERR_NOMEM;
   }
   int dev = 0;
-  rc = check_device(&dev);
-  if (rc != NYS_OK) return rc;
+  if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
   std::unique_lock<std::mutex> held;
   if (pl.total && !workspace) {
     rc = operator_workspace(dev, pl.total, stream, &workspace, &held);
@@ -502,8 +504,7 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
     if (ws_bytes < pl.total) return NYS_ERR_NOMEM;
   }
   int dev = 0;
-  rc = check_device(&dev);
-  if (rc != NYS_OK) return rc;
+  if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
   std::unique_lock<std::mutex> held;
   if (!workspace) {
     rc = operator_workspace(dev, pl.total, stream, &workspace, &held);

@@ -436,6 +436,11 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     bars.abort = 0;
     fence_barrier_init();
   }
+  // All CTAs of the grid run at once, so what follows may be set up beside them. A
+  // kernel set up so waits for the one before it here, before it takes TMEM that
+  // the other may still need.
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&bars.tmem))
                  : "memory");
@@ -445,8 +450,6 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   __syncthreads();
   cluster_sync();  // both CTAs' barriers and TMEM are there
   tc_fence_after_sync();
-  // all CTAs of the grid run at once: a join behind it may take its place
-  cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t tmem = bars.tmem;
 
   if (warp == 0 || warp == 2) {
@@ -724,12 +727,12 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
     bars.abort = 0;
     fence_barrier_init();
   }
+  cudaTriggerProgrammaticLaunchCompletion();  // as above
+  cudaGridDependencySynchronize();
   if (warp == 1) tmem_alloc(&bars.tmem, L::kAlloc);
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
-  // all CTAs of the grid run at once: a join behind it may take its place
-  cudaTriggerProgrammaticLaunchCompletion();
   const uint32_t tmem = bars.tmem;
 
   if (warp == 0) {
@@ -912,6 +915,17 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 
 // ------------------------------------------------------------------- host
 
+// Tensor maps are encoded by the driver, which wants a context that is current in
+// the calling thread; a thread whose first CUDA call this is has none yet.
+inline int have_context(int dev) {
+  static thread_local int bound = -1;
+  if (bound == dev) return NYS_OK;
+  const cudaError_t e = cudaSetDevice(dev);
+  if (e != cudaSuccess) return set_cuda_error(e);
+  bound = dev;
+  return NYS_OK;
+}
+
 // A matrix of `rows` rows of `cols` elements, `stride` elements apart, in
 // `planes` copies `plane` elements apart.
 struct Matrix {
@@ -982,9 +996,7 @@ int start(const char* name, Kernel kernel, int grid, int threads, int bytes, con
           cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
-  KernelScope scope(name, st);
-  kernel<<<grid, threads, bytes, st>>>(maps, p);
-  return launch_status();
+  return launch_behind(name, kernel, dim3(grid), dim3(threads), bytes, st, maps, p);
 }
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {

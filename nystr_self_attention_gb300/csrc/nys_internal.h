@@ -88,6 +88,12 @@ inline int launch_status() {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? NYS_OK : set_cuda_error(e);
 }
+// Launches a kernel that begins with cudaGridDependencySynchronize (or does so
+// before it touches memory): it may be set up while the kernel before it in the
+// stream still runs.
+template <typename... Formal, typename... Actual>
+int launch_behind(const char* name, void (*kernel)(Formal...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                  Actual... args);
 int check_shape(int B, int H, int n, int d, int m, int iters, int ks, int dtype);
 int check_args(const void* q, const void* k, const void* v, const float* conv_w, const void* out,
                int B, int H, int n, int d, int m, int iters, int ks, int dtype);
@@ -253,5 +259,23 @@ std::string describe_plan(const Shape& s);
 int launch_forward(const Shape& s, const void* q, const void* k, const void* v,
                    const float* conv_w, void* out, char* ws, const Layout& L,
                    cudaStream_t stream, int dev);
+
+template <typename... Formal, typename... Actual>
+int launch_behind(const char* name, void (*kernel)(Formal...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                  Actual... args) {
+  KernelScope scope(name, stream);
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  cudaLaunchKernelEx(&cfg, kernel, static_cast<Formal>(args)...);
+  return launch_status();
+}
 
 }  // namespace nys

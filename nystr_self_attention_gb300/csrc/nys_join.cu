@@ -25,6 +25,7 @@ __device__ __forceinline__ void add(float4& a, const float4& b) {
 template <typename T>
 __global__ void __launch_bounds__(256)
 join_rows(const Join j, int parts) {
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int quads = j.N / 4;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x;
@@ -44,6 +45,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 join_turned(const Join j) {
   __shared__ float tile[32][33];
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32;
   const int n = n0 + threadIdx.x / 8, m = m0 + (threadIdx.x & 7) * 4;
@@ -68,6 +70,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 join_gated_rows(const JoinGated j, int act) {
   constexpr bool kFast = sizeof(T) == 2;
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int quads = j.N / 4;
   const long long e = (long long)blockIdx.x * 256 + threadIdx.x, m = e / quads;
@@ -98,6 +101,7 @@ __global__ void __launch_bounds__(256)
 join_gated_turned(const JoinGated j, int act) {
   constexpr bool kFast = sizeof(T) == 2;
   __shared__ float gs[32][33], us[32][33];
+  cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   const int n0 = blockIdx.x * 32, m0 = blockIdx.y * 32;
   const int n = n0 + threadIdx.x / 8, m = m0 + (threadIdx.x & 7) * 4;
@@ -131,18 +135,7 @@ join_gated_turned(const JoinGated j, int act) {
 
 template <typename K, typename... Args>
 int start(const char* name, K kernel, dim3 grid, cudaStream_t st, Args... args) {
-  KernelScope scope(name, st);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = grid;
-  cfg.blockDim = dim3(256);
-  cfg.stream = st;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, kernel, args...);
-  return launch_status();
+  return launch_behind(name, kernel, grid, dim3(256), 0, st, args...);
 }
 
 }  // namespace

@@ -125,6 +125,8 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
   constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
   __shared__ float slots[2 * THREADS / 32][1];
   int phase = 0;
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const int across = GROUPS == 1 ? blockDim.x : TPR, t = threadIdx.x % TPR;  // threads of a row
   const int step = gridDim.x * GROUPS;
   int row = blockIdx.x * GROUPS + threadIdx.x / TPR;
@@ -214,6 +216,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
   extern __shared__ float sums[];  // [GROUPS][d] where a CTA holds several rows
   int phase = 0;
   cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   const int across = GROUPS == 1 ? blockDim.x : TPR, t = threadIdx.x % TPR, group = threadIdx.x / TPR;
   const int step = gridDim.x * GROUPS;
   int row = blockIdx.x * GROUPS + group;
@@ -411,10 +414,8 @@ int launch_fwd(const nys_add_rms_norm_t& a, const void* x, const void* res, cons
     const int threads = cta_threads<TPR, V>(a.d);
     auto go = [&](auto kernel, int per_sm) {
       const int grid = grid_of(a.rows, THREADS / TPR, per_sm / threads);
-      KernelScope scope("add_rms_norm", st);
-      kernel<<<grid, threads, 0, st>>>(p, static_cast<const T*>(x), static_cast<const T*>(res), weight,
-                                       static_cast<T*>(sum), static_cast<T*>(y));
-      return launch_status();
+      return launch_behind("add_rms_norm", kernel, dim3(grid), dim3(threads), 0, st, p, static_cast<const T*>(x),
+                           static_cast<const T*>(res), weight, static_cast<T*>(sum), static_cast<T*>(y));
     };
     constexpr int with = fwd_threads<T, TPR, true>(), without = fwd_threads<T, TPR, false>();
     if (res)
@@ -431,11 +432,9 @@ int launch_bwd(const nys_add_rms_norm_t& a, const void* s, const void* gy, const
     constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
     constexpr int GROUPS = THREADS / TPR;
     const size_t smem = GROUPS > 1 && part ? (size_t)GROUPS * a.d * sizeof(float) : 0;  // at most 16 KB
-    KernelScope scope("add_rms_norm_back", st);
-    add_rms_norm_back<T, TPR, V><<<back_grid<TPR, V>(a), cta_threads<TPR, V>(a.d), smem, st>>>(
-        p, static_cast<const T*>(s), static_cast<const T*>(gy), static_cast<const T*>(gs), weight,
-        static_cast<T*>(dx), part);
-    return launch_status();
+    return launch_behind("add_rms_norm_back", add_rms_norm_back<T, TPR, V>, dim3(back_grid<TPR, V>(a)),
+                         dim3(cta_threads<TPR, V>(a.d)), smem, st, p, static_cast<const T*>(s),
+                         static_cast<const T*>(gy), static_cast<const T*>(gs), weight, static_cast<T*>(dx), part);
   });
 }
 
@@ -523,18 +522,8 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
   rc = p->dtype == NYS_BF16 ? launch_bwd<__nv_bfloat16>(*p, s, gy, gs, weight, dx, part, stream)
                             : launch_bwd<float>(*p, s, gy, gs, weight, dx, part, stream);
   if (rc != NYS_OK || !dweight) return rc;
-  KernelScope scope("norm_weight_grad", stream);
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((p->d + 31) / 32);
-  cfg.blockDim = dim3(1024);
-  cfg.stream = stream;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  cudaLaunchKernelEx(&cfg, norm_weight_grad, static_cast<const float*>(part), dweight, p->d, back_ctas(*p));
-  return launch_status();
+  return launch_behind("norm_weight_grad", norm_weight_grad, dim3((p->d + 31) / 32), dim3(1024), 0, stream,
+                       static_cast<const float*>(part), dweight, p->d, back_ctas(*p));
 }
 
 }  // extern "C"

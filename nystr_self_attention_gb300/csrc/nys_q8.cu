@@ -62,6 +62,8 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t top, uint32_t* slots) {
 template <typename T, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 q8_write(const WriteParams p, const T* __restrict__ x) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   __shared__ uint32_t slots[kThreads / 32];
   const int blocks = (p.K + kBlock - 1) / kBlock;
   const int block = blockIdx.x % (unsigned)blocks, r0 = (int)(blockIdx.x / (unsigned)blocks) * kTile;
@@ -108,6 +110,8 @@ q8_write(const WriteParams p, const T* __restrict__ x) {
 template <typename T, bool SHARED>
 __global__ void __launch_bounds__(kThreads)
 q8_write_turned(const WriteParams p, const T* __restrict__ x) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   constexpr int kPitch = kTile + 16;
   __shared__ uint32_t slots[kThreads / 32];
   __shared__ __align__(16) uint32_t tops[16][kTile];
@@ -183,6 +187,8 @@ __device__ __forceinline__ void store8(__nv_bfloat16* p, const float (&v)[8]) {
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 q8_read(const WriteParams p, T* __restrict__ out) {
+  cudaTriggerProgrammaticLaunchCompletion();
+  cudaGridDependencySynchronize();
   constexpr int kAhead = 4;
   const int blocks = (p.K + kBlock - 1) / kBlock;
   const int block = blockIdx.x % (unsigned)blocks, r0 = (int)(blockIdx.x / (unsigned)blocks) * (16 * kAhead);
@@ -258,9 +264,7 @@ int nystrom_q8_write(const nys_q8_t* q, const void* x, long long row_stride, lon
   auto go = [&](auto type) {
     using T = decltype(type);
     auto launch = [&](auto kernel) {
-      KernelScope scope("q8_write", stream);
-      kernel<<<grid, kThreads, 0, stream>>>(p, static_cast<const T*>(x));
-      return launch_status();
+      return launch_behind("q8_write", kernel, dim3(grid), dim3(kThreads), 0, stream, p, static_cast<const T*>(x));
     };
     if (turned) return block_rows == 1 ? launch(q8_write_turned<T, false>) : launch(q8_write_turned<T, true>);
     return block_rows == 1 ? launch(q8::q8_write<T, false>) : launch(q8::q8_write<T, true>);
@@ -281,12 +285,11 @@ int nystrom_q8_read(const nys_q8_t* q, void* out, long long stride, int dtype, n
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
   const WriteParams p = params_of(*q, stride);
-  KernelScope scope("q8_read", stream);
   if (dtype == NYS_BF16)
-    q8::q8_read<__nv_bfloat16><<<grid, kThreads, 0, stream>>>(p, static_cast<__nv_bfloat16*>(out));
-  else
-    q8::q8_read<float><<<grid, kThreads, 0, stream>>>(p, static_cast<float*>(out));
-  return launch_status();
+    return launch_behind("q8_read", q8::q8_read<__nv_bfloat16>, dim3(grid), dim3(kThreads), 0, stream, p,
+                         static_cast<__nv_bfloat16*>(out));
+  return launch_behind("q8_read", q8::q8_read<float>, dim3(grid), dim3(kThreads), 0, stream, p,
+                       static_cast<float*>(out));
 }
 
 }  // extern "C"

@@ -70,8 +70,8 @@ inline int check_q8(const nys_q8_t* q, bool out) {
   if (q->rows < 1 || q->rows >= 0x7fffffff - 1023 || q->K < 1 || q->K % 16 || q->K > (1 << 20))
     return NYS_ERR_SHAPE;
   if (q->stride < 0 || (out && q->rows > 1 && q->stride < q->K)) return NYS_ERR_ARG;
-  if (((reinterpret_cast<uintptr_t>(q->codes) | reinterpret_cast<uintptr_t>(q->scales)) & 15u) ||
-      q->stride % 16)
+  if ((reinterpret_cast<uintptr_t>(q->codes) & 15u) || (reinterpret_cast<uintptr_t>(q->scales) & 3u) ||
+      (q->rows > 1 && q->stride % 16))
     return NYS_ERR_ALIGN;
   return q->codes == q->scales ? NYS_ERR_ARG : NYS_OK;
 }

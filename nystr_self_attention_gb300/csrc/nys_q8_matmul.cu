@@ -85,8 +85,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
     if (ws_bytes < plan.bytes) return NYS_ERR_NOMEM;
   }
   int dev = 0;
-  rc = check_device(&dev);
-  if (rc != NYS_OK) return rc;
+  if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
   std::unique_lock<std::mutex> held;
   if (plan.bytes && !workspace) {
     rc = operator_workspace(dev, plan.bytes, stream, &workspace, &held);

@@ -24,7 +24,7 @@ def q8(N, codes=256, scales=512, rows=4, K=256, stride=None):
 BAD_Q8 = [
     (dict(codes=None), E_ARG), (dict(scales=None), E_ARG), (dict(rows=0), E_SHAPE), (dict(K=0), E_SHAPE),
     (dict(K=264), E_SHAPE), (dict(K=(1 << 20) + 16), E_SHAPE), (dict(rows=2 ** 31 - 1), E_SHAPE),
-    (dict(stride=-16), E_ARG), (dict(stride=264), E_ALIGN), (dict(codes=264), E_ALIGN), (dict(scales=520), E_ALIGN),
+    (dict(stride=-16), E_ARG), (dict(stride=264), E_ALIGN), (dict(codes=264), E_ALIGN), (dict(scales=514), E_ALIGN),
     (dict(codes=512), E_ARG),
 ]
 
