@@ -313,16 +313,13 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
     for (int i = 0; i < 2; ++i) ok = ok && (io ? map_mn(&maps.a[i], w[i]) : map_k(&maps.a[i], w[i], 128));
     ok = ok && map_k(&maps.b[0], xm, q.bn) &&
          map_out(&maps.c[0], Matrix{ws + pl.part, a.f, q.bn, q.bn, 4, 2 * q.splits, (long long)a.f * q.bn}, q.bn == 16 ? 16 : 32);
-    maps.b[1] = maps.b[0];
   } else {
     ok = map_k(&maps.a[0], xm, 128);
-    maps.a[1] = maps.a[0];
     for (int i = 0; i < 2; ++i)
       ok = ok && (io ? map_mn(&maps.b[i], w[i]) : map_k(&maps.b[i], w[i], q.bn / 2));
     if (direct) {
       const int e = pl.f32 ? 4 : 2;
       ok = ok && map_out(&maps.c[0], Matrix{h, a.T, a.f, a.h, e});
-      maps.c[1] = maps.c[2] = maps.c[0];
       if (gate)
         ok = ok && map_out(&maps.c[1], Matrix{gate, a.T, a.f, a.gate, e}) &&
              map_out(&maps.c[2], Matrix{up, a.T, a.f, a.up, e});

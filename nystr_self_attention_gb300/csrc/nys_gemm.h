@@ -329,15 +329,14 @@ __device__ __forceinline__ void scale_loop(const Params& p, Bars& bars, uint8_t*
 template <int KIND, typename OutT>
 struct PairLayout {
   // 8-bit tiles leave TMEM columns for the scales beside two accumulators
-  static constexpr int kCols = KIND == kMx8 ? 224 : 256;           // most columns of a tile
-  static constexpr int kA = 128 * 128, kB = kCols / 2 * 128;       // a CTA's halves of A and B
-  static constexpr int kStep = kA + kB, kSteps = KIND == kMx8 ? 2 : 1, kStage = kSteps * kStep;
+  static constexpr int kCols = KIND == kMx8 ? 224 : 256;  // most columns of a tile
+  static constexpr int kA = 128 * 128;                    // a CTA's half of A, a step
+  static constexpr int kSteps = KIND == kMx8 ? 2 : 1;     // of a stage
   static constexpr int kBox = 32 * 32 * sizeof(OutT), kBoxes = sizeof(OutT) == 4 ? 1 : 2;
   static constexpr int kStaging = 8 * kBoxes * kBox;
   static constexpr int kScaleSlot = 512 + 1024, kScales = KIND == kMx8 ? kSlots * kScaleSlot : 0;
-  static constexpr int kStages = (kSmem - 1024 - kStaging - kScales - kBarBytes) / kStage;
-  static_assert(kStages >= 3, "shared memory");
-  static constexpr int kBytes = 1024 + kStages * kStage + kStaging + kScales + kBarBytes;
+  static constexpr int kRing = (kSmem - 1024 - kStaging - kScales - kBarBytes) / 1024 * 1024;  // of the stages
+  static constexpr int kBytes = 1024 + kRing + kStaging + kScales + kBarBytes;
   static constexpr int kScaleCol = 2 * kCols, kScaleCols = 12;  // TMEM columns of the scales, of a slot
   static_assert(KIND != kMx8 || kScaleCol + kSlots * kScaleCols <= 512, "TMEM columns");
   static constexpr int kFirst = KIND == kMx8 ? 4 : 3;  // warps that carry out
@@ -408,19 +407,27 @@ template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<KIND, OutT>::kThreads, 1)
 gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using L = PairLayout<KIND, OutT>;
-  constexpr int S = L::kStages;
   constexpr bool kSum = sizeof(OutT) == 4;  // sums move to registers
   extern __shared__ uint8_t raw[];
   uint8_t* sm = align1024(raw);
-  uint8_t* staging = sm + S * L::kStage;
+  uint8_t* staging = sm + L::kRing;
   uint8_t* scales = staging + L::kStaging;
   Bars& bars = *reinterpret_cast<Bars*>(scales + L::kScales);
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_rank();
+  // B's lines per CTA, in whole boxes where they are MN-major; as many stages as fit
+  const int lines = p.bn / 2, held = BMN ? (lines + 63) / 64 * 64 : lines;
+  const uint32_t step_bytes = L::kA + held * 128, stage_bytes = L::kSteps * step_bytes;
+  const uint32_t S = min(12u, L::kRing / stage_bytes);
+
+  if (warp == 0 && lane < 7) {
+    const CUtensorMap* maps_of[7] = {&maps.a[0], &maps.a[1], &maps.b[0], &maps.b[1], &maps.c[0], &maps.c[1], &maps.c[2]};
+    tma_prefetch(maps_of[lane]);
+  }
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < S; ++i) {
+    for (uint32_t i = 0; i < S; ++i) {
       mbar_init(&bars.full[i], 1);
       mbar_init(&bars.empty[i], 1);
     }
@@ -458,13 +465,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     // to issue as the products take to run (16384 tokens, 2048 -> 5632: forward
     // 761,000 cycles, gradients of the weights 779,000; with two 726,000, 747,000).
     const bool first = warp == 0;
-    if (elect_one()) {
-      for (int i = 0; i < 2; ++i) tma_prefetch(first ? &maps.a[i] : &maps.b[i]);
-    }
     uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, stages filled
-    const int lines = p.bn / 2, blocks = (lines + 63) / 64;  // of this CTA's half of B
-    const uint32_t bytes = 2 * (L::kA + (BMN ? blocks * 64 : lines) * 128);  // of both CTAs, a step
-    const int half = !first && blocks == 1 ? 0 : 1;  // a second box of 64 (MN-major)
+    const bool second = first || held > 64;  // a second box of 64 (MN-major)
     bool ok = true;
     for (GridWalk walk(p); ok && walk.more; walk.next(p)) {
       const Tile& tile = walk.tile;
@@ -480,17 +482,17 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
         }
         const int count = min(L::kSteps, tile.it1 - it);
         if (elect_one()) {
-          if (first && rank == 0) mbar_arrive_expect_tx(&bars.full[st], count * bytes);
+          if (first && rank == 0) mbar_arrive_expect_tx(&bars.full[st], count * 2 * step_bytes);
           const uint32_t bar = in_first(&bars.full[st]);
           Step at = s;
           for (int j = 0; j < count; ++j, at.next(p)) {
-            uint8_t* to = sm + st * L::kStage + j * L::kStep + (first ? 0 : L::kA);
+            uint8_t* to = sm + st * stage_bytes + j * step_bytes + (first ? 0 : L::kA);
             const int k = at.kb * (KIND == kMx8 ? 128 : 64), z = first ? term_of_a(p, at.pair) : term_of_b(p, at.pair);
             const CUtensorMap* map = first ? &maps.a[map_of(p.a_by, tile, at)]
                                            : &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, at)];
             if (first ? AMN : BMN) {
               pair_load_3d(to, map, bar, r0, k, z);
-              if (half) pair_load_3d(to + 8192, map, bar, r0 + 64, k, z);
+              if (second) pair_load_3d(to + 8192, map, bar, r0 + 64, k, z);
             } else {
               pair_load_3d(to, map, bar, k, r0, z);
             }
@@ -549,8 +551,8 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
 #pragma unroll
               for (int i = 0; i < 3; ++i) pair_copy_scales(sf + 4 * i, from + 512 * i);
             }
-            uint64_t ad = a0 + st * (L::kStage / 16), bd = b0 + st * (L::kStage / 16);
-            for (int j = 0; j < count; ++j, ad += L::kStep / 16, bd += L::kStep / 16) {
+            uint64_t ad = a0 + st * (stage_bytes / 16), bd = b0 + st * (stage_bytes / 16);
+            for (int j = 0; j < count; ++j, ad += step_bytes / 16, bd += step_bytes / 16) {
               const uint32_t id = KIND == kMx8 ? idesc_mx8(256, p.bn, (it + j) & 3) : idesc;
 #pragma unroll
               for (int kk = 0; kk < 4; ++kk) {
@@ -660,7 +662,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
         send(&maps.c[0], 0);
       }
     }
-    if (lane == 0) bulk_wait0();
+    if (lane == 0) bulk_wait_read0();  // shared memory stays until it has been read
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
     // Of this CTA's rows of A and of all columns, which both CTAs need.
@@ -710,6 +712,10 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
   volatile int* abort_flag = &bars.abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
+  if (warp == 0 && lane < 5) {
+    const CUtensorMap* maps_of[5] = {&maps.a[0], &maps.a[1], &maps.b[0], &maps.b[1], &maps.c[0]};
+    tma_prefetch(maps_of[lane]);
+  }
   if (threadIdx.x == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(&bars.full[i], 1);
@@ -737,12 +743,6 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
 
   if (warp == 0) {
     // -------------------------------------------------------------- copies
-    if (elect_one()) {
-      for (int i = 0; i < 2; ++i) {
-        tma_prefetch(&maps.a[i]);
-        tma_prefetch(&maps.b[i]);
-      }
-    }
     uint32_t st = 0, round = 0, n = 0;  // stage, times round the stages, copies issued
     bool ok = true;
     for (LineWalk walk(p); ok && walk.more; walk.next(p)) {
@@ -897,7 +897,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
         }
       }
     }
-    if (lane == 0) bulk_wait0();
+    if (lane == 0) bulk_wait_read0();  // shared memory stays until it has been read
   } else if (KIND == kMx8) {
     // -------------------------------------------------------------- scales
     scale_loop<2, LineWalk>(
@@ -991,12 +991,22 @@ struct JoinGated {
 };
 int join_gated(const JoinGated& j, int act, int dtype, cudaStream_t st);
 
+// Every map is fetched ahead, used or not: those that a call leaves out are copies.
+inline Maps filled(Maps m) {
+  for (CUtensorMap* x : {&m.a[1], &m.b[0], &m.b[1], &m.c[0], &m.c[1], &m.c[2]}) {
+    bool none = true;
+    for (auto word : x->opaque) none = none && word == 0;
+    if (none) *x = m.a[0];
+  }
+  return m;
+}
+
 template <typename Kernel>
 int start(const char* name, Kernel kernel, int grid, int threads, int bytes, const Maps& maps, const Params& p,
           cudaStream_t st) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
-  return launch_behind(name, kernel, dim3(grid), dim3(threads), bytes, st, maps, p);
+  return launch_behind(name, kernel, dim3(grid), dim3(threads), bytes, st, filled(maps), p);
 }
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {

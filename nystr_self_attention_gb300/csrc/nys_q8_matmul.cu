@@ -120,8 +120,6 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   else
     ok = ok && map_out(&maps.c[0], Matrix{workspace, T, N, N, 4, plan.splits, (long long)T * N});
   if (!ok) return tensor_map_error(__FILE__, __LINE__);
-  maps.a[1] = maps.a[0];
-  maps.b[1] = maps.b[0];
   const char* name = "q8_matmul";
   if (plan.turned)
     rc = launch_tokens<kMx8, false>(name, plan.bn, plan.line.ctas, maps, p, stream);
