@@ -261,7 +261,7 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
   p.chunk = pairs > 1 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
   p.a_by = a_by;
   p.b_by = b_by;
-  p.group = 8;
+  p.group = 16;
   p.status = status;
   return p;
 }

@@ -29,6 +29,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -64,7 +65,8 @@ struct Params {
   int pairs;             // 1, or 6 pairs of the three terms of fp32 operands
   int a_by, b_by;        // By
   int c_by_part;         // results of part i to c[i]; else to plane split * parts + part of c[0]
-  int group;             // row tiles that neighbouring CTAs share
+  int group;             // row tiles that neighbouring CTAs share: 16 (8: 486 us for the
+                         // feed-forward of 16384 tokens, 16: 471, 32: 474, 64: 508)
   int act, keep;         // kGated
   int* status;
   // 8-bit operands: scale words [groups][rows]
@@ -1001,12 +1003,19 @@ inline Maps filled(Maps m) {
   return m;
 }
 
-template <typename Kernel>
-int start(const char* name, Kernel kernel, int grid, int threads, int bytes, const Maps& maps, const Params& p,
-          cudaStream_t st) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
-  return launch_behind(name, kernel, dim3(grid), dim3(threads), bytes, st, filled(maps), p);
+// KERNEL with its dynamic shared memory, which a device is told of once.
+template <auto KERNEL>
+int start(const char* name, int grid, int threads, int bytes, const Maps& maps, const Params& p, cudaStream_t st) {
+  static std::atomic<unsigned long long> told{0};  // a bit per device
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_cuda_error(cudaGetLastError());
+  const unsigned long long bit = 1ull << (dev & 63);
+  if (!(told.load(std::memory_order_relaxed) & bit)) {
+    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return set_cuda_error(cudaGetLastError());
+    told.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return launch_behind(name, KERNEL, dim3(grid), dim3(threads), bytes, st, filled(maps), p);
 }
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
 int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_t st) {
@@ -1014,15 +1023,15 @@ int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_
   const long long tiles = (long long)p.m_tiles * p.n_tiles * p.parts * p.splits;
   if (tiles >= (1ll << 31) - 1024) return NYS_ERR_SHAPE;
   const int most = plan_sms() / 2;
-  return start(name, gemm_pair<KIND, AMN, BMN, EPI, OutT>, 2 * (tiles < most ? (int)tiles : most), L::kThreads,
-               L::kBytes, maps, p, st);
+  return start<gemm_pair<KIND, AMN, BMN, EPI, OutT>>(name, 2 * (tiles < most ? (int)tiles : most), L::kThreads,
+                                                     L::kBytes, maps, p, st);
 }
 template <int KIND, bool AMN>
 int launch_tokens(const char* name, int bn, int ctas, const Maps& maps, const Params& p, cudaStream_t st) {
   auto go = [&](auto n) {
     constexpr int BN = decltype(n)::value;
     using L = TokensLayout<KIND, BN>;
-    return start(name, gemm_tokens<KIND, AMN, BN>, ctas, L::kThreads, L::kBytes, maps, p, st);
+    return start<gemm_tokens<KIND, AMN, BN>>(name, ctas, L::kThreads, L::kBytes, maps, p, st);
   };
   using std::integral_constant;
   switch (bn) {

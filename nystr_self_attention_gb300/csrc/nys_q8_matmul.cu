@@ -104,7 +104,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   p.its_per_split = plan.its_per_split;
   p.bn = plan.bn;
   p.chunk = 8;
-  p.group = 8;
+  p.group = 16;
   p.a_scales = static_cast<const uint32_t*>(rows.scales);
   p.b_scales = static_cast<const uint32_t*>(cols.scales);
   p.a_rows = rows.rows;
