@@ -625,12 +625,14 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
  *
  * nystrom_gated_ff_bwd - its gradients, from x, the weights, the kept g and u,
  * and the gradient gh of h (stride p->h):
- *   dg = gh u act'(g), du = gh act(g)     (rounded to dtype; act'(0) = 0 for RELU)
+ *   dg = gh u act'(g), du = gh act(g)     (act'(0) = 0 for RELU)
  *   dx = dg W_gate^T + du W_up^T, dW_gate = x^T dg, dW_up = x^T du
  * dx: stride p->dx, NULL if not wanted; dw_gate, dw_up: the weights' layout, row
  * stride p->dw, both or neither NULL.
  *
- * Sums are fp32 in the matrix units, in a fixed order; one rounding to dtype.
+ * Sums are fp32 in the matrix units, in a fixed order; one rounding to dtype. For
+ * NYS_BF16 dg and du enter the products rounded to bf16, of up to 128 tokens to two
+ * bf16 terms (16 bits).
  * NYS_FP32 operands enter the products as sums of three bfloat16 terms (24 bits;
  * six of the nine products, all that matter at 2^-24), so an infinity gives NaN
  * where a finite sum could not, values beyond 3.38e38 are infinite, and bits

@@ -15,7 +15,10 @@
 // the weights then stream at HBM's pace.
 //
 // fp32: an operand is split into three bf16 terms, 24 bits in all, in a pass of
-// its own, and the product sums the six pairs that matter at 2^-24.
+// its own, and the product sums the six pairs that matter at 2^-24. bf16: dg and
+// du enter the products rounded to bf16, an error as large as the results' own
+// rounding; of few tokens, where nothing averages it and the weights' bytes bound
+// the time, as two terms (16 bits).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -46,6 +49,19 @@ __device__ __forceinline__ void store_terms(__nv_bfloat16* to, long long plane, 
     *reinterpret_cast<uint4*>(to + k * plane) =
         make_uint4(pack_bf16x2(t[0][k], t[1][k]), pack_bf16x2(t[2][k], t[3][k]), pack_bf16x2(t[4][k], t[5][k]),
                    pack_bf16x2(t[6][k], t[7][k]));
+}
+
+__device__ __forceinline__ void store_bf16(__nv_bfloat16* to, const float (&v)[8]) {
+  *reinterpret_cast<uint4*>(to) =
+      make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+}
+// What rounding to bf16 left (nothing of an infinity or a NaN).
+__device__ __forceinline__ void rest_of(float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float r = v[i] - __bfloat162float(__float2bfloat16_rn(v[i]));
+    v[i] = r - r == 0.f ? r : 0.f;
+  }
 }
 
 __device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
@@ -105,9 +121,10 @@ struct GradParams {
   long long T;
   int f;
   unsigned ctas;  // those behind split the matrices of `more`
+  int two;        // bf16: two terms
 };
 
-// dg, du [T][f]; of fp32 as terms [3][T][f]. Eight elements per thread.
+// dg, du as terms [1, 2 or (fp32) 3][T][f]. Eight elements per thread.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
 gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Splits more, const T* __restrict__ gate, const T* __restrict__ up, const T* __restrict__ gh,
@@ -138,10 +155,14 @@ gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Spli
     store_terms(dg + at, p.T * p.f, g);
     store_terms(du + at, p.T * p.f, u);
   } else {
-    *reinterpret_cast<uint4*>(dg + at) =
-        make_uint4(pack_bf16x2(g[0], g[1]), pack_bf16x2(g[2], g[3]), pack_bf16x2(g[4], g[5]), pack_bf16x2(g[6], g[7]));
-    *reinterpret_cast<uint4*>(du + at) =
-        make_uint4(pack_bf16x2(u[0], u[1]), pack_bf16x2(u[2], u[3]), pack_bf16x2(u[4], u[5]), pack_bf16x2(u[6], u[7]));
+    store_bf16(dg + at, g);
+    store_bf16(du + at, u);
+    if (p.two) {
+      rest_of(g);
+      rest_of(u);
+      store_bf16(dg + p.T * p.f + at, g);
+      store_bf16(du + p.T * p.f + at, u);
+    }
   }
 }
 
@@ -166,14 +187,14 @@ Product product_of(long long M, long long N, long long k, int k_parts, int parts
   q.its = steps * pairs;
   if (q.turned) {
     q.bn = columns_of((int)M);
-    q.line = line_of(N, q.its, parts, pairs > 1 ? pairs : 2, q.bn);
+    q.line = line_of(N, q.its, parts, pairs > 2 ? pairs : 2, q.bn);
     q.splits = most_planes(q.line);
     q.m_tiles = q.line.m_tiles;
     q.n_tiles = 1;
     q.bytes = align256((size_t)q.splits * parts * N * q.bn * 4);
     return q;
   }
-  const Cut cut = cut_pair(M, N, steps, 1, pairs, parts, 256, gated ? 64 : 32, gated, pairs > 1 ? 1 : 4);
+  const Cut cut = cut_pair(M, N, steps, 1, pairs, parts, 256, gated ? 64 : 32, gated, pairs > 2 ? 1 : 4);
   q.bn = cut.bn;
   q.splits = cut.splits;
   q.its_per_split = range_of(steps, q.splits, 1) * pairs;  // all pairs of a block
@@ -186,7 +207,9 @@ Product product_of(long long M, long long N, long long k, int k_parts, int parts
 
 struct Plan {
   bool f32;
-  int pairs;
+  int pairs;       // of the forward product
+  int grad_terms;  // of dg and du: 1, 2 (few tokens), or fp32's 3
+  int grad_pairs;  // products summed for a gradient
   Product fwd, dx, dw;
   // byte offsets in the workspace
   size_t x, wg, wu, dg, du, part, total;
@@ -196,7 +219,9 @@ Plan plan_of(const nys_gated_ff_t& a, bool back, bool want_dx, bool want_dw) {
   Plan pl{};
   pl.f32 = a.dtype == NYS_FP32;
   pl.pairs = pl.f32 ? 6 : 1;
-  const size_t T = a.T, d = a.d, f = a.f, terms = pl.f32 ? 3 : 1;
+  pl.grad_terms = pl.f32 ? 3 : a.T <= kMostTokens ? 2 : 1;
+  pl.grad_pairs = pl.f32 ? 6 : pl.grad_terms;
+  const size_t T = a.T, d = a.d, f = a.f;
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += align256(bytes); return o; };
   const bool io = a.layout == NYS_FF_IN_OUT;
@@ -210,14 +235,14 @@ Plan plan_of(const nys_gated_ff_t& a, bool back, bool want_dx, bool want_dw) {
     pl.fwd = product_of(a.T, a.f, a.d, 1, 2, pl.pairs, true, true);
     part = pl.fwd.bytes;
   } else {
-    pl.dg = take(terms * T * f * 2);
-    pl.du = take(terms * T * f * 2);
+    pl.dg = take(pl.grad_terms * T * f * 2);
+    pl.du = take(pl.grad_terms * T * f * 2);
     if (want_dx) {
-      pl.dx = product_of(a.T, a.d, a.f, 2, 1, pl.pairs, false, true);
+      pl.dx = product_of(a.T, a.d, a.f, 2, 1, pl.grad_pairs, false, true);
       part = pl.dx.bytes;
     }
     if (want_dw) {
-      pl.dw = product_of(io ? a.d : a.f, io ? a.f : a.d, a.T, 1, 2, pl.pairs, false, false);
+      pl.dw = product_of(io ? a.d : a.f, io ? a.f : a.d, a.T, 1, 2, pl.grad_pairs, false, false);
       if (pl.dw.bytes > part) part = pl.dw.bytes;
     }
   }
@@ -245,8 +270,13 @@ int check_common(const nys_gated_ff_t* p) {
 
 // ----------------------------------------------------------------- launches
 
-Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int* status) {
+// a_terms, b_terms: how many each operand has.
+Params params_of(const Product& q, int parts, int a_terms, int b_terms, int a_by, int b_by, int* status) {
   Params p{};
+  const int pairs = a_terms == 3 ? 6 : a_terms > b_terms ? a_terms : b_terms;
+  if (pairs == 6) p.a_terms = kTermsA, p.b_terms = kTermsB;
+  if (pairs == 2) (a_terms == 2 ? p.a_terms : p.b_terms) = 0x01;  // the small one first
+
   p.m_tiles = q.m_tiles;
   p.n_tiles = q.n_tiles;
   p.parts = parts;
@@ -256,9 +286,9 @@ Params params_of(const Product& q, int parts, int pairs, int a_by, int b_by, int
   p.its_per_split = q.its_per_split;
   p.pairs = pairs;
   p.bn = q.bn;
-  p.unit = pairs > 1 ? pairs : 2;
+  p.unit = pairs > 2 ? pairs : 2;
   p.units = q.line.units;
-  p.chunk = pairs > 1 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
+  p.chunk = pairs > 2 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
   p.a_by = a_by;
   p.b_by = b_by;
   p.group = 16;
@@ -279,9 +309,9 @@ int launch_plain(const char* name, bool wide, const Maps& maps, const Params& p,
               : launch_pair<kBf16, AMN, BMN, kPlain, __nv_bfloat16>(name, maps, p, st);
 }
 
-// Operand of `rows` lines of `k`, or stored [k][rows] (mn), in one or three terms.
-Matrix operand(const void* at, long long rows, long long cols, long long stride, bool f32) {
-  return f32 ? Matrix{at, rows, cols, cols, 2, 3, rows * cols} : Matrix{at, rows, cols, stride, 2};
+// Operand of `rows` lines of `k`, or stored [k][rows] (mn): as it lies, or in terms.
+Matrix operand(const void* at, long long rows, long long cols, long long stride, int terms) {
+  return terms > 1 ? Matrix{at, rows, cols, cols, 2, terms, rows * cols} : Matrix{at, rows, cols, stride, 2};
 }
 
 int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* wg, const void* wu, void* h,
@@ -301,13 +331,14 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
   }
   const Product& q = pl.fwd;
   const bool direct = !q.turned && q.splits == 1;
-  Params p = params_of(q, direct ? 1 : 2, pl.pairs, q.turned ? kByPart : kOnly, q.turned ? kOnly : kByPart, status);
+  const int terms = pl.f32 ? 3 : 1;
+  Params p = params_of(q, direct ? 1 : 2, terms, terms, q.turned ? kByPart : kOnly, q.turned ? kOnly : kByPart, status);
   p.act = a.act;
   p.keep = gate != nullptr;
   Maps maps{};
-  const Matrix xm = operand(x, a.T, a.d, a.x, pl.f32);
-  const Matrix w[2] = {operand(wg, io ? a.d : a.f, io ? a.f : a.d, a.w, pl.f32),
-                       operand(wu, io ? a.d : a.f, io ? a.f : a.d, a.w, pl.f32)};
+  const Matrix xm = operand(x, a.T, a.d, a.x, terms);
+  const Matrix w[2] = {operand(wg, io ? a.d : a.f, io ? a.f : a.d, a.w, terms),
+                       operand(wu, io ? a.d : a.f, io ? a.f : a.d, a.w, terms)};
   bool ok = true;
   if (q.turned) {
     for (int i = 0; i < 2; ++i) ok = ok && (io ? map_mn(&maps.a[i], w[i]) : map_k(&maps.a[i], w[i], 128));
@@ -351,11 +382,14 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
   const bool io = a.layout == NYS_FF_IN_OUT;
   const Product& q = pl.dx;
   const bool direct = !q.turned && q.splits == 1;
-  const Params p = params_of(q, 1, pl.pairs, kByKPart, kByKPart, status);
+  const int terms = pl.f32 ? 3 : 1;  // of the weights
+  const Params p = params_of(q, 1, q.turned ? terms : pl.grad_terms, q.turned ? pl.grad_terms : terms, kByKPart, kByKPart,
+                             status);
   Maps maps{};
-  const Matrix g[2] = {operand(ws + pl.dg, a.T, a.f, a.f, pl.f32), operand(ws + pl.du, a.T, a.f, a.f, pl.f32)};
-  const Matrix w[2] = {operand(wg, io ? a.d : a.f, io ? a.f : a.d, a.w, pl.f32),
-                       operand(wu, io ? a.d : a.f, io ? a.f : a.d, a.w, pl.f32)};
+  const Matrix g[2] = {operand(ws + pl.dg, a.T, a.f, a.f, pl.grad_terms),
+                       operand(ws + pl.du, a.T, a.f, a.f, pl.grad_terms)};
+  const Matrix w[2] = {operand(wg, io ? a.d : a.f, io ? a.f : a.d, a.w, terms),
+                       operand(wu, io ? a.d : a.f, io ? a.f : a.d, a.w, terms)};
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap &wm = q.turned ? maps.a[i] : maps.b[i], &gm = q.turned ? maps.b[i] : maps.a[i];
@@ -389,14 +423,16 @@ int weight_gradients(const nys_gated_ff_t& a, const Plan& pl, const void* x, voi
   const Product& q = pl.dw;
   const bool direct = q.splits == 1;
   const int M = io ? a.d : a.f, N = io ? a.f : a.d;
-  Params p = params_of(q, 2, pl.pairs, io ? kOnly : kByPart, io ? kByPart : kOnly, status);
+  const int terms = pl.f32 ? 3 : 1;  // of x
+  Params p = params_of(q, 2, io ? terms : pl.grad_terms, io ? pl.grad_terms : terms, io ? kOnly : kByPart,
+                       io ? kByPart : kOnly, status);
   p.c_by_part = direct;
   Maps maps{};
   bool ok = true;
   for (int i = 0; i < 2; ++i) {
     CUtensorMap &xm = io ? maps.a[i] : maps.b[i], &gm = io ? maps.b[i] : maps.a[i];
-    ok = ok && map_mn(&xm, operand(x, a.T, a.d, a.x, pl.f32)) &&
-         map_mn(&gm, operand(ws + (i ? pl.du : pl.dg), a.T, a.f, a.f, pl.f32));
+    ok = ok && map_mn(&xm, operand(x, a.T, a.d, a.x, terms)) &&
+         map_mn(&gm, operand(ws + (i ? pl.du : pl.dg), a.T, a.f, a.f, pl.grad_terms));
     if (direct) ok = ok && map_out(&maps.c[i], Matrix{i ? dwu : dwg, M, N, a.dw, pl.f32 ? 4 : 2});
   }
   char* part = ws + pl.part;
@@ -412,7 +448,8 @@ int weight_gradients(const nys_gated_ff_t& a, const Plan& pl, const void* x, voi
 template <typename T>
 int launch_grads(const nys_gated_ff_t& a, const Plan& pl, const void* gate, const void* up, const void* gh,
                  const Splits& more, char* ws, cudaStream_t st) {
-  const GradParams p{a.gate, a.up, a.h, a.T, a.f, (unsigned)(((long long)a.T * (a.f / 8) + 255) / 256)};
+  const GradParams p{a.gate, a.up, a.h, a.T, a.f, (unsigned)(((long long)a.T * (a.f / 8) + 255) / 256),
+                     pl.grad_terms == 2};
   return act::by_act(a.act, [&](auto k) {
     return launch_behind("gated_ff_back", gated_ff_back<T, decltype(k)::value>, dim3(p.ctas + more.ctas()), dim3(256),
                          0, st, p, more, static_cast<const T*>(gate), static_cast<const T*>(up),

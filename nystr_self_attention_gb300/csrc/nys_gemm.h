@@ -62,7 +62,8 @@ struct Params {
   int its, its_per_split;  // K parts x k_blocks x pairs
   int bn;                // columns of a tile (gemm_pair)
   int chunk;             // steps (even) summed in TMEM before the sum moves to registers (fp32 results)
-  int pairs;             // 1, or 6 pairs of the three terms of fp32 operands
+  int pairs;             // products of the operands' terms that are summed: 1, 2 or 6
+  uint32_t a_terms, b_terms;  // the terms of pair i in nibble i
   int a_by, b_by;        // By
   int c_by_part;         // results of part i to c[i]; else to plane split * parts + part of c[0]
   int group;             // row tiles that neighbouring CTAs share: 16 (8: 486 us for the
@@ -252,14 +253,8 @@ struct Staging {
   }
 };
 
-// The terms of pair 0 .. 5 of fp32 operands, small products first: (2,0) (0,2)
-// (1,1) (1,0) (0,1) (0,0).
-__device__ __forceinline__ int term_of_a(const Params& p, int pair) {
-  return p.pairs == 1 ? 0 : (0x001102 >> (4 * pair)) & 15;
-}
-__device__ __forceinline__ int term_of_b(const Params& p, int pair) {
-  return p.pairs == 1 ? 0 : (0x010120 >> (4 * pair)) & 15;
-}
+// The terms of an operand that a pair multiplies: nibbles of a table.
+__device__ __forceinline__ int term_of(uint32_t table, int pair) { return (table >> (4 * pair)) & 15; }
 // Where a tile's first step lies.
 struct Step {
   int pair, kb, kpart;
@@ -489,7 +484,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
           Step at = s;
           for (int j = 0; j < count; ++j, at.next(p)) {
             uint8_t* to = sm + st * stage_bytes + j * step_bytes + (first ? 0 : L::kA);
-            const int k = at.kb * (KIND == kMx8 ? 128 : 64), z = first ? term_of_a(p, at.pair) : term_of_b(p, at.pair);
+            const int k = at.kb * (KIND == kMx8 ? 128 : 64), z = term_of(first ? p.a_terms : p.b_terms, at.pair);
             const CUtensorMap* map = first ? &maps.a[map_of(p.a_by, tile, at)]
                                            : &maps.b[EPI == kGated ? rank : map_of(p.b_by, tile, at)];
             if (first ? AMN : BMN) {
@@ -762,7 +757,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
           Step at = s;
           for (int j = 0; j < count; ++j, at.next(p)) {
             uint8_t* a = sm + st * L::kStage + j * L::kStep;
-            const int k = at.kb * (KIND == kMx8 ? 128 : 64), pa = term_of_a(p, at.pair);
+            const int k = at.kb * (KIND == kMx8 ? 128 : 64), pa = term_of(p.a_terms, at.pair);
             const CUtensorMap* am = &maps.a[map_of(p.a_by, tile, at)];
             if (AMN) {
               tma_load_3d(a, am, bar, tile.m * 128, k, pa);
@@ -770,7 +765,7 @@ gemm_tokens(const __grid_constant__ Maps maps, const __grid_constant__ Params p)
             } else {
               tma_load_3d(a, am, bar, k, tile.m * 128, pa);
             }
-            tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, at)], bar, k, 0, term_of_b(p, at.pair));
+            tma_load_3d(a + L::kA, &maps.b[map_of(p.b_by, tile, at)], bar, k, 0, term_of(p.b_terms, at.pair));
           }
         }
         __syncwarp();
@@ -1043,6 +1038,10 @@ int launch_tokens(const char* name, int bn, int ctas, const Maps& maps, const Pa
 }
 constexpr int kMostTokens = 128;  // of gemm_tokens
 inline int columns_of(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32 : tokens <= 64 ? 64 : 128; }
+
+// Three terms of both operands, all pairs that matter at 2^-24, small products
+// first: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
+constexpr uint32_t kTermsA = 0x001102, kTermsB = 0x010120;
 
 // How gemm_pair's product is cut: columns of a tile and ranges of K, whose partial sums are joined. The time of a choice is counted in
 // steps of a full tile (0.3 us; `pairs` of them for a K block of fp32): rounds of tiles over the CTAs times a tile's steps,

@@ -78,6 +78,26 @@ struct Vec<__nv_bfloat16> {
   __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint4*>(p) = a; }
 };
 
+// Two fp32 operations at a time.
+__device__ __forceinline__ unsigned long long bits(float2 a) { return reinterpret_cast<unsigned long long&>(a); }
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)), "l"(bits(c)));
+  return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(bits(a)), "l"(bits(b)));
+  return reinterpret_cast<float2&>(d);
+}
+__device__ __forceinline__ float2 both(float a) { return make_float2(a, a); }
+__device__ __forceinline__ float2& pair_of(float (&v)[8], int i) { return reinterpret_cast<float2&>(v[2 * i]); }
+
 // Sum of v over the TPR threads of a row, the same bits in each: shuffles, then
 // one slot per warp. The slots alternate between two sets, so one barrier per
 // sum is enough.
@@ -110,6 +130,55 @@ __device__ __forceinline__ void row_sums(float (&v)[N], float (*slots)[N], int& 
   }
 }
 
+// r + low = 1 / sqrt((total + rest) / d + eps), to 1e-14 of it: a step of
+// Newton's on the special-function unit's result, with the remainders of the
+// division, the sum and the product kept (fused multiply-adds have no rounding
+// between their product and their sum).
+__device__ __forceinline__ float2 inverse_root(float total, float rest, float d, float inv_d, float eps) {
+  const float q = total * inv_d, ql = (fmaf(-q, d, total) + rest) * inv_d;
+  const float v = q + eps, b = v - q, vl = (q - (v - b)) + (eps - b) + ql;
+  const float r = rsqrtf(v), h = v * r, hl = fmaf(v, r, -h);
+  const float e = fmaf(-h, r, 1.f) - fmaf(hl, r, vl * r * r);
+  return make_float2(r, 0.5f * r * e);
+}
+
+// The root of a row's mean square to 1e-14 or so of the fp32 sums of its warps: the
+// group's first warp adds those, with what the additions round away, and hands the
+// root on. (Each thread adding them for itself took 7 instructions per element.)
+template <int TPR>
+__device__ __forceinline__ float2 exact_root(float v, float (*slots)[1], float2* roots, int& phase, float d, float inv_d,
+                                             float eps) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (TPR == 32) return inverse_root(v, 0.f, d, inv_d, eps);
+  const int W = TPR >= 256 ? blockDim.x / 32 : TPR / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = TPR >= 256 ? 0 : threadIdx.x / TPR;
+  auto barrier = [&] {
+    if (TPR >= 256)
+      __syncthreads();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(TPR) : "memory");
+  };
+  float(*set)[1] = slots + phase * (blockDim.x / 32);
+  float2* root = roots + phase * 8 + group;
+  phase ^= 1;
+  if (lane == 0) set[warp][0] = v;
+  barrier();
+  if (warp == group * W) {
+    float x = lane < W ? set[group * W + lane][0] : 0.f, low = 0.f;
+#pragma unroll
+    for (int o = TPR / 64; o > 0; o >>= 1) {
+      const float y = __shfl_xor_sync(0xffffffffu, x, o), rest = __shfl_xor_sync(0xffffffffu, low, o);
+      const float sum = x + y, b = sum - x;
+      low = low + rest + ((x - (sum - b)) + (y - b));
+      x = sum;
+    }
+    if (lane == 0) *root = inverse_root(x, low, d, inv_d, eps);
+  }
+  barrier();
+  return *root;
+}
+
 constexpr int threads_of(int tpr) { return tpr < 256 ? 256 : tpr; }
 // Threads per SM that the registers are cut for.
 template <typename T, int TPR, bool RES>
@@ -124,6 +193,7 @@ __global__ void __launch_bounds__(threads_of(TPR), fwd_threads<T, TPR, RES>() / 
 add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restrict__ weight, T* sum, T* y) {
   constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
   __shared__ float slots[2 * THREADS / 32][1];
+  __shared__ float2 roots[2 * 8];
   int phase = 0;
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
@@ -153,7 +223,8 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
   }
   // the threads of a row leave together: `row` is the group's
   for (; row < p.rows; row += step) {
-    float s[V][8], total[1] = {0.f};
+    float s[V][8], total[1];
+    float2 squares = both(0.f);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       nx[i].widen(s[i]);
@@ -161,7 +232,7 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
         float r[8];
         nr[i].widen(r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) s[i][j] += r[j];
+        for (int j = 0; j < 4; ++j) pair_of(s[i], j) = add2(pair_of(s[i], j), pair_of(r, j));
         Vec<T> out;  // s is what is kept: rounded
         out.narrow(s[i]);
         out.widen(s[i]);
@@ -169,16 +240,35 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
         if (sum && c < p.d) out.store(sum + row * p.s + c);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) total[0] = fmaf(s[i][j], s[i][j], total[0]);
+      for (int j = 0; j < 4; ++j) squares = fma2(pair_of(s[i], j), pair_of(s[i], j), squares);
     }
+    total[0] = squares.x + squares.y;
     fetch(row < p.rows - step ? row + step : p.rows);
-    row_sums<TPR, 1>(total, slots, phase);
-    const float r = rsqrtf(fmaf(total[0], p.inv_d, p.eps));
+    // To 8 bits, y is rounded to fp32 once (2^-24): a code next to a border then
+    // differs from the exact one's as rarely as fp32 can have it.
+    float2 root;
+    if (EIGHT) {
+      root = exact_root<TPR>(total[0], slots, roots, phase, (float)p.d, p.inv_d, p.eps);
+    } else {
+      row_sums<TPR, 1>(total, slots, phase);
+      root = make_float2(rsqrtf(fmaf(total[0], p.inv_d, p.eps)), 0.f);
+    }
+    const float low = root.y - root.y == 0.f ? root.y : 0.f;  // none where the sum of squares is infinite
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = 8 * (i * across + t);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[i][j] *= r * w[i][j];
+      for (int j = 0; j < 4; ++j) {
+        float2& v = pair_of(s[i], j);
+        const float2 wj = pair_of(w[i], j);
+        const float2 h = mul2(v, both(root.x));
+        if (EIGHT) {
+          const float2 hl = fma2(v, both(low), fma2(v, both(root.x), make_float2(-h.x, -h.y)));
+          v = fma2(h, wj, mul2(hl, wj));
+        } else {
+          v = mul2(h, wj);
+        }
+      }
       if (!EIGHT) {
         Vec<T> out;
         out.narrow(s[i]);
