@@ -16,6 +16,7 @@
 #include <mutex>
 
 #include "nys_q8.h"
+#include "nys_sm100.h"
 
 namespace nys {
 namespace {
@@ -28,7 +29,12 @@ struct NormParams {
   int rows, d;
   float eps, inv_d;
   uint8_t *codes, *scales;
+  int ring;     // backward: rows of shared memory
+  int* status;  // and where a wait that runs out is reported
 };
+// 16384 x 4096 in bf16: 86 us with three rows, 92 with four, 90 from registers; in
+// fp32 4096 x 8192 87 us with two, 125 from registers.
+constexpr int kMostRing = 3;
 
 // Eight channels as they lie in memory.
 template <typename T>
@@ -186,6 +192,7 @@ constexpr int fwd_threads() {
   return TPR == 1024 ? 1024 : sizeof(T) == 4 && RES ? 1024 : 1536;
 }
 constexpr int kBwdThreads = 512;
+constexpr int bwd_ctas(int threads) { return threads < kBwdThreads ? kBwdThreads / threads : 1; }  // per SM
 
 
 template <typename T, int TPR, int V, bool EIGHT, bool RES>
@@ -294,16 +301,33 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
   }
 }
 
-// part: [CTAs][d] sums of gy h over a CTA's rows, or null.
+// A row of memory to shared memory, reported to a barrier.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   sm100::smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(sm100::smem_u32(bar))
+               : "memory");
+}
+
+// part: [CTAs][d] sums of gy h over a CTA's rows, or null. Rows that a CTA has to
+// itself come through p.ring rows of shared memory, filled by bulk copies that far
+// ahead; the others are loaded into registers one row ahead.
 template <typename T, int TPR, int V>
-__global__ void __launch_bounds__(threads_of(TPR), kBwdThreads / threads_of(TPR))
+__global__ void __launch_bounds__(threads_of(TPR), bwd_ctas(threads_of(TPR)))
 add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, const float* __restrict__ weight,
                   T* dx, float* part) {
+  constexpr bool RING = TPR >= 256;
   constexpr int THREADS = threads_of(TPR), GROUPS = THREADS / TPR;
-  // the weight in registers and the next row in flight as long as both fit
-  constexpr bool ROOMY = V * sizeof(T) <= 4;
+  // the weight in registers, and the next row in flight, as long as both fit
+  constexpr bool ROOMY = RING || V * sizeof(T) <= 4;
+  // the longest rows: read from the ring twice instead of held
+  constexpr bool TWICE = RING && TPR == 1024;
   __shared__ float slots[2 * THREADS / 32][2];
-  extern __shared__ float sums[];  // [GROUPS][d] where a CTA holds several rows
+  extern __shared__ __align__(16) float sums[];  // [GROUPS][d] where a CTA holds several rows; the ring
+  __shared__ uint64_t full[kMostRing];
+  __shared__ int abort_flag;
+  uint8_t* ring = reinterpret_cast<uint8_t*>(sums);
+  const uint32_t row_bytes = p.d * sizeof(T), slot_bytes = (gs ? 3 : 2) * row_bytes;
   int phase = 0;
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
@@ -330,7 +354,30 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
 #pragma unroll
     for (int j = 0; j < 8; ++j) w[j] = c < p.d ? (weight ? weight[c + j] : 1.f) : 0.f;
   };
-  fetch(row);
+  // one thread: row r's three parts to the slot of the CTA's n-th row
+  auto fill = [&](int r, int n) {
+    uint8_t* to = ring + n % p.ring * slot_bytes;
+    uint64_t* bar = &full[n % p.ring];
+    sm100::mbar_arrive_expect_tx(bar, slot_bytes);
+    bulk_load(to, s + r * p.s, row_bytes, bar);
+    bulk_load(to + row_bytes, gy + r * p.y, row_bytes, bar);
+    if (gs) bulk_load(to + 2 * row_bytes, gs + r * p.gs, row_bytes, bar);
+  };
+  int nth = 0;  // of the CTA's rows
+  if (RING) {
+    if (threadIdx.x == 0) {
+      abort_flag = 0;
+      for (int i = 0; i < p.ring; ++i) sm100::mbar_init(&full[i], 1);
+      sm100::fence_barrier_init();
+      for (int i = 0, r = row; i < p.ring && r < p.rows; ++i) {
+        fill(r, i);
+        r = r < p.rows - step ? r + step : p.rows;
+      }
+    }
+    __syncthreads();
+  } else {
+    fetch(row);
+  }
   float kept[ROOMY ? V : 1][8], acc[V][8];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -340,39 +387,71 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
   }
   for (; row < p.rows; row += step) {
     Vec<T> xs[V], xg[V], xa[V];
-    float total[2] = {0.f, 0.f};  // s^2, weight gy s
+    if (RING) {
+      if (!sm100::mbar_wait(&full[nth % p.ring], nth / p.ring & 1, const_cast<volatile int*>(&abort_flag),
+                            2000000000ull)) {
+        abort_flag = 1;
+        atomicExch(p.status, (int)NYS_ERR_TIMEOUT);
+      }
+    }
+    // the row's parts of vector i, from its slot
+    const uint8_t* from = ring + nth % (RING ? p.ring : 1) * slot_bytes;
+    auto read = [&](int i, Vec<T>& a, Vec<T>& g, Vec<T>& e) {
+      const int c = 8 * (i * across + t);
+      a.clear();
+      g.clear();
+      e.clear();
+      if (c >= p.d) return;
+      a.load(reinterpret_cast<const T*>(from) + c);
+      g.load(reinterpret_cast<const T*>(from + row_bytes) + c);
+      if (gs) e.load(reinterpret_cast<const T*>(from + 2 * row_bytes) + c);
+    };
+    float2 ss = both(0.f), gs2 = both(0.f);  // s^2, weight gy s
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      xs[i] = ns[i];
-      xg[i] = ng[i];
-      xa[i] = na[i];
+      if (RING) {
+        read(i, xs[i], xg[i], xa[i]);
+      } else {
+        xs[i] = ns[i];
+        xg[i] = ng[i];
+        xa[i] = na[i];
+      }
       float a[8], g[8], w[8];
       xs[i].widen(a);
       xg[i].widen(g);
       if (!ROOMY) load_weight(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        total[0] = fmaf(a[j], a[j], total[0]);
-        total[1] = fmaf((ROOMY ? kept[ROOMY ? i : 0][j] : w[j]) * g[j], a[j], total[1]);
+      for (int j = 0; j < 4; ++j) {
+        ss = fma2(pair_of(a, j), pair_of(a, j), ss);
+        gs2 = fma2(mul2(ROOMY ? pair_of(kept[ROOMY ? i : 0], j) : pair_of(w, j), pair_of(g, j)), pair_of(a, j), gs2);
       }
     }
+    float total[2] = {ss.x + ss.y, gs2.x + gs2.y};
     const int next = row < p.rows - step ? row + step : p.rows;
-    if (ROOMY) fetch(next);
+    if (ROOMY && !RING) fetch(next);
     row_sums<TPR, 2>(total, slots, phase);
+    auto refill = [&] {  // behind a barrier: every thread has read the slot
+      const long long later = row + (long long)p.ring * step;
+      if (threadIdx.x == 0 && later < p.rows && !abort_flag) fill((int)later, nth + p.ring);
+      ++nth;
+    };
+    if (RING && !TWICE) refill();
     const float r = rsqrtf(fmaf(total[0], p.inv_d, p.eps));
     const float m = -r * r * total[1] * p.inv_d;  // -mean(weight gy h) r
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       float a[8], g[8], e[8], w[8];
+      if (TWICE) read(i, xs[i], xg[i], xa[i]);
       xs[i].widen(a);
       xg[i].widen(g);
       xa[i].widen(e);
       if (!ROOMY) load_weight(i, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float h = a[j] * r;
-        acc[i][j] = fmaf(g[j], h, acc[i][j]);
-        e[j] = fmaf(r, (ROOMY ? kept[ROOMY ? i : 0][j] : w[j]) * g[j], fmaf(h, m, e[j]));
+      for (int j = 0; j < 4; ++j) {
+        const float2 h = mul2(pair_of(a, j), both(r)), gj = pair_of(g, j);
+        const float2 wg = mul2(ROOMY ? pair_of(kept[ROOMY ? i : 0], j) : pair_of(w, j), gj);
+        pair_of(acc[i], j) = fma2(gj, h, pair_of(acc[i], j));
+        pair_of(e, j) = fma2(both(r), wg, fma2(h, both(m), pair_of(e, j)));
       }
       const int c = 8 * (i * across + t);
       Vec<T> out;
@@ -380,6 +459,10 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
       if (c < p.d) out.store(dx + row * p.dx + c);
     }
     if (!ROOMY) fetch(next);
+    if (TWICE) {
+      __syncthreads();
+      refill();
+    }
     if (next == p.rows) break;  // row + step may pass 2^31
   }
   if (!part) return;
@@ -440,7 +523,7 @@ int check_common(const nys_add_rms_norm_t* p) {
 
 // f(TPR, V) for a row of d channels: one vector per thread until a row has 1024
 // threads; backward (MORE), whose threads also carry the weight's sums, two until
-// it has 512. Forward to 8 bits, 65536 x 2048: 160 us with two, 149 with one;
+// it has 1024 as well. Forward to 8 bits, 65536 x 2048: 160 us with two, 149 with one;
 // backward, 16384 x 4096: 91 us with two, 95 with one.
 template <bool MORE, typename F>
 auto by_width(int d, F&& f) {
@@ -453,7 +536,7 @@ auto by_width(int d, F&& f) {
   if (units <= 128) return f(integral_constant<int, 128>{}, integral_constant<int, V>{});
   if (units <= 256) return f(integral_constant<int, 256>{}, integral_constant<int, V>{});
   if (units <= 512) return f(integral_constant<int, 512>{}, integral_constant<int, V>{});
-  return f(integral_constant<int, MORE ? 512 : 1024>{}, integral_constant<int, MORE ? 4 : 2>{});
+  return f(integral_constant<int, 1024>{}, integral_constant<int, 2>{});
 }
 // CTAs: one per group of rows until the GPU is full.
 int grid_of(int rows, int groups, int ctas_per_sm) {
@@ -468,7 +551,7 @@ int cta_threads(int d) {
 }
 template <int TPR, int V>
 int back_grid(const nys_add_rms_norm_t& a) {
-  return grid_of(a.rows, threads_of(TPR) / TPR, kBwdThreads / cta_threads<TPR, V>(a.d));
+  return grid_of(a.rows, threads_of(TPR) / TPR, bwd_ctas(cta_threads<TPR, V>(a.d)));
 }
 
 int back_ctas(const nys_add_rms_norm_t& a) {
@@ -516,15 +599,28 @@ int launch_fwd(const nys_add_rms_norm_t& a, const void* x, const void* res, cons
 
 template <typename T>
 int launch_bwd(const nys_add_rms_norm_t& a, const void* s, const void* gy, const void* gs, const float* weight,
-               void* dx, float* part, cudaStream_t st) {
-  const NormParams p = params_of(a);
+               void* dx, float* part, int* status, cudaStream_t st) {
+  NormParams p = params_of(a);
+  p.status = status;
   return by_width<true>(a.d, [&](auto tpr, auto v) {
     constexpr int TPR = decltype(tpr)::value, V = decltype(v)::value, THREADS = threads_of(TPR);
     constexpr int GROUPS = THREADS / TPR;
-    const size_t smem = GROUPS > 1 && part ? (size_t)GROUPS * a.d * sizeof(float) : 0;  // at most 16 KB
-    return launch_behind("add_rms_norm_back", add_rms_norm_back<T, TPR, V>, dim3(back_grid<TPR, V>(a)),
-                         dim3(cta_threads<TPR, V>(a.d)), smem, st, p, static_cast<const T*>(s),
-                         static_cast<const T*>(gy), static_cast<const T*>(gs), weight, static_cast<T*>(dx), part);
+    const int threads = cta_threads<TPR, V>(a.d);
+    auto go = [&](auto kernel, size_t smem) {
+      if (smem > 32 * 1024 &&  // 48 KB with what is static
+          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return set_cuda_error(cudaGetLastError());
+      return launch_behind("add_rms_norm_back", kernel, dim3(back_grid<TPR, V>(a)), dim3(threads), smem, st, p,
+                           static_cast<const T*>(s), static_cast<const T*>(gy), static_cast<const T*>(gs), weight,
+                           static_cast<T*>(dx), part);
+    };
+    if (TPR >= 256) {  // as many rows as the CTAs of an SM have room for: one of 16384 in fp32
+      const size_t slot = (size_t)(gs ? 3 : 2) * a.d * sizeof(T), room = 220 * 1024 / bwd_ctas(threads);
+      p.ring = (int)(room / slot < kMostRing ? room / slot : kMostRing);
+      return go(add_rms_norm_back<T, TPR, V>, p.ring * slot);
+    }
+    // at most 16 KB
+    return go(add_rms_norm_back<T, TPR, V>, GROUPS > 1 && part ? (size_t)GROUPS * a.d * sizeof(float) : 0);
   });
 }
 
@@ -609,8 +705,10 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
     if (rc != NYS_OK) return rc;
   }
   float* part = dweight ? static_cast<float*>(workspace) : nullptr;
-  rc = p->dtype == NYS_BF16 ? launch_bwd<__nv_bfloat16>(*p, s, gy, gs, weight, dx, part, stream)
-                            : launch_bwd<float>(*p, s, gy, gs, weight, dx, part, stream);
+  int* status = nullptr;
+  if ((rc = operator_status(dev, &status)) != NYS_OK) return rc;
+  rc = p->dtype == NYS_BF16 ? launch_bwd<__nv_bfloat16>(*p, s, gy, gs, weight, dx, part, status, stream)
+                            : launch_bwd<float>(*p, s, gy, gs, weight, dx, part, status, stream);
   if (rc != NYS_OK || !dweight) return rc;
   return launch_behind("norm_weight_grad", norm_weight_grad, dim3((p->d + 31) / 32), dim3(1024), 0, stream,
                        static_cast<const float*>(part), dweight, p->d, back_ctas(*p));
