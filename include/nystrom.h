@@ -633,7 +633,8 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
  * Sums are fp32 in the matrix units, in a fixed order; one rounding to dtype. For
  * NYS_BF16 dg and du enter the products rounded to bf16, of up to 128 tokens to two
  * bf16 terms (16 bits).
- * NYS_FP32 operands enter the products as sums of three bfloat16 terms (24 bits;
+ * Up to 24 tokens of NYS_FP32 are multiplied in fp32 (but for the weights'
+ * gradients); else NYS_FP32 operands enter as sums of three bfloat16 terms (24 bits;
  * six of the nine products, all that matter at 2^-24), so an infinity gives NaN
  * where a finite sum could not, values beyond 3.38e38 are infinite, and bits
  * below 2^-133 are lost.

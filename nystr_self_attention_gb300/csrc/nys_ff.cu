@@ -14,7 +14,8 @@
 // one, with K split over the SMs and the partial sums joined (and gated there):
 // the weights then stream at HBM's pace.
 //
-// fp32: an operand is split into three bf16 terms, 24 bits in all, in a pass of
+// fp32, up to 24 tokens: on the CUDA cores (nys_few.cu), but for the gradients of
+// the weights. More: an operand is split into three bf16 terms, 24 bits in all, in a pass of
 // its own, and the product sums the six pairs that matter at 2^-24. bf16: dg and
 // du enter the products rounded to bf16, an error as large as the results' own
 // rounding; of few tokens, where nothing averages it and the weights' bytes bound
@@ -51,6 +52,10 @@ __device__ __forceinline__ void store_terms(__nv_bfloat16* to, long long plane, 
                    pack_bf16x2(t[6][k], t[7][k]));
 }
 
+__device__ __forceinline__ void store8(float* to, const float (&v)[8]) {
+  reinterpret_cast<float4*>(to)[0] = make_float4(v[0], v[1], v[2], v[3]);
+  reinterpret_cast<float4*>(to)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
 __device__ __forceinline__ void store_bf16(__nv_bfloat16* to, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(to) =
       make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
@@ -122,6 +127,7 @@ struct GradParams {
   int f;
   unsigned ctas;  // those behind split the matrices of `more`
   int two;        // bf16: two terms
+  float *dg32, *du32;  // fp32: as they are, too, or null
 };
 
 // dg, du as terms [1, 2 or (fp32) 3][T][f]. Eight elements per thread.
@@ -154,6 +160,10 @@ gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Spli
   if (sizeof(T) == 4) {
     store_terms(dg + at, p.T * p.f, g);
     store_terms(du + at, p.T * p.f, u);
+    if (p.dg32) {
+      store8(p.dg32 + at, g);
+      store8(p.du32 + at, u);
+    }
   } else {
     store_bf16(dg + at, g);
     store_bf16(du + at, u);
@@ -173,6 +183,7 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // One launch of the products: `parts` results [M][N], K = k_parts x k.
 struct Product {
   bool turned;  // D is the result's transpose: its N are the 128-row operand's rows
+  int range;    // on the CUDA cores (nys_few.cu): K's range; 0: on the tensor cores
   int bn, splits, its, its_per_split, k_blocks, m_tiles, n_tiles;
   Line line;     // turned
   size_t bytes;  // of partial sums
@@ -205,20 +216,30 @@ Product product_of(long long M, long long N, long long k, int k_parts, int parts
   return q;
 }
 
+// Few tokens in fp32, on the CUDA cores.
+Product few_of(long long T, long long N, long long K, bool k_contiguous) {
+  Product q{};
+  q.range = few_range((int)T, (int)N, (int)K, k_contiguous);
+  q.splits = (int)((K + q.range - 1) / q.range);
+  q.bytes = align256((size_t)q.splits * 2 * T * N * 4);
+  return q;
+}
+
 struct Plan {
-  bool f32;
+  bool f32, few;
   int pairs;       // of the forward product
   int grad_terms;  // of dg and du: 1, 2 (few tokens), or fp32's 3
   int grad_pairs;  // products summed for a gradient
   Product fwd, dx, dw;
   // byte offsets in the workspace
-  size_t x, wg, wu, dg, du, part, total;
+  size_t x, wg, wu, dg, du, dg32, du32, part, total;
 };
 
 Plan plan_of(const nys_gated_ff_t& a, bool back, bool want_dx, bool want_dw) {
   Plan pl{};
   pl.f32 = a.dtype == NYS_FP32;
   pl.pairs = pl.f32 ? 6 : 1;
+  pl.few = pl.f32 && a.T <= kMostFew;
   pl.grad_terms = pl.f32 ? 3 : a.T <= kMostTokens ? 2 : 1;
   pl.grad_pairs = pl.f32 ? 6 : pl.grad_terms;
   const size_t T = a.T, d = a.d, f = a.f;
@@ -226,19 +247,23 @@ Plan plan_of(const nys_gated_ff_t& a, bool back, bool want_dx, bool want_dw) {
   auto take = [&](size_t bytes) { size_t o = off; off += align256(bytes); return o; };
   const bool io = a.layout == NYS_FF_IN_OUT;
   size_t part = 0;
-  if (pl.f32 && (!back || want_dw)) pl.x = take(3 * T * d * 2);
-  if (pl.f32 && (!back || want_dx)) {
+  if (pl.f32 && (back ? want_dw : !pl.few)) pl.x = take(3 * T * d * 2);
+  if (pl.f32 && !pl.few && (!back || want_dx)) {
     pl.wg = take(3 * d * f * 2);
     pl.wu = take(3 * d * f * 2);
   }
   if (!back) {
-    pl.fwd = product_of(a.T, a.f, a.d, 1, 2, pl.pairs, true, true);
+    pl.fwd = pl.few ? few_of(a.T, a.f, a.d, !io) : product_of(a.T, a.f, a.d, 1, 2, pl.pairs, true, true);
     part = pl.fwd.bytes;
   } else {
     pl.dg = take(pl.grad_terms * T * f * 2);
     pl.du = take(pl.grad_terms * T * f * 2);
     if (want_dx) {
-      pl.dx = product_of(a.T, a.d, a.f, 2, 1, pl.grad_pairs, false, true);
+      pl.dx = pl.few ? few_of(a.T, a.d, a.f, io) : product_of(a.T, a.d, a.f, 2, 1, pl.grad_pairs, false, true);
+      if (pl.few) {
+        pl.dg32 = take(T * f * 4);
+        pl.du32 = take(T * f * 4);
+      }
       part = pl.dx.bytes;
     }
     if (want_dw) {
@@ -318,6 +343,22 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
             void* gate, void* up, char* ws, int* status, cudaStream_t st) {
   const bool io = a.layout == NYS_FF_IN_OUT;
   int rc;
+  if (pl.few) {
+    Few w{};
+    w.x[0] = w.x[1] = static_cast<const float*>(x);
+    w.w[0] = static_cast<const float*>(wg);
+    w.w[1] = static_cast<const float*>(wu);
+    w.x_stride = a.x;
+    w.w_stride = a.w;
+    w.part = reinterpret_cast<float*>(ws + pl.part);
+    w.T = a.T;
+    w.N = a.f;
+    w.K = a.d;
+    w.range = pl.fwd.range;
+    if ((rc = launch_few("gated_ff_few", w, !io, st)) != NYS_OK) return rc;
+    const JoinGated j{w.part, pl.fwd.splits, a.T, a.f, Line{}, h, gate, up, a.h, a.gate, a.up};
+    return join_gated(j, a.act, a.dtype, st);
+  }
   if (pl.f32) {
     const int wr = io ? a.d : a.f, wc = io ? a.f : a.d;
     Splits m{};
@@ -381,6 +422,24 @@ int input_gradient(const nys_gated_ff_t& a, const Plan& pl, const void* wg, cons
                    int* status, cudaStream_t st) {
   const bool io = a.layout == NYS_FF_IN_OUT;
   const Product& q = pl.dx;
+  if (q.range) {
+    Few w{};
+    w.x[0] = reinterpret_cast<const float*>(ws + pl.dg32);
+    w.x[1] = reinterpret_cast<const float*>(ws + pl.du32);
+    w.w[0] = static_cast<const float*>(wg);
+    w.w[1] = static_cast<const float*>(wu);
+    w.x_stride = a.f;
+    w.w_stride = a.w;
+    w.part = reinterpret_cast<float*>(ws + pl.part);
+    w.T = a.T;
+    w.N = a.d;
+    w.K = a.f;
+    w.range = q.range;
+    const int rc = launch_few("gated_ff_few", w, io, st);
+    if (rc != NYS_OK) return rc;
+    const Join j{w.part, 2 * q.splits, a.T, a.d, Line{}, {dx, nullptr}, {a.dx, 0}};
+    return join(j, 1, a.dtype, st);
+  }
   const bool direct = !q.turned && q.splits == 1;
   const int terms = pl.f32 ? 3 : 1;  // of the weights
   const Params p = params_of(q, 1, q.turned ? terms : pl.grad_terms, q.turned ? pl.grad_terms : terms, kByKPart, kByKPart,
@@ -449,7 +508,8 @@ template <typename T>
 int launch_grads(const nys_gated_ff_t& a, const Plan& pl, const void* gate, const void* up, const void* gh,
                  const Splits& more, char* ws, cudaStream_t st) {
   const GradParams p{a.gate, a.up, a.h, a.T, a.f, (unsigned)(((long long)a.T * (a.f / 8) + 255) / 256),
-                     pl.grad_terms == 2};
+                     pl.grad_terms == 2, pl.dx.range ? reinterpret_cast<float*>(ws + pl.dg32) : nullptr,
+                     pl.dx.range ? reinterpret_cast<float*>(ws + pl.du32) : nullptr};
   return act::by_act(a.act, [&](auto k) {
     return launch_behind("gated_ff_back", gated_ff_back<T, decltype(k)::value>, dim3(p.ctas + more.ctas()), dim3(256),
                          0, st, p, more, static_cast<const T*>(gate), static_cast<const T*>(up),
@@ -553,7 +613,7 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
     more.add(x, p->x, ws + pl.x, p->T, p->d);
     xs = ws + pl.x;
   }
-  if (pl.f32 && dx) {
+  if (pl.f32 && dx && !pl.few) {
     more.add(w_gate, p->w, ws + pl.wg, wr, wc);
     more.add(w_up, p->w, ws + pl.wu, wr, wc);
     wg = ws + pl.wg;

@@ -988,6 +988,21 @@ struct JoinGated {
 };
 int join_gated(const JoinGated& j, int act, int dtype, cudaStream_t st);
 
+// Products of a few fp32 rows with fp32 weights on the CUDA cores (nys_few.cu):
+// plane 2 split + i of part [T][N] is x[i] times w[i] over K's range `split`.
+struct Few {
+  const float *x[2], *w[2];
+  long long x_stride, w_stride;  // w: [N][K] (k_contiguous) or [K][N]
+  float* part;
+  int T, N, K, range;
+  int splits() const { return (K + range - 1) / range; }
+};
+// Tokens; 24 of them through 4096 -> 4712 twice take 88 to 115 us on the CUDA cores,
+// 112 to 117 in terms on the tensor cores; one takes 29 against 110.
+constexpr int kMostFew = 24;
+int few_range(int T, int N, int K, bool k_contiguous);
+int launch_few(const char* name, const Few& p, bool k_contiguous, cudaStream_t st);
+
 // Every map is fetched ahead, used or not: those that a call leaves out are copies.
 inline Maps filled(Maps m) {
   for (CUtensorMap* x : {&m.a[1], &m.b[0], &m.b[1], &m.c[0], &m.c[1], &m.c[2]}) {
