@@ -656,6 +656,7 @@ int nystrom_add_rms_norm_fwd(const nys_add_rms_norm_t* p, const void* x, const v
   }
   if (reinterpret_cast<uintptr_t>(weight) & 3u) return NYS_ERR_ALIGN;
   if (sum && sum == y) return NYS_ERR_ARG;
+  if (weight && (sum == weight || y == weight)) return NYS_ERR_ARG;
   if ((sum && (!apart_or_same(sum, p->sum, x, p->x, p->rows) ||
                !apart_or_same(sum, p->sum, residual, p->residual, p->rows))) ||
       (y && (!apart_or_same(y, p->y, x, p->x, p->rows) ||

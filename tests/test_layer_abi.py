@@ -118,6 +118,7 @@ def test_norm_pointers(N):
     assert fwd(y=None, y8=q8(N, 256, 8192, 4, 64)) == E_ARG   # codes over x
     assert fwd(r=None) == E_ARG                            # a sum without a residual
     assert fwd(s=2048) == E_ARG                            # sum and y at one address
+    assert fwd(s=16) == E_ARG and fwd(y=16) == E_ARG       # over the weight
     assert fwd(s=256, sum=128) == E_ARG                    # in place with another stride
     assert fwd(x=264) == E_ALIGN and fwd(w=18) == E_ALIGN
 
