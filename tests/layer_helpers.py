@@ -58,6 +58,16 @@ def act_code(N, name):
             "relu": N.NYS_ACT_RELU}[name]
 
 
+def own_status(N):
+    """A forward pass in the library's own workspace: nystrom_get_status reads the
+    last one's status word, and a workspace that an earlier test gave may be gone."""
+    import torch
+    q = torch.zeros(1, 1, 64, 32, dtype=torch.bfloat16, device="cuda")
+    N.nystrom_attention(q, q, q, None, 8, 2)
+    torch.cuda.synchronize()
+    N.nystrom_get_status()
+
+
 def done(N):
     import torch
     torch.cuda.synchronize()

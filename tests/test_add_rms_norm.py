@@ -15,7 +15,7 @@ least 300 groups)."""
 import numpy as np
 import pytest
 
-from layer_helpers import HALF, U, done, eight, empty, host, untouched, upload
+from layer_helpers import HALF, U, done, eight, empty, host, own_status, untouched, upload
 from oracle import layer_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -28,6 +28,8 @@ def library():
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     torch.cuda.set_device(0)
+    import nystr_self_attention_gb300 as N
+    own_status(N)
 
 
 def inputs(rows, d, dtype, seed=1):

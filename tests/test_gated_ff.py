@@ -12,7 +12,7 @@ themselves (bf16: __expf's argument, up to 30 here, at 2^-23 each) or 16 u."""
 import numpy as np
 import pytest
 
-from layer_helpers import ACTS, HALF, U, act_code, done, empty, host, untouched, upload
+from layer_helpers import ACTS, HALF, U, act_code, done, empty, host, own_status, untouched, upload
 from oracle import layer_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -25,6 +25,8 @@ def library():
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     torch.cuda.set_device(0)
+    import nystr_self_attention_gb300 as N
+    own_status(N)
 
 
 def weight(w, dtype, order, pad=0):

@@ -7,7 +7,7 @@ import threading
 import numpy as np
 import pytest
 
-from layer_helpers import HALF, act_code, done, eight, empty, host, tdtype, upload, upload_eight
+from layer_helpers import HALF, act_code, done, eight, empty, host, own_status, tdtype, upload, upload_eight
 from oracle import layer_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -20,6 +20,8 @@ def library():
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     torch.cuda.set_device(0)
+    import nystr_self_attention_gb300 as N
+    own_status(N)
 
 
 def norm_back(seed, rows, d, dtype):

@@ -11,7 +11,7 @@ plus the rounding."""
 import numpy as np
 import pytest
 
-from layer_helpers import HALF, U, done, eight, empty, host, tdtype, untouched, upload, upload_eight
+from layer_helpers import HALF, U, done, eight, empty, host, own_status, tdtype, untouched, upload, upload_eight
 from oracle import layer_ref as R
 
 pytestmark = pytest.mark.gpu
@@ -24,6 +24,8 @@ def library():
     build.build()
     assert torch.cuda.is_available(), "GPU tests need a GPU"
     torch.cuda.set_device(0)
+    import nystr_self_attention_gb300 as N
+    own_status(N)
 
 
 def values(rows, K, dtype, seed):
