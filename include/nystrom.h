@@ -515,11 +515,13 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
  * product. These operators take matrices: rows are tokens (or a weight's output
  * channels), each a run of contiguous elements, `stride` elements apart, so a
  * slice of a wider matrix is read and written in place. Addresses are 16-byte
- * aligned and strides multiples of 16 bytes (else NYS_ERR_ALIGN); rows of an
- * output do not overlap (a stride below the row's length, with more than one
- * row, is NYS_ERR_ARG; the stride of a single row does not matter). Outputs overlap neither one another nor an input,
- * except where an operator says so; one at the very address of another, or of
- * an input it may not be, is refused (NYS_ERR_ARG).
+ * aligned and strides multiples of 16 bytes (else NYS_ERR_ALIGN). Rows of an
+ * output do not overlap, nor those of a factor of nystrom_q8_matmul (a, w) and
+ * nystrom_gated_ff (x, the weights): a stride below the row's length, with more
+ * than one row, is NYS_ERR_ARG. Rows of other inputs may, down to a stride of 0
+ * (one row for all). The stride of a single row does not matter. Outputs overlap
+ * neither one another nor an input, except where an operator says so; one at the
+ * very address of another, or of an input it may not be, is refused (NYS_ERR_ARG).
  */
 
 /*
@@ -632,12 +634,11 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
  *
  * Sums are fp32 in the matrix units, in a fixed order; one rounding to dtype. For
  * NYS_BF16 dg and du enter the products rounded to bf16, of up to 128 tokens to two
- * bf16 terms (16 bits).
- * Up to 24 tokens of NYS_FP32 are multiplied in fp32 (but for the weights'
- * gradients); else NYS_FP32 operands enter as sums of three bfloat16 terms (24 bits;
- * six of the nine products, all that matter at 2^-24), so an infinity gives NaN
- * where a finite sum could not, values beyond 3.38e38 are infinite, and bits
- * below 2^-133 are lost.
+ * bf16 terms (16 bits). Up to 24 tokens of NYS_FP32 are multiplied in fp32 (but for
+ * the weights' gradients); else NYS_FP32 operands enter as sums of three bfloat16
+ * terms (24 bits; six of the nine products, all that matter at 2^-24), so an
+ * infinity gives NaN where a finite sum could not, values beyond 3.38e38 are
+ * infinite, and bits below 2^-133 are lost.
  * Shape rules (else NYS_ERR_SHAPE): T, d, f >= 1, d % 8 == f % 8 == 0, d, f <= 2^20,
  * T <= 2^30.
  * workspace: as above (back: 0 forward, 1 backward).

@@ -15,9 +15,9 @@
 // the weights then stream at HBM's pace.
 //
 // fp32, up to 24 tokens: on the CUDA cores (nys_few.cu), but for the gradients of
-// the weights. More: an operand is split into three bf16 terms, 24 bits in all, in a pass of
-// its own, and the product sums the six pairs that matter at 2^-24. bf16: dg and
-// du enter the products rounded to bf16, an error as large as the results' own
+// the weights. More: an operand is split into three bf16 terms, 24 bits in all, in a
+// pass of its own, and the product sums the six pairs that matter at 2^-24. bf16: dg
+// and du enter the products rounded to bf16, an error as large as the results' own
 // rounding; of few tokens, where nothing averages it and the weights' bytes bound
 // the time, as two terms (16 bits).
 #include <cuda_bf16.h>
@@ -133,8 +133,9 @@ struct GradParams {
 // dg, du as terms [1, 2 or (fp32) 3][T][f]. Eight elements per thread.
 template <typename T, int ACT>
 __global__ void __launch_bounds__(256)
-gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Splits more, const T* __restrict__ gate, const T* __restrict__ up, const T* __restrict__ gh,
-              __nv_bfloat16* __restrict__ dg, __nv_bfloat16* __restrict__ du) {
+gated_ff_back(const __grid_constant__ GradParams p, const __grid_constant__ Splits more, const T* __restrict__ gate,
+              const T* __restrict__ up, const T* __restrict__ gh, __nv_bfloat16* __restrict__ dg,
+              __nv_bfloat16* __restrict__ du) {
   cudaTriggerProgrammaticLaunchCompletion();
   cudaGridDependencySynchronize();
   if (sizeof(T) == 4 && blockIdx.x >= p.ctas) {
@@ -384,7 +385,8 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
   if (q.turned) {
     for (int i = 0; i < 2; ++i) ok = ok && (io ? map_mn(&maps.a[i], w[i]) : map_k(&maps.a[i], w[i], 128));
     ok = ok && map_k(&maps.b[0], xm, q.bn) &&
-         map_out(&maps.c[0], Matrix{ws + pl.part, a.f, q.bn, q.bn, 4, 2 * q.splits, (long long)a.f * q.bn}, q.bn == 16 ? 16 : 32);
+         map_out(&maps.c[0], Matrix{ws + pl.part, a.f, q.bn, q.bn, 4, 2 * q.splits, (long long)a.f * q.bn},
+                 q.bn == 16 ? 16 : 32);
   } else {
     ok = map_k(&maps.a[0], xm, 128);
     for (int i = 0; i < 2; ++i)
@@ -413,7 +415,8 @@ int forward(const nys_gated_ff_t& a, const Plan& pl, const void* x, const void* 
             : launch_pair<kBf16, false, false, kGated, __nv_bfloat16>("gated_ff", maps, p, st);
   }
   if (rc != NYS_OK || direct) return rc;
-  const JoinGated j{reinterpret_cast<const float*>(ws + pl.part), q.splits, a.T, a.f, q.line, h, gate, up, a.h, a.gate, a.up};
+  const JoinGated j{reinterpret_cast<const float*>(ws + pl.part), q.splits, a.T, a.f, q.line, h, gate, up, a.h, a.gate,
+                    a.up};
   return join_gated(j, a.act, a.dtype, st);
 }
 
@@ -543,11 +546,11 @@ int nystrom_gated_ff_fwd(const nys_gated_ff_t* p, const void* x, const void* w_g
   if (!x || !w_gate || !w_up || !h || (gate == nullptr) != (up == nullptr)) return NYS_ERR_ARG;
   const bool io = p->layout == NYS_FF_IN_OUT;
   const int wr = io ? p->d : p->f, wc = io ? p->f : p->d;
-  auto rows = [&](const void* at, long long stride, int n, int width, bool out) {
-    return at ? q8::check_rows(at, stride, n, width, p->dtype, out) : NYS_OK;
+  auto rows = [&](const void* at, long long stride, int n, int width, bool apart) {
+    return at ? q8::check_rows(at, stride, n, width, p->dtype, apart) : NYS_OK;
   };
-  if ((rc = rows(x, p->x, p->T, p->d, false)) != NYS_OK || (rc = rows(w_gate, p->w, wr, wc, false)) != NYS_OK ||
-      (rc = rows(w_up, p->w, wr, wc, false)) != NYS_OK || (rc = rows(h, p->h, p->T, p->f, true)) != NYS_OK ||
+  if ((rc = rows(x, p->x, p->T, p->d, true)) != NYS_OK || (rc = rows(w_gate, p->w, wr, wc, true)) != NYS_OK ||
+      (rc = rows(w_up, p->w, wr, wc, true)) != NYS_OK || (rc = rows(h, p->h, p->T, p->f, true)) != NYS_OK ||
       (rc = rows(gate, p->gate, p->T, p->f, true)) != NYS_OK || (rc = rows(up, p->up, p->T, p->f, true)) != NYS_OK)
     return rc;
   if (among(h, x, w_gate, w_up, gate, up) || among(gate, x, w_gate, w_up, up) || among(up, x, w_gate, w_up))
@@ -580,11 +583,11 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
     return NYS_ERR_ARG;
   const bool io = p->layout == NYS_FF_IN_OUT;
   const int wr = io ? p->d : p->f, wc = io ? p->f : p->d;
-  auto rows = [&](const void* at, long long stride, int n, int width, bool out) {
-    return at ? q8::check_rows(at, stride, n, width, p->dtype, out) : NYS_OK;
+  auto rows = [&](const void* at, long long stride, int n, int width, bool apart) {
+    return at ? q8::check_rows(at, stride, n, width, p->dtype, apart) : NYS_OK;
   };
-  if ((want_dw && (rc = rows(x, p->x, p->T, p->d, false)) != NYS_OK) ||
-      (dx && ((rc = rows(w_gate, p->w, wr, wc, false)) != NYS_OK || (rc = rows(w_up, p->w, wr, wc, false)) != NYS_OK)) ||
+  if ((want_dw && (rc = rows(x, p->x, p->T, p->d, true)) != NYS_OK) ||
+      (dx && ((rc = rows(w_gate, p->w, wr, wc, true)) != NYS_OK || (rc = rows(w_up, p->w, wr, wc, true)) != NYS_OK)) ||
       (rc = rows(gate, p->gate, p->T, p->f, false)) != NYS_OK || (rc = rows(up, p->up, p->T, p->f, false)) != NYS_OK ||
       (rc = rows(gh, p->h, p->T, p->f, false)) != NYS_OK || (rc = rows(dx, p->dx, p->T, p->d, true)) != NYS_OK ||
       (rc = rows(dw_gate, p->dw, wr, wc, true)) != NYS_OK || (rc = rows(dw_up, p->dw, wr, wc, true)) != NYS_OK)

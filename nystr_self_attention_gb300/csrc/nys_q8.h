@@ -64,24 +64,25 @@ __device__ __forceinline__ void store_scale(uint8_t* scales, int block, int bloc
     for (int j = 1; j < 4 - (block & 3); ++j) at[j] = 0;
 }
 
-// Host checks of a matrix; NYS_OK or the code of include/nystrom.h.
-inline int check_q8(const nys_q8_t* q, bool out) {
+// Host checks of a matrix; NYS_OK or the code of include/nystrom.h. apart: its rows
+// may not overlap (an output, or read by tensor maps).
+inline int check_q8(const nys_q8_t* q, bool apart) {
   if (!q || !q->codes || !q->scales) return NYS_ERR_ARG;
   if (q->rows < 1 || q->rows >= 0x7fffffff - 1023 || q->K < 1 || q->K % 16 || q->K > (1 << 20))
     return NYS_ERR_SHAPE;
-  if (q->stride < 0 || (out && q->rows > 1 && q->stride < q->K)) return NYS_ERR_ARG;
+  if (q->stride < 0) return NYS_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(q->codes) & 15u) || (reinterpret_cast<uintptr_t>(q->scales) & 3u) ||
       (q->rows > 1 && q->stride % 16))
     return NYS_ERR_ALIGN;
-  return q->codes == q->scales ? NYS_ERR_ARG : NYS_OK;
+  return q->codes == q->scales || (apart && q->rows > 1 && q->stride < q->K) ? NYS_ERR_ARG : NYS_OK;
 }
 
 // Host checks of a matrix of rows x `width` in dtype.
-inline int check_rows(const void* p, long long stride, int rows, int width, int dtype, bool out) {
+inline int check_rows(const void* p, long long stride, int rows, int width, int dtype, bool apart) {
   const long long per = dtype == NYS_FP32 ? 4 : 8;  // elements in 16 bytes
-  if (stride < 0 || (out && rows > 1 && stride < width)) return NYS_ERR_ARG;
+  if (stride < 0) return NYS_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(p) & 15u) || (rows > 1 && stride % per)) return NYS_ERR_ALIGN;
-  return NYS_OK;
+  return apart && rows > 1 && stride < width ? NYS_ERR_ARG : NYS_OK;
 }
 
 }  // namespace q8

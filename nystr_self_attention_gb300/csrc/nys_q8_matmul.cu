@@ -72,7 +72,7 @@ size_t nystrom_q8_matmul_workspace_bytes(int T, int N, int K, int dtype) {
 int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long out_stride, int dtype,
                       void* workspace, size_t ws_bytes, nys_stream_t stream) {
   int rc;
-  if ((rc = q8::check_q8(a, false)) != NYS_OK || (rc = q8::check_q8(w, false)) != NYS_OK) return rc;
+  if ((rc = q8::check_q8(a, true)) != NYS_OK || (rc = q8::check_q8(w, true)) != NYS_OK) return rc;
   if (!out || (dtype != NYS_FP32 && dtype != NYS_BF16)) return NYS_ERR_ARG;
   if (a->K != w->K) return NYS_ERR_SHAPE;
   const int T = a->rows, N = w->rows, K = a->K;

@@ -182,3 +182,24 @@ def test_ff_pointers(N):
         assert N.nystrom_gated_ff_workspace_bytes(ff(N), back) % 256 == 0
     assert N.nystrom_gated_ff_workspace_bytes(ff(N), True) > 0
     assert N.load_library().nystrom_gated_ff_workspace_bytes(ctypes.byref(ff(N)), 2) == 0
+
+
+def test_factors_rows_do_not_overlap(N):
+    lib = N.load_library()
+    over = [dict(a=0), dict(a=128), dict(w=0), dict(w=240)]  # bytes between rows of 256
+
+    def mm(a=256, w=256, T=4, n=64):
+        return lib.nystrom_q8_matmul(q8(N, 1024, 1536, T, 256, stride=a), q8(N, 2048, 4096, n, 256, stride=w), 8192, 64,
+                                     1, None, 0, None)
+    for kw in over:
+        assert mm(**kw) == E_ARG
+    for T in (4, 400):
+        for kw in (dict(x=0), dict(x=32), dict(w=0), dict(w=64)):
+            for dtype in (0, 1):
+                for layout in (0, 1):
+                    p = ff(N, T=T, dtype=dtype, layout=layout, **{**dict(w=128, dw=128), **kw})
+                    a = [256 * i for i in range(1, 10)]
+                    if layout == 1 and kw == dict(w=64):
+                        continue  # rows of 64: side by side
+                    assert lib.nystrom_gated_ff_fwd(ctypes.byref(p), *a[:6], None, 0, None) == E_ARG
+                    assert lib.nystrom_gated_ff_bwd(ctypes.byref(p), *a, None, 0, None) == E_ARG

@@ -306,6 +306,110 @@ def test_a_process_s_first_call_may_be_captured(which):
     assert r.returncode == 0, r.stderr[-2000:]
 
 
+# ------------------------------------------------- one row for all, one tensor twice
+
+def spread(t, rows):
+    """A row for all rows, at a stride of 0, and its copies."""
+    one = t[:1].expand(rows, t.shape[1])
+    return one, one.contiguous()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,d", [(7, 264), (600, 2056), (40, 8200), (900, 1032)])
+def test_norm_of_rows_that_overlap(rows, d, dtype):
+    import torch
+    import nystr_self_attention_gb300 as N
+    g = torch.Generator(device="cuda").manual_seed(rows)
+    x, r, w = (torch.randn(n, d, generator=g, device="cuda") for n in (rows, rows, 1))
+    x, r, w = x.to(tdtype(dtype)), r.to(tdtype(dtype)), w[0]
+    out = []
+    for one in zip(spread(x, rows), spread(r, rows)):
+        s, y = torch.empty_like(x), torch.empty_like(x)
+        N.nystrom_add_rms_norm_fwd(x, one[1], w, s, y)
+        N.nystrom_add_rms_norm_fwd(one[0], r, w, None, y2 := torch.empty_like(x))
+        dx, dw = torch.empty_like(x), torch.empty_like(w)
+        N.nystrom_add_rms_norm_bwd(one[0], x, one[1], w, dx, dw)
+        dx2, dw2 = torch.empty_like(x), torch.empty_like(w)
+        N.nystrom_add_rms_norm_bwd(x, one[1], one[0], w, dx2, dw2)
+        out.append([s, y, y2, dx, dw, dx2, dw2])
+    done(N)
+    assert same(*out)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("block", [1, 128])
+def test_eight_bits_of_rows_that_overlap(block, dtype):
+    import torch
+    import nystr_self_attention_gb300 as N
+    x = torch.randn(1, 1040, device="cuda").to(tdtype(dtype))
+    out = []
+    for one in spread(x, 300):
+        q = eight(N, 300, 1040)
+        N.nystrom_q8_write(q, one, block)
+        out.append([q.codes, q.scales])
+    assert same(*out)
+    codes = out[0][0][:1].expand(300, 1040)
+    back, want = torch.empty(300, 1040, device="cuda"), torch.empty(300, 1040, device="cuda")
+    N.nystrom_q8_read(N.NystromQ8(codes, out[0][1]), back)
+    N.nystrom_q8_read(N.NystromQ8(*out[0]), want)
+    done(N)
+    assert torch.equal(back, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 20, 100, 300])
+def test_gradients_of_one_row_for_all(T, dtype):
+    """gh of a sum over the tokens; g and u of one token."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    d, f = 136, 264
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, wg, wu, gate, up, gh = (torch.randn(s, generator=g, device="cuda").to(tdtype(dtype))
+                               for s in ((T, d), (d, f), (d, f), (T, f), (T, f), (T, f)))
+    out = []
+    for i in range(2):
+        dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+        N.nystrom_gated_ff_bwd(x, wg, wu, spread(gate, T)[i], spread(up, T)[i], spread(gh, T)[i], dx, dwg, dwu)
+        out.append([dx, dwg, dwu])
+    done(N)
+    assert same(*out)
+    h = torch.empty(T, f, dtype=x.dtype, device="cuda")
+    one = x[:1].expand(T, d)
+    for call in (lambda: N.nystrom_gated_ff_fwd(one, wg, wu, h),
+                 lambda: N.nystrom_gated_ff_bwd(one, wg, wu, gate, up, gh, None, dwg, dwu)):
+        with pytest.raises(N.NystromError):
+            call()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [3, 100, 300])
+def test_one_tensor_as_several_inputs(T, dtype):
+    import torch
+    import nystr_self_attention_gb300 as N
+    d = 136
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x, w = (torch.randn(s, generator=g, device="cuda").to(tdtype(dtype)) for s in ((T, d), (d, d)))
+    out = []
+    for many in (False, True):
+        t = (lambda a: a.clone()) if many else (lambda a: a)
+        h, dx, dwg, dwu = (torch.empty_like(a) for a in (x, x, w, w))
+        N.nystrom_gated_ff_fwd(x, w, t(w), h)
+        N.nystrom_gated_ff_bwd(x, w, t(w), t(x), t(x), t(x), dx, dwg, dwu)
+        y, s, dn = (torch.empty_like(x) for _ in range(3))
+        N.nystrom_add_rms_norm_fwd(x, t(x), None, s, y)
+        N.nystrom_add_rms_norm_bwd(x, t(x), t(x), None, dn)
+        q = eight(N, T // 8 * 8 or 8, 256)
+        N.nystrom_q8_write(q, torch.ones(q.rows, 256, device="cuda"))
+        p = eight(N, q.rows, 256)
+        N.nystrom_q8_write(p, torch.ones(q.rows, 256, device="cuda"))
+        o = torch.empty(q.rows, q.rows, device="cuda")
+        N.nystrom_q8_matmul(q, p if many else q, o)
+        out.append([h, dx, dwg, dwu, y, s, dn, o])
+    done(N)
+    assert same(*out)
+    assert bool((out[0][-1] == 256).all())
+
+
 # ------------------------------------------------------- past 32-bit offsets
 
 def test_norm_past_32_bits():
