@@ -70,9 +70,9 @@ struct Params {
                          // feed-forward of 16384 tokens, 16: 471, 32: 474, 64: 508)
   int act, keep;         // kGated
   int* status;
-  // 8-bit operands: scale words [groups][rows]
+  // 8-bit operands: scale words, groups of four K blocks x rows
   const uint32_t *a_scales, *b_scales;
-  int a_rows, b_rows, groups;
+  int a_rows, b_rows;
 };
 
 // One output tile of a CTA's walk.
@@ -288,11 +288,11 @@ template <typename Walk>
 struct ScaleWalk {
   Walk walk;
   int group;
-  __device__ __forceinline__ explicit ScaleWalk(const Params& p) : walk(p), group(walk.tile.it0 >> 2) {}
+  __device__ __forceinline__ explicit ScaleWalk(const Params& p) : walk(p), group(walk.more ? walk.tile.it0 >> 2 : 0) {}
   __device__ __forceinline__ void next(const Params& p) {
     if (++group <= (walk.tile.it1 - 1) >> 2) return;
     walk.next(p);
-    group = walk.tile.it0 >> 2;
+    if (walk.more) group = walk.tile.it0 >> 2;
   }
 };
 
@@ -957,12 +957,9 @@ inline bool map_out(CUtensorMap* map, const Matrix& x, int columns = 32) {
                   columns * x.esize == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B);
 }
 
-// Sums of the partial planes of a split product (nys_join.cu): part holds
-// planes of fp32, plane split * parts + part, each [M][N] (rows of a result) or,
-// of gemm_tokens, [N][width] (a result's columns, its rows side by side).
-// Results in dtype; set up while the product still runs.
-struct Line {  // gemm_tokens' division: a tile of 128 columns has the planes of its CTAs
-  int width;   // 0: not turned
+// gemm_tokens' division: a tile of 128 columns has the planes of its CTAs.
+struct Line {
+  int width;  // 0: not turned
   int m_tiles, units, ctas;
   long long line;
   __host__ __device__ __forceinline__ int planes(int part, int column) const {
@@ -970,11 +967,15 @@ struct Line {  // gemm_tokens' division: a tile of 128 columns has the planes of
     return line_cta(line, ctas, u + units - 1) - line_cta(line, ctas, u) + 1;
   }
 };
+// Sums of the partial planes of a split product (nys_join.cu): part holds
+// planes of fp32, plane split * parts + part, each [M][N] (rows of a result) or,
+// of gemm_tokens, [N][width] (a result's columns, its rows side by side).
+// Results in dtype; set up while the product still runs.
 struct Join {
   const float* part;
   int splits, M, N;
   Line line;
-  void* out[2];             // [M][N] of part 0, 1
+  void* out[2];  // [M][N] of part 0, 1
   long long stride[2];
 };
 int join(const Join& j, int parts, int dtype, cudaStream_t st);
@@ -1058,10 +1059,11 @@ inline int columns_of(int tokens) { return tokens <= 16 ? 16 : tokens <= 32 ? 32
 // first: (2,0) (0,2) (1,1) (1,0) (0,1) (0,0).
 constexpr uint32_t kTermsA = 0x001102, kTermsB = 0x010120;
 
-// How gemm_pair's product is cut: columns of a tile and ranges of K, whose partial sums are joined. The time of a choice is counted in
-// steps of a full tile (0.3 us; `pairs` of them for a K block of fp32): rounds of tiles over the CTAs times a tile's steps,
-// two more for its start and end, and for more than one range the join (ten
-// steps' time to begin, then its bytes, write and read, at 5 TB/s).
+// How gemm_pair's product is cut: columns of a tile and ranges of K, whose partial
+// sums are joined. The time of a choice is counted in steps of a full tile (0.3 us;
+// `pairs` of them for a K block of fp32): rounds of tiles over the CTAs times a
+// tile's steps, two more for its start and end, and for more than one range the join
+// (ten steps' time to begin, then its bytes, write and read, at 5 TB/s).
 struct Cut {
   int bn, splits;
 };
@@ -1088,8 +1090,8 @@ inline int most_planes(const Line& l) {
   const long long n = (l.units + least - 2) / least + 1;
   return (int)(n < l.ctas ? n : l.ctas);
 }
-inline Cut cut_pair(long long M, long long N, int steps, int unit, int pairs, int parts, int most_bn, int bn_step, bool gated,
-                    int least) {
+inline Cut cut_pair(long long M, long long N, int steps, int unit, int pairs, int parts, int most_bn, int bn_step,
+                    bool gated, int least) {
   const int clusters = plan_sms() / 2;
   Cut best{most_bn, 1};
   double best_time = 1e30;

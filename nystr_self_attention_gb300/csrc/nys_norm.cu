@@ -5,8 +5,8 @@
 // output.
 //
 // TPR threads share a row (or as many as it needs, where it has a CTA to itself), V
-// vectors of eight channels each; vector i of thread t is channels 8 (i TPR + t), so 16 neighbouring threads hold the 128 channels
-// of one 8-bit block. A CTA holds several short rows or one long one and walks
+// vectors of eight channels each; vector i of thread t is channels 8 (i TPR + t), so
+// 16 neighbouring threads hold the 128 channels of one 8-bit block. A CTA holds several short rows or one long one and walks
 // rows with the grid's step; the weight stays in registers, and the next row's
 // loads are in flight while this one is summed.
 #include <cuda_bf16.h>
@@ -193,7 +193,6 @@ constexpr int fwd_threads() {
 }
 constexpr int kBwdThreads = 512;
 constexpr int bwd_ctas(int threads) { return threads < kBwdThreads ? kBwdThreads / threads : 1; }  // per SM
-
 
 template <typename T, int TPR, int V, bool EIGHT, bool RES>
 __global__ void __launch_bounds__(threads_of(TPR), fwd_threads<T, TPR, RES>() / threads_of(TPR))
@@ -522,9 +521,9 @@ int check_common(const nys_add_rms_norm_t* p) {
 }
 
 // f(TPR, V) for a row of d channels: one vector per thread until a row has 1024
-// threads; backward (MORE), whose threads also carry the weight's sums, two until
-// it has 1024 as well. Forward to 8 bits, 65536 x 2048: 160 us with two, 149 with one;
-// backward, 16384 x 4096: 91 us with two, 95 with one.
+// threads; backward (MORE), whose threads also carry the weight's sums, two, and one
+// where a warp then holds a row. Forward to 8 bits, 65536 x 2048: 160 us with two,
+// 149 with one; backward, 16384 x 4096: 91 us with two, 95 with one.
 template <bool MORE, typename F>
 auto by_width(int d, F&& f) {
   using std::integral_constant;
