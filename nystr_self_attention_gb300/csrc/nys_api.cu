@@ -72,6 +72,29 @@ int check_args(const void* q, const void* k, const void* v, const float* conv_w,
   return NYS_OK;
 }
 
+int allow_shared(const void* kernel, size_t bytes) {
+  constexpr int kMostKernels = 256;  // the library has fewer
+  static std::mutex mu;
+  static struct {
+    const void* kernel;
+    size_t bytes[kMaxDevices];
+  } allowed[kMostKernels];
+  static int used = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return set_cuda_error(cudaGetLastError());
+  if (dev < 0 || dev >= kMaxDevices) return NYS_ERR_UNSUPPORTED;
+  std::lock_guard<std::mutex> lk(mu);
+  int i = 0;
+  while (i < used && allowed[i].kernel != kernel) ++i;
+  if (i == kMostKernels) return NYS_ERR_UNSUPPORTED;
+  if (i == used) allowed[used++].kernel = kernel;
+  if (bytes <= allowed[i].bytes[dev]) return NYS_OK;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes) != cudaSuccess)
+    return set_cuda_error(cudaGetLastError());
+  allowed[i].bytes[dev] = bytes;
+  return NYS_OK;
+}
+
 int plan_sms() {
   static int cache[kMaxDevices] = {0};
   int dev = 0;

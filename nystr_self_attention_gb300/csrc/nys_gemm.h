@@ -29,7 +29,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -1014,18 +1013,10 @@ inline Maps filled(Maps m) {
   return m;
 }
 
-// KERNEL with its dynamic shared memory, which a device is told of once.
 template <auto KERNEL>
 int start(const char* name, int grid, int threads, int bytes, const Maps& maps, const Params& p, cudaStream_t st) {
-  static std::atomic<unsigned long long> told{0};  // a bit per device
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return set_cuda_error(cudaGetLastError());
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(told.load(std::memory_order_relaxed) & bit)) {
-    if (cudaFuncSetAttribute(KERNEL, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-      return set_cuda_error(cudaGetLastError());
-    told.fetch_or(bit, std::memory_order_relaxed);
-  }
+  const int rc = allow_shared(reinterpret_cast<const void*>(KERNEL), bytes);
+  if (rc != NYS_OK) return rc;
   return launch_behind(name, KERNEL, dim3(grid), dim3(threads), bytes, st, filled(maps), p);
 }
 template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>

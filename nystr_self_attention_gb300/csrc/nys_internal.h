@@ -88,6 +88,11 @@ inline int launch_status() {
   const cudaError_t e = cudaGetLastError();
   return e == cudaSuccess ? NYS_OK : set_cuda_error(e);
 }
+// Lets `kernel` have `bytes` of dynamic shared memory on the current device. The
+// limit is the kernel's, not a call's, so it only ever rises: lowered to a smaller
+// call's size, another thread's launch between its own setting and its start would
+// fail.
+int allow_shared(const void* kernel, size_t bytes);
 // Launches a kernel that begins with cudaGridDependencySynchronize (or does so
 // before it touches memory): it may be set up while the kernel before it in the
 // stream still runs.

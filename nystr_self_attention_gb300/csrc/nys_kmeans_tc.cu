@@ -485,19 +485,12 @@ int launch_kmeans_round_tc(const Shape& s, const void* q, const void* mu3, const
   p.off_oh = k.off_oh;
   const dim3 grid((unsigned)k.S, (unsigned)BH);
   {
+    auto kern = k.dch == 1 ? kmeans_round_tc<1> : kmeans_round_tc<2>;
+    int rc = allow_shared(reinterpret_cast<const void*>(kern), k.smem);
+    if (rc != NYS_OK) return rc;
     KernelScope scope("kmeans_round_tc", st);
-    if (k.dch == 1) {
-      if (cudaFuncSetAttribute(kmeans_round_tc<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)k.smem) != cudaSuccess)
-        return set_cuda_error(cudaGetLastError());
-      kmeans_round_tc<1><<<grid, kThreads, k.smem, st>>>(maps, p);
-    } else {
-      if (cudaFuncSetAttribute(kmeans_round_tc<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               (int)k.smem) != cudaSuccess)
-        return set_cuda_error(cudaGetLastError());
-      kmeans_round_tc<2><<<grid, kThreads, k.smem, st>>>(maps, p);
-    }
-    const int rc = launch_status();
+    kern<<<grid, kThreads, k.smem, st>>>(maps, p);
+    rc = launch_status();
     if (rc != NYS_OK) return rc;
   }
   KernelScope scope("kmeans_reduce", st);

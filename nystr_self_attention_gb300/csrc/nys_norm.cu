@@ -606,9 +606,10 @@ int launch_bwd(const nys_add_rms_norm_t& a, const void* s, const void* gy, const
     constexpr int GROUPS = THREADS / TPR;
     const int threads = cta_threads<TPR, V>(a.d);
     auto go = [&](auto kernel, size_t smem) {
-      if (smem > 32 * 1024 &&  // 48 KB with what is static
-          cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-        return set_cuda_error(cudaGetLastError());
+      if (smem > 32 * 1024) {  // 48 KB with what is static
+        const int rc = allow_shared(reinterpret_cast<const void*>(kernel), smem);
+        if (rc != NYS_OK) return rc;
+      }
       return launch_behind("add_rms_norm_back", kernel, dim3(back_grid<TPR, V>(a)), dim3(threads), smem, st, p,
                            static_cast<const T*>(s), static_cast<const T*>(gy), static_cast<const T*>(gs), weight,
                            static_cast<T*>(dx), part);

@@ -984,9 +984,9 @@ int launch_pinv_tc(const Shape& s, const float* qt, const float* kt, const float
            : three ? (MP == 32 ? pinv_tc<32, false, true> : (MP == 64 ? pinv_tc<64, false, true> : pinv_tc<128, false, true>))
                    : (MP == 32 ? pinv_tc<32, false, false> : (MP == 64 ? pinv_tc<64, false, false> : pinv_tc<128, false, false>));
   // (two CTAs per SM for MP <= 64: the largest shared-memory carveout)
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+  const int rc = allow_shared(reinterpret_cast<const void*>(kern), smem);
+  if (rc != NYS_OK) return rc;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
   const unsigned grid = (unsigned)((p.BH + p.hp - 1) / p.hp);
   KernelScope scope("pinv_tc", stream);
@@ -1017,9 +1017,9 @@ int launch_w_tc(const Shape& s, const float* z, const float* g, float* w, void* 
   else if (NC == 32) kern = MP == 32 ? w_tc<32, 32> : (MP == 64 ? w_tc<64, 32> : w_tc<128, 32>);
   else kern = MP == 32 ? w_tc<32, 64> : (MP == 64 ? w_tc<64, 64> : w_tc<128, 64>);
   // three CTAs per SM: the largest shared-memory carveout
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess ||
-      cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
+  const int rc = allow_shared(reinterpret_cast<const void*>(kern), smem);
+  if (rc != NYS_OK) return rc;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess)
     return set_cuda_error(cudaGetLastError());
   KernelScope scope("w_tc", stream);
   kern<<<dim3((unsigned)(s.d / NC), (unsigned)s.bh()), kThreads, smem, stream>>>(p);

@@ -690,8 +690,8 @@ int launch_rows_tc(const Shape& s, const void* qt_bf16, const void* k, const voi
   const size_t smem = qbytes + stage + ns * tile + 1024;
   const int grid = (p.total + p.tpc - 1) / p.tpc;
   auto kern = DP == 64 ? rows_tc<64> : rows_tc<128>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
+  const int rc = allow_shared(reinterpret_cast<const void*>(kern), smem);
+  if (rc != NYS_OK) return rc;
   KernelScope scope("rows_tc", stream);
   kern<<<grid, kThreads, smem, stream>>>(maps, p);
   return launch_status();

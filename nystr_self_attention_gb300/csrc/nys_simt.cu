@@ -979,9 +979,10 @@ int conv_mask_t(const Shape& s, const void* v, const float* conv_w, void* out, c
   const size_t smem = s.ks > 0 ? nbuf * vbuf + taps : 0;
   auto kern = per_channel ? (narrow ? conv_mask<T, true, true> : conv_mask<T, true, false>)
                           : (narrow ? conv_mask<T, false, true> : conv_mask<T, false, false>);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
+  if (smem > 48 * 1024) {
+    const int rc = allow_shared(reinterpret_cast<const void*>(kern), smem);
+    if (rc != NYS_OK) return rc;
+  }
   KernelScope ks_("conv_mask", stream);
   // blocks per CTA: up to CV_BLOCKS (the taps staged once for all of them),
   // fewer where that would leave SMs idle. (One wave of longer CTAs, sized
@@ -1048,10 +1049,10 @@ int tokens_t(const Shape& s, const void* q, const void* v, const float* kt, cons
   const int rad = s.ks > 0 ? (s.ks - 1) / 2 : 0;
   const size_t smem = sizeof(float) * (TK_ROWS * s.d + TK_LM * (s.d + 1) + TK_LM * s.d +
                                        TK_ROWS * 33 + 2 * TK_ROWS + (TK_ROWS + 2 * rad) * s.d);
-  if (smem > 48 * 1024 &&
-      cudaFuncSetAttribute(tokens_simt<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           (int)smem) != cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
+  if (smem > 48 * 1024) {
+    const int rc = allow_shared(reinterpret_cast<const void*>(tokens_simt<T>), smem);
+    if (rc != NYS_OK) return rc;
+  }
   KernelScope ks_("tokens_simt", stream);
   tokens_simt<T><<<dim3((s.n + TK_ROWS - 1) / TK_ROWS, (unsigned)s.bh()), 256, smem, stream>>>(
       static_cast<const T*>(q), static_cast<const T*>(v), kt, w, conv_w, static_cast<T*>(out), s.H,

@@ -446,9 +446,8 @@ int launch_tokens_big(const Shape& s, const void* q, const void* v, const void* 
   p.off_qv = p.off_t + pl.t_bytes;
   p.off_stage = p.off_qv + pl.qv_bytes;
   p.nbox = pl.nbox;
-  if (cudaFuncSetAttribute(tokens_big, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem) !=
-      cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
+  const int rc = allow_shared(reinterpret_cast<const void*>(tokens_big), pl.smem);
+  if (rc != NYS_OK) return rc;
   KernelScope scope("tokens_big", stream);
   tokens_big<<<grid, kThreads, pl.smem, stream>>>(maps, p);
   return launch_status();

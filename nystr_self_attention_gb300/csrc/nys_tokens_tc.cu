@@ -686,9 +686,8 @@ int launch_tokens_tc(const Shape& s, const void* q, const void* v, const void* k
   p.off_l = p.off_t + p.nt * p.t_bytes;
 
   auto kern = DP == 64 ? tokens_tc<64> : tokens_tc<128>;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)pl.smem) !=
-      cudaSuccess)
-    return set_cuda_error(cudaGetLastError());
+  const int rc = allow_shared(reinterpret_cast<const void*>(kern), pl.smem);
+  if (rc != NYS_OK) return rc;
   KernelScope scope("tokens_tc", stream);
   kern<<<grid, kThreads, pl.smem, stream>>>(maps, p);
   return launch_status();
