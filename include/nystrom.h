@@ -44,11 +44,12 @@
  *  - Thread safety: calls may come from several host threads; the cached
  *    workspace of nystrom_attn_fwd is shared per device, so concurrent calls
  *    on different streams of one device must use nystrom_attn_fwd_ws with
- *    their own workspaces. The same holds for the cached workspace that
- *    nystrom_qk_norm_rope_bwd and nystrom_kv4_attn_fwd use where none is given:
- *    they are two kernels with the workspace between them, which no other
- *    thread's call of theirs separates, but on another stream they may run at
- *    the same time.
+ *    their own workspaces. nystrom_qk_norm_rope_bwd, nystrom_kv4_attn_fwd,
+ *    nystrom_q8_matmul, nystrom_add_rms_norm_bwd, nystrom_gated_ff_fwd and
+ *    nystrom_gated_ff_bwd share another one where none is given. Those calls may
+ *    come from any threads and streams: one whose stream is not the last one's
+ *    waits there, on the device, for the last one's kernels. Calls that shall
+ *    run side by side are given workspaces.
  */
 #ifndef NYSTROM_H_
 #define NYSTROM_H_

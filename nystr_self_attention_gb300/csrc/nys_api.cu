@@ -140,12 +140,15 @@ struct DeviceCache {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   void* last_ws = nullptr;  // status word of the most recent call
-  // the operators around a cached attention layer: their cached workspace, held
-  // by one call at a time, and their status word (operator_workspace,
-  // operator_status)
+  // the operators around a cached attention layer and the attention module: their
+  // cached workspace (OperatorWorkspace) with an event behind its last call and that
+  // call's stream, and their status word (operator_status)
   std::mutex op_mu;
   void* op_ws = nullptr;
   size_t op_ws_bytes = 0;
+  cudaEvent_t op_done = nullptr;
+  bool op_pending = false;  // the event was recorded, behind a call on this stream:
+  unsigned long long op_stream = 0;
   int* op_status = nullptr;
   void* stage = nullptr;    // host-entry staging buffers
   size_t stage_bytes = 0;
@@ -210,8 +213,7 @@ namespace {
 __device__ int g_op_status;
 }  // namespace
 
-int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out,
-                       std::unique_lock<std::mutex>* held) {
+int OperatorWorkspace::take(int dev, size_t bytes, cudaStream_t stream, void** out) {
   // a graph would keep the buffer's address past the next growth
   cudaStreamCaptureStatus capturing = cudaStreamCaptureStatusNone;
   if (cudaStreamIsCapturing(stream, &capturing) != cudaSuccess) {
@@ -219,10 +221,34 @@ int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out,
     return NYS_ERR_ARG;
   }
   if (capturing != cudaStreamCaptureStatusNone) return NYS_ERR_ARG;
-  *held = std::unique_lock<std::mutex>(g_dev[dev].op_mu);
-  const int rc = ensure_buffer(&g_dev[dev].op_ws, &g_dev[dev].op_ws_bytes, bytes, stream);
-  if (rc == NYS_OK) *out = g_dev[dev].op_ws;
-  return rc;
+  DeviceCache& dc = g_dev[dev];
+  std::unique_lock<std::mutex> lk(dc.op_mu);
+  unsigned long long id = 0;  // unlike a handle, not used again when a stream is destroyed
+  cudaError_t e = cudaStreamGetId(stream, &id);
+  if (e == cudaSuccess && !dc.op_done) e = cudaEventCreateWithFlags(&dc.op_done, cudaEventDisableTiming);
+  if (e == cudaSuccess && dc.op_pending && id != dc.op_stream) e = cudaStreamWaitEvent(stream, dc.op_done, 0);
+  if (e != cudaSuccess) {
+    cudaGetLastError();
+    return set_cuda_error(e);
+  }
+  const int rc = ensure_buffer(&dc.op_ws, &dc.op_ws_bytes, bytes, stream);
+  if (rc != NYS_OK) return rc;
+  dc.op_stream = id;
+  *out = dc.op_ws;
+  held_ = std::move(lk);
+  dev_ = dev;
+  stream_ = stream;
+  return NYS_OK;
+}
+
+OperatorWorkspace::~OperatorWorkspace() {
+  if (!held_.owns_lock()) return;
+  DeviceCache& dc = g_dev[dev_];
+  dc.op_pending = cudaEventRecord(dc.op_done, stream_) == cudaSuccess;
+  if (!dc.op_pending) {  // nothing to wait for later: wait now
+    cudaGetLastError();
+    cudaStreamSynchronize(stream_);
+  }
 }
 
 int operator_status(int dev, int** out) {

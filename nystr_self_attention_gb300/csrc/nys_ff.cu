@@ -23,7 +23,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
 
 #include "nys_gemm.h"
 #include "nys_q8.h"
@@ -562,9 +561,9 @@ int nystrom_gated_ff_fwd(const nys_gated_ff_t* p, const void* x, const void* w_g
   }
   int dev = 0;
   if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (pl.total && !workspace) {
-    rc = operator_workspace(dev, pl.total, stream, &workspace, &held);
+    rc = own.take(dev, pl.total, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   int* status = nullptr;
@@ -602,9 +601,9 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
   }
   int dev = 0;
   if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (!workspace) {
-    rc = operator_workspace(dev, pl.total, stream, &workspace, &held);
+    rc = own.take(dev, pl.total, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   int* status = nullptr;

@@ -116,13 +116,24 @@ inline bool apart_or_same_rows(const void* out, const nys_strides_t& os, const v
 // The library's cached workspace of this device, grown to `bytes` (NULL and
 // *rc < 0 on failure).
 void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc);
-// The cached workspace of the operators around a cached attention layer, in a
-// buffer of its own (nystrom_get_status reads the other one's first word).
-// NYS_ERR_ARG while `stream` is being captured. *held keeps other threads from
-// it: the caller holds on until all its kernels are enqueued, so that no other
-// call's come in between.
-int operator_workspace(int dev, size_t bytes, cudaStream_t stream, void** out,
-                       std::unique_lock<std::mutex>* held);
+// The cached workspace of the operators around a cached attention layer and
+// around the attention module, in a buffer of its own. One call has it at a time,
+// from take() to the end of the object's life, by which all its kernels are
+// enqueued; an event behind them keeps the next call back if that one's stream is
+// another. take: NYS_ERR_ARG while `stream` is being captured.
+class OperatorWorkspace {
+ public:
+  OperatorWorkspace() = default;
+  ~OperatorWorkspace();
+  OperatorWorkspace(const OperatorWorkspace&) = delete;
+  OperatorWorkspace& operator=(const OperatorWorkspace&) = delete;
+  int take(int dev, size_t bytes, cudaStream_t stream, void** out);
+
+ private:
+  std::unique_lock<std::mutex> held_;
+  int dev_ = 0;
+  cudaStream_t stream_ = nullptr;
+};
 // Device address of those operators' status word on device `dev` (current):
 // zero until a kernel sets it, cleared when nystrom_get_status reports it.
 int operator_status(int dev, int** out);

@@ -943,9 +943,9 @@ int nystrom_kv4_attn_fwd(const nys_kv4_cache_t* cache, const void* q, void* out,
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
   if (!apart_or_same_rows(out, *out_strides, q, *q_strides, B, Hq, nq)) return NYS_ERR_ARG;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (!workspace && pl.total > 0) {
-    rc = operator_workspace(dev, pl.total, stream, &workspace, &held);
+    rc = own.take(dev, pl.total, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   AttnParams p{};

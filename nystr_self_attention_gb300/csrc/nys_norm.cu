@@ -13,7 +13,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 
 #include "nys_q8.h"
 #include "nys_sm100.h"
@@ -700,9 +699,9 @@ int nystrom_add_rms_norm_bwd(const nys_add_rms_norm_t* p, const void* s, const v
   int dev = 0;
   rc = check_device(&dev);
   if (rc != NYS_OK) return rc;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (dweight && !workspace) {
-    rc = operator_workspace(dev, need, stream, &workspace, &held);
+    rc = own.take(dev, need, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   float* part = dweight ? static_cast<float*>(workspace) : nullptr;

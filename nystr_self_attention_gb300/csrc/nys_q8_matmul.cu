@@ -11,7 +11,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <mutex>
 
 #include "nys_gemm.h"
 #include "nys_q8.h"
@@ -86,9 +85,9 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   }
   int dev = 0;
   if ((rc = check_device(&dev)) != NYS_OK || (rc = have_context(dev)) != NYS_OK) return rc;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (plan.bytes && !workspace) {
-    rc = operator_workspace(dev, plan.bytes, stream, &workspace, &held);
+    rc = own.take(dev, plan.bytes, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   const nys_q8_t &rows = plan.turned ? *w : *a, &cols = plan.turned ? *a : *w;

@@ -784,9 +784,9 @@ int nystrom_qk_norm_rope_bwd(const nys_qk_rope_t* a, const void* q, const void* 
                     dk == gq))
     return NYS_ERR_ARG;
   if (dq_weight && dq_weight == dk_weight) return NYS_ERR_ARG;
-  std::unique_lock<std::mutex> held;
+  OperatorWorkspace own;
   if (sums && !workspace) {
-    rc = operator_workspace(dev, need, stream, &workspace, &held);
+    rc = own.take(dev, need, stream, &workspace);
     if (rc != NYS_OK) return rc;
   }
   const Grid g = grid_of(*a, true);

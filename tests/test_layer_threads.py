@@ -1,4 +1,5 @@
-"""Calls of different sizes from two host threads at once."""
+"""Calls of different sizes from two host threads at once, and of one thread on two
+streams without workspaces."""
 import ctypes
 import threading
 
@@ -105,3 +106,69 @@ def test_attention_of_two_sizes(dtype, sizes):
     torch.cuda.synchronize()
     own_status(N)  # nystrom_get_status reads the last call's workspace, one of these
     assert all(torch.equal(outs[0], w) for (_, outs), w in zip(made, want))
+
+
+def partial_sums(seed):
+    """Calls of C entries that keep something in a workspace between their kernels:
+    (call on a stream, outputs) of each."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    from layer_helpers import eight
+    lib = N.load_library()
+    g = torch.Generator(device="cuda").manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=g, device="cuda")
+    made = []
+    a, w, out = eight(N, 200, 8192), eight(N, 264, 8192), torch.empty(200, 264, device="cuda")
+    N.nystrom_q8_write(a, randn(200, 8192))
+    N.nystrom_q8_write(w, randn(264, 8192))
+    made.append((lambda st: lib.nystrom_q8_matmul(a.desc, w.desc, out.data_ptr(), 264, N.NYS_FP32, None, 0, st), [out],
+                 (a, w)))
+    T, d, f = 150, 520, 1032
+    x, wg, wu, gh = randn(T, d), randn(d, f), randn(d, f), randn(T, f)
+    h, gate, up = (torch.empty(T, f, device="cuda") for _ in range(3))
+    ff = N.NysGatedFf(T, d, f, 0, 0, N.NYS_FP32, d, f, f, f, f, d, f)
+    made.append((lambda st: lib.nystrom_gated_ff_fwd(ctypes.byref(ff), x.data_ptr(), wg.data_ptr(), wu.data_ptr(),
+                                                     h.data_ptr(), gate.data_ptr(), up.data_ptr(), None, 0, st),
+                 [h, gate, up], (x, wg, wu, ff)))
+    kept = randn(T, f), randn(T, f)
+    dx, dwg, dwu = torch.empty_like(x), torch.empty_like(wg), torch.empty_like(wu)
+    made.append((lambda st: lib.nystrom_gated_ff_bwd(
+        ctypes.byref(ff), x.data_ptr(), wg.data_ptr(), wu.data_ptr(), kept[0].data_ptr(), kept[1].data_ptr(),
+        gh.data_ptr(), dx.data_ptr(), dwg.data_ptr(), dwu.data_ptr(), None, 0, st), [dx, dwg, dwu], (kept, gh)))
+    s, gy = randn(3000, 1032), randn(3000, 1032)
+    ds, dw = torch.empty_like(s), torch.empty(1032, device="cuda")
+    norm = N.NysAddRmsNorm(3000, 1032, N.NYS_FP32, 1e-6, *[1032] * 6)
+    made.append((lambda st: lib.nystrom_add_rms_norm_bwd(ctypes.byref(norm), s.data_ptr(), gy.data_ptr(), None, None,
+                                                         ds.data_ptr(), dw.data_ptr(), None, 0, st), [ds, dw], (s, gy, norm)))
+    return made
+
+
+def test_two_streams_without_workspaces():
+    """The library's workspace passes from one stream's call to the other's."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    made = [partial_sums(1), partial_sums(2)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    busy = torch.zeros(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    want = []
+    for m in made:
+        for call, outs, _ in m:
+            assert call(0) == N.NYS_OK
+            torch.cuda.synchronize()
+            want.append([t.clone() for t in outs])
+    for turn in range(12):
+        for t in (t for m in made for _, outs, _ in m for t in outs):
+            t.fill_(3.0)
+        torch.cuda.synchronize()
+        with torch.cuda.stream(streams[turn % 2]):
+            busy.add_(1.0)
+        for i in range(4):
+            for m, st in zip(made, streams):
+                assert m[(i + turn) % 4][0](st.cuda_stream) == N.NYS_OK
+        torch.cuda.synchronize()
+        got = [outs for m in made for _, outs, _ in m]
+        assert all(torch.equal(a, b) for o, w in zip(got, want) for a, b in zip(o, w))
+    done(N)
