@@ -313,7 +313,7 @@ Params params_of(const Product& q, int parts, int a_terms, int b_terms, int a_by
   p.bn = q.bn;
   p.unit = pairs > 2 ? pairs : 2;
   p.units = q.line.units;
-  p.chunk = pairs > 2 ? pairs : q.its + (q.its & 1);  // fp32: the six products of a K block
+  p.chunk = pairs > 2 ? pairs : kLongest;  // fp32: the six products of a K block
   p.a_by = a_by;
   p.b_by = b_by;
   p.group = 16;

@@ -21,9 +21,12 @@
 // lie. Coordinates past a matrix's end read zeros and are not stored.
 //
 // The matrix units cut sums off towards zero: 120 instructions in a row leave
-// 2e-6 of a result, too much for fp32. Kernels with fp32 results therefore sum a
-// few K blocks at a time in TMEM and add those sums in registers, rounding to
-// nearest (relative error 1e-7).
+// 2e-6 of a result (of values of both signs; of one sign each takes up to 1e-7 of
+// the sum), too much for fp32. Kernels with fp32 results therefore sum a few K
+// blocks at a time in TMEM and add those sums in registers, rounding to nearest
+// (relative error 1e-7). So do those with bf16 results whose K takes more than
+// kLongest steps: 2^20 tokens of one sign left 0.6 % of a weight's gradient, always
+// towards zero, and leave 0.01 % so.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -43,6 +46,7 @@ namespace gemm {
 using namespace nys::sm100;
 
 constexpr uint64_t kWaitNs = 2000000000ull;
+constexpr int kLongest = 256;  // steps, of four instructions, summed in TMEM for bf16 results
 
 enum Kind { kBf16, kMx8 };
 enum Epilogue { kPlain, kGated };
@@ -60,7 +64,7 @@ struct Params {
   int k_blocks;          // 128-byte blocks of one K part
   int its, its_per_split;  // K parts x k_blocks x pairs
   int bn;                // columns of a tile (gemm_pair)
-  int chunk;             // steps (even) summed in TMEM before the sum moves to registers (fp32 results)
+  int chunk;             // steps (even) summed in TMEM before the sum moves to registers
   int pairs;             // products of the operands' terms that are summed: 1, 2 or 6
   uint32_t a_terms, b_terms;  // the terms of pair i in nibble i
   int a_by, b_by;        // By
@@ -398,12 +402,12 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
 
 // Tiles of 256 rows x p.bn columns, a multiple of 32; EPI kGated: half of them are
 // the gate's (B of the first CTA), half the same columns of the other projection
-// (B of the second), bn is a multiple of 64, and the result has bn / 2.
-template <int KIND, bool AMN, bool BMN, int EPI, typename OutT>
+// (B of the second), bn is a multiple of 64, and the result has bn / 2. SUM: sums
+// move to registers every p.chunk steps; else K is a single chunk.
+template <int KIND, bool AMN, bool BMN, int EPI, typename OutT, bool SUM>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(PairLayout<KIND, OutT>::kThreads, 1)
 gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
   using L = PairLayout<KIND, OutT>;
-  constexpr bool kSum = sizeof(OutT) == 4;  // sums move to registers
   extern __shared__ uint8_t raw[];
   uint8_t* sm = align1024(raw);
   uint8_t* staging = sm + L::kRing;
@@ -520,7 +524,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
         for (int it = tile.it0; it < tile.it1; it += L::kSteps) {
           const bool first = left == 0;
           if (first) {
-            left = kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
+            left = SUM ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
             d = tmem + (nc & 1) * L::kCols;
             if (nc >= 2 && !warp_wait(&bars.acc_empty[nc & 1], (nc / 2 - 1) & 1, p.status, abort_flag)) {
               ok = false;
@@ -591,7 +595,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
     for (GridWalk walk(p); ok && walk.more; walk.next(p)) {
       const Tile& tile = walk.tile;
       float f[4][32];  // a lane's row: columns of the result, or of g (0, 1) and u (2, 3)
-      if (kSum) {
+      if (SUM) {
 #pragma unroll
         for (int i = 0; i < 128; ++i) f[i / 32][i % 32] = 0.f;
       }
@@ -608,7 +612,7 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
           const int c = (2 * (i % kTurns) + half) * 32;  // of the result
           if (c >= width) continue;
           const uint32_t at = d + c + (i >= kTurns ? width : 0);
-          if constexpr (!kSum) {
+          if constexpr (!SUM) {
             tmem_ld32(at, reinterpret_cast<uint32_t(&)[4][32]>(f)[i]);
           } else {
 #pragma unroll
@@ -621,12 +625,12 @@ gemm_pair(const __grid_constant__ Maps maps, const __grid_constant__ Params p) {
             }
           }
         }
-        if (!kSum) tmem_ld_wait();
+        if (!SUM) tmem_ld_wait();
         tc_fence_before_sync();
         __syncwarp();
         if (lane == 0) arrive_in_first(&bars.acc_empty[nc & 1]);
         ++nc;
-        it += kSum ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
+        it += SUM ? min(p.chunk, tile.it1 - it) : tile.it1 - it;
       }
       if (!ok) break;
       const int y = tile.m * 256 + rank * 128 + quarter * 32, x = tile.n * width;
@@ -1013,6 +1017,7 @@ inline Maps filled(Maps m) {
   return m;
 }
 
+// KERNEL with its dynamic shared memory.
 template <auto KERNEL>
 int start(const char* name, int grid, int threads, int bytes, const Maps& maps, const Params& p, cudaStream_t st) {
   const int rc = allow_shared(reinterpret_cast<const void*>(KERNEL), bytes);
@@ -1025,8 +1030,11 @@ int launch_pair(const char* name, const Maps& maps, const Params& p, cudaStream_
   const long long tiles = (long long)p.m_tiles * p.n_tiles * p.parts * p.splits;
   if (tiles >= (1ll << 31) - 1024) return NYS_ERR_SHAPE;
   const int most = plan_sms() / 2;
-  return start<gemm_pair<KIND, AMN, BMN, EPI, OutT>>(name, 2 * (tiles < most ? (int)tiles : most), L::kThreads,
-                                                     L::kBytes, maps, p, st);
+  const int grid = 2 * (tiles < most ? (int)tiles : most);
+  if constexpr (sizeof(OutT) == 2)
+    if (p.its_per_split <= p.chunk)
+      return start<gemm_pair<KIND, AMN, BMN, EPI, OutT, false>>(name, grid, L::kThreads, L::kBytes, maps, p, st);
+  return start<gemm_pair<KIND, AMN, BMN, EPI, OutT, true>>(name, grid, L::kThreads, L::kBytes, maps, p, st);
 }
 template <int KIND, bool AMN>
 int launch_tokens(const char* name, int bn, int ctas, const Maps& maps, const Params& p, cudaStream_t st) {

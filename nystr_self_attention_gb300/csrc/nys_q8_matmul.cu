@@ -102,7 +102,6 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   p.k_blocks = p.its = (K + 127) / 128;
   p.its_per_split = plan.its_per_split;
   p.bn = plan.bn;
-  p.chunk = 8;
   p.group = 16;
   p.a_scales = static_cast<const uint32_t*>(rows.scales);
   p.b_scales = static_cast<const uint32_t*>(cols.scales);
@@ -111,6 +110,7 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
   Maps maps{};
   bool ok = map_k(&maps.a[0], codes_of(rows), 128) && map_k(&maps.b[0], codes_of(cols), plan.turned ? plan.bn : plan.bn / 2);
   const bool direct = !plan.turned && plan.splits == 1;
+  p.chunk = direct && dtype == NYS_BF16 ? kLongest : 8;
   if (direct)
     ok = ok && map_out(&maps.c[0], Matrix{out, T, N, out_stride, dtype == NYS_FP32 ? 4 : 2});
   else if (plan.turned)
