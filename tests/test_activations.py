@@ -1,0 +1,61 @@
+"""The feed-forward product's activations far from zero, against fp64.
+
+With z the exponential's argument (silu: g; gelu_tanh: 1.6 (g + 0.045 g^3), off by
+4 u |z|, u = 2^-24): the exponential is off by (2 + 1.173 |z|) units of 2^-23 (bf16:
+the documented bound of __expf; expf's is smaller), the division by two, the
+products and the sum by three in all, so a factor of the activation is off by
+(8 + 3.3 |z|) 2^-23 of itself. gelu: erfc is off by four units, its argument y by
+2 u of itself, erfc by 2 y^2 times that (its logarithmic slope is below 2 y + 2 / y):
+(8 + 4 y^2) 2^-23. A factor below fp32's normal range is off by up to 2^-149
+besides, which g multiplies."""
+import numpy as np
+import pytest
+
+from layer_helpers import ACTS, HALF, act_code, done, empty, host, own_status, upload
+from oracle import layer_ref as R
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    import torch
+    from nystr_self_attention_gb300 import build
+    build.build()
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    torch.cuda.set_device(0)
+    import nystr_self_attention_gb300 as N
+    own_status(N)
+
+
+GATES = np.array([-104, -100, -95, -92, -90, -89, -88.5, -88, -87, -80, -60, -40, -30, -20, -14, -13, -12, -11, -10,
+                  -9.5, -9, -8, -6, -4, -2, -1, -0.5, 0, 0.5, 1, 2, 4, 8, 16, 30, 60, 88, 90, 100, 104])
+
+
+def relative(g, name):
+    if name == "relu":
+        return np.zeros_like(g)
+    if name == "gelu":
+        return (8 + 2 * g * g) * 2.0 ** -23
+    z = g if name == "silu" else 1.5957691216057308 * (g + 0.044715 * g ** 3)
+    return (8 + 3.3 * np.abs(z)) * 2.0 ** -23
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("T", [4, 100, 200])
+def test_values(T, name, dtype):
+    """g comes as it is: one of x's channels times one."""
+    import nystr_self_attention_gb300 as N
+    x, wg, wu = np.zeros((T, 16)), np.zeros((16, 40)), np.zeros((16, 40))
+    x[:, 0], wg[0] = 1.0, GATES
+    x[:, 1], wu[1] = 1.0, 1.0
+    h = empty(T, 40, dtype)
+    N.nystrom_gated_ff_fwd(upload(x, dtype), upload(wg, dtype), upload(wu, dtype), h, activation=act_code(N, name))
+    done(N)
+    g = R.rounded(GATES, dtype)
+    with np.errstate(over="ignore"):
+        want = R.act(g, name)[0]
+    least = np.abs(g) * 2.0 ** -149 + 2.0 ** -149 + (2.0 ** -134 if dtype == "bf16" else 0)
+    bound = (relative(g, name) + HALF[dtype]) * np.abs(want) + least
+    assert (np.abs(host(h) - want) <= bound).all()
