@@ -54,7 +54,8 @@ __device__ __forceinline__ void with_slope(float g, float& a, float& slope) {
   } else if (ACT == NYS_ACT_GELU_TANH) {
     const Sigmoid y = sigmoid<FAST>(g * fmaf(kTanh3, g * g, kTanh1));
     a = g * y.s;
-    slope = fmaf(g * y.s * y.rest, fmaf(3.f * kTanh3, g * g, kTanh1), y.s);
+    // from |g| = 16 on one of the factors is 0; g^2 itself would pass fp32's range
+    slope = fmaf(g * y.s * y.rest, fmaf(3.f * kTanh3, fminf(g * g, 256.f), kTanh1), y.s);
   } else {
     a = value<NYS_ACT_RELU, FAST>(g);
     slope = g > 0.f ? 1.f : (g != g ? g : 0.f);

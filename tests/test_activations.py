@@ -59,3 +59,23 @@ def test_values(T, name, dtype):
     least = np.abs(g) * 2.0 ** -149 + 2.0 ** -149 + (2.0 ** -134 if dtype == "bf16" else 0)
     bound = (relative(g, name) + HALF[dtype]) * np.abs(want) + least
     assert (np.abs(host(h) - want) <= bound).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("name", ACTS)
+@pytest.mark.parametrize("T", [8, 136])
+def test_slopes_of_large_gates(T, name, dtype):
+    """dg = act'(g), du = act(g), read through the weights' gradients of an identity.
+    Slopes of these gates are 0 or 1 (|g| e^-|g| is below 1e-127); the sigmoid's own
+    error and the terms' are below 2^-20."""
+    import nystr_self_attention_gb300 as N
+    gates = np.array([-3e38, -1e30, -1e20, -4.5e19, -2e19, -1e10, -1e4, -300, 300, 1e4, 1e10, 2e19, 4.5e19, 1e20, 1e30, 3e38])
+    g = R.rounded(np.repeat(gates[None], T, 0), dtype)
+    one, eye, w = np.ones((T, 16)), np.eye(T), np.ones((T, 16))
+    dwg, dwu = empty(T, 16, dtype), empty(T, 16, dtype)
+    N.nystrom_gated_ff_bwd(upload(eye, dtype), upload(w, dtype), upload(w, dtype), upload(g, dtype), upload(one, dtype),
+                           upload(one, dtype), None, dwg, dwu, activation=act_code(N, name))
+    done(N)
+    slope, value = (g > 0).astype(float), np.where(g > 0, g, 0.0)
+    assert (np.abs(host(dwg) - slope) <= 2.0 ** -20 * slope).all()
+    assert (np.abs(host(dwu) - value) <= (2.0 ** -20 + HALF[dtype]) * value).all()
