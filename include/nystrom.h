@@ -667,9 +667,10 @@ int nystrom_gated_ff_bwd(const nys_gated_ff_t* p, const void* x, const void* w_g
 
 /*
  * nystrom_get_status - waits for `stream`, then returns and clears the
- * device-side status word of the most recent call on the current device
- * (NYS_OK, or NYS_ERR_TIMEOUT if a bounded wait inside a kernel ran out),
- * then that of the cache operators and of those around the attention module
+ * device-side status word of the most recent forward call on the current device
+ * (NYS_OK, or NYS_ERR_TIMEOUT if a bounded wait inside a kernel ran out; the
+ * word is the library's, not part of a workspace, and a call that runs at the
+ * same time on another stream sets the same one), then that of the cache operators and of those around the attention module
  * (NYS_ERR_INDEX of nystrom_kv4_*, NYS_ERR_TIMEOUT since it was last read).
  * Returns NYS_ERR_CUDA if the stream reports an error.
  */

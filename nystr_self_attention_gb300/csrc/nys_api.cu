@@ -139,7 +139,7 @@ struct DeviceCache {
   std::mutex mu;
   void* ws = nullptr;
   size_t ws_bytes = 0;
-  void* last_ws = nullptr;  // status word of the most recent call
+  int* status = nullptr;  // the forward calls' status word (begin_call)
   // the operators around a cached attention layer and the attention module: their
   // cached workspace (OperatorWorkspace) with an event behind its last call and that
   // call's stream, and their status word (operator_status)
@@ -188,17 +188,31 @@ int ensure_buffer(void** ptr, size_t* have, size_t need, cudaStream_t stream) {
 
 }  // namespace
 
-int begin_call(char* ws, const Layout& L, cudaStream_t stream, int dev, bool clear_status) {
-  {
-    std::lock_guard<std::mutex> lk(g_dev[dev].mu);
-    g_dev[dev].last_ws = ws;
-  }
-  // each call starts with a clear status word (kernels only ever set it)
-  if (clear_status) {
-    cudaError_t e = cudaMemsetAsync(ws + L.status, 0, sizeof(int), stream);
+namespace {
+// Set by kernels, read and cleared by nystrom_get_status: that of the forward calls,
+// which each of them clears as it begins, and that of the operators. Device
+// variables: no call has to allocate them, and no workspace's end takes them away.
+__device__ int g_status, g_op_status;
+
+int status_word(int dev, int* DeviceCache::*known, const int& symbol, int** out) {
+  std::lock_guard<std::mutex> lk(g_dev[dev].mu);
+  int*& at = g_dev[dev].*known;
+  if (!at) {
+    void* p = nullptr;
+    const cudaError_t e = cudaGetSymbolAddress(&p, symbol);
     if (e != cudaSuccess) return set_cuda_error(e);
+    at = static_cast<int*>(p);
   }
+  *out = at;
   return NYS_OK;
+}
+}  // namespace
+
+int begin_call(cudaStream_t stream, int dev, int** status, bool clear_status) {
+  const int rc = status_word(dev, &DeviceCache::status, g_status, status);
+  if (rc != NYS_OK || !clear_status) return rc;
+  const cudaError_t e = cudaMemsetAsync(*status, 0, sizeof(int), stream);
+  return e == cudaSuccess ? NYS_OK : set_cuda_error(e);
 }
 
 void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc) {
@@ -206,12 +220,6 @@ void* cached_workspace(int dev, size_t bytes, cudaStream_t stream, int* rc) {
   *rc = ensure_buffer(&g_dev[dev].ws, &g_dev[dev].ws_bytes, bytes, stream);
   return *rc == NYS_OK ? g_dev[dev].ws : nullptr;
 }
-
-namespace {
-// Set by the cache operators' kernels, read and cleared by
-// nystrom_get_status. A device variable: no call has to allocate or clear it.
-__device__ int g_op_status;
-}  // namespace
 
 int OperatorWorkspace::take(int dev, size_t bytes, cudaStream_t stream, void** out) {
   // a graph would keep the buffer's address past the next growth
@@ -252,23 +260,16 @@ OperatorWorkspace::~OperatorWorkspace() {
 }
 
 int operator_status(int dev, int** out) {
-  std::lock_guard<std::mutex> lk(g_dev[dev].mu);
-  if (!g_dev[dev].op_status) {
-    void* p = nullptr;
-    const cudaError_t e = cudaGetSymbolAddress(&p, g_op_status);
-    if (e != cudaSuccess) return set_cuda_error(e);
-    g_dev[dev].op_status = static_cast<int*>(p);
-  }
-  *out = g_dev[dev].op_status;
-  return NYS_OK;
+  return status_word(dev, &DeviceCache::op_status, g_op_status, out);
 }
 
 int run(const Shape& s, const void* q, const void* k, const void* v, const float* conv_w,
         void* out, char* ws, cudaStream_t stream, int dev, bool clear_status) {
   const Layout L = make_layout(s);
-  const int rc = begin_call(ws, L, stream, dev, clear_status);
+  int* status = nullptr;
+  const int rc = begin_call(stream, dev, &status, clear_status);
   if (rc != NYS_OK) return rc;
-  return launch_forward(s, q, k, v, conv_w, out, ws, L, stream, dev);
+  return launch_forward(s, q, k, v, conv_w, out, ws, L, status, stream, dev);
 }
 
 int scratch_mats(const Shape& s) { return pinv_big_supported(s) ? 5 : 3; }
@@ -296,7 +297,6 @@ Layout make_layout(const Shape& s) {
   }
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off = align256(off + bytes); return o; };
-  L.status = take(256);
   L.q_tilde = take(bh * md * 4);
   L.k_tilde = take(bh * md * 4);
   L.g_part = take(bh * L.splits * md * 4);
@@ -540,13 +540,13 @@ int nystrom_get_status(nys_stream_t stream) {
   if (rc != NYS_OK) return rc;
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return set_cuda_error(e);
-  void* words[2];  // the most recent forward call's, the cache operators'
+  int* words[2];  // the forward calls', the operators'; null before the first one
   {
     std::lock_guard<std::mutex> lk(g_dev[dev].mu);
-    words[0] = g_dev[dev].last_ws;
+    words[0] = g_dev[dev].status;
     words[1] = g_dev[dev].op_status;
   }
-  for (void* word : words) {
+  for (int* word : words) {
     if (!word) continue;
     int status = 0;
     if ((e = cudaMemcpy(&status, word, sizeof(int), cudaMemcpyDeviceToHost)) != cudaSuccess)

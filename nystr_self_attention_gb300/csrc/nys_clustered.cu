@@ -171,7 +171,7 @@ broadcast_rows(const float* __restrict__ g, const int* __restrict__ assign, T* _
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 struct ClusteredLayout {
-  Layout attn;  // the landmark-row partials, G, the status word, scratch
+  Layout attn;  // the landmark-row partials, G, scratch
   size_t assign, mu_a, mu_b, total;
   bool tc;                          // K-means on the tensor cores
   size_t mu3, norms, part, cnt;     // its workspace (tc only)
@@ -287,7 +287,8 @@ int nystrom_clustered_attn_fwd(const void* q, const void* k, const void* v, void
     ws = static_cast<char*>(cached_workspace(dev, L.total, stream, &rc));
     if (!ws) return rc;
   }
-  rc = begin_call(ws, L.attn, stream, dev);
+  int* status = nullptr;
+  rc = begin_call(stream, dev, &status);
   if (rc != NYS_OK) return rc;
   const bool bf16 = dtype == NYS_BF16;
   auto at = [&](size_t off) { return ws + off; };
@@ -296,7 +297,6 @@ int nystrom_clustered_attn_fwd(const void* q, const void* k, const void* v, void
   // initial centroids: segment means of Q (K is not read)
   rc = launch_landmarks(s, q, nullptr, mu[0], nullptr, nullptr, nullptr, stream);
   if (rc != NYS_OK) return error_in("initial centroids", rc);
-  int* status = reinterpret_cast<int*>(at(L.attn.status));
   int cur = 0;
   if (L.tc) {
     void* mu3 = at(L.mu3);

@@ -89,7 +89,7 @@ T* at(char* ws, size_t off) { return reinterpret_cast<T*>(ws + off); }
 // batch entries: bh0 is a multiple of H).
 int run_group(const Shape& full, const Shape& sg_in, long long bh0, const void* q, const void* k,
               const void* v, const float* conv_w, void* out, char* ws, const Layout& L,
-              cudaStream_t st, DeviceStreams* beside) {
+              int* status, cudaStream_t st, DeviceStreams* beside) {
   Shape sg = sg_in;
   if (full.lengths) sg.lengths = full.lengths + bh0 / full.H;
   const size_t esz = full.dtype == NYS_FP32 ? 4 : 2;
@@ -109,7 +109,6 @@ int run_group(const Shape& full, const Shape& sg_in, long long bh0, const void* 
   float* z = at<float>(ws, L.z) + bh0 * mm;
   float* w = at<float>(ws, L.w) + bh0 * md;
   float* scr = at<float>(ws, L.scratch) + bh0 * scratch_mats(full) * mm;
-  int* status = at<int>(ws, L.status);
   const bool bf16 = full.dtype == NYS_BF16;
   const bool tc_tokens = tokens_tc_smem(full) > 0;
   const bool big_tokens = !tc_tokens && tokens_big_supported(full);
@@ -177,23 +176,23 @@ int rows_tc_ctas(const Shape& s) {
 }
 
 int launch_forward(const Shape& s, const void* q, const void* k, const void* v,
-                   const float* conv_w, void* out, char* ws, const Layout& L,
+                   const float* conv_w, void* out, char* ws, const Layout& L, int* status,
                    cudaStream_t stream, int dev) {
   const int groups = choose_groups(s);
   const bool beside = groups <= 1 && z_beside_rows(s);
-  if (groups <= 1 && !beside) return run_group(s, s, 0, q, k, v, conv_w, out, ws, L, stream, nullptr);
+  if (groups <= 1 && !beside) return run_group(s, s, 0, q, k, v, conv_w, out, ws, L, status, stream, nullptr);
   int rc = ensure_streams(dev);
   if (rc != NYS_OK) return rc;
   DeviceStreams& d = g_streams[dev];
   std::lock_guard<std::mutex> lk(d.enqueue);
-  if (beside) return run_group(s, s, 0, q, k, v, conv_w, out, ws, L, stream, &d);
+  if (beside) return run_group(s, s, 0, q, k, v, conv_w, out, ws, L, status, stream, &d);
   cudaError_t e = cudaEventRecord(d.fork, stream);
   for (int i = 1; i < groups && e == cudaSuccess; ++i) e = cudaStreamWaitEvent(d.aux[i], d.fork, 0);
   if (e != cudaSuccess) return set_cuda_error(e);
   Shape sg = s;
   sg.B = s.B / groups;
   for (int i = 0; i < groups; ++i) {
-    rc = run_group(s, sg, (long long)i * sg.bh(), q, k, v, conv_w, out, ws, L,
+    rc = run_group(s, sg, (long long)i * sg.bh(), q, k, v, conv_w, out, ws, L, status,
                    i == 0 ? stream : d.aux[i], nullptr);
     if (rc != NYS_OK) return rc;
   }

@@ -32,7 +32,6 @@ struct Shape {
 // Byte offsets of the workspace regions (all 256-byte aligned). Every
 // region is per head, head-major (b*H + h).
 struct Layout {
-  size_t status;   // int32 status word (+ padding)
   size_t q_tilde;  // f32 [m][d]
   size_t k_tilde;  // f32 [m][d]
   size_t g_part;   // f32 [splits][m][d]  unnormalised partial sums
@@ -103,9 +102,10 @@ int check_shape(int B, int H, int n, int d, int m, int iters, int ks, int dtype)
 int check_args(const void* q, const void* k, const void* v, const float* conv_w, const void* out,
                int B, int H, int n, int d, int m, int iters, int ks, int dtype);
 int check_device(int* dev_out);  // current device, must be compute capability 10.3
-// Makes `ws` the workspace nystrom_get_status reads for this device and
-// clears its status word on `stream` (unless told not to).
-int begin_call(char* ws, const Layout& L, cudaStream_t stream, int dev, bool clear_status = true);
+// Device address of the forward calls' status word on device `dev` (current),
+// cleared on `stream` (unless told not to). It is the library's own: a caller's
+// workspace is the caller's again when nystrom_get_status reads the word.
+int begin_call(cudaStream_t stream, int dev, int** status, bool clear_status = true);
 // Whether an output at the address of an input has its rows in the same places
 // (an axis with one entry has no stride); at another address, true.
 inline bool apart_or_same_rows(const void* out, const nys_strides_t& os, const void* in,
@@ -270,10 +270,10 @@ int launch_pinv_big(const Shape& s, const float* qt, const float* kt, const floa
 std::string describe_plan(const Shape& s);
 
 // Enqueue the whole forward pass (nys_forward.cu). Pointers are device
-// pointers; ws has Layout::total bytes; dev is the current device. Returns
-// NYS_OK or NYS_ERR_CUDA (a failed launch).
+// pointers; ws has Layout::total bytes; dev is the current device, status its
+// status word. Returns NYS_OK or NYS_ERR_CUDA (a failed launch).
 int launch_forward(const Shape& s, const void* q, const void* k, const void* v,
-                   const float* conv_w, void* out, char* ws, const Layout& L,
+                   const float* conv_w, void* out, char* ws, const Layout& L, int* status,
                    cudaStream_t stream, int dev);
 
 template <typename... Formal, typename... Actual>
