@@ -361,14 +361,14 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
     bulk_load(to + row_bytes, gy + r * p.y, row_bytes, bar);
     if (gs) bulk_load(to + 2 * row_bytes, gs + r * p.gs, row_bytes, bar);
   };
-  int nth = 0;  // of the CTA's rows
+  int nth = 0, filled = 0;  // of the CTA's rows; slots filled (the thread that fills them)
   if (RING) {
     if (threadIdx.x == 0) {
       abort_flag = 0;
       for (int i = 0; i < p.ring; ++i) sm100::mbar_init(&full[i], 1);
       sm100::fence_barrier_init();
-      for (int i = 0, r = row; i < p.ring && r < p.rows; ++i) {
-        fill(r, i);
+      for (int r = row; filled < p.ring && r < p.rows; ++filled) {
+        fill(r, filled);
         r = r < p.rows - step ? r + step : p.rows;
       }
     }
@@ -430,7 +430,7 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
     row_sums<TPR, 2>(total, slots, phase);
     auto refill = [&] {  // behind a barrier: every thread has read the slot
       const long long later = row + (long long)p.ring * step;
-      if (threadIdx.x == 0 && later < p.rows && !abort_flag) fill((int)later, nth + p.ring);
+      if (threadIdx.x == 0 && later < p.rows && !abort_flag) fill((int)later, filled++);
       ++nth;
     };
     if (RING && !TWICE) refill();
@@ -463,6 +463,10 @@ add_rms_norm_back(const NormParams p, const T* s, const T* gy, const T* gs, cons
     }
     if (next == p.rows) break;  // row + step may pass 2^31
   }
+  // where a wait ran out: nothing may land in shared memory behind the kernel's end
+  if (RING && threadIdx.x == 0 && abort_flag)
+    for (int i = filled > p.ring ? filled - p.ring : 0; i < filled; ++i)
+      sm100::mbar_wait(&full[i % p.ring], i / p.ring & 1, nullptr, 2000000000ull);
   if (!part) return;
   float* dst = part + (size_t)blockIdx.x * p.d;
   if constexpr (GROUPS == 1) {
