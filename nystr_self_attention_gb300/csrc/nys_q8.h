@@ -70,7 +70,7 @@ inline int check_q8(const nys_q8_t* q, bool apart) {
   if (!q || !q->codes || !q->scales) return NYS_ERR_ARG;
   if (q->rows < 1 || q->rows >= 0x7fffffff - 1023 || q->K < 1 || q->K % 16 || q->K > (1 << 20))
     return NYS_ERR_SHAPE;
-  if (q->stride < 0) return NYS_ERR_ARG;
+  if (q->rows > 1 && q->stride < 0) return NYS_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(q->codes) & 15u) || (reinterpret_cast<uintptr_t>(q->scales) & 3u) ||
       (q->rows > 1 && q->stride % 16))
     return NYS_ERR_ALIGN;
@@ -80,7 +80,7 @@ inline int check_q8(const nys_q8_t* q, bool apart) {
 // Host checks of a matrix of rows x `width` in dtype.
 inline int check_rows(const void* p, long long stride, int rows, int width, int dtype, bool apart) {
   const long long per = dtype == NYS_FP32 ? 4 : 8;  // elements in 16 bytes
-  if (stride < 0) return NYS_ERR_ARG;
+  if (rows > 1 && stride < 0) return NYS_ERR_ARG;
   if ((reinterpret_cast<uintptr_t>(p) & 15u) || (rows > 1 && stride % per)) return NYS_ERR_ALIGN;
   return apart && rows > 1 && stride < width ? NYS_ERR_ARG : NYS_OK;
 }

@@ -203,3 +203,20 @@ def test_factors_rows_do_not_overlap(N):
                         continue  # rows of 64: side by side
                     assert lib.nystrom_gated_ff_fwd(ctypes.byref(p), *a[:6], None, 0, None) == E_ARG
                     assert lib.nystrom_gated_ff_bwd(ctypes.byref(p), *a, None, 0, None) == E_ARG
+
+
+def test_the_stride_of_a_single_row_does_not_matter(N):
+    """Any stride is taken: what is refused is the workspace."""
+    lib = N.load_library()
+    for stride in (-16, -5, 3, 0):
+        one = dict(x=stride, h=stride, gate=stride, up=stride, dx=stride)
+        a = [256 * i for i in range(1, 10)]
+        for ws, nbytes, code in ((128, 1 << 30, E_ALIGN), (256, 8, E_NOMEM)):
+            assert lib.nystrom_q8_matmul(q8(N, 1024, 1536, 1, 256, stride=stride), q8(N, 2048, 4096, 64, 256), 8192,
+                                         stride, 1, ws, nbytes, None) == code
+            p = norm(N, rows=1, **{k: stride for k in ("x", "residual", "sum", "y", "gs", "dx")})
+            assert lib.nystrom_add_rms_norm_bwd(p, 256, 512, 1024, 16, 2048, 64, ws, nbytes, None) == code
+            for dtype in (0, 1):
+                f = ctypes.byref(ff(N, T=1, dtype=dtype, **one))
+                assert lib.nystrom_gated_ff_fwd(f, *a[:6], ws, nbytes, None) == code
+                assert lib.nystrom_gated_ff_bwd(f, *a, ws, nbytes, None) == code
