@@ -79,3 +79,35 @@ def test_slopes_of_large_gates(T, name, dtype):
     slope, value = (g > 0).astype(float), np.where(g > 0, g, 0.0)
     assert (np.abs(host(dwg) - slope) <= 2.0 ** -20 * slope).all()
     assert (np.abs(host(dwu) - value) <= (2.0 ** -20 + HALF[dtype]) * value).all()
+
+
+def test_relu_gradients_against_differences():
+    """Away from its corner: gh is 0 where a gate is nearer to 0 than the step can
+    move it. The loss is of second degree there, so the difference is exact but for
+    what g and u are off by, 20 u of the sums of their magnitudes (64 products summed
+    in order by 8 warps, u = 2^-24), in both losses, and the like in dx itself."""
+    import torch
+    import nystr_self_attention_gb300 as N
+    torch.manual_seed(3)
+    T, d, f, e = 6, 64, 128, 2.0 ** -5
+    x, wg, wu, gh = (torch.randn(s, device="cuda") for s in ((T, d), (d, f), (d, f), (T, f)))
+    wg, wu = wg / 8, wu / 8
+    h, g, u = (torch.empty(T, f, device="cuda") for _ in range(3))
+    N.nystrom_gated_ff_fwd(x, wg, wu, h, g, u, activation=N.NYS_ACT_RELU)
+    gh[g.abs() <= 2 * e * wg.abs().amax(0)] = 0.0
+    assert float((gh != 0).float().mean()) > 0.8
+
+    def loss(x_):
+        N.nystrom_gated_ff_fwd(x_, wg, wu, h, activation=N.NYS_ACT_RELU)
+        return float((h.double() * gh).sum())
+    dx = torch.empty_like(x)
+    N.nystrom_gated_ff_bwd(x, wg, wu, g, u, gh, dx, activation=N.NYS_ACT_RELU)
+    eg, eu = (20 * 2.0 ** -24 * (x.abs() @ w.abs()) for w in (wg, wu))
+    off = float((gh.abs() * (eg * u.abs() + eu * g.abs())).sum())
+    for i in ((0, 0), (3, 17), (5, 63)):
+        up, down = x.clone(), x.clone()
+        up[i] += e
+        down[i] -= e
+        diff = (loss(up) - loss(down)) / (2 * e)
+        assert abs(diff - float(dx[i])) <= 2 * off / (2 * e) + 2.0 ** -18
+    done(N)

@@ -177,3 +177,26 @@ def test_refusals_in_python():
         N.nystrom_q8_matmul(q, q, torch.zeros(4, 8, device="cuda"))
     with pytest.raises(N.NystromError):
         N.nystrom_q8_matmul(q, q, torch.zeros(4, 4, device="cuda"))  # columns in eights
+
+
+def test_write_ties_and_borders_with_their_signs():
+    """The codes of test_write_ties_and_borders bit for bit, and those of negative
+    zeros and of values that round to one."""
+    import nystr_self_attention_gb300 as N
+    mags = R.VALUES[:127]
+    mid = (mags[1:] + mags[:-1]) / 2
+    x = np.zeros((8, 128), np.float64)
+    x[0, :126], x[1, :126] = mid, -mid
+    above, below = (np.nextafter(mid.astype(np.float32), np.float32(v)) for v in (np.inf, 0))
+    x[2, :126], x[3, :126], x[4, :126] = above, below, -below
+    x[:5, 127] = 448
+    x[5, ::2] = -0.0
+    x[6, :3], x[7, :3] = (-448, -2.0 ** -10, 2.0 ** -10), (-3.3e38, -1.0, 1.0)
+    for turned in (False, True):
+        for block in (1, 128):
+            codes, bytes_ = R.q8_write(x, block)
+            q = eight(N, 8, 128)
+            N.nystrom_q8_write(q, upload(x.T, "f32").T if turned else upload(x, "f32"), block)
+            done(N)
+            assert (q.scales.cpu().numpy() == R.q8_words(bytes_)).all()
+            assert (q.codes.cpu().numpy() == codes).all()
