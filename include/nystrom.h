@@ -583,6 +583,8 @@ int nystrom_q8_matmul(const nys_q8_t* a, const nys_q8_t* w, void* out, long long
  * nystrom_add_rms_norm_fwd - the residual's addition and the norm of the sum:
  *   s = x + residual, rounded to dtype (residual NULL: s = x, sum NULL)
  *   y = weight * s / sqrt(mean(s^2) + eps)
+ * The sum of squares is fp32: a row whose sum passes 3.4e38 (values of 1e17 and more)
+ * has y = 0, and with eps = 0 one whose sum is below 1e-45 has infinities or NaN.
  * x, residual, sum, y: [rows][d] in `dtype`, row strides p->x, p->residual,
  * p->sum, p->y. weight: device float [d], or NULL for all ones. sum and y may each
  * be x or residual (same address and stride). In place of y, y8: an 8-bit

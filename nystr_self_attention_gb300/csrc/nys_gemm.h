@@ -3,10 +3,10 @@
 //
 // Two kernels, both persistent: a warp issues the TMA copies, one the products,
 // and others carry finished tiles out while the next ones run. A step of K is 128
-// bytes, 64 bf16 or 128 e4m3, four instructions. A stage is a step of bf16 (two:
-// 670,000 against 700,000 cycles for a gradient of the input) or two steps of 8
-// bits, whose products are issued with their scales (one: 690,000 cycles for 65536
-// x 4096 x 2048, two: 620,000).
+// bytes, 64 bf16 or 128 e4m3, four instructions. A stage of gemm_pair is one step of
+// bf16 (a gradient of the input: 670,000 cycles; with two, 700,000) or two steps of 8
+// bits, whose products are issued with their scales (65536 x 4096 x 2048: 620,000
+// cycles; with one, 690,000).
 //   gemm_pair: tiles of 256 x 256 by a cluster of two CTAs. Each holds half of A's
 //     rows and half of B's in shared memory and the instruction reads both CTAs'
 //     halves of B, so a CTA fetches 32 KB per step where a tile of its own would

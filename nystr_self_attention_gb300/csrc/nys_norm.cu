@@ -249,8 +249,10 @@ add_rms_norm(const NormParams p, const T* x, const T* res, const float* __restri
     }
     total[0] = squares.x + squares.y;
     fetch(row < p.rows - step ? row + step : p.rows);
-    // To 8 bits, y is rounded to fp32 once (2^-24): a code next to a border then
-    // differs from the exact one's as rarely as fp32 can have it.
+    // To 8 bits, y carries half the error of the fp32 sum of squares (a thread's and
+    // a warp's share of it: 10 or 14 roundings in a row; the sums across warps keep
+    // theirs) and one rounding of its own. A code next to a border may then differ
+    // from the exact one's; in the form below the product and the root add to that.
     float2 root;
     if (EIGHT) {
       root = exact_root<TPR>(total[0], slots, roots, phase, (float)p.d, p.inv_d, p.eps);
